@@ -44,7 +44,7 @@ extern "C" {
 struct CUstream_st;
 typedef struct CUstream_st *satk_stream_t;
 
-enum satk_dtype { SATK_F32 = 0, SATK_BF16 = 1 };
+enum satk_dtype { SATK_F32 = 0, SATK_BF16 = 1, SATK_F16 = 2 };
 enum satk_format { SATK_PAIRS_F32 = 0, SATK_PACKED_BF16 = 1 };
 
 enum satk_rc {
@@ -62,7 +62,16 @@ enum satk_rc {
                                         on the cut: fewer than K ids kept   */
 #define SATK_STATUS_BAD_REQUEST 4    /* satk_dcp_emit_rows: a req_id outside
                                         the block table; that row emits
-                                        nothing                             */
+                                        nothing (also satk_latent_attend)   */
+#define SATK_STATUS_NO_BLOCK 8       /* satk_step_tables: a token on this rank
+                                        has no block (free list or table
+                                        width used up); its slot is -1      */
+#define SATK_STATUS_TOO_MANY_TOKENS 16 /* satk_step_tables: more new tokens
+                                        than the token arrays hold          */
+#define SATK_STATUS_BAD_ROW 32       /* a physical row outside the cache (or
+                                        above 2**31 - 1 in a slot): skipped  */
+#define SATK_STATUS_BAD_POSITION 64  /* satk_latent_store: a position outside
+                                        the cos/sin table; token skipped    */
 
 /* Largest K of satk_topk_rows and of the rescue push. */
 #define SATK_TOPK_MAX_K 4096
@@ -301,6 +310,231 @@ int satk_dcp_emit_rows(const int32_t *ids, int64_t T, int32_t k, int64_t ld_ids,
                        int32_t *rows_out, int64_t ld_rows_out,
                        int32_t *valid_out, int32_t *status,
                        satk_stream_t stream);
+
+/* Largest request count of satk_step_tables. */
+#define SATK_TABLES_MAX_REQUESTS 8192
+/* Largest latent width and rotated tail of the latent operators, the widest
+ * query/key and value of one head of the expanded form, and the most ranks of
+ * a merge. */
+#define SATK_LATENT_MAX 512
+#define SATK_LATENT_TAIL_MAX 64
+#define SATK_EXPANDED_MAX_QK 256
+#define SATK_EXPANDED_MAX_V 128
+#define SATK_LATENT_MAX_RANKS 64
+
+/*
+ * The latent cache.  A cached token is one row of `dl` latent values followed
+ * by `dr` rotated values, all 16-bit (`dtype` SATK_BF16 or SATK_F16); a key is
+ * the whole row, a value its first dl columns.  Rows are addressed as
+ * satk_dcp_emit_rows does it: token l of a request (its local index on this
+ * rank) lives in row block_table[req][l / block_size] * stride_rows +
+ * l % block_size.  The attention calls below share these rules:
+ *  - softmax over the keys a token sees of scale * (query . key); sums and
+ *    statistics in 32 bits, the weights rounded to `dtype` before the product
+ *    with the values, the output rounded once;
+ *  - a token that sees no key gets an output of zeros and an lse of -inf;
+ *  - lse (nullable, float [T, H] contiguous) is the natural logarithm of the
+ *    sum of exp(score), what satk_latent_merge takes;
+ *  - keys that no token of a call's row group sees are not read; infinities
+ *    and NaN in keys that a token does not see do not reach its output.  A
+ *    non-finite key row that it does see may make its whole output row NaN.
+ */
+
+/*
+ * satk_step_tables -- the metadata of one step from request lengths: extends
+ * the block table and writes, per new token, what satk_topk_rows,
+ * satk_dcp_emit_rows, satk_latent_store and satk_latent_attend take.
+ *
+ * context_lens, new_lens : int32 [R], tokens of each request before the step
+ *               and new in it (global counts; negative counts as 0).  Global
+ *               token p belongs to rank p % W as its local token p / W.
+ * free_blocks : int32 [n_free], physical blocks, taken from the front in
+ *               request order.
+ * block_table : int32 [R, ld_block_table], extended in place: columns
+ *               [ceil(local(context) / block_size), ceil(local(context + new)
+ *               / block_size)) receive free blocks, others are not written.
+ *               local(p) = tokens below p that dcp_rank holds.
+ * T           : capacity of the per-token arrays.  New tokens come in request
+ *               order, each request's in position order; entries past the
+ *               last one get req_id 0, position 0, row_end 0, slot -1.
+ * drafted     : 0: row_ends[t] = local(position + 1) (causal, the token
+ *               itself included); 1: local(context) for every token of the
+ *               request (tokens of a drafted tree, whose own visibility is a
+ *               mask).
+ * token_starts: int32 [R + 1], first token of each request and the total,
+ *               each at most T.  lens: int32 [R], local tokens after the step.
+ * req_id, positions, row_ends, slots : int32 [T].  slots: the physical row of
+ *               a token this rank holds, else -1.
+ * blocks_used : int32 [1], blocks taken from free_blocks.
+ * Errors : SATK_EINVAL for a NULL pointer (free_blocks may be NULL when n_free
+ *          is 0; lens/token arrays may not), R or T or n_free negative or
+ *          >= 2**31, W < 1, dcp_rank outside [0, W), block_size < 1,
+ *          stride_rows < 0, max_blocks < 0, ld_block_table < max_blocks,
+ *          drafted not 0 or 1; SATK_EUNSUPPORTED for R >
+ *          SATK_TABLES_MAX_REQUESTS.
+ */
+int satk_step_tables(const int32_t *context_lens, const int32_t *new_lens,
+                     int32_t R, int32_t W, int32_t dcp_rank,
+                     int32_t block_size, int64_t stride_rows,
+                     const int32_t *free_blocks, int64_t n_free,
+                     int32_t *block_table, int64_t ld_block_table,
+                     int32_t max_blocks, int32_t drafted, int64_t T,
+                     int32_t *token_starts, int32_t *lens, int32_t *req_id,
+                     int32_t *positions, int32_t *row_ends, int32_t *slots,
+                     int32_t *blocks_used, int32_t *status,
+                     satk_stream_t stream);
+
+/*
+ * satk_latent_store -- writes new tokens into the latent cache: row slots[t]
+ * receives [latent * rsqrt(mean(latent^2) + eps) * weight | rotated tail].
+ *
+ * latent  : [T, ld_latent] of `dtype`, dl columns; weight: nullable float [dl]
+ *           (NULL: the latent is stored as it is, no norm).
+ * tail    : [T, ld_tail] of `dtype`, dr columns (NULL when dr is 0);
+ *           cos_sin: nullable float [n_positions, dr], dr/2 cosines then dr/2
+ *           sines; positions: int32 [T] (NULL cos_sin: stored as it is).
+ *           Pair i is columns (i, i + dr/2), or (2i, 2i + 1) when
+ *           `interleaved`; (a, b) becomes (a cos - b sin, a sin + b cos).
+ * slots   : int32 [T]; a negative slot skips the token.
+ * cache   : [cache_rows, ld_cache] of `dtype`, ld_cache >= dl + dr; only
+ *           columns [0, dl + dr) of the slots' rows are written.  Two tokens
+ *           with one slot: one of them is kept, unspecified which.
+ * Errors  : SATK_EINVAL for NULL latent/slots/cache, NULL tail with dr > 0,
+ *           NULL positions with cos_sin, T or cache_rows or n_positions < 0,
+ *           T >= 2**31, dl < 1, dr < 0, dr odd, ld_latent < dl, ld_tail < dr,
+ *           ld_cache < dl + dr, a dtype other than SATK_BF16 / SATK_F16;
+ *           SATK_EUNSUPPORTED for dl > SATK_LATENT_MAX or dr >
+ *           SATK_LATENT_TAIL_MAX.
+ */
+int satk_latent_store(const void *latent, int64_t ld_latent, const void *tail,
+                      int64_t ld_tail, int dtype, int64_t T, int32_t dl,
+                      int32_t dr, const float *weight, float eps,
+                      const float *cos_sin, int64_t n_positions,
+                      const int32_t *positions, int32_t interleaved,
+                      const int32_t *slots, void *cache, int64_t cache_rows,
+                      int64_t ld_cache, int32_t *status, satk_stream_t stream);
+
+/* Bytes of the workspace of satk_latent_attend and satk_latent_attend_rows
+ * (the same for every call of these H and dl on the current device); 0 for
+ * invalid arguments.  It need not be initialised, belongs to one call at a
+ * time and holds nothing between calls. */
+size_t satk_latent_workspace_bytes(int32_t H, int32_t dl);
+
+/*
+ * satk_latent_attend -- attention of query tokens over their requests' whole
+ * caches (the absorbed form: every head reads the same latent rows).
+ *
+ * q        : [T, H, dl + dr] of `dtype`, token and head strides ld_q_t and
+ *            ld_q_h, unit stride inside; already projected into the latent
+ *            space.  Consecutive tokens with one req_id share their key reads.
+ * cache    : [cache_rows, ld_cache] of `dtype`.
+ * req_id   : int32 [T]; block_table [table_rows, ld_block_table], max_blocks,
+ *            block_size, stride_rows: as in satk_dcp_emit_rows.
+ * row_ends : int32 [T]; token t sees its request's local tokens
+ *            [0, row_ends[t]) (clamped to the table's max_blocks * block_size).
+ * tree     : nullable, int32 [T, tree_words]: it also sees local token
+ *            row_ends[t] + b for each set bit b (bit b % 32 of word b / 32) --
+ *            the drafted tokens on its path, itself among them.
+ * out      : [T, H, dl] of `dtype`, strides ld_out_t and ld_out_h.
+ * A req_id outside the table, and a row outside [0, cache_rows), raise
+ * SATK_STATUS_BAD_REQUEST / SATK_STATUS_BAD_ROW; what they name is not seen.
+ * Errors   : SATK_EINVAL for NULL q/cache/req_id/block_table/row_ends/out/
+ *            workspace, T < 0, T >= 2**31, H < 1, dl < 1, dr < 0, a stride
+ *            below its extent (ld_q_t, ld_q_h, ld_cache, ld_block_table,
+ *            ld_out_t, ld_out_h; token strides are not used at T = 1, head
+ *            strides at H = 1), cache_rows < 0, table_rows < 0,
+ *            max_blocks < 0, block_size < 1, tree_words < 1 with a tree, a
+ *            scale that is not finite, workspace not 16-byte aligned or
+ *            smaller than satk_latent_workspace_bytes, a dtype other than
+ *            SATK_BF16 / SATK_F16; SATK_EUNSUPPORTED for H > 1024,
+ *            dl > SATK_LATENT_MAX, dr > SATK_LATENT_TAIL_MAX or
+ *            tree_words > 32.
+ */
+int satk_latent_attend(const void *q, int dtype, int64_t T, int32_t H,
+                       int32_t dl, int32_t dr, int64_t ld_q_t, int64_t ld_q_h,
+                       const void *cache, int64_t cache_rows, int64_t ld_cache,
+                       const int32_t *req_id, const int32_t *block_table,
+                       int64_t table_rows, int64_t ld_block_table,
+                       int32_t max_blocks, int32_t block_size,
+                       int64_t stride_rows, const int32_t *row_ends,
+                       const int32_t *tree, int32_t tree_words, float scale,
+                       void *out, int64_t ld_out_t, int64_t ld_out_h,
+                       float *lse, void *workspace, size_t workspace_bytes,
+                       int32_t *status, satk_stream_t stream);
+
+/*
+ * satk_latent_attend_rows -- the same attention over each token's selected
+ * cache rows, as satk_dcp_emit_rows writes them.
+ *
+ * rows   : int32 [T, ld_rows], columns [0, k): physical rows; a negative entry
+ *          is skipped, a row named twice counts twice.
+ * counts : nullable int32 [T] (the valid_out of satk_dcp_emit_rows): only the
+ *          first clamp(counts[t], 0, k) entries are read.
+ * All other arguments, results and errors as in satk_latent_attend; also
+ * SATK_EINVAL for NULL rows, k < 1 or ld_rows < k.
+ */
+int satk_latent_attend_rows(const void *q, int dtype, int64_t T, int32_t H,
+                            int32_t dl, int32_t dr, int64_t ld_q_t,
+                            int64_t ld_q_h, const void *cache,
+                            int64_t cache_rows, int64_t ld_cache,
+                            const int32_t *rows, int64_t ld_rows, int32_t k,
+                            const int32_t *counts, float scale, void *out,
+                            int64_t ld_out_t, int64_t ld_out_h, float *lse,
+                            void *workspace, size_t workspace_bytes,
+                            int32_t *status, satk_stream_t stream);
+
+/*
+ * satk_latent_attend_expanded -- prompt attention with the latent expanded to
+ * keys and values per head (the rotated tail of a key stays shared by the
+ * heads), over ragged requests.
+ *
+ * q    : [T, H, dn + dr] of `dtype`, strides ld_q_t, ld_q_h.
+ * k    : [S, H, dn], strides ld_k_s, ld_k_h; tail: [S, ld_tail], dr columns
+ *        (NULL when dr is 0); v: [S, H, dv], strides ld_v_s, ld_v_h.
+ * token_starts, key_starts : int32 [R + 1], ascending: request r owns tokens
+ *        [token_starts[r], token_starts[r+1]) and keys [key_starts[r],
+ *        key_starts[r+1]).  Tokens outside every request get empty rows.
+ * row_ends : int32 [T]; token t sees its request's first row_ends[t] keys
+ *        (clamped to the request's keys).
+ * out  : [T, H, dv] of `dtype`, strides ld_out_t, ld_out_h.
+ * Errors : SATK_EINVAL for NULL q/k/v/token_starts/key_starts/row_ends/out,
+ *        NULL tail with dr > 0, T or S or R < 0 or >= 2**31, H < 1, dn < 1,
+ *        dr < 0, dv < 1, a stride below its extent, a scale that is not
+ *        finite, a dtype other than SATK_BF16 / SATK_F16; SATK_EUNSUPPORTED
+ *        for H > 1024, dn + dr > SATK_EXPANDED_MAX_QK, dv >
+ *        SATK_EXPANDED_MAX_V.
+ */
+int satk_latent_attend_expanded(const void *q, int dtype, int64_t T, int32_t H,
+                                int32_t dn, int32_t dr, int64_t ld_q_t,
+                                int64_t ld_q_h, const void *k, int64_t S,
+                                int64_t ld_k_s, int64_t ld_k_h,
+                                const void *tail, int64_t ld_tail,
+                                const void *v, int32_t dv, int64_t ld_v_s,
+                                int64_t ld_v_h, const int32_t *token_starts,
+                                const int32_t *key_starts, int32_t R,
+                                const int32_t *row_ends, float scale,
+                                void *out, int64_t ld_out_t, int64_t ld_out_h,
+                                float *lse, satk_stream_t stream);
+
+/*
+ * satk_latent_merge -- joins W partial attention results over disjoint keys
+ * (the ranks of a decode, or a prompt chunk and its context):
+ * lse_out = log sum_w exp(lse_w), out = sum_w exp(lse_w - lse_out) parts_w.
+ *
+ * parts : [W, T, H, dv] of `dtype`, strides ld_w, ld_t, ld_h, unit inside.
+ * lse   : float [W, T, H] contiguous.  A part whose lse is -inf is not read.
+ * out   : [T, H, dv] of `dtype`, strides ld_out_t, ld_out_h; lse_out: nullable
+ *         float [T, H].  All parts empty: zeros and -inf.
+ * Errors: SATK_EINVAL for NULL parts/lse/out, W < 1, T < 0, T * H >= 2**31,
+ *         H < 1, dv < 1, a stride below its extent, a dtype other than
+ *         SATK_BF16 / SATK_F16; SATK_EUNSUPPORTED for W >
+ *         SATK_LATENT_MAX_RANKS.
+ */
+int satk_latent_merge(const void *parts, int dtype, int32_t W, int64_t T,
+                      int32_t H, int32_t dv, int64_t ld_w, int64_t ld_t,
+                      int64_t ld_h, const float *lse, void *out,
+                      int64_t ld_out_t, int64_t ld_out_h, float *lse_out,
+                      satk_stream_t stream);
 
 /*
  * satk_debug_flags -- the bounds-check bits of the debug build.  A library

@@ -12,25 +12,38 @@ import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsatk.so")
 
-SATK_F32, SATK_BF16 = 0, 1
+SATK_F32, SATK_BF16, SATK_F16 = 0, 1, 2
 SATK_PAIRS_F32, SATK_PACKED_BF16 = 0, 1
 STATUS_SLOTS_EXCEEDED = 1
 STATUS_DUPLICATE_KEYS = 2
 STATUS_BAD_REQUEST = 4
+STATUS_NO_BLOCK = 8
+STATUS_TOO_MANY_TOKENS = 16
+STATUS_BAD_ROW = 32
+STATUS_BAD_POSITION = 64
 TOPK_MAX_K = 4096
 MERGE_MAX_CANDIDATES = 32768
+TABLES_MAX_REQUESTS = 8192
+LATENT_MAX = 512
+LATENT_TAIL_MAX = 64
+EXPANDED_MAX_QK = 256
+EXPANDED_MAX_V = 128
+LATENT_MAX_RANKS = 64
 
 EXPORTS = ("satk_topk_rows", "satk_dcp_pack", "satk_dcp_merge_select",
            "satk_dcp_rescue_select", "satk_rescue_recv_words", "satk_status_string",
            "satk_dcp_emit_rows", "satk_topk_rows_sorted", "topk_rows", "topk_rows_sorted",
            "dcp_pack", "dcp_merge_select", "dcp_rescue_select", "dcp_emit_rows",
-           "satk_dcp_topk_pack", "dcp_topk_pack", "satk_debug_flags")
+           "satk_dcp_topk_pack", "dcp_topk_pack", "satk_debug_flags", "satk_step_tables",
+           "satk_latent_store", "satk_latent_workspace_bytes", "satk_latent_attend",
+           "satk_latent_attend_rows", "satk_latent_attend_expanded", "satk_latent_merge")
 
 _lock = threading.Lock()
 _lib = None
@@ -48,6 +61,7 @@ def load(path: str) -> ctypes.CDLL:
                         "`python -m sparse_attention_indexer_radix_gb300.build`")
     L = ctypes.CDLL(path)
     vp, i32, i64, c_int = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int
+    f32, size = ctypes.c_float, ctypes.c_size_t
     sigs = {
         "satk_topk_rows": [vp, c_int, i64, i64, i64, vp, i32, vp, i64, vp],
         "satk_topk_rows_sorted": [vp, c_int, i64, i64, i64, vp, i32, vp, i64, vp],
@@ -58,6 +72,20 @@ def load(path: str) -> ctypes.CDLL:
                                    i64, vp, vp],
         "satk_dcp_emit_rows": [vp, i64, i32, i64, i32, i32, vp, vp, i64, i64, i32, i32,
                                i64, vp, i64, vp, vp, vp],
+        "satk_step_tables": [vp, vp, i32, i32, i32, i32, i64, vp, i64, vp, i64, i32, i32, i64,
+                             vp, vp, vp, vp, vp, vp, vp, vp, vp],
+        "satk_latent_store": [vp, i64, vp, i64, c_int, i64, i32, i32, vp, f32, vp, i64, vp, i32,
+                              vp, vp, i64, i64, vp, vp],
+        "satk_latent_attend": [vp, c_int, i64, i32, i32, i32, i64, i64, vp, i64, i64, vp, vp,
+                               i64, i64, i32, i32, i64, vp, vp, i32, f32, vp, i64, i64, vp, vp,
+                               size, vp, vp],
+        "satk_latent_attend_rows": [vp, c_int, i64, i32, i32, i32, i64, i64, vp, i64, i64, vp,
+                                    i64, i32, vp, f32, vp, i64, i64, vp, vp, size, vp, vp],
+        "satk_latent_attend_expanded": [vp, c_int, i64, i32, i32, i32, i64, i64, vp, i64, i64,
+                                        i64, vp, i64, vp, i32, i64, i64, vp, vp, i32, vp, f32,
+                                        vp, i64, i64, vp, vp],
+        "satk_latent_merge": [vp, c_int, i32, i64, i32, i32, i64, i64, i64, vp, vp, i64, i64,
+                              vp, vp],
     }
     for name, args in sigs.items():
         f = getattr(L, name)
@@ -65,6 +93,8 @@ def load(path: str) -> ctypes.CDLL:
         f.restype = c_int
     L.satk_rescue_recv_words.argtypes = [i64, i32, i32]
     L.satk_rescue_recv_words.restype = ctypes.c_size_t
+    L.satk_latent_workspace_bytes.argtypes = [i32, i32]
+    L.satk_latent_workspace_bytes.restype = size
     L.satk_status_string.argtypes = [c_int]
     L.satk_status_string.restype = ctypes.c_char_p
     L.satk_debug_flags.argtypes = [c_int]
@@ -357,3 +387,327 @@ def dcp_emit_rows(ids: torch.Tensor, W: int, dcp_rank: int, req_id: torch.Tensor
                                   _ptr(status), _stream(ids.device))
     _check(rc, "satk_dcp_emit_rows")
     return rows_out, valid_out
+
+
+def _dtype16(t, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return SATK_BF16
+    if t.dtype == torch.float16:
+        return SATK_F16
+    raise SatkError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+
+
+def _int32_vec(t, n: int, name: str):
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+        raise SatkError(f"{name} must be contiguous int32 with {n} entries")
+
+
+def _same_device(*ts):
+    """Every tensor on one CUDA device."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise SatkError("every tensor must live on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise SatkError(f"tensors on two devices: {dev} and {t.device}")
+
+
+def _unit_last(t, name: str, dims: int):
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise SatkError(f"{name} must be {dims}-D with unit stride in its last dimension, got "
+                        f"{tuple(t.shape)} {t.stride()}")
+
+
+def _lse_out(lse, T: int, H: int, device):
+    if lse is None:
+        return torch.empty((T, H), dtype=torch.float32, device=device)
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+        raise SatkError(f"lse must be contiguous float32 [{T}, {H}]")
+    return lse
+
+
+def _heads_out(out, T: int, H: int, width: int, like, name: str = "out"):
+    if out is None:
+        return torch.empty((T, H, width), dtype=like.dtype, device=like.device)
+    _unit_last(out, name, 3)
+    if out.dtype != like.dtype or tuple(out.shape) != (T, H, width):
+        raise SatkError(f"{name} must be {like.dtype} [{T}, {H}, {width}]")
+    return out
+
+
+class StepTables(NamedTuple):
+    """What step_tables writes: token_starts [R + 1], lens [R], blocks_used [1]
+    and the per-token req_id, positions, row_ends, slots [tokens], all int32."""
+    token_starts: torch.Tensor
+    lens: torch.Tensor
+    req_id: torch.Tensor
+    positions: torch.Tensor
+    row_ends: torch.Tensor
+    slots: torch.Tensor
+    blocks_used: torch.Tensor
+
+
+def step_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor,
+                block_table: torch.Tensor, *, tokens: int, block_size: int, stride_rows: int,
+                W: int = 1, dcp_rank: int = 0, drafted: bool = False,
+                max_blocks: int | None = None, out: StepTables | None = None,
+                status: torch.Tensor | None = None) -> StepTables:
+    """One step's metadata from request lengths: extends ``block_table``
+    (int32 [R, width], in place) with blocks taken from the front of
+    ``free_blocks`` and returns the per-token arrays that topk_rows
+    (row_ends), dcp_emit_rows (req_id), latent_store (positions, slots) and
+    latent_attend take.  ``tokens`` is their capacity; entries past the last
+    new token are padding (row_end 0, slot -1).  ``drafted`` gives every new
+    token its request's context as row_end."""
+    _same_device(context_lens, new_lens, free_blocks, block_table, status,
+                 *(out if out is not None else ()))
+    _rowmajor_2d(block_table, "block_table")
+    if block_table.dtype != torch.int32:
+        raise SatkError("block_table must be int32")
+    R, width = block_table.shape
+    _int32_vec(context_lens, R, "context_lens")
+    _int32_vec(new_lens, R, "new_lens")
+    _int32_vec(free_blocks, 0, "free_blocks")
+    max_blocks = width if max_blocks is None else max_blocks
+    if tokens < 0:
+        raise SatkError("tokens must not be negative")
+    sizes = (R + 1, R, tokens, tokens, tokens, tokens, 1)
+    if out is None:
+        # one allocation; each array starts on its own 16-byte boundary
+        room = [(n + 3) // 4 * 4 for n in sizes]
+        buf = torch.empty(sum(room), dtype=torch.int32, device=block_table.device)
+        out = StepTables(*(part[:n] for part, n in zip(buf.split(room), sizes)))
+    for name, t, n in zip(StepTables._fields, out, sizes):
+        _int32_vec(t, n, name)
+    if status is not None:
+        _int32_vec(status, 1, "status")
+    ld = block_table.stride(0) if R > 1 else max(width, 1)
+    p = [_ptr(t, True) for t in out]
+    rc = lib().satk_step_tables(
+        _ptr(context_lens, True), _ptr(new_lens, True), R, W, dcp_rank, block_size, stride_rows,
+        _ptr(free_blocks, True), free_blocks.numel(), _ptr(block_table, True), ld, max_blocks,
+        int(drafted), tokens, *p, _ptr(status), _stream(block_table.device))
+    _check(rc, "satk_step_tables")
+    return out
+
+
+def latent_store(latent: torch.Tensor, tail: torch.Tensor | None, slots: torch.Tensor,
+                 cache: torch.Tensor, *, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 cos_sin: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                 interleaved: bool = False, status: torch.Tensor | None = None) -> torch.Tensor:
+    """Writes rows [norm(latent) * weight | rotated tail] of new tokens into
+    ``cache`` ([rows, >= dl + dr] bfloat16 or float16, in place) at ``slots``
+    (int32 [T], negative: skipped).  ``weight`` float32 [dl] or None (no
+    norm); ``cos_sin`` float32 [P, dr] (cosines, then sines) with
+    ``positions`` int32 [T], or None (no rotation).  Returns ``cache``."""
+    _same_device(latent, tail, slots, cache, weight, cos_sin, positions, status)
+    _rowmajor_2d(latent, "latent")
+    _rowmajor_2d(cache, "cache")
+    dt = _dtype16(cache, "cache")
+    T, dl = latent.shape
+    dr = 0
+    if tail is not None:
+        _rowmajor_2d(tail, "tail")
+        dr = tail.shape[1]
+        if tail.dtype != cache.dtype or tail.shape[0] != T:
+            raise SatkError(f"tail must be {cache.dtype} [{T}, dr]")
+    if latent.dtype != cache.dtype or cache.shape[1] < dl + dr:
+        raise SatkError(f"latent must be {cache.dtype} and cache at least {dl + dr} wide")
+    _int32_vec(slots, T, "slots")
+    if weight is not None and (weight.dtype != torch.float32 or not weight.is_contiguous()
+                               or weight.numel() != dl):
+        raise SatkError(f"weight must be contiguous float32 [{dl}]")
+    P = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or \
+                cos_sin.dim() != 2 or cos_sin.shape[1] != dr:
+            raise SatkError(f"cos_sin must be contiguous float32 [P, {dr}]")
+        if positions is None:
+            raise SatkError("cos_sin needs positions")
+        _int32_vec(positions, T, "positions")
+        P = cos_sin.shape[0]
+    rows = cache.shape[0]
+    ld_cache = cache.stride(0) if rows > 1 else cache.shape[1]
+    e = T == 0
+    rc = lib().satk_latent_store(
+        _ptr(latent, e), latent.stride(0) if T > 1 else dl, _ptr(tail if dr else None, e),
+        tail.stride(0) if dr and T > 1 else dr, dt, T, dl, dr, _ptr(weight), eps,
+        _ptr(cos_sin if dr else None, True), P, _ptr(positions, e), int(interleaved),
+        _ptr(slots, e), _ptr(cache, True), rows, ld_cache, _ptr(status), _stream(cache.device))
+    _check(rc, "satk_latent_store")
+    return cache
+
+
+def latent_workspace_bytes(heads: int, latent_dim: int) -> int:
+    """Bytes of the scratch of latent_attend and latent_attend_rows."""
+    return int(lib().satk_latent_workspace_bytes(heads, latent_dim))
+
+
+def _latent_call(q, cache, latent_dim, out, lse, workspace):
+    """Shared checks of the two attentions over cache rows."""
+    _unit_last(q, "q", 3)
+    _rowmajor_2d(cache, "cache")
+    dt = _dtype16(q, "q")
+    T, H, D = q.shape
+    if cache.dtype != q.dtype or cache.shape[1] < D:
+        raise SatkError(f"cache must be {q.dtype} and at least {D} wide")
+    if not 0 < latent_dim <= D:
+        raise SatkError(f"latent_dim must be in 1..{D}")
+    out = _heads_out(out, T, H, latent_dim, q)
+    lse = _lse_out(lse, T, H, q.device)
+    need = lib().satk_latent_workspace_bytes(H, latent_dim)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    if not workspace.is_contiguous():
+        raise SatkError("workspace must be contiguous")
+    ld_t = q.stride(0) if T > 1 else H * D
+    ld_h = q.stride(1) if H > 1 else D
+    lo_t = out.stride(0) if T > 1 else H * latent_dim
+    lo_h = out.stride(1) if H > 1 else latent_dim
+    rows = cache.shape[0]
+    ld_cache = cache.stride(0) if rows > 1 else cache.shape[1]
+    e = T == 0
+    head = (_ptr(q, e), dt, T, H, latent_dim, D - latent_dim, ld_t, ld_h, _ptr(cache, True), rows,
+            ld_cache)
+    end = (_ptr(out, e), lo_t, lo_h, _ptr(lse, e), _ptr(workspace),
+           workspace.numel() * workspace.element_size())
+    return T, head, end, out, lse
+
+
+def latent_attend(q: torch.Tensor, cache: torch.Tensor, req_id: torch.Tensor,
+                  block_table: torch.Tensor, row_ends: torch.Tensor, *, block_size: int,
+                  stride_rows: int, latent_dim: int, scale: float,
+                  tree: torch.Tensor | None = None, max_blocks: int | None = None,
+                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, status: torch.Tensor | None = None):
+    """Attention of ``q`` ([T, H, D] bfloat16 or float16) over the requests'
+    paged latent caches: token t sees its request's local tokens
+    [0, row_ends[t]) and, with ``tree`` (int32 [T, words]), local token
+    row_ends[t] + b for each set bit b.  Keys are whole cache rows, values
+    their first ``latent_dim`` columns.  Returns (out [T, H, latent_dim], lse
+    float32 [T, H])."""
+    _same_device(q, cache, req_id, block_table, row_ends, tree, out, lse, workspace, status)
+    T, head, end, out, lse = _latent_call(q, cache, latent_dim, out, lse, workspace)
+    _rowmajor_2d(block_table, "block_table")
+    if block_table.dtype != torch.int32:
+        raise SatkError("block_table must be int32")
+    _int32_vec(req_id, T, "req_id")
+    _int32_vec(row_ends, T, "row_ends")
+    words = 0
+    if tree is not None:
+        if tree.dtype != torch.int32 or tree.dim() != 2 or tree.shape[0] != T or \
+                not tree.is_contiguous() or tree.shape[1] < 1:
+            raise SatkError(f"tree must be contiguous int32 [{T}, >= 1]")
+        words = tree.shape[1]
+    R, width = block_table.shape
+    max_blocks = width if max_blocks is None else max_blocks
+    e = T == 0
+    rc = lib().satk_latent_attend(
+        *head, _ptr(req_id, e), _ptr(block_table, True), R,
+        block_table.stride(0) if R > 1 else max(width, 1), max_blocks, block_size, stride_rows,
+        _ptr(row_ends, e), _ptr(tree, e), words, scale, *end, _ptr(status), _stream(q.device))
+    _check(rc, "satk_latent_attend")
+    return out, lse
+
+
+def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, rows: torch.Tensor, *,
+                       latent_dim: int, scale: float, counts: torch.Tensor | None = None,
+                       k: int | None = None, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       status: torch.Tensor | None = None):
+    """Attention of ``q`` ([T, H, D]) over each token's selected cache rows:
+    ``rows`` int32 [T, >= k] and ``counts`` int32 [T] as dcp_emit_rows writes
+    them (negative entries and those past the count are skipped).  Returns
+    (out [T, H, latent_dim], lse float32 [T, H])."""
+    _same_device(q, cache, rows, counts, out, lse, workspace, status)
+    T, head, end, out, lse = _latent_call(q, cache, latent_dim, out, lse, workspace)
+    _rowmajor_2d(rows, "rows")
+    k = rows.shape[1] if k is None else k
+    if rows.dtype != torch.int32 or rows.shape[0] != T or rows.shape[1] < k:
+        raise SatkError(f"rows must be int32 [{T}, >= {k}]")
+    if counts is not None:
+        _int32_vec(counts, T, "counts")
+    e = T == 0
+    rc = lib().satk_latent_attend_rows(
+        *head, _ptr(rows, e), rows.stride(0) if T > 1 else rows.shape[1], k, _ptr(counts, e),
+        scale, *end, _ptr(status), _stream(q.device))
+    _check(rc, "satk_latent_attend_rows")
+    return out, lse
+
+
+def latent_attend_expanded(q: torch.Tensor, k: torch.Tensor, tail: torch.Tensor | None,
+                           v: torch.Tensor, token_starts: torch.Tensor, key_starts: torch.Tensor,
+                           row_ends: torch.Tensor, *, scale: float,
+                           out: torch.Tensor | None = None, lse: torch.Tensor | None = None):
+    """Prompt attention with per-head keys and values: ``q`` [T, H, dn + dr],
+    ``k`` [S, H, dn], ``tail`` [S, dr] (shared by the heads, or None), ``v``
+    [S, H, dv]; request r owns tokens token_starts[r:r+2] and keys
+    key_starts[r:r+2]; token t sees its request's first row_ends[t] keys.
+    Returns (out [T, H, dv], lse float32 [T, H])."""
+    _same_device(q, k, tail, v, token_starts, key_starts, row_ends, out, lse)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _unit_last(t, name, 3)
+        if t.dtype != q.dtype:
+            raise SatkError(f"{name} must be {q.dtype}")
+    dt = _dtype16(q, "q")
+    T, H, D = q.shape
+    S, _, dn = k.shape
+    dv = v.shape[2]
+    dr = 0
+    if tail is not None:
+        _rowmajor_2d(tail, "tail")
+        dr = tail.shape[1]
+        if tail.dtype != q.dtype or tail.shape[0] != S:
+            raise SatkError(f"tail must be {q.dtype} [{S}, dr]")
+    if k.shape[1] != H or tuple(v.shape[:2]) != (S, H) or D != dn + dr:
+        raise SatkError(f"k, v and q must be [{S}, {H}, dn], [{S}, {H}, dv] and [T, {H}, dn + dr]")
+    R = token_starts.numel() - 1
+    if R < 0:
+        raise SatkError("token_starts must have at least one entry")
+    _int32_vec(token_starts, R + 1, "token_starts")
+    _int32_vec(key_starts, R + 1, "key_starts")
+    _int32_vec(row_ends, T, "row_ends")
+    out = _heads_out(out, T, H, dv, q)
+    lse = _lse_out(lse, T, H, q.device)
+
+    def strides(t, rows, width):
+        return (t.stride(0) if rows > 1 else H * width, t.stride(1) if H > 1 else width)
+    e = T == 0
+    q_t, q_h = strides(q, T, D)
+    k_s, k_h = strides(k, S, dn)
+    v_s, v_h = strides(v, S, dv)
+    o_t, o_h = strides(out, T, dv)
+    rc = lib().satk_latent_attend_expanded(
+        _ptr(q, e), dt, T, H, dn, dr, q_t, q_h, _ptr(k, True), S, k_s, k_h,
+        _ptr(tail if dr else None, True), tail.stride(0) if dr and S > 1 else dr, _ptr(v, True),
+        dv, v_s, v_h, _ptr(token_starts), _ptr(key_starts), R, _ptr(row_ends, e), scale,
+        _ptr(out, e), o_t, o_h, _ptr(lse, e), _stream(q.device))
+    _check(rc, "satk_latent_attend_expanded")
+    return out, lse
+
+
+def latent_merge(parts: torch.Tensor, lse: torch.Tensor, *, out: torch.Tensor | None = None,
+                 lse_out: torch.Tensor | None = None):
+    """Joins W partial attention results over disjoint keys: ``parts``
+    [W, T, H, dv] bfloat16 or float16, ``lse`` float32 [W, T, H] contiguous.
+    Returns (out [T, H, dv], lse float32 [T, H])."""
+    _same_device(parts, lse, out, lse_out)
+    _unit_last(parts, "parts", 4)
+    dt = _dtype16(parts, "parts")
+    W, T, H, dv = parts.shape
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (W, T, H) or not lse.is_contiguous():
+        raise SatkError(f"lse must be contiguous float32 [{W}, {T}, {H}]")
+    out = _heads_out(out, T, H, dv, parts)
+    lse_out = _lse_out(lse_out, T, H, parts.device)
+    e = T == 0
+    rc = lib().satk_latent_merge(
+        _ptr(parts, e), dt, W, T, H, dv, parts.stride(0) if W > 1 else T * H * dv,
+        parts.stride(1) if T > 1 else H * dv, parts.stride(2) if H > 1 else dv, _ptr(lse, e),
+        _ptr(out, e), out.stride(0) if T > 1 else H * dv, out.stride(1) if H > 1 else dv,
+        _ptr(lse_out, e), _stream(parts.device))
+    _check(rc, "satk_latent_merge")
+    return out, lse_out

@@ -1,0 +1,196 @@
+// step_tables.cu -- satk_step_tables: the block table, slots, requests and
+// causal ends of one step's new tokens, from request lengths.
+//
+// Two exclusive prefix sums over the requests (new tokens, new blocks) decide
+// everything else; a token or a new block finds its request by binary search
+// in the prefix.  The scan is small (8 bytes a request), so every CTA does it
+// again for itself in shared memory instead of a second launch, and then
+// takes its share of the tokens and of the new blocks.  A token whose block
+// is new this step reads its id from the free list, not from the table, so no
+// CTA waits for another's table writes.  Latency-bound: one launch, about two
+// dependent rounds of loads.
+#include "satk_host.hpp"
+#include "satk_device.cuh"
+
+namespace satk {
+namespace {
+
+constexpr int kTablesBlock = 512;
+constexpr int kTablesTokens = 1024;  // tokens per CTA
+
+struct TablesArgs {
+  const int32_t *context_lens, *new_lens;
+  int R, W, rank, block_size;
+  int64_t stride_rows;
+  const int32_t *free_blocks;
+  int64_t n_free;
+  int32_t *table;
+  int64_t ld_table;
+  int max_blocks, drafted;
+  int64_t T;
+  int32_t *token_starts, *lens, *req_id, *positions, *row_ends, *slots, *blocks_used, *status;
+};
+
+struct Request {
+  int64_t ctx, fresh;  // tokens before the step, new tokens
+  int have, need;      // table columns in use before and after the step
+};
+
+__device__ __forceinline__ int64_t local_count(const TablesArgs &a, int64_t p) {
+  return (p + a.W - 1 - a.rank) / a.W;
+}
+
+__device__ __forceinline__ Request request(const TablesArgs &a, int r) {
+  Request q;
+  q.ctx = max(a.context_lens[r], 0);
+  q.fresh = max(a.new_lens[r], 0);
+  auto blocks = [&](int64_t p) {
+    const int64_t b = (local_count(a, p) + a.block_size - 1) / a.block_size;
+    return static_cast<int>(b < a.max_blocks ? b : a.max_blocks);
+  };
+  q.have = blocks(q.ctx);
+  q.need = blocks(q.ctx + q.fresh);
+  return q;
+}
+
+// Exclusive scan of one value per thread over the CTA; *total its sum.
+__device__ __forceinline__ int64_t scan64(int64_t v, int64_t *warp_sum, int64_t *total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) warp_sum[w] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+  for (int i = 0; i < kTablesBlock / 32; ++i) {
+    if (i < w) before += warp_sum[i];
+    all += warp_sum[i];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// The last r in [0, R) with starts[r] <= x (starts ascending, starts[0] <= x).
+__device__ __forceinline__ int find(const int32_t *starts, int R, int32_t x) {
+  int lo = 0, hi = R;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kTablesBlock) step_tables_kernel(TablesArgs a) {
+  extern __shared__ int32_t prefix[];
+  int32_t *tok = prefix, *blk = prefix + a.R;  // first token and first new block of each request
+  __shared__ int64_t warp_sum[2][kTablesBlock / 32];
+  const int tid = threadIdx.x;
+  const int per = (a.R + kTablesBlock - 1) / kTablesBlock;
+  const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+  int64_t nt = 0, nb = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Request q = request(a, r);
+    nt += q.fresh;
+    nb += q.need - q.have;
+  }
+  int64_t tokens, blocks;
+  int64_t t = scan64(nt, warp_sum[0], &tokens), b = scan64(nb, warp_sum[1], &blocks);
+  const bool first = blockIdx.x == 0;
+  for (int r = r0; r < r1; ++r) {
+    const Request q = request(a, r);
+    tok[r] = static_cast<int32_t>(min(t, a.T));
+    blk[r] = static_cast<int32_t>(min(b, a.n_free));
+    if (first) {
+      a.token_starts[r] = tok[r];
+      a.lens[r] = static_cast<int32_t>(local_count(a, q.ctx + q.fresh));
+    }
+    t += q.fresh;
+    b += q.need - q.have;
+  }
+  const int32_t n = static_cast<int32_t>(min(tokens, a.T));
+  const int32_t used = static_cast<int32_t>(min(blocks, a.n_free));
+  if (first && tid == 0) {
+    a.token_starts[a.R] = n;
+    a.blocks_used[0] = used;
+    if (a.status != nullptr && tokens > a.T) atomicOr(a.status, SATK_STATUS_TOO_MANY_TOKENS);
+  }
+  __syncthreads();
+
+  // new blocks: the i-th free block goes to the request whose share covers it
+  for (int32_t i = blockIdx.x * kTablesBlock + tid; i < used; i += gridDim.x * kTablesBlock) {
+    const int r = find(blk, a.R, i);
+    const int col = request(a, r).have + (i - blk[r]);
+    a.table[static_cast<int64_t>(r) * a.ld_table + col] = a.free_blocks[i];
+  }
+
+  int bad = 0;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTablesTokens;
+  const int64_t t1 = min(t0 + kTablesTokens, a.T);
+  for (int64_t i = t0 + tid; i < t1; i += kTablesBlock) {
+    int req = 0, slot = -1;
+    int64_t pos = 0, end = 0;
+    if (i < n) {
+      req = find(tok, a.R, static_cast<int32_t>(i));
+      const Request q = request(a, req);
+      pos = q.ctx + (i - tok[req]);
+      end = local_count(a, a.drafted ? q.ctx : pos + 1);
+      if (pos % a.W == a.rank) {
+        const int64_t l = pos / a.W, col = l / a.block_size;
+        int32_t id = -1;
+        if (col < q.have) {
+          id = a.table[req * a.ld_table + col];
+        } else if (col < q.need) {
+          const int64_t f = blk[req] + (col - q.have);
+          if (f < a.n_free) id = a.free_blocks[f];
+        }
+        if (id < 0) {
+          bad |= SATK_STATUS_NO_BLOCK;
+        } else {
+          const int64_t row = id * a.stride_rows + l % a.block_size;
+          if (row > INT32_MAX) bad |= SATK_STATUS_BAD_ROW;
+          else slot = static_cast<int>(row);
+        }
+      }
+    }
+    a.req_id[i] = req;
+    a.positions[i] = static_cast<int32_t>(pos);
+    a.row_ends[i] = static_cast<int32_t>(end);
+    a.slots[i] = slot;
+  }
+  if (bad != 0 && a.status != nullptr) atomicOr(a.status, bad);
+}
+
+}  // namespace
+}  // namespace satk
+
+extern "C" int satk_step_tables(const int32_t *context_lens, const int32_t *new_lens, int32_t R,
+                                int32_t W, int32_t dcp_rank, int32_t block_size,
+                                int64_t stride_rows, const int32_t *free_blocks, int64_t n_free,
+                                int32_t *block_table, int64_t ld_block_table, int32_t max_blocks,
+                                int32_t drafted, int64_t T, int32_t *token_starts, int32_t *lens,
+                                int32_t *req_id, int32_t *positions, int32_t *row_ends,
+                                int32_t *slots, int32_t *blocks_used, int32_t *status,
+                                satk_stream_t stream) {
+  using namespace satk;
+  if (context_lens == nullptr || new_lens == nullptr || block_table == nullptr ||
+      token_starts == nullptr || lens == nullptr || req_id == nullptr || positions == nullptr ||
+      row_ends == nullptr || slots == nullptr || blocks_used == nullptr ||
+      (free_blocks == nullptr && n_free > 0) || R < 0 || T < 0 || T > INT32_MAX || n_free < 0 ||
+      n_free > INT32_MAX || W < 1 || dcp_rank < 0 || dcp_rank >= W || block_size < 1 ||
+      stride_rows < 0 || max_blocks < 0 || ld_block_table < max_blocks || drafted < 0 ||
+      drafted > 1)
+    return SATK_EINVAL;
+  if (R > SATK_TABLES_MAX_REQUESTS) return SATK_EUNSUPPORTED;
+  TablesArgs a{context_lens, new_lens,    R,           W,          dcp_rank,  block_size,
+               stride_rows,  free_blocks, n_free,      block_table, ld_block_table, max_blocks,
+               drafted,      T,           token_starts, lens,      req_id,    positions,
+               row_ends,     slots,       blocks_used, status};
+  const size_t smem = sizeof(int32_t) * 2 * static_cast<size_t>(R);
+  if (!allow_smem(step_tables_kernel, smem)) return SATK_ECUDA;
+  const int64_t grid = T > kTablesTokens ? (T + kTablesTokens - 1) / kTablesTokens : 1;
+  step_tables_kernel<<<static_cast<unsigned>(grid), kTablesBlock, smem, as_stream(stream)>>>(a);
+  return launch_status();
+}
