@@ -72,6 +72,9 @@ enum satk_rc {
                                         above 2**31 - 1 in a slot): skipped  */
 #define SATK_STATUS_BAD_POSITION 64  /* satk_latent_store: a position outside
                                         the cos/sin table; token skipped    */
+#define SATK_STATUS_STALLED 128      /* an attention kernel gave up a wait
+                                        inside the GPU (about two seconds):
+                                        its outputs are not to be used       */
 
 /* Largest K of satk_topk_rows and of the rescue push. */
 #define SATK_TOPK_MAX_K 4096

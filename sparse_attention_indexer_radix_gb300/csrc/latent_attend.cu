@@ -27,7 +27,10 @@ int check(const LatentArgs &a, int dtype, int64_t T, int64_t dr, float scale,
   return SATK_OK;
 }
 
-int dispatch(const LatentArgs &a, int dtype, cudaStream_t stream) {
+int dispatch(const LatentArgs &a, int dtype, int tokens_per_request, void *workspace,
+             cudaStream_t stream) {
+  if (latent_attend_mma_fits(a))
+    return latent_attend_mma(a, dtype, tokens_per_request, workspace, stream);
   return latent_attend_warp(a, dtype, stream);
 }
 
@@ -36,7 +39,7 @@ int dispatch(const LatentArgs &a, int dtype, cudaStream_t stream) {
 
 extern "C" size_t satk_latent_workspace_bytes(int32_t H, int32_t dl) {
   if (H < 1 || H > 1024 || dl < 1 || dl > SATK_LATENT_MAX) return 0;
-  return 16;
+  return satk::latent_attend_mma_workspace(H, dl);
 }
 
 extern "C" int satk_latent_attend(const void *q, int dtype, int64_t T, int32_t H, int32_t dl,
@@ -66,7 +69,8 @@ extern "C" int satk_latent_attend(const void *q, int dtype, int64_t T, int32_t H
                status};
   const int rc = check(a, dtype, T, dr, scale, workspace, workspace_bytes);
   if (rc != SATK_OK || T == 0) return rc;
-  return dispatch(a, dtype, as_stream(stream));
+  const int64_t per = table_rows > 0 ? (T + table_rows - 1) / table_rows : 1;
+  return dispatch(a, dtype, static_cast<int>(per), workspace, as_stream(stream));
 }
 
 extern "C" int satk_latent_attend_rows(const void *q, int dtype, int64_t T, int32_t H, int32_t dl,
@@ -90,5 +94,5 @@ extern "C" int satk_latent_attend_rows(const void *q, int dtype, int64_t T, int3
                status};
   const int rc = check(a, dtype, T, dr, scale, workspace, workspace_bytes);
   if (rc != SATK_OK || T == 0) return rc;
-  return dispatch(a, dtype, as_stream(stream));
+  return dispatch(a, dtype, 1, workspace, as_stream(stream));
 }

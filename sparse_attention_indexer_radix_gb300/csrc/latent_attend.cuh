@@ -86,4 +86,11 @@ __device__ __forceinline__ int64_t key_row(const LatentArgs &a, int t, int r, in
 // The general kernel: any widths, strides and alignment (latent_attend_warp.cu).
 int latent_attend_warp(const LatentArgs &a, int dtype, cudaStream_t stream);
 
+// The tensor-core kernel (latent_attend_mma.cu): whether it takes this call, its
+// workspace, and the call; tokens_per_request is the host's estimate.
+bool latent_attend_mma_fits(const LatentArgs &a);
+size_t latent_attend_mma_workspace(int H, int dl);
+int latent_attend_mma(const LatentArgs &a, int dtype, int tokens_per_request, void *workspace,
+                      cudaStream_t stream);
+
 }  // namespace satk
