@@ -234,6 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
   tc_fence_after();
   const uint32_t tmem = sm.tmem, o_at = tmem + 2 * N;
 
+  // 128 registers a thread at launch: 128 x 200 + 384 x 104 = 512 x 128.
+  if (warp < 4) regs_raise<200>(); else regs_lower<104>();
   if (warp < 4) {
     // ------------------------------------------------------- softmax, results
     constexpr int C = N / 2;  // columns per thread: [half C, half C + C) of key kk
@@ -320,16 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
         for (int x = 0; x < C; ++x) pass |= s[x] - ref[x] > kLag;
         if (named_any(1, kSoftmax, pass)) {
           // Move the references to the running maxima.
-          float mx[C];
 #pragma unroll
           for (int x = 0; x < C; ++x) {
-            mx[x] = s[x];
+            float mx = s[x];
 #pragma unroll
-            for (int d = 8; d > 0; d >>= 1) mx[x] = fmaxf(mx[x], __shfl_xor_sync(~0u, mx[x], d));
-          }
-          if ((lane & 15) == 0) {
-#pragma unroll
-            for (int x = 0; x < C; ++x) sm.red[warp][c0 + x] = mx[x];
+            for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+            if ((lane & 15) == 0) sm.red[warp][c0 + x] = mx;
           }
           named_sync(1, kSoftmax);
 #pragma unroll
@@ -385,10 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
       for (int x = 0; x < C; ++x) {
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) l[x] += __shfl_xor_sync(~0u, l[x], d);
-      }
-      if ((lane & 15) == 0) {
-#pragma unroll
-        for (int x = 0; x < C; ++x) sm.red[warp][c0 + x] = l[x];
+        if ((lane & 15) == 0) sm.red[warp][c0 + x] = l[x];
       }
       named_sync(1, kSoftmax);
       float *part = m.parts + (blockIdx.x * 2 + slot) * m.part_stride;
@@ -447,63 +442,70 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
     }
   } else if (warp == 4) {
     // -------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
-      constexpr uint32_t dq = mma_desc(bf16, false, false, kTile, N);
-      constexpr uint32_t dp = mma_desc(bf16, true, true, 128, N);
-      const int ksteps = (a.D + 15) / 16;
-      Walk wq, wp;
-      wq.seek(m.plan, groups, m.nh, u0);
-      wp = wq;
-      int iq = 0, ip = 0, q_stage = 0, q_use = 0, p_stage = 0, seg = 0;
-      bool q_first = true, p_first = true;
-      long long t0 = clock64();
-      while (ip < n_tiles) {
-        bool moved = false;
-        if (iq < n_tiles && mbar_poll(bar(sm.full[q_stage]), q_use & 1) &&
-            (iq < 2 || mbar_poll(bar(sm.s_empty[iq & 1]), ((iq >> 1) - 1) & 1)) &&
-            (!q_first || mbar_poll(bar(sm.q_full), seg & 1))) {
-          tc_fence_after();
-          const uint32_t k_at = base + q_stage * stage_bytes;
-          for (int ks = 0; ks < ksteps; ++ks)
-            mma_ss(tmem + (iq & 1) * N,
-                   tile_desc(k_at + (ks >> 2) * kPanel + (ks & 3) * 32, 16, 1024),
-                   tile_desc(q_at + (ks >> 2) * q_panel + (ks & 3) * 32, 16, 1024), dq, ks > 0);
-          tc_commit(bar(sm.s_full[iq & 1]));
-          q_first = u0 + iq + 1 == wq.e;
-          if (q_first) {
-            tc_commit(bar(sm.q_empty));
-            ++seg;
-            if (iq + 1 < n_tiles) wq.next();
-          }
-          ++iq;
-          if (++q_stage == m.nst) q_stage = 0, ++q_use;
-          moved = true;
+    constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
+    constexpr uint32_t dq = mma_desc(bf16, false, false, kTile, N);
+    constexpr uint32_t dp = mma_desc(bf16, true, true, 128, N);
+    const int ksteps = (a.D + 15) / 16;
+    // Descriptors hold addresses in units of 16 bytes: steps are added to them.
+    const uint64_t k_desc = tile_desc(base, 16, 1024), q_desc = tile_desc(q_at, 16, 1024);
+    const uint64_t v_desc = tile_desc(base, kPanel, 1024), p_desc = tile_desc(p_at, kPanel, 1024);
+    Walk wq, wp;
+    wq.seek(m.plan, groups, m.nh, u0);
+    wp = wq;
+    int iq = 0, ip = 0, q_stage = 0, q_use = 0, p_stage = 0, seg = 0;
+    bool q_first = true, p_first = true;
+    long long t0 = clock64();
+    while (ip < n_tiles) {
+      bool moved = false;
+      if (iq < n_tiles && warp_poll(bar(sm.full[q_stage]), q_use & 1) &&
+          (iq < 2 || warp_poll(bar(sm.s_empty[iq & 1]), ((iq >> 1) - 1) & 1)) &&
+          (!q_first || warp_poll(bar(sm.q_full), seg & 1))) {
+        tc_fence_after();
+        uint64_t kd = k_desc + ((q_stage * stage_bytes) >> 4), qd = q_desc;
+        const uint32_t s_at = tmem + (iq & 1) * N;
+        int ks = 0;
+        for (; ks + 4 <= ksteps; ks += 4, kd += kPanel >> 4, qd += q_panel >> 4) {
+          mma_ss(s_at, kd, qd, dq, ks > 0);
+          mma_ss(s_at, kd + 2, qd + 2, dq, true);
+          mma_ss(s_at, kd + 4, qd + 4, dq, true);
+          mma_ss(s_at, kd + 6, qd + 6, dq, true);
         }
-        if (ip < iq && mbar_poll(bar(sm.p_full), ip & 1)) {
-          tc_fence_after();
-          const uint32_t v_at = base + p_stage * stage_bytes;
-          for (int b = 0; b < m.nb; ++b)
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_ss(o_at + b * N, tile_desc(v_at + 2 * b * kPanel + ks * 2048, kPanel, 1024),
-                     tile_desc(p_at + ks * 2048, kPanel, 1024), dp, !(p_first && ks == 0));
-          tc_commit(bar(sm.empty[p_stage]));
-          tc_commit(bar(sm.o_done));
-          p_first = u0 + ip + 1 == wp.e;
-          if (p_first && ip + 1 < n_tiles) wp.next();
-          ++ip;
-          if (++p_stage == m.nst) p_stage = 0;
-          moved = true;
+        for (; ks < ksteps; ++ks, kd += 2, qd += 2) mma_ss(s_at, kd, qd, dq, ks > 0);
+        tc_commit(bar(sm.s_full[iq & 1]));
+        q_first = u0 + iq + 1 == wq.e;
+        if (q_first) {
+          tc_commit(bar(sm.q_empty));
+          ++seg;
+          if (iq + 1 < n_tiles) wq.next();
         }
-        if (moved) {
-          t0 = clock64();
-        } else if (*dead != 0 || clock64() - t0 > kWaitClocks) {
-          *dead = 1;
-          break;
+        ++iq;
+        if (++q_stage == m.nst) q_stage = 0, ++q_use;
+        moved = true;
+      }
+      if (ip < iq && warp_poll(bar(sm.p_full), ip & 1)) {
+        tc_fence_after();
+        uint64_t vd = v_desc + ((p_stage * stage_bytes) >> 4);
+        for (int b = 0; b < m.nb; ++b, vd += (2 * kPanel) >> 4) {
+          mma_ss(o_at + b * N, vd, p_desc, dp, !p_first);
+          mma_ss(o_at + b * N, vd + 128, p_desc + 128, dp, true);
+          mma_ss(o_at + b * N, vd + 256, p_desc + 256, dp, true);
+          mma_ss(o_at + b * N, vd + 384, p_desc + 384, dp, true);
         }
+        tc_commit(bar(sm.empty[p_stage]));
+        tc_commit(bar(sm.o_done));
+        p_first = u0 + ip + 1 == wp.e;
+        if (p_first && ip + 1 < n_tiles) wp.next();
+        ++ip;
+        if (++p_stage == m.nst) p_stage = 0;
+        moved = true;
+      }
+      if (moved) {
+        t0 = clock64();
+      } else if (__any_sync(~0u, *dead != 0 || clock64() - t0 > kWaitClocks)) {
+        *dead = 1;
+        break;
       }
     }
-    __syncwarp();
   } else if (warp < 8) {
     // ---------------------------------------------------------------- queries
     const int tid = threadIdx.x - 160, chunks = m.np * 8;

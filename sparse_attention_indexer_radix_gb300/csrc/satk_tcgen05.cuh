@@ -53,19 +53,17 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-__device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *dead) {
-  const long long t0 = clock64();
-  while (!mbar_test(bar, parity)) {
-    if (*dead != 0) return;
-    if (clock64() - t0 > kWaitClocks) {
-      *dead = 1;
-      return;
-    }
-  }
+__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity) {
+  return __all_sync(~0u, mbar_poll(bar, parity));
 }
 // Waits until the barrier's phase of this parity has completed.
 __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
-  if (!mbar_test(bar, parity)) mbar_wait_slow(bar, parity, dead);
+  if (mbar_test(bar, parity)) return;
+  const long long t0 = clock64();
+  while (!mbar_test(bar, parity)) {
+    if (*dead != 0) break;
+    if (clock64() - t0 > kWaitClocks) *dead = 1;
+  }
 }
 
 // Generic-proxy writes to shared memory become visible to the tensor core.
@@ -85,6 +83,17 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
       : "r"(id), "r"(threads), "r"(x ? 1u : 0u)
       : "memory");
   return any != 0;
+}
+
+// Register shares of the warpgroups (whole warpgroups, converged).  The shares
+// of a CTA add up to at most what it was launched with.
+template <int R>
+__device__ __forceinline__ void regs_raise() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_lower() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 // ------------------------------------------------------------- async copies --
@@ -117,10 +126,18 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// The barrier's phase gets one arrival when this thread's MMAs so far are done.
+// The MMAs and their commits are written for a whole, converged warp of which
+// one elected lane issues (the same one every time): under warp-uniform control
+// flow the descriptors stay in uniform registers, where the instruction wants
+// them.  Issued from a branch of one lane instead, each MMA cost about 90
+// cycles of moving its operands there.
+
+// The barrier's phase gets one arrival when the elected lane's MMAs so far are done.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          bar)
       : "memory");
 }
 
@@ -139,8 +156,8 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lbo, uint3
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                        bool accumulate) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
