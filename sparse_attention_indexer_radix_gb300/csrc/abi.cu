@@ -1,5 +1,6 @@
 // abi.cu -- status strings, the short-name aliases of the C ABI, and the
 // host helpers that keep state (the resident-CTA cache).
+#include <cuda.h>
 #include <mutex>
 #include <unordered_map>
 
@@ -26,6 +27,31 @@ int64_t resident_ctas(const void *kernel, int block, size_t smem) {
   std::lock_guard<std::mutex> g(mu);
   cache[dev][kernel] = n;
   return n;
+}
+
+bool tensor_map_16bit(void *map, bool bf16, const void *base, int64_t rows, int64_t cols,
+                      int64_t ld, int box_rows) {
+  // The driver's function is looked up through the runtime, so the library
+  // needs no link to libcuda; the result is the same for the whole process.
+  static const auto encode = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
+  }();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+  return encode(static_cast<CUtensorMap *>(map),
+                bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                const_cast<void *>(base), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 }  // namespace satk

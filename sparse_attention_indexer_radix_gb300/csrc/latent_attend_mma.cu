@@ -16,15 +16,23 @@
 // the CTA), so most tiles need no cross-key reduction at all; l is summed per
 // thread and joined once at the end.
 //
-// Roles (512 threads): warps 0-3 softmax and results, warp 4 issues the MMAs,
-// warps 5-7 bring the queries, warps 8-15 gather key rows with 16-byte
-// asynchronous copies into 2 to 4 stages (skipped rows are zero-filled, not
-// read), each stage owned by its own warps so that loads of several tiles are
-// in flight.
+// Key rows reach shared memory in two ways, each its own instantiation:
+//  - BOX, where pages give runs of 8 or more keys that lie together: TMA boxes
+//    of a run x 64 columns.  256 threads: warps 0-3 softmax and results, warp 4
+//    issues the MMAs, warps 5-6 the boxes (every second panel of 64 columns
+//    each), warp 7 brings the queries.
+//  - else (selected rows, tiny pages): 16-byte asynchronous copies by eight
+//    warps, each stage owned by its own warps so that several tiles are in
+//    flight.  512 threads: warps 0-3 and 4 as above, 5-7 queries, 8-15 keys.
+//    (TMA's gather of four rows a request moved 512 bytes in 56 cycles, a third
+//    of what HBM gives an SM; the copies move twice that.)
+// A row that is skipped or not in the cache is masked; if what was read in its
+// place is not finite, the softmax role clears it in the tile.
 //
 // Split: the tiles of all groups form one line that is cut into equal pieces,
 // one per SM (plan kernel); a group cut across SMs leaves unnormalised partial
 // results in the workspace that a last kernel joins in a fixed order.
+#include <cuda.h>
 #include <type_traits>
 
 #include "latent_attend.cuh"
@@ -35,7 +43,8 @@ namespace {
 
 constexpr int kTile = 64;                // keys per tile
 constexpr int kPanel = kTile * 128;      // bytes of 64 columns of a tile
-constexpr int kThreads = 512;
+constexpr int threads_of(bool box) { return box ? 256 : 512; }
+constexpr int query_threads(bool box) { return box ? 32 : 96; }
 constexpr int kSoftmax = 128;            // threads of the softmax role
 constexpr int kMaxStages = 4;
 constexpr int kSmall = 3072;             // barriers and per-column arrays
@@ -68,6 +77,8 @@ struct MmaArgs {
   int nb;        // 128-column blocks of a value
   int64_t part_stride;
   int q_vec, out_vec;
+  int run;           // rows of a box: consecutive keys that share a block (1: copies)
+  CUtensorMap rows;  // the cache, in boxes of 64 columns x run rows
 };
 
 __device__ __forceinline__ int group_tiles(const Group &g) {
@@ -184,16 +195,18 @@ struct Small {
   float red[4][64];
   float sum[64], ref[64], factor[64];
   int end[64], token[64];
-  unsigned char valid[kMaxStages][kTile];
+  uint32_t valid[kMaxStages][2];  // bit per key
+  int key[2][kTile];
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t s_full[2], s_empty[2], p_full, o_done, q_full, q_empty;
+  uint64_t s_full[2], s_empty[2], p_full, o_done, q_full, q_empty, issued;
   uint32_t tmem;
   int dead;
 };
 static_assert(sizeof(Small) <= kSmall, "small shared arrays");
 
-template <class E, int N>
-__global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __grid_constant__ MmaArgs m) {
+template <class E, int N, bool BOX>
+__global__ void __launch_bounds__(threads_of(BOX), 1)
+    latent_attend_mma_kernel(const __grid_constant__ MmaArgs m) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const LatentArgs &a = m.a;
   const int64_t per = m.plan->per, total = m.plan->tiles;
@@ -211,10 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
   auto bar = [&](uint64_t &b) { return smem_addr(&b); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wps = 8 / m.nst;  // producer warps per stage
+  const int wps = 8 / m.nst;  // copies: producer warps per stage
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(bar(sm.full[s]), wps * 32);
+      mbar_init(bar(sm.full[s]), BOX ? 2 : wps * 32);
       mbar_init(bar(sm.empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -223,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
     }
     mbar_init(bar(sm.p_full), kSoftmax);
     mbar_init(bar(sm.o_done), 1);
-    mbar_init(bar(sm.q_full), 96);
+    mbar_init(bar(sm.issued), 1);
+    mbar_init(bar(sm.q_full), query_threads(BOX));
     mbar_init(bar(sm.q_empty), 1);
     sm.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -234,8 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
   tc_fence_after();
   const uint32_t tmem = sm.tmem, o_at = tmem + 2 * N;
 
-  // 128 registers a thread at launch: 128 x 200 + 384 x 104 = 512 x 128.
-  if (warp < 4) regs_raise<200>(); else regs_lower<104>();
+  if constexpr (!BOX) {  // 128 x 200 + 384 x 104 registers = 512 x 128 at launch
+    if (warp < 4) regs_raise<200>(); else regs_lower<104>();
+  }
   if (warp < 4) {
     // ------------------------------------------------------- softmax, results
     constexpr int C = N / 2;  // columns per thread: [half C, half C + C) of key kk
@@ -278,14 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
         tc_fence_before();
         mbar_arrive(bar(sm.s_empty[i & 1]));
         const int j = static_cast<int>(u - w.s) * kTile + kk;
-        const bool live = sm.valid[stage][kk] != 0;
+        const bool live = (sm.valid[stage][kk >> 5] >> (kk & 31)) & 1;
         float s[C];
 #pragma unroll
         for (int x = 0; x < C; ++x) s[x] = __uint_as_float(raw[x]) * a.scale_log2;
-        if (!live) {
-#pragma unroll
-          for (int x = 0; x < C; ++x) s[x] = -INFINITY;
-        } else if (j >= low) {
+        if (!live || j >= low) {
           // Some column may not see this key.  A masked score that is not
           // finite may come from a key row that is not: such a row would turn
           // the column's 0 weight into NaN, so it is cleared; columns that do
@@ -294,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
 #pragma unroll
           for (int x = 0; x < C; ++x) {
             const int end = sm.end[c0 + x];
-            if (j >= end && !(a.tree != nullptr && tree_bit(a, sm.token[c0 + x], j - end))) {
+            if (!live ||
+                (j >= end && !(a.tree != nullptr && tree_bit(a, sm.token[c0 + x], j - end)))) {
               odd |= !(fabsf(s[x]) < INFINITY);
               s[x] = -INFINITY;
             }
@@ -442,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
     }
   } else if (warp == 4) {
     // -------------------------------------------------------------- MMA issue
+    const uint32_t leader = elect_leader();
     constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
     constexpr uint32_t dq = mma_desc(bf16, false, false, kTile, N);
     constexpr uint32_t dp = mma_desc(bf16, true, true, 128, N);
@@ -465,16 +479,16 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
         const uint32_t s_at = tmem + (iq & 1) * N;
         int ks = 0;
         for (; ks + 4 <= ksteps; ks += 4, kd += kPanel >> 4, qd += q_panel >> 4) {
-          mma_ss(s_at, kd, qd, dq, ks > 0);
-          mma_ss(s_at, kd + 2, qd + 2, dq, true);
-          mma_ss(s_at, kd + 4, qd + 4, dq, true);
-          mma_ss(s_at, kd + 6, qd + 6, dq, true);
+          mma_ss(leader, s_at, kd, qd, dq, ks > 0);
+          mma_ss(leader, s_at, kd + 2, qd + 2, dq, true);
+          mma_ss(leader, s_at, kd + 4, qd + 4, dq, true);
+          mma_ss(leader, s_at, kd + 6, qd + 6, dq, true);
         }
-        for (; ks < ksteps; ++ks, kd += 2, qd += 2) mma_ss(s_at, kd, qd, dq, ks > 0);
-        tc_commit(bar(sm.s_full[iq & 1]));
+        for (; ks < ksteps; ++ks, kd += 2, qd += 2) mma_ss(leader, s_at, kd, qd, dq, ks > 0);
+        tc_commit(leader, bar(sm.s_full[iq & 1]));
         q_first = u0 + iq + 1 == wq.e;
         if (q_first) {
-          tc_commit(bar(sm.q_empty));
+          tc_commit(leader, bar(sm.q_empty));
           ++seg;
           if (iq + 1 < n_tiles) wq.next();
         }
@@ -486,13 +500,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
         tc_fence_after();
         uint64_t vd = v_desc + ((p_stage * stage_bytes) >> 4);
         for (int b = 0; b < m.nb; ++b, vd += (2 * kPanel) >> 4) {
-          mma_ss(o_at + b * N, vd, p_desc, dp, !p_first);
-          mma_ss(o_at + b * N, vd + 128, p_desc + 128, dp, true);
-          mma_ss(o_at + b * N, vd + 256, p_desc + 256, dp, true);
-          mma_ss(o_at + b * N, vd + 384, p_desc + 384, dp, true);
+          mma_ss(leader, o_at + b * N, vd, p_desc, dp, !p_first);
+          mma_ss(leader, o_at + b * N, vd + 128, p_desc + 128, dp, true);
+          mma_ss(leader, o_at + b * N, vd + 256, p_desc + 256, dp, true);
+          mma_ss(leader, o_at + b * N, vd + 384, p_desc + 384, dp, true);
         }
-        tc_commit(bar(sm.empty[p_stage]));
-        tc_commit(bar(sm.o_done));
+        tc_commit(leader, bar(sm.empty[p_stage]));
+        tc_commit(leader, bar(sm.o_done));
         p_first = u0 + ip + 1 == wp.e;
         if (p_first && ip + 1 < n_tiles) wp.next();
         ++ip;
@@ -506,15 +520,56 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
         break;
       }
     }
-  } else if (warp < 8) {
+    tc_commit(leader, bar(sm.issued));
+    mbar_drain(bar(sm.issued), 0);
+  } else if (BOX && warp < 7) {
+    // --------------------------------------------------------------- key rows
+    const int mine = warp - 5, panels = (m.np + 1 - mine) >> 1;  // mine, mine + 2, ...
+    Walk w;
+    w.seek(m.plan, groups, m.nh, u0);
+    int2 row;  // this lane's keys: lane and lane + 32 of the tile
+    auto rows_of = [&](int64_t u) {
+      if (u >= w.e) w.next();
+      const int j = static_cast<int>(u - w.s) * kTile + lane;
+      row.x = j < w.g.extent ? static_cast<int>(key_row(a, w.g.t0, w.g.req, j)) : -1;
+      row.y = j + 32 < w.g.extent ? static_cast<int>(key_row(a, w.g.t0, w.g.req, j + 32)) : -1;
+    };
+    rows_of(u0);
+    int *key = sm.key[mine];
+    const uint32_t leader = elect_leader();
+    for (int i = 0, stage = 0, use = 0; i < n_tiles; ++i) {
+      if (use > 0) mbar_wait(bar(sm.empty[stage]), (use - 1) & 1, dead);
+      if (mine == 0) {
+        const unsigned lo = __ballot_sync(~0u, row.x >= 0), hi = __ballot_sync(~0u, row.y >= 0);
+        if (lane == 0) sm.valid[stage][0] = lo, sm.valid[stage][1] = hi;
+      }
+      key[lane] = max(row.x, 0);
+      key[lane + 32] = max(row.y, 0);
+      __syncwarp();
+      const uint32_t full = bar(sm.full[stage]);
+      if (lane == 0) mbar_expect(full, panels * kPanel);
+      __syncwarp();
+      const uint32_t dst = base + stage * stage_bytes + mine * kPanel;
+      for (int r = 0; r < kTile; r += m.run) {
+        const int first = key[r];
+        for (int p = 0; p < panels; ++p)
+          tma_box(leader, dst + p * 2 * kPanel + r * 128, &m.rows, (2 * p + mine) * 64, first, full);
+      }
+      if (i + 1 < n_tiles) rows_of(u0 + i + 1);
+      if (++stage == m.nst) stage = 0, ++use;
+    }
+    for (int i = max(0, n_tiles - m.nst); i < n_tiles; ++i)
+      mbar_drain(bar(sm.full[i % m.nst]), (i / m.nst) & 1);
+  } else if (warp == 7 || (!BOX && warp < 8)) {
     // ---------------------------------------------------------------- queries
-    const int tid = threadIdx.x - 160, chunks = m.np * 8;
+    constexpr int threads = query_threads(BOX);
+    const int tid = static_cast<int>(threadIdx.x) - (256 - threads), chunks = m.np * 8;
     Walk w;
     w.seek(m.plan, groups, m.nh, u0);
     for (int seg = 0;; ++seg) {
       if (seg > 0) mbar_wait(bar(sm.q_empty), (seg - 1) & 1, dead);
       const int ncol = w.columns(m);
-      for (int x = tid; x < N * chunks; x += 96) {
+      for (int x = tid; x < N * chunks; x += threads) {
         const int n = x / chunks, ch = x - n * chunks, col = ch * 8;
         const int tok = n / m.hc;
         const bool live = n < ncol && col < a.D;
@@ -542,9 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
       w.next();
     }
   } else {
-    // --------------------------------------------------------------- key rows
+    // ---------------------------------------------------- key rows, by copies
     const int pw = warp - 8, stage = pw / wps, rows = kTile / wps, r0 = (pw - stage * wps) * rows;
-    if (stage < m.nst && stage < n_tiles) {
+    if (!BOX && stage < m.nst && stage < n_tiles) {
       Walk w;
       w.seek(m.plan, groups, m.nh, u0);
       auto row_of = [&](int64_t u) {
@@ -552,24 +607,29 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_mma_kernel(const __
         const int j = static_cast<int>(u - w.s) * kTile + r0 + lane;
         return lane < rows && j < w.g.extent ? static_cast<int>(key_row(a, w.g.t0, w.g.req, j)) : -1;
       };
-      const int ch = lane & 7, width = (a.D + 15) & ~15;
+      const int ch = lane & 7, whole = a.D / 64, width = (a.D + 15) & ~15;
+      const E *cache = static_cast<const E *>(a.cache);
+      unsigned short *valid16 = reinterpret_cast<unsigned short *>(sm.valid[stage]);
       int row = row_of(u0 + stage);
       int use = 0;
       for (int i = stage; i < n_tiles; i += m.nst, ++use) {
         if (use > 0) mbar_wait(bar(sm.empty[stage]), (use - 1) & 1, dead);
-        if (lane < rows) sm.valid[stage][r0 + lane] = row >= 0;
+        __syncwarp();
+        const unsigned live_rows = __ballot_sync(~0u, row >= 0);
+        if (lane == 0) {
+          if (rows == 16) valid16[r0 / 16] = static_cast<unsigned short>(live_rows);
+          else sm.valid[stage][r0 / 32] = live_rows;
+        }
         for (int g = 0; g < rows; g += 4) {
           const int rr = g + (lane >> 3), r = r0 + rr;
           const int at = __shfl_sync(~0u, row, rr);
           const bool live = at >= 0;
-          const E *src = static_cast<const E *>(a.cache) + (live ? at : 0) * a.ld_cache + ch * 8;
-          const uint32_t dst = base + stage * stage_bytes + r * 128 + ((ch ^ (r & 7)) << 4);
-          for (int p = 0; p < m.np; ++p) {
-            const int col = p * 64 + ch * 8;
-            const bool read = live && col < a.D;
-            if (col < width)
-              cp_async16(dst + p * kPanel, read ? src + p * 64 : static_cast<const E *>(a.cache), read);
-          }
+          const E *src = cache + (live ? at : 0) * a.ld_cache + ch * 8;
+          uint32_t dst = base + stage * stage_bytes + r * 128 + ((ch ^ (r & 7)) << 4);
+#pragma unroll 4
+          for (int p = 0; p < whole; ++p, src += 64, dst += kPanel) cp_async16(dst, src, live);
+          const int col = whole * 64 + ch * 8;
+          if (col < width) cp_async16(dst, col < a.D ? src : cache, live && col < a.D);
         }
         if (i + m.nst < n_tiles) row = row_of(u0 + i + m.nst);
         cp_async_wait_all();
@@ -658,25 +718,32 @@ int columns_for(int hc, int tpg) {
 
 size_t group_bytes() { return (sizeof(Plan) + 15) / 16 * 16 + sizeof(Group) * kMaxTokens; }
 
-template <class E, int N>
+template <class E, int N, bool BOX>
 int launch(const MmaArgs &m, int ctas, int smem, cudaStream_t stream) {
-  if (!allow_smem(latent_attend_mma_kernel<E, N>, smem)) return SATK_ECUDA;
-  latent_attend_mma_kernel<E, N><<<ctas, kThreads, smem, stream>>>(m);
+  if (!allow_smem(latent_attend_mma_kernel<E, N, BOX>, smem)) return SATK_ECUDA;
+  latent_attend_mma_kernel<E, N, BOX><<<ctas, threads_of(BOX), smem, stream>>>(m);
   latent_join_kernel<E><<<dim3(ctas, kCombineY), 256, 0, stream>>>(m, N);
   return launch_status();
 }
 
-template <class E>
+template <class E, bool BOX>
 int launch_columns(const MmaArgs &m, int N, int ctas, int smem, cudaStream_t stream) {
-  return N == 16   ? launch<E, 16>(m, ctas, smem, stream)
-         : N == 32 ? launch<E, 32>(m, ctas, smem, stream)
-                   : launch<E, 64>(m, ctas, smem, stream);
+  return N == 16   ? launch<E, 16, BOX>(m, ctas, smem, stream)
+         : N == 32 ? launch<E, 32, BOX>(m, ctas, smem, stream)
+                   : launch<E, 64, BOX>(m, ctas, smem, stream);
+}
+
+template <class E>
+int launch_all(const MmaArgs &m, int N, int ctas, int smem, cudaStream_t stream) {
+  return m.run > 1 ? launch_columns<E, true>(m, N, ctas, smem, stream)
+                   : launch_columns<E, false>(m, N, ctas, smem, stream);
 }
 
 }  // namespace
 
 bool latent_attend_mma_fits(const LatentArgs &a) {
-  return a.D % 8 == 0 && a.ld_cache % 8 == 0 && aligned16(a.cache) && a.cache_rows <= INT32_MAX;
+  return a.D % 8 == 0 && a.ld_cache % 8 == 0 && aligned16(a.cache) && a.cache_rows > 0 &&
+         a.cache_rows <= INT32_MAX;
 }
 
 size_t latent_attend_mma_workspace(int H, int dl) {
@@ -709,6 +776,17 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
             (args.H == 1 || args.ld_q_h % 8 == 0);
   m.out_vec = (reinterpret_cast<uintptr_t>(args.out) & 3u) == 0 && args.dl % 2 == 0 &&
               (args.T == 1 || args.ld_out_t % 2 == 0) && (args.H == 1 || args.ld_out_h % 2 == 0);
+  // Rows that consecutive keys of a tile share in one block (a run is in the
+  // cache as a whole, or from its first key on is not).
+  m.run = 1;
+  if (args.rows == nullptr && args.stride_rows >= args.block_size) {
+    while (m.run < kTile && args.block_size % (2 * m.run) == 0) m.run *= 2;
+    if (m.run < 8) m.run = 1;
+  }
+  if (m.run > 1 &&
+      !tensor_map_16bit(&m.rows, dtype == SATK_BF16, args.cache, args.cache_rows, args.D,
+                        args.ld_cache, m.run))
+    return SATK_ECUDA;
   unsigned char *ws = static_cast<unsigned char *>(workspace);
   m.group = reinterpret_cast<Group *>(ws + (sizeof(Plan) + 15) / 16 * 16);
   m.parts = reinterpret_cast<float *>(ws + group_bytes());
@@ -728,8 +806,8 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
       if (args.tree != nullptr) a.tree = args.tree + static_cast<int64_t>(t) * args.tree_words;
     }
     latent_plan_kernel<<<1, 1024, 0, stream>>>(m, ctas);
-    const int rc = dtype == SATK_BF16 ? launch_columns<__nv_bfloat16>(m, N, ctas, smem, stream)
-                                      : launch_columns<__half>(m, N, ctas, smem, stream);
+    const int rc = dtype == SATK_BF16 ? launch_all<__nv_bfloat16>(m, N, ctas, smem, stream)
+                                      : launch_all<__half>(m, N, ctas, smem, stream);
     if (rc != SATK_OK) return rc;
   }
   return SATK_OK;

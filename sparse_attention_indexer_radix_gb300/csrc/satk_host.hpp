@@ -32,4 +32,11 @@ inline bool allow_smem(K kernel, size_t bytes) {
 // device.  0 on error.
 int64_t resident_ctas(const void *kernel, int block, size_t smem);
 
+// The tensor map of a row-major 16-bit matrix [rows, cols] (row stride ld
+// elements, base and stride multiples of 16 bytes) read in boxes of 64 columns
+// x box_rows rows with the 128-byte swizzle; columns past `cols` read as zeros.
+// False if the driver refuses it.
+bool tensor_map_16bit(void *map, bool bf16, const void *base, int64_t rows, int64_t cols,
+                      int64_t ld, int box_rows);
+
 }  // namespace satk

@@ -66,6 +66,14 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same for a role's own copies or MMAs in flight before it leaves: waits
+// although the CTA is `dead`, as long as any wait may last.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_test(bar, parity) && clock64() - t0 < kWaitClocks) {
+  }
+}
+
 // Generic-proxy writes to shared memory become visible to the tensor core.
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -98,9 +106,27 @@ __device__ __forceinline__ void regs_lower() {
 
 // ------------------------------------------------------------- async copies --
 
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+// A box of a tensor map (64 columns from `col`, a multiple of 64, of the map's
+// rows from `row` on) into consecutive 128-byte rows; rows outside the tensor
+// read as zeros.  For a whole converged warp of which the leader issues, as with
+// the MMAs below.
+__device__ __forceinline__ void tma_box(uint32_t leader, uint32_t dst, const void *map, int col,
+                                        int row, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %5, 0;\n"
+      "@e cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+      "l"(map), "r"(col), "r"(row), "r"(bar), "r"(leader)
+      : "memory");
+}
+
 // 16 bytes global -> shared; zeros, and no read, when !live.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(live ? 16 : 0)
                : "memory");
 }
@@ -127,17 +153,25 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // The MMAs and their commits are written for a whole, converged warp of which
-// one elected lane issues (the same one every time): under warp-uniform control
-// flow the descriptors stay in uniform registers, where the instruction wants
-// them.  Issued from a branch of one lane instead, each MMA cost about 90
+// one lane issues (`leader`, the same one every time): under warp-uniform
+// control flow the descriptors stay in uniform registers, where the instruction
+// wants them.  Issued from a branch of one lane instead, each MMA cost about 90
 // cycles of moving its operands there.
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t leader;
+  asm volatile(
+      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\nselp.u32 %0, 1, 0, e;\n}\n"
+      : "=r"(leader));
+  return leader;
+}
 
 // The barrier's phase gets one arrival when the elected lane's MMAs so far are done.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
+__device__ __forceinline__ void tc_commit(uint32_t leader, uint32_t bar) {
   asm volatile(
-      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %1, 0;\n"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          bar)
+          bar),
+      "r"(leader)
       : "memory");
 }
 
@@ -153,12 +187,12 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lbo, uint3
   return (static_cast<uint64_t>(addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lbo >> 4) << 16) |
          (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
-                                       bool accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t desc, bool accumulate) {
   asm volatile(
-      "{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+      "{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 e, %5, 0;\n"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u)
+      "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u), "r"(leader)
       : "memory");
 }
 
