@@ -29,8 +29,9 @@ int64_t resident_ctas(const void *kernel, int block, size_t smem) {
   return n;
 }
 
-bool tensor_map_16bit(void *map, bool bf16, const void *base, int64_t rows, int64_t cols,
-                      int64_t ld, int box_rows) {
+bool tensor_map_16bit(void *map, bool bf16, const void *base, int64_t cols, int64_t rows,
+                      int64_t ld_rows, int box_rows, int64_t outer, int64_t ld_outer,
+                      int box_outer) {
   // The driver's function is looked up through the runtime, so the library
   // needs no link to libcuda; the result is the same for the whole process.
   static const auto encode = [] {
@@ -43,12 +44,16 @@ bool tensor_map_16bit(void *map, bool bf16, const void *base, int64_t rows, int6
     return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
   }();
   if (encode == nullptr) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld_rows) * 2,
+                                 static_cast<cuuint64_t>(ld_outer) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(box_outer)};
+  const cuuint32_t step[3] = {1, 1, 1};
   return encode(static_cast<CUtensorMap *>(map),
-                bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                const_cast<void *>(base), dims, strides, box, step,
+                bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                outer > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;

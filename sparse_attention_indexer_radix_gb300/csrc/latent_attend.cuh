@@ -65,22 +65,29 @@ __device__ __forceinline__ int token_extent(const LatentArgs &a, int t, int end)
   return end;
 }
 
-// Physical cache row of key j of token t, or -1 (a skipped entry, or a row
-// outside the cache, which raises its status bit).
-__device__ __forceinline__ int64_t key_row(const LatentArgs &a, int t, int r, int j) {
-  int64_t row;
+// The load behind key j of token t: its row, or its block. The row itself, or -1
+// (a skipped entry, or a row outside the cache, which raises its status bit),
+// comes from it in a second step, so that the load can be in flight meanwhile.
+__device__ __forceinline__ int key_entry(const LatentArgs &a, int t, int r, int j) {
+  if (a.rows != nullptr) return a.rows[t * a.ld_rows + j];
+  return a.block_table[r * a.ld_table + (a.b_shift >= 0 ? j >> a.b_shift : j / a.block_size)];
+}
+__device__ __forceinline__ int64_t entry_row(const LatentArgs &a, int entry, int j) {
+  int64_t row = entry;
   if (a.rows != nullptr) {
-    row = a.rows[t * a.ld_rows + j];
     if (row < 0) return -1;
   } else {
-    const int b = a.b_shift >= 0 ? j >> a.b_shift : j / a.block_size;
-    row = a.block_table[r * a.ld_table + b] * a.stride_rows + (j - b * a.block_size);
+    row = row * a.stride_rows +
+          (a.b_shift >= 0 ? j & ((1 << a.b_shift) - 1) : j % a.block_size);
   }
   if (row < 0 || row >= a.cache_rows) {
     if (a.status != nullptr) atomicOr(a.status, SATK_STATUS_BAD_ROW);
     return -1;
   }
   return row;
+}
+__device__ __forceinline__ int64_t key_row(const LatentArgs &a, int t, int r, int j) {
+  return entry_row(a, key_entry(a, t, r, j), j);
 }
 
 // The general kernel: any widths, strides and alignment (latent_attend_warp.cu).

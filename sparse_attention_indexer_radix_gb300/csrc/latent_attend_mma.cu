@@ -19,19 +19,23 @@
 // Key rows reach shared memory in two ways, each its own instantiation:
 //  - BOX, where pages give runs of 8 or more keys that lie together: TMA boxes
 //    of a run x 64 columns.  256 threads: warps 0-3 softmax and results, warp 4
-//    issues the MMAs, warps 5-6 the boxes (every second panel of 64 columns
-//    each), warp 7 brings the queries.
+//    issues the MMAs, warps 5-6 the boxes, warp 7 brings the queries.
 //  - else (selected rows, tiny pages): 16-byte asynchronous copies by eight
-//    warps, each stage owned by its own warps so that several tiles are in
-//    flight.  512 threads: warps 0-3 and 4 as above, 5-7 queries, 8-15 keys.
-//    (TMA's gather of four rows a request moved 512 bytes in 56 cycles, a third
-//    of what HBM gives an SM; the copies move twice that.)
+//    warps, eight rows of a tile each.  512 threads: warps 0-3 and 4 as above, 5-7 queries, 8-15 keys.
+//    (Random rows of 1088 bytes, nothing else running: these copies 6.3 TB/s,
+//    TMA's gather of four rows a request 5.0, bulk copies of a row 3.7.)
+// A stage is handed over in two halves of its columns: the scores of the first
+// columns begin while the others arrive, and the first columns' values are
+// given back while the others' products run.
+//
 // A row that is skipped or not in the cache is masked; if what was read in its
 // place is not finite, the softmax role clears it in the tile.
 //
 // Split: the tiles of all groups form one line that is cut into equal pieces,
-// one per SM (plan kernel); a group cut across SMs leaves unnormalised partial
-// results in the workspace that a last kernel joins in a fixed order.
+// one per SM (kItemTiles more for each group, for its queries and results); a
+// group cut across SMs leaves unnormalised partial results in the
+// workspace that a second kernel joins in a fixed order.  Up to kInline tokens
+// every CTA works out the line for itself; a kernel before does it for more.
 #include <cuda.h>
 #include <type_traits>
 
@@ -49,7 +53,9 @@ constexpr int kSoftmax = 128;            // threads of the softmax role
 constexpr int kMaxStages = 4;
 constexpr int kSmall = 3072;             // barriers and per-column arrays
 constexpr int kMaxTokens = 16384;        // tokens per launch (the plan's size)
-constexpr int kCombineY = 16;
+constexpr int kInline = 512;             // tokens up to which CTAs plan for themselves
+constexpr int kJoinY = 8;                // CTAs that share a join, one warp a column
+constexpr int kItemTiles = 3;            // tiles that a group's own costs are worth
 constexpr int kMinTiles = 2;             // tiles per SM below which no group is cut
 constexpr float kUnset = -1e30f;         // reference of a column without a score
 constexpr float kLag = 8.f;              // log2 by which scores may pass m_n
@@ -63,22 +69,30 @@ struct Group {
 
 struct Plan {
   int64_t tiles, per;  // on the line, per CTA
-  int ngroups, pad;
+  int ngroups, pad[3];
+  __device__ Group *groups() { return reinterpret_cast<Group *>(this + 1); }
 };
+constexpr size_t plan_bytes(int groups) { return (sizeof(Plan) + sizeof(Group) * groups + 15) / 16 * 16; }
 
 struct MmaArgs {
   LatentArgs a;
-  Plan *plan;
-  Group *group;
+  unsigned char *plans;  // one, or one per CTA
+  int4 *joins;           // per CTA: token, column count, first head, parts (0: none)
+  int inline_plan;
   float *parts;
+  __device__ Plan *plan(int cta) const {
+    return reinterpret_cast<Plan *>(plans + (inline_plan ? cta * plan_bytes(kInline) : 0));
+  }
   int nh, hc;    // head chunks and heads per chunk
   int tpg;       // tokens per group
   int np, nst;   // 64-column panels of a key row, stages
+  int np0;       // panels of a stage's first half (all of them: there is no second)
   int nb;        // 128-column blocks of a value
   int64_t part_stride;
-  int q_vec, out_vec;
+  int q_box, q_vec, out_vec;  // queries by TMA, by 16-byte copies; paired stores
   int run;           // rows of a box: consecutive keys that share a block (1: copies)
   CUtensorMap rows;  // the cache, in boxes of 64 columns x run rows
+  CUtensorMap q;     // the queries, in boxes of 64 columns x hc heads x tpg tokens
 };
 
 __device__ __forceinline__ int group_tiles(const Group &g) {
@@ -90,19 +104,26 @@ __device__ __forceinline__ int64_t per_cta(int64_t tiles, int ctas) {
   return per < kMinTiles ? kMinTiles : per;
 }
 
-// Groups in token order, and the prefix sum of their tiles.  One CTA.
-__global__ void __launch_bounds__(1024) latent_plan_kernel(MmaArgs m, int ctas) {
+struct PlanScratch {
+  int64_t tiles[32];
+  int groups[32];
+};
+
+// Groups in token order, and the prefix sum of their tiles, by one CTA of up to
+// 1024 threads.
+__device__ void make_plan(const MmaArgs &m, int ctas, Plan *plan, PlanScratch &scratch) {
   const LatentArgs &a = m.a;
-  __shared__ int64_t wt[32];
-  __shared__ int wg[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.T + 1023) / 1024;
+  int64_t *wt = scratch.tiles;
+  int *wg = scratch.groups;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int per = (a.T + threads - 1) / threads;
   const int b = min(tid * per, a.T), e = min(b + per, a.T);
   auto leader = [&](int t) {
     return m.tpg == 1 || t % m.tpg == 0 || a.req_id[t] != a.req_id[t - 1];
   };
   auto group = [&](int t) {
     Group g;
+    g.start = 0;
     g.t0 = t;
     g.req = a.rows == nullptr ? a.req_id[t] : 0;
     g.ntok = 0;
@@ -120,7 +141,7 @@ __global__ void __launch_bounds__(1024) latent_plan_kernel(MmaArgs m, int ctas) 
   for (int t = b; t < e; ++t)
     if (leader(t)) {
       g = group(t);
-      tiles += static_cast<int64_t>(group_tiles(g)) * m.nh;
+      tiles += static_cast<int64_t>(group_tiles(g) + kItemTiles) * m.nh;
       ++groups;
     }
   int64_t st = tiles;
@@ -135,69 +156,113 @@ __global__ void __launch_bounds__(1024) latent_plan_kernel(MmaArgs m, int ctas) 
   __syncthreads();
   int64_t all = 0;
   int n = 0;
-  for (int w = 0; w < 32; ++w) {
+  for (int w = 0; w < threads / 32; ++w) {
     if (w < warp) st += wt[w], sg += wg[w];
     all += wt[w];
     n += wg[w];
   }
   st -= tiles;
   sg -= groups;
-  Group *out = m.group;
+  Group *out = plan->groups();
   for (int t = b; t < e; ++t)
     if (leader(t)) {
       if (groups > 1) g = group(t);
       g.start = st;
       out[sg++] = g;
-      st += static_cast<int64_t>(group_tiles(g)) * m.nh;
+      st += static_cast<int64_t>(group_tiles(g) + kItemTiles) * m.nh;
     }
   if (tid == 0) {
-    m.plan->tiles = all;
-    m.plan->per = per_cta(all, ctas);
-    m.plan->ngroups = n;
+    plan->tiles = all;
+    plan->per = per_cta(all, ctas);
+    plan->ngroups = n;
   }
 }
 
-// A position on the line: item (group, head chunk) with tiles [s, e).
-struct Walk {
+__global__ void __launch_bounds__(1024) latent_plan_kernel(const __grid_constant__ MmaArgs m, int ctas) {
+  __shared__ PlanScratch scratch;
+  make_plan(m, ctas, m.plan(0), scratch);
+}
+
+// One CTA's piece of the line: `length` positions from u0 on.
+struct Piece {
   const Group *group;
-  int nh, gi, c;
-  int64_t s, e;
-  Group g;
-  __device__ void seek(const Plan *plan, const Group *groups, int heads, int64_t u) {
-    group = groups;
-    nh = heads;
+  int nh, length;
+};
+
+// The items (group, head chunk) of a piece, in order, with the tiles [k0, k1) of
+// each that the piece covers.
+struct Walk {
+  int gi, c, k0, k1, s;  // s: where the item starts, counted from u0
+  int t0, ntok, extent, req;
+  __device__ void load(const Piece &piece) {
+    const Group g = piece.group[gi];
+    t0 = g.t0;
+    ntok = g.ntok;
+    extent = g.extent;
+    req = g.req;
+  }
+  __device__ int tiles() const { return extent > 0 ? (extent + kTile - 1) / kTile : 1; }
+  __device__ void start(const Piece &piece, const Plan *plan, int64_t u0) {
     int lo = 0, hi = plan->ngroups;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (group[mid].start <= u) lo = mid; else hi = mid;
+      if (piece.group[mid].start <= u0) lo = mid; else hi = mid;
     }
     gi = lo;
-    g = group[gi];
-    const int tiles = group_tiles(g);
-    c = static_cast<int>((u - g.start) / tiles);
-    s = g.start + static_cast<int64_t>(c) * tiles;
-    e = s + tiles;
+    load(piece);
+    const int64_t past = u0 - piece.group[gi].start;
+    c = static_cast<int>(past / (tiles() + kItemTiles));
+    s = static_cast<int>(static_cast<int64_t>(c) * (tiles() + kItemTiles) - past);
+    cut(piece);
+    if (done()) next(piece);
   }
-  __device__ void next() {
-    if (++c == nh) {
-      c = 0;
-      g = group[++gi];
+  __device__ void cut(const Piece &piece) {
+    k0 = max(-s, 0);
+    k1 = min(piece.length - s, tiles());
+  }
+  __device__ bool done() const { return k0 >= k1; }
+  __device__ void next(const Piece &piece) {
+    s += tiles() + kItemTiles;
+    if (s >= piece.length) {
+      k0 = k1 = 0;
+      return;
     }
-    s = e;
-    e = s + group_tiles(g);
+    if (++c == piece.nh) {
+      c = 0;
+      ++gi;
+      load(piece);
+    }
+    cut(piece);
   }
   // Heads of this chunk, and score columns in use.
   __device__ int heads(const MmaArgs &m) const { return min(m.hc, m.a.H - c * m.hc); }
-  __device__ int columns(const MmaArgs &m) const { return g.ntok == 1 ? heads(m) : g.ntok * m.hc; }
+  __device__ int columns(const MmaArgs &m) const { return ntok == 1 ? heads(m) : ntok * m.hc; }
+};
+
+// One tile after the other.
+struct Cursor {
+  Walk w;
+  int k;
+  __device__ explicit Cursor(const Walk &from) : w(from), k(from.k0) {}
+  __device__ bool more() const { return k < w.k1; }
+  __device__ bool first() const { return k == w.k0; }
+  __device__ bool last() const { return k + 1 == w.k1; }
+  __device__ void step(const Piece &piece) {
+    if (++k == w.k1) {
+      w.next(piece);
+      k = w.k0;
+    }
+  }
 };
 
 struct Small {
   float red[4][64];
-  float sum[64], ref[64], factor[64];
+  float ref[64];
+  float factor[64];  // of a rescaling; at a group's end 1 / sum
   int end[64], token[64];
+  unsigned long long sees[64];  // of a tile's keys, per column; at a group's end the output's offset
   uint32_t valid[kMaxStages][2];  // bit per key
-  int key[2][kTile];
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages][2], empty[kMaxStages][2];
   uint64_t s_full[2], s_empty[2], p_full, o_done, q_full, q_empty, issued;
   uint32_t tmem;
   int dead;
@@ -209,11 +274,23 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
     latent_attend_mma_kernel(const __grid_constant__ MmaArgs m) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const LatentArgs &a = m.a;
-  const int64_t per = m.plan->per, total = m.plan->tiles;
+  Plan *const plan = m.plan(blockIdx.x);
+  wait_for_previous_kernel();
+  if (m.inline_plan) {
+    make_plan(m, gridDim.x, plan, *reinterpret_cast<PlanScratch *>(smem));
+    fence_async_shared();
+    __syncthreads();
+  }
+  const int64_t per = plan->per, total = plan->tiles;
   const int64_t u0 = min(blockIdx.x * per, total), u1 = min(u0 + per, total);
-  if (u0 >= u1) return;
-  const int n_tiles = static_cast<int>(u1 - u0);
-  const Group *groups = m.group;
+  const Piece piece{plan->groups(), m.nh, static_cast<int>(u1 - u0)};
+  Walk w;
+  w.k0 = w.k1 = 0;
+  if (u0 < u1) w.start(piece, plan, u0);
+  if (w.done()) {
+    if (threadIdx.x == 0) m.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
 
   const int stage_bytes = m.np * kPanel, q_panel = N * 128;
   const uint32_t base = smem_addr(smem);
@@ -224,11 +301,12 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
   auto bar = [&](uint64_t &b) { return smem_addr(&b); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wps = 8 / m.nst;  // copies: producer warps per stage
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(bar(sm.full[s]), BOX ? 2 : wps * 32);
-      mbar_init(bar(sm.empty[s]), 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(bar(sm.full[s][h]), BOX ? 1 : 256);
+        mbar_init(bar(sm.empty[s][h]), 1);
+      }
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(sm.s_full[s]), 1);
@@ -237,7 +315,7 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
     mbar_init(bar(sm.p_full), kSoftmax);
     mbar_init(bar(sm.o_done), 1);
     mbar_init(bar(sm.issued), 1);
-    mbar_init(bar(sm.q_full), query_threads(BOX));
+    mbar_init(bar(sm.q_full), m.q_box ? 1 : query_threads(BOX));
     mbar_init(bar(sm.q_empty), 1);
     sm.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -248,43 +326,46 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem, o_at = tmem + 2 * N;
 
-  if constexpr (!BOX) {  // 128 x 200 + 384 x 104 registers = 512 x 128 at launch
-    if (warp < 4) regs_raise<200>(); else regs_lower<104>();
+  if constexpr (!BOX) {  // 128 x 216 + 384 x 96 registers, of 512 x 128 at launch
+    if (warp < 4) regs_raise<216>(); else regs_lower<96>();
   }
   if (warp < 4) {
     // ------------------------------------------------------- softmax, results
     constexpr int C = N / 2;  // columns per thread: [half C, half C + C) of key kk
     const int kk = warp * 16 + (lane & 15), half = lane >> 4, c0 = half * C;
-    Walk w;
-    w.seek(m.plan, groups, m.nh, u0);
-    int64_t u = u0;
     int i = 0, stage = 0, use = 0;  // tile of this CTA, its stage, the stage's use
-    while (u < u1) {
-      const int64_t stop = min(w.e, u1);
+    for (; !w.done(); w.next(piece)) {
       const int ncol = w.columns(m);
       // Per column, the token and the end below which it sees every key.  A
       // group of one token without a tree needs no mask: keys past its end
       // come as skipped rows.
       if (threadIdx.x < N) {
         const int n = threadIdx.x;
-        const int t = w.g.t0 + min(n / m.hc, w.g.ntok - 1);
-        const bool masked = a.rows == nullptr && (w.g.ntok > 1 || a.tree != nullptr) && n < ncol;
+        const int t = w.t0 + min(n / m.hc, w.ntok - 1);
+        const bool masked = a.rows == nullptr && (w.ntok > 1 || a.tree != nullptr) && n < ncol;
         sm.token[n] = t;
         sm.end[n] = masked ? max(a.row_ends[t], 0) : INT32_MAX;
       }
       named_sync(1, kSoftmax);
       int low = INT32_MAX;
 #pragma unroll
-      for (int x = 0; x < C; ++x) low = min(low, sm.end[c0 + x]);
+      for (int x = 0; x < N; ++x) low = min(low, sm.end[x]);
       float l[C], ref[C];
 #pragma unroll
       for (int x = 0; x < C; ++x) l[x] = 0.f, ref[x] = kUnset;
-      const bool whole = u == w.s && stop == w.e;
-      const int slot = u == w.s ? 1 : 0;
+      const bool whole = w.k0 == 0 && w.k1 == w.tiles();
+      const int slot = w.k0 == 0 ? 1 : 0;
+      // The CTA in which a group starts and does not end has it joined.
+      if (threadIdx.x == 0) {
+        const int end = w.s + w.tiles();  // that of its tiles
+        m.joins[blockIdx.x] = make_int4(w.t0, ncol, w.c * m.hc,
+                                        w.k0 == 0 && end > piece.length
+                                            ? static_cast<int>((end - 1) / per) + 1 : 0);
+      }
       bool first = true;
-      for (; u < stop; ++u, ++i) {
+      for (int k = w.k0; k < w.k1; ++k, ++i) {
         mbar_wait(bar(sm.s_full[i & 1]), (i >> 1) & 1, dead);
-        mbar_wait(bar(sm.full[stage]), use & 1, dead);  // the stage's valid flags
+        mbar_wait(bar(sm.full[stage][0]), use & 1, dead);  // the stage's valid flags
         __syncwarp();
         tc_fence_after();
         uint32_t raw[C];
@@ -292,12 +373,28 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
         tmem_wait_ld();
         tc_fence_before();
         mbar_arrive(bar(sm.s_empty[i & 1]));
-        const int j = static_cast<int>(u - w.s) * kTile + kk;
+        const int j0 = k * kTile;
+        if (j0 + kTile > low) {
+          // Some column may not see some key: bit kk of sees[n].
+          if (threadIdx.x < N) {
+            const int n = threadIdx.x, past = j0 - sm.end[n];  // first key past the end
+            unsigned long long sees = past >= 0 ? 0 : past <= -kTile ? ~0ull : ~0ull >> (kTile + past);
+            if (a.tree != nullptr && n < ncol)
+              for (int y = max(past >> 5, 0); y <= (past + kTile - 1) >> 5 && y < a.tree_words; ++y) {
+                const unsigned long long bits = static_cast<uint32_t>(
+                    a.tree[static_cast<int64_t>(sm.token[n]) * a.tree_words + y]);
+                const int at = y * 32 - past;  // tile position of the word's first bit
+                sees |= at >= 0 ? bits << at : bits >> -at;
+              }
+            sm.sees[n] = sees;
+          }
+          named_sync(1, kSoftmax);
+        }
         const bool live = (sm.valid[stage][kk >> 5] >> (kk & 31)) & 1;
-        float s[C];
+        float s[C];  // scores in log2, less their references
 #pragma unroll
-        for (int x = 0; x < C; ++x) s[x] = __uint_as_float(raw[x]) * a.scale_log2;
-        if (!live || j >= low) {
+        for (int x = 0; x < C; ++x) s[x] = fmaf(__uint_as_float(raw[x]), a.scale_log2, -ref[x]);
+        if (!live || j0 + kk >= low) {
           // Some column may not see this key.  A masked score that is not
           // finite may come from a key row that is not: such a row would turn
           // the column's 0 weight into NaN, so it is cleared; columns that do
@@ -305,9 +402,7 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
           bool odd = false;
 #pragma unroll
           for (int x = 0; x < C; ++x) {
-            const int end = sm.end[c0 + x];
-            if (!live ||
-                (j >= end && !(a.tree != nullptr && tree_bit(a, sm.token[c0 + x], j - end)))) {
+            if (!live || !((sm.sees[c0 + x] >> kk) & 1)) {
               odd |= !(fabsf(s[x]) < INFINITY);
               s[x] = -INFINITY;
             }
@@ -332,12 +427,12 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
         }
         bool pass = first;
 #pragma unroll
-        for (int x = 0; x < C; ++x) pass |= s[x] - ref[x] > kLag;
+        for (int x = 0; x < C; ++x) pass |= s[x] > kLag;
         if (named_any(1, kSoftmax, pass)) {
           // Move the references to the running maxima.
 #pragma unroll
           for (int x = 0; x < C; ++x) {
-            float mx = s[x];
+            float mx = s[x] == -INFINITY ? s[x] : __uint_as_float(raw[x]) * a.scale_log2;
 #pragma unroll
             for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
             if ((lane & 15) == 0) sm.red[warp][c0 + x] = mx;
@@ -351,6 +446,7 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
             const float f = exp2_fast(ref[x] - now);
             l[x] *= f;
             ref[x] = now;
+            if (s[x] != -INFINITY) s[x] = fmaf(__uint_as_float(raw[x]), a.scale_log2, -now);
             if (warp == 0 && (lane & 15) == 0) sm.factor[n] = f, sm.ref[n] = now;
           }
           named_sync(1, kSoftmax);
@@ -375,7 +471,7 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
         Pack8<E> p[C / 8];
 #pragma unroll
         for (int x = 0; x < C; x += 2) {
-          const float p0 = exp2_fast(s[x] - ref[x]), p1 = exp2_fast(s[x + 1] - ref[x + 1]);
+          const float p0 = exp2_fast(s[x]), p1 = exp2_fast(s[x + 1]);
           l[x] += p0;
           l[x + 1] += p1;
           p[x / 8].h[(x % 8) / 2] = Elem<E>::from2(p0, p1);
@@ -404,7 +500,8 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
         const int n = threadIdx.x;
         const float sum = sm.red[0][n] + sm.red[1][n] + sm.red[2][n] + sm.red[3][n];
         if (whole) {
-          sm.sum[n] = sum == 0.f ? 0.f : 1.f / sum;
+          sm.factor[n] = sum == 0.f ? 0.f : 1.f / sum;
+          sm.sees[n] = sm.token[n] * a.ld_out_t + (w.c * m.hc + n % m.hc) * a.ld_out_h;
           if (a.lse != nullptr && n < ncol)
             a.lse[static_cast<int64_t>(sm.token[n]) * a.H + w.c * m.hc + n % m.hc] =
                 sum == 0.f ? -INFINITY : (sm.ref[n] + log2f(sum)) * kLn2;
@@ -427,14 +524,13 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
           // Lanes of a pair swap so that each stores two columns of one head.
 #pragma unroll
           for (int y = 0; y < 16; y += 2) {
-            const float x0 = __uint_as_float(o[y]) * sm.sum[n0 + y];
-            const float x1 = __uint_as_float(o[y + 1]) * sm.sum[n0 + y + 1];
+            const float x0 = __uint_as_float(o[y]) * sm.factor[n0 + y];
+            const float x1 = __uint_as_float(o[y + 1]) * sm.factor[n0 + y + 1];
             const float got = __shfl_xor_sync(~0u, (lane & 1) ? x0 : x1, 1);
             const int n = n0 + y + (lane & 1), d = dim & ~1;
             const float lo = (lane & 1) ? got : x0, hi = (lane & 1) ? x1 : got;
             if (n < ncol) {
-              E *out = static_cast<E *>(a.out) + sm.token[n] * a.ld_out_t +
-                       (w.c * m.hc + n % m.hc) * a.ld_out_h + d;
+              E *out = static_cast<E *>(a.out) + static_cast<int64_t>(sm.sees[n]) + d;
               if (m.out_vec) {
                 if (d < a.dl) *reinterpret_cast<typename Elem<E>::T2 *>(out) = Elem<E>::from2(lo, hi);
               } else {
@@ -451,7 +547,6 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
       }
       tc_fence_before();
       named_sync(1, kSoftmax);  // the per-column arrays are free
-      if (u < u1) w.next();
     }
   } else if (warp == 4) {
     // -------------------------------------------------------------- MMA issue
@@ -463,52 +558,61 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
     // Descriptors hold addresses in units of 16 bytes: steps are added to them.
     const uint64_t k_desc = tile_desc(base, 16, 1024), q_desc = tile_desc(q_at, 16, 1024);
     const uint64_t v_desc = tile_desc(base, kPanel, 1024), p_desc = tile_desc(p_at, kPanel, 1024);
-    Walk wq, wp;
-    wq.seek(m.plan, groups, m.nh, u0);
-    wp = wq;
+    Cursor cq(w), cp(w);  // the next tile of the scores and of the values
+    const int ksteps0 = min(m.np0 * 4, ksteps), nb0 = m.np0 < m.np ? m.np0 / 2 : m.nb;
     int iq = 0, ip = 0, q_stage = 0, q_use = 0, p_stage = 0, seg = 0;
-    bool q_first = true, p_first = true;
+    bool q_half = false;  // the scores' first half is issued
+    uint64_t kd = 0, qd = 0;
+    auto scores = [&](int ks, int end) {
+      const uint32_t s_at = tmem + (iq & 1) * N;
+      for (; ks + 4 <= end; ks += 4, kd += kPanel >> 4, qd += q_panel >> 4) {
+        mma_ss(leader, s_at, kd, qd, dq, ks > 0);
+        mma_ss(leader, s_at, kd + 2, qd + 2, dq, true);
+        mma_ss(leader, s_at, kd + 4, qd + 4, dq, true);
+        mma_ss(leader, s_at, kd + 6, qd + 6, dq, true);
+      }
+      for (; ks < end; ++ks, kd += 2, qd += 2) mma_ss(leader, s_at, kd, qd, dq, ks > 0);
+    };
     long long t0 = clock64();
-    while (ip < n_tiles) {
+    while (cp.more()) {
       bool moved = false;
-      if (iq < n_tiles && warp_poll(bar(sm.full[q_stage]), q_use & 1) &&
+      if (cq.more() && !q_half && warp_poll(bar(sm.full[q_stage][0]), q_use & 1) &&
           (iq < 2 || warp_poll(bar(sm.s_empty[iq & 1]), ((iq >> 1) - 1) & 1)) &&
-          (!q_first || warp_poll(bar(sm.q_full), seg & 1))) {
+          (!cq.first() || warp_poll(bar(sm.q_full), seg & 1))) {
         tc_fence_after();
-        uint64_t kd = k_desc + ((q_stage * stage_bytes) >> 4), qd = q_desc;
-        const uint32_t s_at = tmem + (iq & 1) * N;
-        int ks = 0;
-        for (; ks + 4 <= ksteps; ks += 4, kd += kPanel >> 4, qd += q_panel >> 4) {
-          mma_ss(leader, s_at, kd, qd, dq, ks > 0);
-          mma_ss(leader, s_at, kd + 2, qd + 2, dq, true);
-          mma_ss(leader, s_at, kd + 4, qd + 4, dq, true);
-          mma_ss(leader, s_at, kd + 6, qd + 6, dq, true);
-        }
-        for (; ks < ksteps; ++ks, kd += 2, qd += 2) mma_ss(leader, s_at, kd, qd, dq, ks > 0);
+        kd = k_desc + ((q_stage * stage_bytes) >> 4);
+        qd = q_desc;
+        scores(0, ksteps0);
+        q_half = moved = true;
+      }
+      if (q_half && (m.np0 == m.np || warp_poll(bar(sm.full[q_stage][1]), q_use & 1))) {
+        tc_fence_after();
+        scores(ksteps0, ksteps);
         tc_commit(leader, bar(sm.s_full[iq & 1]));
-        q_first = u0 + iq + 1 == wq.e;
-        if (q_first) {
+        if (cq.last()) {
           tc_commit(leader, bar(sm.q_empty));
           ++seg;
-          if (iq + 1 < n_tiles) wq.next();
         }
+        cq.step(piece);
         ++iq;
         if (++q_stage == m.nst) q_stage = 0, ++q_use;
+        q_half = false;
         moved = true;
       }
       if (ip < iq && warp_poll(bar(sm.p_full), ip & 1)) {
         tc_fence_after();
         uint64_t vd = v_desc + ((p_stage * stage_bytes) >> 4);
+        const bool more = !cp.first();
         for (int b = 0; b < m.nb; ++b, vd += (2 * kPanel) >> 4) {
-          mma_ss(leader, o_at + b * N, vd, p_desc, dp, !p_first);
+          mma_ss(leader, o_at + b * N, vd, p_desc, dp, more);
           mma_ss(leader, o_at + b * N, vd + 128, p_desc + 128, dp, true);
           mma_ss(leader, o_at + b * N, vd + 256, p_desc + 256, dp, true);
           mma_ss(leader, o_at + b * N, vd + 384, p_desc + 384, dp, true);
+          if (b + 1 == nb0) tc_commit(leader, bar(sm.empty[p_stage][0]));
         }
-        tc_commit(leader, bar(sm.empty[p_stage]));
+        if (m.np0 < m.np) tc_commit(leader, bar(sm.empty[p_stage][1]));
         tc_commit(leader, bar(sm.o_done));
-        p_first = u0 + ip + 1 == wp.e;
-        if (p_first && ip + 1 < n_tiles) wp.next();
+        cp.step(piece);
         ++ip;
         if (++p_stage == m.nst) p_stage = 0;
         moved = true;
@@ -523,50 +627,88 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
     tc_commit(leader, bar(sm.issued));
     mbar_drain(bar(sm.issued), 0);
   } else if (BOX && warp < 7) {
-    // --------------------------------------------------------------- key rows
-    const int mine = warp - 5, panels = (m.np + 1 - mine) >> 1;  // mine, mine + 2, ...
-    Walk w;
-    w.seek(m.plan, groups, m.nh, u0);
-    int2 row;  // this lane's keys: lane and lane + 32 of the tile
-    auto rows_of = [&](int64_t u) {
-      if (u >= w.e) w.next();
-      const int j = static_cast<int>(u - w.s) * kTile + lane;
-      row.x = j < w.g.extent ? static_cast<int>(key_row(a, w.g.t0, w.g.req, j)) : -1;
-      row.y = j + 32 < w.g.extent ? static_cast<int>(key_row(a, w.g.t0, w.g.req, j + 32)) : -1;
-    };
-    rows_of(u0);
-    int *key = sm.key[mine];
-    const uint32_t leader = elect_leader();
-    for (int i = 0, stage = 0, use = 0; i < n_tiles; ++i) {
-      if (use > 0) mbar_wait(bar(sm.empty[stage]), (use - 1) & 1, dead);
-      if (mine == 0) {
-        const unsigned lo = __ballot_sync(~0u, row.x >= 0), hi = __ballot_sync(~0u, row.y >= 0);
-        if (lane == 0) sm.valid[stage][0] = lo, sm.valid[stage][1] = hi;
+    // ------------------------------------------------------ key rows, in boxes
+    // Warp 5 fills the stages' first halves, warp 6 the second ones.
+    const int half = warp - 5, p0 = half == 0 ? 0 : m.np0, p1 = half == 0 ? m.np0 : m.np;
+    if (p0 < p1) {
+      // First rows of a tile's runs (m.run keys each), looked up for as many
+      // tiles of the item at once as the warp has lanes for.
+      const int runs = kTile / m.run, batch = 32 / runs;
+      const uint32_t leader = elect_leader();
+      Cursor c(w);
+      int first_row = -1, k_batch = 0;
+      int i = 0;
+      for (int stage = 0, use = 0; c.more(); ++i) {
+        if (c.first() || c.k == k_batch + batch) {
+          k_batch = c.k;
+          const int j = (k_batch + lane / runs) * kTile + lane % runs * m.run;
+          first_row = j < c.w.extent && k_batch + lane / runs < c.w.k1
+                          ? static_cast<int>(key_row(a, c.w.t0, c.w.req, j))
+                          : -1;
+        }
+        const int lane0 = (c.k - k_batch) * runs;
+        if (use > 0) mbar_wait(bar(sm.empty[stage][half]), (use - 1) & 1, dead);
+        __syncwarp();
+        if (half == 0) {
+          bool live[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int key = lane + x * 32;
+            const int64_t row = __shfl_sync(~0u, first_row, lane0 + key / m.run);
+            live[x] = row >= 0 && c.k * kTile + key < c.w.extent;
+            if (live[x] && row + key % m.run >= a.cache_rows) {
+              live[x] = false;
+              if (a.status != nullptr) atomicOr(a.status, SATK_STATUS_BAD_ROW);
+            }
+          }
+          const unsigned lo = __ballot_sync(~0u, live[0]), hi = __ballot_sync(~0u, live[1]);
+          if (lane == 0) sm.valid[stage][0] = lo, sm.valid[stage][1] = hi;
+        }
+        const uint32_t full = bar(sm.full[stage][half]);
+        if (lane == 0) mbar_expect(full, (p1 - p0) * kPanel);
+        __syncwarp();
+        const uint32_t dst = base + stage * stage_bytes;
+        for (int r = 0; r < runs; ++r) {
+          const int first = max(__shfl_sync(~0u, first_row, lane0 + r), 0);
+          for (int p = p0; p < p1; ++p)
+            tma_box(leader, dst + p * kPanel + r * m.run * 128, &m.rows, p * 64, first, full);
+        }
+        __syncwarp();
+        c.step(piece);
+        if (++stage == m.nst) stage = 0, ++use;
       }
-      key[lane] = max(row.x, 0);
-      key[lane + 32] = max(row.y, 0);
-      __syncwarp();
-      const uint32_t full = bar(sm.full[stage]);
-      if (lane == 0) mbar_expect(full, panels * kPanel);
-      __syncwarp();
-      const uint32_t dst = base + stage * stage_bytes + mine * kPanel;
-      for (int r = 0; r < kTile; r += m.run) {
-        const int first = key[r];
-        for (int p = 0; p < panels; ++p)
-          tma_box(leader, dst + p * 2 * kPanel + r * 128, &m.rows, (2 * p + mine) * 64, first, full);
-      }
-      if (i + 1 < n_tiles) rows_of(u0 + i + 1);
-      if (++stage == m.nst) stage = 0, ++use;
+      for (int x = max(0, i - m.nst); x < i; ++x)
+        mbar_drain(bar(sm.full[x % m.nst][half]), (x / m.nst) & 1);
     }
-    for (int i = max(0, n_tiles - m.nst); i < n_tiles; ++i)
-      mbar_drain(bar(sm.full[i % m.nst]), (i / m.nst) & 1);
   } else if (warp == 7 || (!BOX && warp < 8)) {
     // ---------------------------------------------------------------- queries
     constexpr int threads = query_threads(BOX);
     const int tid = static_cast<int>(threadIdx.x) - (256 - threads), chunks = m.np * 8;
-    Walk w;
-    w.seek(m.plan, groups, m.nh, u0);
-    for (int seg = 0;; ++seg) {
+    if (m.q_box && warp == 7) {
+      // Rows that no box writes stay zeros.
+      const int used = m.hc * m.tpg, spare = N - used;
+      for (int x = lane; x < spare * chunks; x += 32) {
+        const int p = x / (spare * 8), y = x - p * spare * 8;
+        *reinterpret_cast<uint4 *>(smem + (q_at - base) + p * q_panel + used * 128 + y * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      fence_async_shared();
+      __syncwarp();
+      const uint32_t leader = elect_leader();
+      int seg = 0;
+      for (;; ++seg) {
+        if (seg > 0) mbar_wait(bar(sm.q_empty), (seg - 1) & 1, dead);
+        __syncwarp();
+        if (lane == 0) mbar_expect(bar(sm.q_full), used * m.np * 128);
+        __syncwarp();
+        for (int p = 0; p < m.np; ++p)
+          tma_box3(leader, q_at + p * q_panel, &m.q, p * 64, w.c * m.hc, w.t0, bar(sm.q_full));
+        w.next(piece);
+        if (w.done()) break;
+      }
+      mbar_drain(bar(sm.q_full), seg & 1);
+    }
+    for (int seg = 0; !m.q_box; ++seg) {
       if (seg > 0) mbar_wait(bar(sm.q_empty), (seg - 1) & 1, dead);
       const int ncol = w.columns(m);
       for (int x = tid; x < N * chunks; x += threads) {
@@ -576,7 +718,7 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
         const uint32_t dst = q_at + (ch >> 3) * q_panel + n * 128 + (((ch & 7) ^ (n & 7)) << 4);
         const E *src = static_cast<const E *>(a.q);
         if (live)
-          src += static_cast<int64_t>(w.g.t0 + tok) * a.ld_q_t +
+          src += static_cast<int64_t>(w.t0 + tok) * a.ld_q_t +
                  static_cast<int64_t>(w.c * m.hc + n - tok * m.hc) * a.ld_q_h + col;
         if (m.q_vec) {
           cp_async16(dst, src, live);
@@ -593,51 +735,87 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
       cp_async_wait_all();
       fence_async_shared();
       mbar_arrive(bar(sm.q_full));
-      if (w.e >= u1) break;
-      w.next();
+      w.next(piece);
+      if (w.done()) break;
     }
   } else {
     // ---------------------------------------------------- key rows, by copies
-    const int pw = warp - 8, stage = pw / wps, rows = kTile / wps, r0 = (pw - stage * wps) * rows;
-    if (!BOX && stage < m.nst && stage < n_tiles) {
-      Walk w;
-      w.seek(m.plan, groups, m.nh, u0);
-      auto row_of = [&](int64_t u) {
-        while (u >= w.e) w.next();
-        const int j = static_cast<int>(u - w.s) * kTile + r0 + lane;
-        return lane < rows && j < w.g.extent ? static_cast<int>(key_row(a, w.g.t0, w.g.req, j)) : -1;
+    // Each warp copies eight rows of every tile.  Their numbers are looked up
+    // for four tiles at once (lanes 8 q .. 8 q + 7: the q-th of them), one such
+    // batch ahead; when they arrive the rows start on their way from HBM to L2,
+    // as the stages alone do not hold what HBM's latency takes.
+    constexpr int kRows = kTile / 8, kBatch = 4;
+    const int pw = warp - 8, r0 = pw * kRows, ch = lane & 7, width = (a.D + 15) & ~15;
+    const E *cache = static_cast<const E *>(a.cache);
+    Cursor ahead(w);
+    int seen = 0;                  // tiles looked up so far
+    int entry = -1, entry_j = -1;  // of the next batch: -1 for none
+    auto look_up = [&]() {
+      entry_j = -1;
+      for (int q = 0; q < kBatch && ahead.more(); ++q, ++seen, ahead.step(piece)) {
+        const int j = ahead.k * kTile + r0 + (lane & 7);
+        if ((lane >> 3) == q && j < ahead.w.extent) {
+          entry = key_entry(a, ahead.w.t0, ahead.w.req, j);
+          entry_j = j;
+        }
+      }
+    };
+    auto resolve = [&]() {
+      const int row = entry_j >= 0 ? static_cast<int>(entry_row(a, entry, entry_j)) : -1;
+      if (row >= 0) prefetch_bulk(cache + row * a.ld_cache, a.D * 2);
+      return row;
+    };
+    if (!BOX) {
+      look_up();
+      int row = resolve(), next_row = -1;
+      // Panels [p0, p1) of tile q's rows, four rows x 128 bytes a request.
+      auto copy = [&](int q, int stage, int p0, int p1) {
+        const int whole = min(a.D / 64 - p0, p1 - p0);
+#pragma unroll
+        for (int g = 0; g < kRows; g += 4) {
+          const int rr = g + (lane >> 3), r = r0 + rr;
+          const int at = __shfl_sync(~0u, row, q * kRows + rr);
+          const bool live = at >= 0;
+          const E *src = cache + (live ? at : 0) * a.ld_cache + ch * 8 + p0 * 64;
+          const uint32_t dst = base + stage * stage_bytes + p0 * kPanel + r * 128 + ((ch ^ (r & 7)) << 4);
+#pragma unroll
+          for (int p = 0; p < 5; ++p)
+            if (p < whole) cp_async16(dst + p * kPanel, src + p * 64, live);
+          const int col = (p0 + whole) * 64 + ch * 8;
+          if (p0 + whole < p1 && col < width)
+            cp_async16(dst + whole * kPanel, col < a.D ? src + whole * 64 : cache, live && col < a.D);
+        }
       };
-      const int ch = lane & 7, whole = a.D / 64, width = (a.D + 15) & ~15;
-      const E *cache = static_cast<const E *>(a.cache);
-      unsigned short *valid16 = reinterpret_cast<unsigned short *>(sm.valid[stage]);
-      int row = row_of(u0 + stage);
-      int use = 0;
-      for (int i = stage; i < n_tiles; i += m.nst, ++use) {
-        if (use > 0) mbar_wait(bar(sm.empty[stage]), (use - 1) & 1, dead);
+      int i = 0;
+      for (int stage = 0, use = 0; i < seen; ++i) {
+        const int q = i % kBatch;
+        if (use > 0) mbar_wait(bar(sm.empty[stage][0]), (use - 1) & 1, dead);
         __syncwarp();
         const unsigned live_rows = __ballot_sync(~0u, row >= 0);
-        if (lane == 0) {
-          if (rows == 16) valid16[r0 / 16] = static_cast<unsigned short>(live_rows);
-          else sm.valid[stage][r0 / 32] = live_rows;
+        if (lane == 0)
+          reinterpret_cast<unsigned char *>(sm.valid[stage])[pw] = live_rows >> (q * kRows) & 0xff;
+        copy(q, stage, 0, m.np0);
+        cp_async_commit();
+        if (m.np0 < m.np) {
+          if (use > 0) mbar_wait(bar(sm.empty[stage][1]), (use - 1) & 1, dead);
+          __syncwarp();
+          copy(q, stage, m.np0, m.np);
         }
-        for (int g = 0; g < rows; g += 4) {
-          const int rr = g + (lane >> 3), r = r0 + rr;
-          const int at = __shfl_sync(~0u, row, rr);
-          const bool live = at >= 0;
-          const E *src = cache + (live ? at : 0) * a.ld_cache + ch * 8;
-          uint32_t dst = base + stage * stage_bytes + r * 128 + ((ch ^ (r & 7)) << 4);
-#pragma unroll 4
-          for (int p = 0; p < whole; ++p, src += 64, dst += kPanel) cp_async16(dst, src, live);
-          const int col = whole * 64 + ch * 8;
-          if (col < width) cp_async16(dst, col < a.D ? src : cache, live && col < a.D);
-        }
-        if (i + m.nst < n_tiles) row = row_of(u0 + i + m.nst);
+        cp_async_commit();
+        if (q == 0) look_up();
+        cp_async_wait_but_one();
+        fence_async_shared();
+        mbar_arrive(bar(sm.full[stage][0]));
         cp_async_wait_all();
         fence_async_shared();
-        mbar_arrive(bar(sm.full[stage]));
+        mbar_arrive(bar(sm.full[stage][1]));
+        if (q == 0) next_row = resolve();
+        if (q == kBatch - 1) row = next_row;
+        if (++stage == m.nst) stage = 0, ++use;
       }
     }
   }
+  let_next_kernel_start();
   __syncthreads();
   if (warp == 4) tmem_free(tmem, 512);
   if (threadIdx.x == 0 && *dead != 0 && a.status != nullptr)
@@ -645,61 +823,52 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
 }
 
 // Joins the partial results of the group that CTA x leaves unfinished: weights
-// 2^(m_i - max m) / sum, parts added in line order.
+// 2^(m_i - max m) / sum, parts added in line order.  One warp per column.
 template <class E>
-__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ MmaArgs m, int N) {
+__global__ void __launch_bounds__(256, 6) latent_join_kernel(const __grid_constant__ MmaArgs m, int N) {
+  wait_for_previous_kernel();
   const LatentArgs &a = m.a;
-  const int64_t per = m.plan->per, total = m.plan->tiles;
-  const int64_t u0 = min(blockIdx.x * per, total), u1 = min(u0 + per, total);
-  if (u0 >= u1 || u1 >= total) return;
-  Walk w;
-  w.seek(m.plan, m.group, m.nh, u1 - 1);
-  if (w.s < u0 || w.e <= u1) return;
-  const int n_parts = static_cast<int>((w.e - 1) / per) - blockIdx.x + 1;
-  __shared__ float weight[256], red[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ncol = w.columns(m);
+  const int4 join = m.joins[blockIdx.x];
+  const int n_parts = join.w, ncol = join.y;
+  if (n_parts == 0) return;
+  const int lane = threadIdx.x & 31;
   auto part = [&](int i) {
     return m.parts + ((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * m.part_stride;
   };
-  for (int n = blockIdx.y; n < ncol; n += kCombineY) {
-    float top = kUnset, sum = 0.f;
-    const bool mine = static_cast<int>(threadIdx.x) < n_parts;
-    if (mine) {
-      const float *p = part(threadIdx.x) + static_cast<int64_t>(N) * a.dl;
-      top = p[n];
-      sum = p[N + n];
-    }
-    float mx = top;
+  for (int n = blockIdx.y * 8 + (threadIdx.x >> 5); n < ncol; n += kJoinY * 8) {
+    const int64_t stat = static_cast<int64_t>(N) * a.dl + n;
+    float mx = kUnset, l = 0.f;
+    for (int i = lane; i < n_parts; i += 32) mx = fmaxf(mx, part(i)[stat]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-    if (lane == 0) red[warp] = mx;
-    __syncthreads();
-    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, red[i]);
-    const float f = mine ? exp2_fast(top - mx) : 0.f;
-    weight[threadIdx.x] = f;
-    float l = f * sum;
-    if (!mine) l = 0.f;
+    const int tok = n / m.hc, t = join.x + tok, h = join.z + n - tok * m.hc;
+    constexpr int kPer = SATK_LATENT_MAX / 32;
+    float acc[kPer] = {};
+    for (int i0 = 0; i0 < n_parts; i0 += 32) {
+      float f = 0.f;
+      if (i0 + lane < n_parts) {
+        const float *p = part(i0 + lane) + stat;
+        f = exp2_fast(p[0] - mx);
+        l += f * p[N];
+      }
+      const int count = min(32, n_parts - i0);
+      for (int i = 0; i < count; ++i) {
+        const float fi = __shfl_sync(~0u, f, i);
+        const float *o = part(i0 + i) + static_cast<int64_t>(n) * a.dl + lane;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x)
+          if (x * 32 + lane < a.dl) acc[x] = fmaf(fi, o[x * 32], acc[x]);
+      }
+    }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-    __syncthreads();
-    if (lane == 0) red[warp] = l;
-    __syncthreads();
-    l = 0.f;
-    for (int i = 0; i < 8; ++i) l += red[i];
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int tok = n / m.hc, t = w.g.t0 + tok, h = w.c * m.hc + n - tok * m.hc;
-    E *out = static_cast<E *>(a.out) + t * a.ld_out_t + h * a.ld_out_h;
-    for (int d = threadIdx.x; d < a.dl; d += 256) {
-      float acc = 0.f;
-#pragma unroll 4
-      for (int i = 0; i < n_parts; ++i)
-        acc = fmaf(weight[i], part(i)[static_cast<int64_t>(n) * a.dl + d], acc);
-      out[d] = Elem<E>::from(acc * inv);
-    }
-    if (threadIdx.x == 0 && a.lse != nullptr)
+    E *out = static_cast<E *>(a.out) + t * a.ld_out_t + h * a.ld_out_h + lane;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x)
+      if (x * 32 + lane < a.dl) out[x * 32] = Elem<E>::from(acc[x] * inv);
+    if (lane == 0 && a.lse != nullptr)
       a.lse[static_cast<int64_t>(t) * a.H + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
-    __syncthreads();
   }
 }
 
@@ -716,14 +885,38 @@ int columns_for(int hc, int tpg) {
   return n <= 16 ? 16 : n <= 32 ? 32 : 64;
 }
 
-size_t group_bytes() { return (sizeof(Plan) + 15) / 16 * 16 + sizeof(Group) * kMaxTokens; }
+size_t plans_bytes(int ctas) {
+  const size_t one = plan_bytes(kMaxTokens), each = plan_bytes(kInline) * ctas;
+  return one > each ? one : each;
+}
+
+// Launches after the stream's previous kernel without waiting for its end; the
+// kernel waits for it itself.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, int smem, cudaStream_t stream,
+                         A... args) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = dim3(block);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
 
 template <class E, int N, bool BOX>
 int launch(const MmaArgs &m, int ctas, int smem, cudaStream_t stream) {
   if (!allow_smem(latent_attend_mma_kernel<E, N, BOX>, smem)) return SATK_ECUDA;
   latent_attend_mma_kernel<E, N, BOX><<<ctas, threads_of(BOX), smem, stream>>>(m);
-  latent_join_kernel<E><<<dim3(ctas, kCombineY), 256, 0, stream>>>(m, N);
-  return launch_status();
+  int rc = launch_status();
+  if (rc == SATK_OK &&
+      launch_early(latent_join_kernel<E>, dim3(ctas, kJoinY), 256, 0, stream, m, N) != cudaSuccess)
+    rc = SATK_ECUDA;
+  return rc;
 }
 
 template <class E, bool BOX>
@@ -749,7 +942,7 @@ bool latent_attend_mma_fits(const LatentArgs &a) {
 size_t latent_attend_mma_workspace(int H, int dl) {
   (void)H;
   const int ctas = sm_count();
-  return group_bytes() + sizeof(float) * 2 * ctas * (64 * static_cast<size_t>(dl) + 128);
+  return plans_bytes(ctas) + sizeof(int4) * ctas + sizeof(float) * 2 * ctas * (64 * static_cast<size_t>(dl) + 128);
 }
 
 int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request, void *workspace,
@@ -766,14 +959,16 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
   m.tpg = N / m.hc < m.tpg ? N / m.hc : m.tpg;
   m.np = (args.D + 63) / 64;
   m.nb = (args.dl + 127) / 128;
+  m.np0 = (m.nb + 1) / 2 * 2;
+  if (m.np0 > m.np) m.np0 = m.np;
   m.part_stride = static_cast<int64_t>(N) * args.dl + 2 * N;
-  m.plan = static_cast<Plan *>(workspace);
   const int fixed = m.np * N * 128 + kPanel + kSmall, limit = 227 * 1024;
   m.nst = (limit - fixed) / (m.np * kPanel);
   if (m.nst > kMaxStages) m.nst = kMaxStages;
   const int smem = fixed + m.nst * m.np * kPanel;
   m.q_vec = aligned16(args.q) && (args.T == 1 || args.ld_q_t % 8 == 0) &&
             (args.H == 1 || args.ld_q_h % 8 == 0);
+  m.q_box = m.q_vec;
   m.out_vec = (reinterpret_cast<uintptr_t>(args.out) & 3u) == 0 && args.dl % 2 == 0 &&
               (args.T == 1 || args.ld_out_t % 2 == 0) && (args.H == 1 || args.ld_out_h % 2 == 0);
   // Rows that consecutive keys of a tile share in one block (a run is in the
@@ -783,13 +978,13 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
     while (m.run < kTile && args.block_size % (2 * m.run) == 0) m.run *= 2;
     if (m.run < 8) m.run = 1;
   }
-  if (m.run > 1 &&
-      !tensor_map_16bit(&m.rows, dtype == SATK_BF16, args.cache, args.cache_rows, args.D,
-                        args.ld_cache, m.run))
+  const bool bf16 = dtype == SATK_BF16;
+  if (m.run > 1 && !tensor_map_16bit(&m.rows, bf16, args.cache, args.D, args.cache_rows,
+                                     args.ld_cache, m.run))
     return SATK_ECUDA;
-  unsigned char *ws = static_cast<unsigned char *>(workspace);
-  m.group = reinterpret_cast<Group *>(ws + (sizeof(Plan) + 15) / 16 * 16);
-  m.parts = reinterpret_cast<float *>(ws + group_bytes());
+  m.plans = static_cast<unsigned char *>(workspace);
+  m.joins = reinterpret_cast<int4 *>(m.plans + plans_bytes(ctas));
+  m.parts = reinterpret_cast<float *>(m.joins + ctas);
   for (int t = 0; t < args.T; t += kMaxTokens) {
     LatentArgs &a = m.a;
     a = args;
@@ -805,7 +1000,12 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
       a.row_ends = args.row_ends + t;
       if (args.tree != nullptr) a.tree = args.tree + static_cast<int64_t>(t) * args.tree_words;
     }
-    latent_plan_kernel<<<1, 1024, 0, stream>>>(m, ctas);
+    // Strides of dimensions of one are free: any multiple of 16 bytes.
+    if (m.q_box && !tensor_map_16bit(&m.q, bf16, a.q, a.D, a.H, a.H == 1 ? 1024 : a.ld_q_h, m.hc,
+                                     a.T, args.T == 1 ? 1024 : a.ld_q_t, m.tpg))
+      m.q_box = 0;
+    m.inline_plan = a.T <= kInline;
+    if (!m.inline_plan) latent_plan_kernel<<<1, 1024, 0, stream>>>(m, ctas);
     const int rc = dtype == SATK_BF16 ? launch_all<__nv_bfloat16>(m, N, ctas, smem, stream)
                                       : launch_all<__half>(m, N, ctas, smem, stream);
     if (rc != SATK_OK) return rc;

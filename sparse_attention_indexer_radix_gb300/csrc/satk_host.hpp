@@ -32,11 +32,13 @@ inline bool allow_smem(K kernel, size_t bytes) {
 // device.  0 on error.
 int64_t resident_ctas(const void *kernel, int block, size_t smem);
 
-// The tensor map of a row-major 16-bit matrix [rows, cols] (row stride ld
-// elements, base and stride multiples of 16 bytes) read in boxes of 64 columns
-// x box_rows rows with the 128-byte swizzle; columns past `cols` read as zeros.
-// False if the driver refuses it.
-bool tensor_map_16bit(void *map, bool bf16, const void *base, int64_t rows, int64_t cols,
-                      int64_t ld, int box_rows);
+// The tensor map of 16-bit elements [outer, rows, cols] (strides in elements;
+// base and strides multiples of 16 bytes) read in boxes of 64 columns x box_rows
+// x box_outer with the 128-byte swizzle; what a box covers outside the tensor
+// reads as zeros.  outer = 0: a matrix [rows, cols].  False if the driver
+// refuses it.
+bool tensor_map_16bit(void *map, bool bf16, const void *base, int64_t cols, int64_t rows,
+                      int64_t ld_rows, int box_rows, int64_t outer = 0, int64_t ld_outer = 0,
+                      int box_outer = 1);
 
 }  // namespace satk

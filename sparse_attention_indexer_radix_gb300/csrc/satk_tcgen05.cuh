@@ -104,6 +104,15 @@ __device__ __forceinline__ void regs_lower() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// Programmatic dependent launch: a kernel launched with the attribute may start
+// before its predecessor in the stream has finished, up to this wait.
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------- async copies --
 
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
@@ -124,14 +133,35 @@ __device__ __forceinline__ void tma_box(uint32_t leader, uint32_t dst, const voi
       : "memory");
 }
 
+__device__ __forceinline__ void tma_box3(uint32_t leader, uint32_t dst, const void *map, int col,
+                                         int row, int outer, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %6, 0;\n"
+      "@e cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
+      "l"(map), "r"(col), "r"(row), "r"(outer), "r"(bar), "r"(leader)
+      : "memory");
+}
+
+// `bytes` (a multiple of 16) from a 16-byte aligned address into L2 alone.
+__device__ __forceinline__ void prefetch_bulk(const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // 16 bytes global -> shared; zeros, and no read, when !live.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(live ? 16 : 0)
                : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async_wait_but_one() {
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
 
 // ------------------------------------------------------------------- tcgen05 --

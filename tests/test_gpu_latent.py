@@ -394,6 +394,68 @@ def test_rows_bad_row_and_extreme_scores():
         assert_close(lse[t], w[1], w[3], f"lse, token {t}")
 
 
+@pytest.mark.parametrize("dl", [64, 128, 192, 256, 320, 384, 448, 512])
+@pytest.mark.parametrize("dr,H,block", [(0, 16, 64), (64, 16, 16), (32, 33, 2), (48, 24, 8)])
+def test_many_tiles_a_processor(dl, dr, H, block):
+    """Enough keys that every SM goes through its stages several times, for
+    every split of the columns, in pages that lie together and tiny ones, and
+    the same rows as a selection."""
+    g, rng = gen(dl + dr), np.random.RandomState(dl)
+    D, R = dl + dr, 24
+    ends = [int(x) for x in rng.randint(2500, 3500, R)]
+    pg = Paged(g, rng, ends, D, block, BF16)
+    q = torch.randn(R, H, D, generator=g, device=DEV).to(BF16)
+    o, lse, st = run_paged(q, pg, range(R), ends, dl, 0.05)
+    rows = np.full((R, max(ends)), -1, dtype=np.int32)
+    for t in range(R):
+        rows[t, :ends[t]] = rng.permutation(pg.rows(t, np.arange(ends[t])).numpy())
+    o2, lse2 = satk.latent_attend_rows(q, pg.cache, i32(rows), latent_dim=dl, scale=0.05)
+    assert st == 0
+    for t in range(R):
+        w = one_token(q[t], pg.keys(t, np.arange(ends[t])), dl, 0.05, U[BF16])
+        assert_close(o[t], w[0], w[2], f"paged out, token {t}")
+        assert_close(lse[t], w[1], w[3], f"paged lse, token {t}")
+        assert_close(o2[t], w[0], w[2], f"rows out, token {t}")
+        assert_close(lse2[t], w[1], w[3], f"rows lse, token {t}")
+
+
+@pytest.mark.parametrize("H,new,context", [(16, 24, 3000), (64, 3, 2900), (6, 40, 1500)])
+def test_many_tiles_of_trees(H, new, context):
+    g, rng = gen(H), np.random.RandomState(H)
+    dl, D, R, words = 256, 288, 8, 2
+    lens = [int(c) + new for c in rng.randint(context - 500, context, R)]
+    lens[3] = new  # nothing but drafted tokens
+    pg = Paged(g, rng, lens, D, 16, F16)
+    bits = np.concatenate([make_tree(rng, new, words) for _ in range(R)])
+    req, ends = np.repeat(np.arange(R), new), np.repeat([n - new for n in lens], new)
+    q = torch.randn(R * new, H, D, generator=g, device=DEV).to(F16)
+    o, lse, st = run_paged(q, pg, req, ends, dl, 0.05, dtype=F16,
+                           tree=torch.from_numpy(bits.view(np.int32)).to(DEV))
+    assert st == 0
+    for t in range(0, R * new, 5):
+        j = list(range(ends[t])) + [ends[t] + b for b in range(64)
+                                    if int(bits[t, b // 32]) >> (b % 32) & 1]
+        w = one_token(q[t], pg.keys(req[t], j), dl, 0.05, U[F16])
+        assert_close(o[t], w[0], w[2], f"out, token {t}")
+        assert_close(lse[t], w[1], w[3], f"lse, token {t}")
+
+
+def test_more_tokens_than_one_plan():
+    """More tokens than one launch plans, most of them short."""
+    g, rng = gen(5), np.random.RandomState(5)
+    T, D, dl, N = 17000, 48, 32, 3000
+    cache = latent_rows(g, N, D, BF16)
+    rows = torch.randint(0, N, (T, 9), generator=g, device=DEV).int()
+    counts = torch.randint(0, 10, (T,), generator=g, device=DEV).int()
+    q = torch.randn(T, 3, D, generator=g, device=DEV).to(BF16)
+    o, lse = satk.latent_attend_rows(q, cache, rows, counts=counts, latent_dim=dl, scale=0.1)
+    for t in list(range(0, T, 997)) + [16383, 16384, T - 1]:
+        n = int(counts[t])
+        w = one_token(q[t], cache[rows[t, :n].long()], dl, 0.1, U[BF16])
+        assert_close(o[t], w[0], w[2], f"out, token {t}")
+        assert_close(lse[t], w[1], w[3], f"lse, token {t}")
+
+
 def test_attend_empty_calls():
     cache = torch.zeros(0, 96, dtype=BF16, device=DEV)
     q = torch.randn(2, 4, 96, device=DEV).to(BF16)
