@@ -21,7 +21,7 @@
 //    of a run x 64 columns.  256 threads: warps 0-3 softmax and results, warp 4
 //    issues the MMAs, warps 5-6 the boxes, warp 7 brings the queries.
 //  - else (selected rows, tiny pages): 16-byte asynchronous copies by eight
-//    warps, eight rows of a tile each.  512 threads: warps 0-3 and 4 as above, 5-7 queries, 8-15 keys.
+//    warps, each stage filled by its own.  512 threads: warps 0-3 and 4 as above, 5-7 queries, 8-15 keys.
 //    (Random rows of 1088 bytes, nothing else running: these copies 6.3 TB/s,
 //    TMA's gather of four rows a request 5.0, bulk copies of a row 3.7.)
 // A stage is handed over in two halves of its columns: the scores of the first
@@ -88,6 +88,7 @@ struct MmaArgs {
   int np, nst;   // 64-column panels of a key row, stages
   int np0;       // panels of a stage's first half (all of them: there is no second)
   int nb;        // 128-column blocks of a value
+  int part_ld;   // a partial result: N rows of part_ld values, N references, N sums
   int64_t part_stride;
   int q_box, q_vec, out_vec;  // queries by TMA, by 16-byte copies; paired stores
   int run;           // rows of a box: consecutive keys that share a block (1: copies)
@@ -301,10 +302,11 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
   auto bar = [&](uint64_t &b) { return smem_addr(&b); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wps = 8 / m.nst;  // copies: warps per stage
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       for (int h = 0; h < 2; ++h) {
-        mbar_init(bar(sm.full[s][h]), BOX ? 1 : 256);
+        mbar_init(bar(sm.full[s][h]), BOX ? 1 : wps * 32);
         mbar_init(bar(sm.empty[s][h]), 1);
       }
     }
@@ -506,8 +508,8 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
             a.lse[static_cast<int64_t>(sm.token[n]) * a.H + w.c * m.hc + n % m.hc] =
                 sum == 0.f ? -INFINITY : (sm.ref[n] + log2f(sum)) * kLn2;
         } else {
-          part[static_cast<int64_t>(N) * a.dl + n] = sm.ref[n];
-          part[static_cast<int64_t>(N) * a.dl + N + n] = sum;
+          part[static_cast<int64_t>(N) * m.part_ld + n] = sm.ref[n];
+          part[static_cast<int64_t>(N) * m.part_ld + N + n] = sum;
         }
       }
       named_sync(1, kSoftmax);
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
         } else if (dim < a.dl) {
 #pragma unroll
           for (int y = 0; y < 16; ++y)
-            part[static_cast<int64_t>(n0 + y) * a.dl + dim] = __uint_as_float(o[y]);
+            part[static_cast<int64_t>(n0 + y) * m.part_ld + dim] = __uint_as_float(o[y]);
         }
       }
       tc_fence_before();
@@ -740,41 +742,34 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
     }
   } else {
     // ---------------------------------------------------- key rows, by copies
-    // Each warp copies eight rows of every tile.  Their numbers are looked up
-    // for four tiles at once (lanes 8 q .. 8 q + 7: the q-th of them), one such
-    // batch ahead; when they arrive the rows start on their way from HBM to L2,
-    // as the stages alone do not hold what HBM's latency takes.
-    constexpr int kRows = kTile / 8, kBatch = 4;
-    const int pw = warp - 8, r0 = pw * kRows, ch = lane & 7, width = (a.D + 15) & ~15;
-    const E *cache = static_cast<const E *>(a.cache);
-    Cursor ahead(w);
-    int seen = 0;                  // tiles looked up so far
-    int entry = -1, entry_j = -1;  // of the next batch: -1 for none
-    auto look_up = [&]() {
-      entry_j = -1;
-      for (int q = 0; q < kBatch && ahead.more(); ++q, ++seen, ahead.step(piece)) {
-        const int j = ahead.k * kTile + r0 + (lane & 7);
-        if ((lane >> 3) == q && j < ahead.w.extent) {
-          entry = key_entry(a, ahead.w.t0, ahead.w.req, j);
-          entry_j = j;
-        }
-      }
-    };
-    auto resolve = [&]() {
-      const int row = entry_j >= 0 ? static_cast<int>(entry_row(a, entry, entry_j)) : -1;
-      if (row >= 0) prefetch_bulk(cache + row * a.ld_cache, a.D * 2);
-      return row;
-    };
-    if (!BOX) {
+    // A stage's warps share its rows.  While a tile's copies are in flight the
+    // numbers of the stage's next rows are looked up, and when those arrive the
+    // rows start on their way from HBM to L2: the stages alone do not hold what
+    // HBM's latency takes.
+    const int pw = warp - 8, stage = pw / wps, rows = kTile / wps, r0 = (pw - stage * wps) * rows;
+    Cursor c(w);
+    for (int i = 0; i < stage && c.more(); ++i) c.step(piece);
+    if (!BOX && stage < m.nst && c.more()) {
+      const int ch = lane & 7, width = (a.D + 15) & ~15;
+      const E *cache = static_cast<const E *>(a.cache);
+      int entry = 0, entry_j = -1;  // -1: no key
+      auto look_up = [&]() {
+        const int j = c.k * kTile + r0 + lane;
+        entry_j = lane < rows && j < c.w.extent ? j : -1;
+        if (entry_j >= 0) entry = key_entry(a, c.w.t0, c.w.req, j);
+      };
+      auto resolve = [&]() {
+        return entry_j >= 0 ? static_cast<int>(entry_row(a, entry, entry_j)) : -1;
+      };
       look_up();
-      int row = resolve(), next_row = -1;
-      // Panels [p0, p1) of tile q's rows, four rows x 128 bytes a request.
-      auto copy = [&](int q, int stage, int p0, int p1) {
+      int row = resolve();
+      // Panels [p0, p1) of this warp's rows, four rows x 128 bytes a request.
+      auto copy = [&](int p0, int p1) {
         const int whole = min(a.D / 64 - p0, p1 - p0);
-#pragma unroll
-        for (int g = 0; g < kRows; g += 4) {
+#pragma unroll 2
+        for (int g = 0; g < rows; g += 4) {
           const int rr = g + (lane >> 3), r = r0 + rr;
-          const int at = __shfl_sync(~0u, row, q * kRows + rr);
+          const int at = __shfl_sync(~0u, row, rr);
           const bool live = at >= 0;
           const E *src = cache + (live ? at : 0) * a.ld_cache + ch * 8 + p0 * 64;
           const uint32_t dst = base + stage * stage_bytes + p0 * kPanel + r * 128 + ((ch ^ (r & 7)) << 4);
@@ -786,32 +781,39 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
             cp_async16(dst + whole * kPanel, col < a.D ? src + whole * 64 : cache, live && col < a.D);
         }
       };
-      int i = 0;
-      for (int stage = 0, use = 0; i < seen; ++i) {
-        const int q = i % kBatch;
+      for (int use = 0;; ++use) {
         if (use > 0) mbar_wait(bar(sm.empty[stage][0]), (use - 1) & 1, dead);
         __syncwarp();
         const unsigned live_rows = __ballot_sync(~0u, row >= 0);
-        if (lane == 0)
-          reinterpret_cast<unsigned char *>(sm.valid[stage])[pw] = live_rows >> (q * kRows) & 0xff;
-        copy(q, stage, 0, m.np0);
+        if (lane == 0) {
+          if (rows == 16) reinterpret_cast<unsigned short *>(sm.valid[stage])[r0 / 16] = live_rows;
+          else sm.valid[stage][r0 / 32] = live_rows;
+        }
+        copy(0, m.np0);
         cp_async_commit();
         if (m.np0 < m.np) {
           if (use > 0) mbar_wait(bar(sm.empty[stage][1]), (use - 1) & 1, dead);
           __syncwarp();
-          copy(q, stage, m.np0, m.np);
+          copy(m.np0, m.np);
         }
         cp_async_commit();
-        if (q == 0) look_up();
+        for (int i = 0; i < m.nst && c.more(); ++i) c.step(piece);
+        const bool more = c.more();
+        if (more) look_up();
         cp_async_wait_but_one();
         fence_async_shared();
         mbar_arrive(bar(sm.full[stage][0]));
         cp_async_wait_all();
         fence_async_shared();
         mbar_arrive(bar(sm.full[stage][1]));
-        if (q == 0) next_row = resolve();
-        if (q == kBatch - 1) row = next_row;
-        if (++stage == m.nst) stage = 0, ++use;
+        if (!more) break;
+        row = resolve();
+        for (int g = 0; g < rows; g += 4) {
+          const int at = __shfl_sync(~0u, row, g + (lane >> 3));
+          if (at >= 0)
+            for (int col = ch * 64; col < a.D; col += 512)
+              prefetch_line(cache + at * a.ld_cache + col);
+        }
       }
     }
   }
@@ -823,7 +825,8 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
 }
 
 // Joins the partial results of the group that CTA x leaves unfinished: weights
-// 2^(m_i - max m) / sum, parts added in line order.  One warp per column.
+// 2^(m_i - max m) / sum, parts added in line order.  One warp per column and 128
+// of its values, four parts' loads in flight.
 template <class E>
 __global__ void __launch_bounds__(256, 6) latent_join_kernel(const __grid_constant__ MmaArgs m, int N) {
   wait_for_previous_kernel();
@@ -835,39 +838,73 @@ __global__ void __launch_bounds__(256, 6) latent_join_kernel(const __grid_consta
   auto part = [&](int i) {
     return m.parts + ((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * m.part_stride;
   };
-  for (int n = blockIdx.y * 8 + (threadIdx.x >> 5); n < ncol; n += kJoinY * 8) {
-    const int64_t stat = static_cast<int64_t>(N) * a.dl + n;
-    float mx = kUnset, l = 0.f;
-    for (int i = lane; i < n_parts; i += 32) mx = fmaxf(mx, part(i)[stat]);
+  for (int x = blockIdx.y * 8 + (threadIdx.x >> 5); x < ncol * m.nb; x += kJoinY * 8) {
+    const int n = x / m.nb, d = (x - n * m.nb) * 128 + lane * 4;
+    const int64_t stat = static_cast<int64_t>(N) * m.part_ld + n;
+    const int64_t value = static_cast<int64_t>(n) * m.part_ld + d;
+    // Statistics of the first 32 parts and values of the first four, all in
+    // flight together; few groups have more.
+    float top = kUnset, sum = 0.f;
+    if (lane < n_parts) {
+      const float *p = part(lane) + stat;
+      top = __ldcg(p);
+      sum = __ldcg(p + N);
+    }
+    float4 v[4];
+    auto load = [&](int i) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-    const int tok = n / m.hc, t = join.x + tok, h = join.z + n - tok * m.hc;
-    constexpr int kPer = SATK_LATENT_MAX / 32;
-    float acc[kPer] = {};
-    for (int i0 = 0; i0 < n_parts; i0 += 32) {
-      float f = 0.f;
-      if (i0 + lane < n_parts) {
-        const float *p = part(i0 + lane) + stat;
-        f = exp2_fast(p[0] - mx);
-        l += f * p[N];
+      for (int y = 0; y < 4; ++y)
+        v[y] = i + y < n_parts && d < m.part_ld
+                   ? __ldcg(reinterpret_cast<const float4 *>(part(i + y) + value))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    float mx = top;
+    for (int i = lane + 32; i < n_parts; i += 32) mx = fmaxf(mx, part(i)[stat]);
+#pragma unroll
+    for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, y));
+    float f = exp2_fast(top - mx), l = f * sum;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n_parts; i += 4) {
+      if (i > 0) {
+        load(i);
+        if ((i & 31) == 0) {
+          f = 0.f;
+          if (i + lane < n_parts) {
+            const float *p = part(i + lane) + stat;
+            f = exp2_fast(p[0] - mx);
+            l += f * p[N];
+          }
+        }
       }
-      const int count = min(32, n_parts - i0);
-      for (int i = 0; i < count; ++i) {
-        const float fi = __shfl_sync(~0u, f, i);
-        const float *o = part(i0 + i) + static_cast<int64_t>(n) * a.dl + lane;
 #pragma unroll
-        for (int x = 0; x < kPer; ++x)
-          if (x * 32 + lane < a.dl) acc[x] = fmaf(fi, o[x * 32], acc[x]);
+      for (int y = 0; y < 4; ++y) {
+        const float fi = __shfl_sync(~0u, f, (i + y) & 31);
+        if (i + y < n_parts) {
+          acc.x = fmaf(fi, v[y].x, acc.x);
+          acc.y = fmaf(fi, v[y].y, acc.y);
+          acc.z = fmaf(fi, v[y].z, acc.z);
+          acc.w = fmaf(fi, v[y].w, acc.w);
+        }
       }
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+    for (int y = 16; y > 0; y >>= 1) l += __shfl_xor_sync(~0u, l, y);
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    E *out = static_cast<E *>(a.out) + t * a.ld_out_t + h * a.ld_out_h + lane;
-#pragma unroll
-    for (int x = 0; x < kPer; ++x)
-      if (x * 32 + lane < a.dl) out[x * 32] = Elem<E>::from(acc[x] * inv);
-    if (lane == 0 && a.lse != nullptr)
+    const int tok = n / m.hc, t = join.x + tok, h = join.z + n - tok * m.hc;
+    E *out = static_cast<E *>(a.out) + t * a.ld_out_t + h * a.ld_out_h + d;
+    using T2 = typename Elem<E>::T2;
+    const T2 lo = Elem<E>::from2(acc.x * inv, acc.y * inv), hi = Elem<E>::from2(acc.z * inv, acc.w * inv);
+    if (m.out_vec) {  // dl is even, and pairs are aligned
+      if (d < a.dl) *reinterpret_cast<T2 *>(out) = lo;
+      if (d + 2 < a.dl) *reinterpret_cast<T2 *>(out + 2) = hi;
+    } else {
+      if (d < a.dl) out[0] = lo.x;
+      if (d + 1 < a.dl) out[1] = lo.y;
+      if (d + 2 < a.dl) out[2] = hi.x;
+      if (d + 3 < a.dl) out[3] = hi.y;
+    }
+    if (d == 0 && a.lse != nullptr)
       a.lse[static_cast<int64_t>(t) * a.H + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
   }
 }
@@ -911,9 +948,9 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, int smem, c
 template <class E, int N, bool BOX>
 int launch(const MmaArgs &m, int ctas, int smem, cudaStream_t stream) {
   if (!allow_smem(latent_attend_mma_kernel<E, N, BOX>, smem)) return SATK_ECUDA;
-  latent_attend_mma_kernel<E, N, BOX><<<ctas, threads_of(BOX), smem, stream>>>(m);
-  int rc = launch_status();
-  if (rc == SATK_OK &&
+  int rc = SATK_OK;
+  if (launch_early(latent_attend_mma_kernel<E, N, BOX>, dim3(ctas), threads_of(BOX), smem, stream,
+                   m) != cudaSuccess ||
       launch_early(latent_join_kernel<E>, dim3(ctas, kJoinY), 256, 0, stream, m, N) != cudaSuccess)
     rc = SATK_ECUDA;
   return rc;
@@ -942,7 +979,7 @@ bool latent_attend_mma_fits(const LatentArgs &a) {
 size_t latent_attend_mma_workspace(int H, int dl) {
   (void)H;
   const int ctas = sm_count();
-  return plans_bytes(ctas) + sizeof(int4) * ctas + sizeof(float) * 2 * ctas * (64 * static_cast<size_t>(dl) + 128);
+  return plans_bytes(ctas) + sizeof(int4) * ctas + sizeof(float) * 2 * ctas * (64 * static_cast<size_t>(dl + 3) + 128);
 }
 
 int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request, void *workspace,
@@ -961,7 +998,8 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
   m.nb = (args.dl + 127) / 128;
   m.np0 = (m.nb + 1) / 2 * 2;
   if (m.np0 > m.np) m.np0 = m.np;
-  m.part_stride = static_cast<int64_t>(N) * args.dl + 2 * N;
+  m.part_ld = (args.dl + 3) & ~3;
+  m.part_stride = static_cast<int64_t>(N) * m.part_ld + 2 * N;
   const int fixed = m.np * N * 128 + kPanel + kSmall, limit = 227 * 1024;
   m.nst = (limit - fixed) / (m.np * kPanel);
   if (m.nst > kMaxStages) m.nst = kMaxStages;

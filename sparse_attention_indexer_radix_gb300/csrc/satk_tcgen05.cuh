@@ -133,6 +133,11 @@ __device__ __forceinline__ void tma_box(uint32_t leader, uint32_t dst, const voi
       : "memory");
 }
 
+// The 128 bytes around an address into L2 alone.
+__device__ __forceinline__ void prefetch_line(const void *src) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
+}
+
 __device__ __forceinline__ void tma_box3(uint32_t leader, uint32_t dst, const void *map, int col,
                                          int row, int outer, uint32_t bar) {
   asm volatile(
@@ -141,11 +146,6 @@ __device__ __forceinline__ void tma_box3(uint32_t leader, uint32_t dst, const vo
       "[%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
       "l"(map), "r"(col), "r"(row), "r"(outer), "r"(bar), "r"(leader)
       : "memory");
-}
-
-// `bytes` (a multiple of 16) from a 16-byte aligned address into L2 alone.
-__device__ __forceinline__ void prefetch_bulk(const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 // 16 bytes global -> shared; zeros, and no read, when !live.
