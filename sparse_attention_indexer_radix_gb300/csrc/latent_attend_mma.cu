@@ -90,7 +90,7 @@ struct MmaArgs {
   int nb;        // 128-column blocks of a value
   int part_ld;   // a partial result: N rows of part_ld values, N references, N sums
   int64_t part_stride;
-  int q_box, q_vec, out_vec;  // queries by TMA, by 16-byte copies; paired stores
+  int q_box, q_vec, out_vec;  // queries by TMA, by 16-byte copies; 8-byte stores
   int run;           // rows of a box: consecutive keys that share a block (1: copies)
   CUtensorMap rows;  // the cache, in boxes of 64 columns x run rows
   CUtensorMap q;     // the queries, in boxes of 64 columns x hc heads x tpg tokens
@@ -255,6 +255,25 @@ struct Cursor {
     }
   }
 };
+
+// Four consecutive results, of which the first `left` exist.
+template <class E>
+__device__ __forceinline__ void store4(E *out, float4 v, int left, bool vec) {
+  union {
+    typename Elem<E>::T2 h[2];
+    uint2 u;
+  } p;
+  p.h[0] = Elem<E>::from2(v.x, v.y);
+  p.h[1] = Elem<E>::from2(v.z, v.w);
+  if (vec) {  // rows are 8-byte aligned and a multiple of four long
+    if (left > 0) *reinterpret_cast<uint2 *>(out) = p.u;
+  } else {
+    if (left > 0) out[0] = p.h[0].x;
+    if (left > 1) out[1] = p.h[0].y;
+    if (left > 2) out[2] = p.h[1].x;
+    if (left > 3) out[3] = p.h[1].y;
+  }
+}
 
 struct Small {
   float red[4][64];
@@ -516,35 +535,33 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
       mbar_wait(bar(sm.o_done), (i - 1) & 1, dead);
       __syncwarp();
       tc_fence_after();
+      // A warp turns its 32 lanes x 16 columns through its quarter of the weights'
+      // buffer, so that eight lanes store 32 consecutive values of a column
+      // (stored as they come, a lane a value, 64 columns x 512 took 14 us).
+      float *turn = reinterpret_cast<float *>(p_ptr) + warp * 512;
+      const int y0 = lane >> 3, d0 = warp * 32 + (lane & 7) * 4;
       for (int col = 0; col < m.nb * N; col += 16) {
-        const int n0 = col & (N - 1), dim = (col / N) * 128 + warp * 32 + lane;
+        const int n0 = col & (N - 1), d = (col / N) * 128 + d0;
         if (n0 >= ncol) continue;
         uint32_t o[16];
         tmem_ld16(o, o_at + col + (static_cast<uint32_t>(warp * 32) << 16));
         tmem_wait_ld();
-        if (whole) {
-          // Lanes of a pair swap so that each stores two columns of one head.
+        __syncwarp();
 #pragma unroll
-          for (int y = 0; y < 16; y += 2) {
-            const float x0 = __uint_as_float(o[y]) * sm.factor[n0 + y];
-            const float x1 = __uint_as_float(o[y + 1]) * sm.factor[n0 + y + 1];
-            const float got = __shfl_xor_sync(~0u, (lane & 1) ? x0 : x1, 1);
-            const int n = n0 + y + (lane & 1), d = dim & ~1;
-            const float lo = (lane & 1) ? got : x0, hi = (lane & 1) ? x1 : got;
-            if (n < ncol) {
-              E *out = static_cast<E *>(a.out) + static_cast<int64_t>(sm.sees[n]) + d;
-              if (m.out_vec) {
-                if (d < a.dl) *reinterpret_cast<typename Elem<E>::T2 *>(out) = Elem<E>::from2(lo, hi);
-              } else {
-                if (d < a.dl) out[0] = Elem<E>::from(lo);
-                if (d + 1 < a.dl) out[1] = Elem<E>::from(hi);
-              }
-            }
+        for (int y = 0; y < 16; ++y) turn[y * 32 + lane] = __uint_as_float(o[y]);
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < 16; y += 4) {
+          const int n = n0 + y + y0;
+          const float4 v = *reinterpret_cast<const float4 *>(turn + (y + y0) * 32 + (lane & 7) * 4);
+          if (!whole) {
+            if (d < m.part_ld)
+              __stcg(reinterpret_cast<float4 *>(part + static_cast<int64_t>(n) * m.part_ld + d), v);
+          } else if (n < ncol) {
+            const float f = sm.factor[n];
+            store4<E>(static_cast<E *>(a.out) + static_cast<int64_t>(sm.sees[n]) + d,
+                      make_float4(v.x * f, v.y * f, v.z * f, v.w * f), a.dl - d, m.out_vec);
           }
-        } else if (dim < a.dl) {
-#pragma unroll
-          for (int y = 0; y < 16; ++y)
-            part[static_cast<int64_t>(n0 + y) * m.part_ld + dim] = __uint_as_float(o[y]);
         }
       }
       tc_fence_before();
@@ -825,8 +842,8 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
 }
 
 // Joins the partial results of the group that CTA x leaves unfinished: weights
-// 2^(m_i - max m) / sum, parts added in line order.  One warp per column and 128
-// of its values, four parts' loads in flight.
+// 2^(m_i - max m) / sum, parts added in line order.  One warp per column and 256
+// of its values.
 template <class E>
 __global__ void __launch_bounds__(256, 6) latent_join_kernel(const __grid_constant__ MmaArgs m, int N) {
   wait_for_previous_kernel();
@@ -838,11 +855,12 @@ __global__ void __launch_bounds__(256, 6) latent_join_kernel(const __grid_consta
   auto part = [&](int i) {
     return m.parts + ((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * m.part_stride;
   };
-  for (int x = blockIdx.y * 8 + (threadIdx.x >> 5); x < ncol * m.nb; x += kJoinY * 8) {
-    const int n = x / m.nb, d = (x - n * m.nb) * 128 + lane * 4;
+  const int per_column = (m.nb + 1) >> 1;
+  for (int x = blockIdx.y * 8 + (threadIdx.x >> 5); x < ncol * per_column; x += kJoinY * 8) {
+    const int n = x / per_column, d = (x - n * per_column) * 256 + lane * 4;
     const int64_t stat = static_cast<int64_t>(N) * m.part_ld + n;
     const int64_t value = static_cast<int64_t>(n) * m.part_ld + d;
-    // Statistics of the first 32 parts and values of the first four, all in
+    // Statistics of the first 32 parts and values of the first two, all in
     // flight together; few groups have more.
     float top = kUnset, sum = 0.f;
     if (lane < n_parts) {
@@ -850,13 +868,15 @@ __global__ void __launch_bounds__(256, 6) latent_join_kernel(const __grid_consta
       top = __ldcg(p);
       sum = __ldcg(p + N);
     }
-    float4 v[4];
+    float4 v[2][2];
     auto load = [&](int i) {
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
-        v[y] = i + y < n_parts && d < m.part_ld
-                   ? __ldcg(reinterpret_cast<const float4 *>(part(i + y) + value))
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          v[y][z] = i + y < n_parts && d + z * 128 < m.part_ld
+                        ? __ldcg(reinterpret_cast<const float4 *>(part(i + y) + value + z * 128))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     load(0);
     float mx = top;
@@ -864,8 +884,8 @@ __global__ void __launch_bounds__(256, 6) latent_join_kernel(const __grid_consta
 #pragma unroll
     for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, y));
     float f = exp2_fast(top - mx), l = f * sum;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n_parts; i += 4) {
+    float4 acc[2] = {};
+    for (int i = 0; i < n_parts; i += 2) {
       if (i > 0) {
         load(i);
         if ((i & 31) == 0) {
@@ -878,13 +898,16 @@ __global__ void __launch_bounds__(256, 6) latent_join_kernel(const __grid_consta
         }
       }
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
+      for (int y = 0; y < 2; ++y) {
         const float fi = __shfl_sync(~0u, f, (i + y) & 31);
         if (i + y < n_parts) {
-          acc.x = fmaf(fi, v[y].x, acc.x);
-          acc.y = fmaf(fi, v[y].y, acc.y);
-          acc.z = fmaf(fi, v[y].z, acc.z);
-          acc.w = fmaf(fi, v[y].w, acc.w);
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            acc[z].x = fmaf(fi, v[y][z].x, acc[z].x);
+            acc[z].y = fmaf(fi, v[y][z].y, acc[z].y);
+            acc[z].z = fmaf(fi, v[y][z].z, acc[z].z);
+            acc[z].w = fmaf(fi, v[y][z].w, acc[z].w);
+          }
         }
       }
     }
@@ -893,17 +916,10 @@ __global__ void __launch_bounds__(256, 6) latent_join_kernel(const __grid_consta
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int tok = n / m.hc, t = join.x + tok, h = join.z + n - tok * m.hc;
     E *out = static_cast<E *>(a.out) + t * a.ld_out_t + h * a.ld_out_h + d;
-    using T2 = typename Elem<E>::T2;
-    const T2 lo = Elem<E>::from2(acc.x * inv, acc.y * inv), hi = Elem<E>::from2(acc.z * inv, acc.w * inv);
-    if (m.out_vec) {  // dl is even, and pairs are aligned
-      if (d < a.dl) *reinterpret_cast<T2 *>(out) = lo;
-      if (d + 2 < a.dl) *reinterpret_cast<T2 *>(out + 2) = hi;
-    } else {
-      if (d < a.dl) out[0] = lo.x;
-      if (d + 1 < a.dl) out[1] = lo.y;
-      if (d + 2 < a.dl) out[2] = hi.x;
-      if (d + 3 < a.dl) out[3] = hi.y;
-    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+      store4<E>(out + z * 128, make_float4(acc[z].x * inv, acc[z].y * inv, acc[z].z * inv, acc[z].w * inv),
+                a.dl - d - z * 128, m.out_vec);
     if (d == 0 && a.lse != nullptr)
       a.lse[static_cast<int64_t>(t) * a.H + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
   }
@@ -1007,8 +1023,8 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
   m.q_vec = aligned16(args.q) && (args.T == 1 || args.ld_q_t % 8 == 0) &&
             (args.H == 1 || args.ld_q_h % 8 == 0);
   m.q_box = m.q_vec;
-  m.out_vec = (reinterpret_cast<uintptr_t>(args.out) & 3u) == 0 && args.dl % 2 == 0 &&
-              (args.T == 1 || args.ld_out_t % 2 == 0) && (args.H == 1 || args.ld_out_h % 2 == 0);
+  m.out_vec = (reinterpret_cast<uintptr_t>(args.out) & 7u) == 0 && args.dl % 4 == 0 &&
+              (args.T == 1 || args.ld_out_t % 4 == 0) && (args.H == 1 || args.ld_out_h % 4 == 0);
   // Rows that consecutive keys of a tile share in one block (a run is in the
   // cache as a whole, or from its first key on is not).
   m.run = 1;
