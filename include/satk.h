@@ -74,7 +74,9 @@ enum satk_rc {
                                         the cos/sin table; token skipped    */
 #define SATK_STATUS_STALLED 128      /* an attention kernel gave up a wait
                                         inside the GPU (about two seconds):
-                                        its outputs are not to be used       */
+                                        its outputs are not to be used (the
+                                        expanded form, which has no status
+                                        word, writes NaN)                    */
 
 /* Largest K of satk_topk_rows and of the rescue push. */
 #define SATK_TOPK_MAX_K 4096

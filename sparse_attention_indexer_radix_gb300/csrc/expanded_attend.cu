@@ -27,5 +27,6 @@ extern "C" int satk_latent_attend_expanded(const void *q, int dtype, int64_t T, 
                  k,    static_cast<int>(S), ld_k_s, ld_k_h,       tail,       ld_tail, v,   ld_v_s,
                  ld_v_h, token_starts,      key_starts, R,        row_ends,   scale * kLog2e,
                  out,  ld_out_t,            ld_out_h, lse};
+  if (expanded_attend_mma_fits(a)) return expanded_attend_mma(a, dtype, as_stream(stream));
   return expanded_attend_warp(a, dtype, as_stream(stream));
 }

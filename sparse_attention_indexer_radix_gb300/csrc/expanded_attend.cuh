@@ -28,4 +28,9 @@ struct ExpandedArgs {
 // The general kernel: any widths, strides and alignment.
 int expanded_attend_warp(const ExpandedArgs &a, int dtype, cudaStream_t stream);
 
+// The tensor-core kernel (expanded_attend_mma.cu): whether it takes this call,
+// and the call.
+bool expanded_attend_mma_fits(const ExpandedArgs &a);
+int expanded_attend_mma(const ExpandedArgs &a, int dtype, cudaStream_t stream);
+
 }  // namespace satk

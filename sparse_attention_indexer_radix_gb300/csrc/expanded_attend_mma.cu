@@ -1,0 +1,497 @@
+// expanded_attend_mma.cu -- expanded (per-head) attention on the tensor cores.
+//
+// A CTA takes one head and up to 256 tokens of one request as two sub-tiles of
+// 128, and goes over the keys in tiles of 128:
+//   S_j[token, key] = Q_j . [K | tail]^T     j = 0, 1
+//   P_j             = exp2(scale S_j - m)    m lags behind the running maximum
+//   O_j            += P_j V
+// While the softmax of one sub-tile runs, the products of the other one keep
+// the tensor core busy.  A token is a TMEM lane and a thread, so maximum and
+// sum need no exchange between threads; O is rescaled only when a score passes
+// the reference by 2^8.  P_j replaces S_j in tensor memory and is the A operand
+// of the second product from there; S_0, S_1, O_0, O_1 fill the 512 columns.
+// Keys, tail and values come by TMA in 128-byte-swizzled panels of 64 columns;
+// K panels are read K-major, V panels MN-major.
+//
+// Bounded by the tensor core: per 256 x 128 tile at 192 query/key and 128 value
+// columns it takes 2560 cycles, the softmax about half of that.
+//
+// Keys past a request's end, or that only some tokens see, are masked by value.
+// In tiles with such keys the value rows are looked over first: one that is not
+// finite would turn a 0 weight into NaN, so it is cleared and the weights of
+// the tokens that see it become NaN.
+//
+// Roles (384 threads): warps 0-3 and 4-7 softmax and results of the sub-tiles,
+// warp 8 issues the MMAs, warp 9 the loads (10-11 only give their registers).
+// Tiles of the last tokens, which see most keys, start first.
+#include <cuda.h>
+#include <type_traits>
+
+#include "expanded_attend.cuh"
+#include "satk_tcgen05.cuh"
+
+namespace satk {
+namespace {
+
+constexpr int kRows = 128;             // tokens of a sub-tile, keys of a tile
+constexpr int kPanel = kRows * 128;    // bytes of 64 columns of a tile
+constexpr int kThreads = 384;
+constexpr int kSmall = 2048;
+constexpr int kMaxStages = 2;
+constexpr float kUnset = -1e30f;
+constexpr float kLag = 8.f;
+
+struct ExpandedMma {
+  ExpandedArgs a;
+  int nsub;          // sub-tiles: 2, or 1 where two do not fit
+  int nope_panels, panels, v_panels;
+  int nk, nv;        // stages
+  int vec;           // 16-byte aligned output rows
+  CUtensorMap q, k, tail, v;
+};
+
+struct Small {
+  uint64_t q_full[2], k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages],
+      v_empty[kMaxStages];
+  uint64_t s_full[2], p_full[2], o_done[2], issued;
+  uint32_t bad[4];       // value rows of the tile that are not finite
+  int scan[12], low[8], high[8];
+  int place[4];          // request's first key, its keys, first token, tokens
+  uint32_t tmem;
+  int dead;
+};
+static_assert(sizeof(Small) <= kSmall, "small shared arrays");
+
+// Which tokens the CTA's tile has: tiles count through the requests in order.
+__device__ void find_tile(const ExpandedArgs &a, int tile, int tokens, Small &sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) sm.place[3] = 0;
+  const int per = (a.R + kThreads - 1) / kThreads;
+  const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+  auto tokens_of = [&](int r) {
+    const int b = min(max(a.token_starts[r], 0), a.T), e = min(max(a.token_starts[r + 1], b), a.T);
+    return make_int2(b, e);
+  };
+  int n = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int2 t = tokens_of(r);
+    n += (t.y - t.x + tokens - 1) / tokens;
+  }
+  int x = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) sm.scan[warp] = x;
+  __syncthreads();
+  int before = x - n;
+  for (int w = 0; w < warp; ++w) before += sm.scan[w];
+  if (tile >= before && tile < before + n)
+    for (int r = r0; r < r1; ++r) {
+      const int2 t = tokens_of(r);
+      const int count = (t.y - t.x + tokens - 1) / tokens;
+      if (tile < before + count) {
+        const int kb = min(max(a.key_starts[r], 0), a.S);
+        const int ke = min(max(a.key_starts[r + 1], kb), a.S);
+        sm.place[0] = kb;
+        sm.place[1] = ke - kb;
+        // the last tiles of a request first
+        const int first = t.x + (count - 1 - (tile - before)) * tokens;
+        sm.place[2] = first;
+        sm.place[3] = min(tokens, t.y - first);
+        break;
+      }
+      before += count;
+    }
+  __syncthreads();
+}
+
+// Empty rows for the tokens that no request has: the last CTAs, one a head.
+template <class E>
+__device__ void outside(const ExpandedArgs &a, int h) {
+  const int b = a.R > 0 ? min(max(a.token_starts[0], 0), a.T) : a.T;
+  const int e = a.R > 0 ? max(a.token_starts[a.R], b) : a.T;
+  for (int t = threadIdx.x >> 5; t < a.T; t += kThreads / 32) {
+    if (t >= b && t < e) {
+      t = ((e - 1 - t) / (kThreads / 32)) * (kThreads / 32) + t;  // the last such t below e
+      continue;
+    }
+    const int lane = threadIdx.x & 31;
+    E *out = static_cast<E *>(a.out) + t * a.ld_out_t + h * a.ld_out_h;
+    for (int c = lane; c < a.dv; c += 32) out[c] = Elem<E>::from(0.f);
+    if (lane == 0 && a.lse != nullptr) a.lse[static_cast<int64_t>(t) * a.H + h] = -INFINITY;
+  }
+}
+
+template <class E>
+__global__ void __launch_bounds__(kThreads, 1)
+    expanded_attend_mma_kernel(const __grid_constant__ ExpandedMma m) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const ExpandedArgs &a = m.a;
+  const uint32_t base = smem_addr(smem);
+  const int tile_bytes = m.panels * kPanel, v_bytes = m.v_panels * kPanel;
+  const uint32_t k_at = base + m.nsub * tile_bytes, v_at = k_at + m.nk * tile_bytes;
+  Small &sm = *reinterpret_cast<Small *>(smem + (v_at - base) + m.nv * v_bytes);
+  volatile int *dead = &sm.dead;
+  auto bar = [&](uint64_t &b) { return smem_addr(&b); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.x % a.H;
+
+  if (blockIdx.x >= gridDim.x - a.H) {
+    outside<E>(a, h);
+    return;
+  }
+  find_tile(a, blockIdx.x / a.H, m.nsub * kRows, sm);
+  const int key0 = sm.place[0], keys = sm.place[1], t0 = sm.place[2], tokens = sm.place[3];
+  if (tokens == 0) return;
+
+  // Softmax threads: this thread's token and its end; tiles of each sub-tile.
+  const int sub = warp >> 2, row = threadIdx.x & 127;
+  const int t = t0 + sub * kRows + row;
+  const bool mine = sub < m.nsub && sub * kRows + row < tokens;
+  int end = mine ? min(max(a.row_ends[t], 0), keys) : INT32_MAX;
+  {
+    int lo = end, hi = mine ? end : 0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      lo = min(lo, __shfl_xor_sync(~0u, lo, d));
+      hi = max(hi, __shfl_xor_sync(~0u, hi, d));
+    }
+    if (lane == 0 && warp < 8) sm.low[warp] = lo, sm.high[warp] = hi;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(bar(sm.k_full[s]), 1);
+      mbar_init(bar(sm.k_empty[s]), 1);
+      mbar_init(bar(sm.v_full[s]), 1);
+      mbar_init(bar(sm.v_empty[s]), 1);
+    }
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(bar(sm.q_full[j]), 1);
+      mbar_init(bar(sm.s_full[j]), 1);
+      mbar_init(bar(sm.p_full[j]), kRows);
+      mbar_init(bar(sm.o_done[j]), 1);
+    }
+    mbar_init(bar(sm.issued), 1);
+    sm.dead = 0;
+    for (int x = 0; x < 4; ++x) sm.bad[x] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) tmem_alloc(smem_addr(&sm.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  int low = INT32_MAX, n_sub[2] = {0, 0};
+  for (int w = 0; w < 8; ++w) {
+    low = min(low, sm.low[w]);
+    n_sub[w >> 2] = max(n_sub[w >> 2], (sm.high[w] + kRows - 1) / kRows);
+  }
+  const int n = max(n_sub[0], n_sub[1]);
+
+  // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168.
+  if (warp < 8) regs_raise<208>(); else regs_lower<88>();
+  if (warp < 8) {
+    // --------------------------------------------------------- softmax, results
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + sub * kRows + lanes, o_at = tmem + 256 + sub * kRows + lanes;
+    const int my_tiles = sub < m.nsub ? n_sub[sub] : 0;
+    float l = 0.f, ref = kUnset;
+    for (int i = 0; i < n; ++i) {
+      const int k0 = i * kRows;
+      const bool work = i < my_tiles;
+      uint32_t raw[kRows];
+      float mx = -INFINITY;
+      if (work) {
+        mbar_wait(bar(sm.s_full[sub]), i & 1, dead);
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(raw, c * 32, s_at + c * 32);
+        tmem_wait_ld();
+      }
+      if (k0 + kRows > low) {
+        // Some token does not see some key.  Two threads look over each value
+        // row; rows that are not finite are cleared and remembered.
+        mbar_wait(bar(sm.v_full[i % m.nv]), (i / m.nv) & 1, dead);
+        unsigned char *v = smem + (v_at - base) + (i % m.nv) * v_bytes + row * 128;
+        const int half = m.v_panels * 4;  // 16-byte chunks of half a row
+        bool odd = false;
+        for (int x = sub * half; x < (sub + 1) * half; ++x) {
+          Pack8<E> p;
+          p.u = *reinterpret_cast<const uint4 *>(v + (x >> 3) * kPanel + ((x & 7) << 4));
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = Elem<E>::to2(p.h[y]);
+            odd |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
+          }
+        }
+        if (odd) atomicOr(&sm.bad[row >> 5], 1u << (row & 31));
+        named_sync(1, 256);
+        const uint32_t bad = sm.bad[row >> 5];
+        if ((bad >> (row & 31)) & 1) {
+          for (int x = sub * half; x < (sub + 1) * half; ++x)
+            *reinterpret_cast<uint4 *>(v + (x >> 3) * kPanel + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_shared();
+        const bool any = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;
+        if (work) {
+#pragma unroll
+          for (int x = 0; x < kRows; ++x) {
+            if (k0 + x >= end) raw[x] = 0xff800000u;  // -inf
+            else if (any && ((sm.bad[x >> 5] >> (x & 31)) & 1)) raw[x] = 0x7fc00000u;
+          }
+        }
+        named_sync(1, 256);
+        if (threadIdx.x < 4) sm.bad[threadIdx.x] = 0;
+        // the next tile's scan writes after another pair of barriers has passed
+        named_sync(1, 256);
+      }
+      if (!work) continue;
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int x = 0; x < kRows; ++x) m4[x & 3] = fmaxf(m4[x & 3], __uint_as_float(raw[x]));
+      mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+      if (__any_sync(~0u, mx - ref > kLag)) {
+        const float now = fmaxf(ref, mx);
+        const float f = exp2_fast(ref - now);
+        l *= f;
+        ref = now;
+        if (i > 0) {
+          // s_full came after this sub-tile's last P V
+          for (int c = 0; c < a.dv; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(o, o_at + c);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+            tmem_st16(o_at + c, o);
+          }
+        }
+      }
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t p[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          const int at = c * 64 + 2 * x;
+          const float p0 = exp2_fast(fmaf(__uint_as_float(raw[at]), a.scale_log2, -ref));
+          const float p1 = exp2_fast(fmaf(__uint_as_float(raw[at + 1]), a.scale_log2, -ref));
+          l4[x & 3] += p0 + p1;
+          union {
+            typename Elem<E>::T2 h;
+            uint32_t u;
+          } pk;
+          pk.h = Elem<E>::from2(p0, p1);
+          p[x] = pk.u;
+        }
+        tmem_st32(s_at + c * 32, p, 0);
+      }
+      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(sm.p_full[sub]));
+    }
+    if (sub < m.nsub) {
+      if (my_tiles > 0) {
+        mbar_wait(bar(sm.o_done[sub]), (my_tiles - 1) & 1, dead);
+        __syncwarp();
+        tc_fence_after();
+      }
+      if (*dead != 0) l = NAN;  // a wait was given up: no result
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      E *out = static_cast<E *>(a.out) + t * a.ld_out_t + h * a.ld_out_h;
+      for (int c = 0; c < a.dv; c += 16) {
+        uint32_t o[16];
+        if (my_tiles > 0) {
+          tmem_ld16(o, o_at + c);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int y = 0; y < 16; ++y) o[y] = 0;
+        }
+        if (mine) {
+          Pack8<E> p[2];
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            p[y >> 2].h[y & 3] = Elem<E>::from2(__uint_as_float(o[2 * y]) * inv,
+                                                __uint_as_float(o[2 * y + 1]) * inv);
+          if (m.vec) {
+            *reinterpret_cast<uint4 *>(out + c) = p[0].u;
+            *reinterpret_cast<uint4 *>(out + c + 8) = p[1].u;
+          } else {
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              out[c + y] = (y & 1) ? p[y >> 3].h[(y & 7) >> 1].y : p[y >> 3].h[(y & 7) >> 1].x;
+          }
+        }
+      }
+      tc_fence_before();
+      if (mine && a.lse != nullptr)
+        a.lse[static_cast<int64_t>(t) * a.H + h] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- MMA issue
+    constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
+    constexpr uint32_t ds = mma_desc(bf16, false, false, kRows, kRows);
+    const uint32_t dp = mma_desc(bf16, false, true, kRows, a.dv);
+    const uint32_t leader = elect_leader();
+    const uint64_t q_desc = tile_desc(base, 16, 1024), k_desc = tile_desc(k_at, 16, 1024);
+    const uint64_t v_desc = tile_desc(v_at, kPanel, 1024);
+    auto scores = [&](int j, int i) {
+      uint64_t qd = q_desc + ((j * tile_bytes) >> 4), kd = k_desc + (((i % m.nk) * tile_bytes) >> 4);
+      const uint32_t d = tmem + j * kRows;
+      bool more = false;
+      for (int p = 0; p < m.panels; ++p, qd += kPanel >> 4, kd += kPanel >> 4) {
+        const int cols = p < m.nope_panels ? a.dn - p * 64 : a.dr;
+        if (cols >= 64) {
+          mma_ss(leader, d, qd, kd, ds, more);
+          mma_ss(leader, d, qd + 2, kd + 2, ds, true);
+          mma_ss(leader, d, qd + 4, kd + 4, ds, true);
+          mma_ss(leader, d, qd + 6, kd + 6, ds, true);
+        } else {
+          for (int x = 0; x < cols >> 4; ++x)
+            mma_ss(leader, d, qd + 2 * x, kd + 2 * x, ds, more || x > 0);
+        }
+        more = true;
+      }
+      tc_commit(leader, bar(sm.s_full[j]));
+    };
+    auto values = [&](int j, int i) {
+      const uint64_t vd = v_desc + (((i % m.nv) * v_bytes) >> 4);
+      const uint32_t d = tmem + 256 + j * kRows, p = tmem + j * kRows;
+#pragma unroll
+      for (int x = 0; x < kRows / 16; ++x)
+        mma_ts(leader, d, p + x * 8, vd + x * 128, dp, i > 0 || x > 0);
+      tc_commit(leader, bar(sm.o_done[j]));
+    };
+    for (int i = -1; i < n; ++i) {
+      // values of tile i, scores of tile i + 1, the sub-tiles in turn
+      for (int j = 0; j < m.nsub; ++j) {
+        if (i >= 0 && i < n_sub[j]) {
+          mbar_wait(bar(sm.v_full[i % m.nv]), (i / m.nv) & 1, dead);
+          mbar_wait(bar(sm.p_full[j]), i & 1, dead);
+          __syncwarp();
+          tc_fence_after();
+          values(j, i);
+        }
+        if (i + 1 < n_sub[j]) {
+          if (i < 0) mbar_wait(bar(sm.q_full[j]), 0, dead);
+          mbar_wait(bar(sm.k_full[(i + 1) % m.nk]), ((i + 1) / m.nk) & 1, dead);
+          __syncwarp();
+          tc_fence_after();
+          scores(j, i + 1);
+        }
+      }
+      if (i >= 0) tc_commit(leader, bar(sm.v_empty[i % m.nv]));
+      if (i + 1 < n) tc_commit(leader, bar(sm.k_empty[(i + 1) % m.nk]));
+    }
+    tc_commit(leader, bar(sm.issued));
+    mbar_drain(bar(sm.issued), 0);
+  } else if (warp == 9) {
+    // -------------------------------------------------------------------- loads
+    const uint32_t leader = elect_leader();
+    if (n > 0)
+      for (int j = 0; j < m.nsub; ++j) {
+        if (lane == 0) mbar_expect(bar(sm.q_full[j]), tile_bytes);
+        __syncwarp();
+        for (int p = 0; p < m.panels; ++p)
+          tma_box3(leader, base + j * tile_bytes + p * kPanel, &m.q,
+                   p < m.nope_panels ? p * 64 : a.dn, h, t0 + j * kRows, bar(sm.q_full[j]));
+      }
+    for (int i = 0; i < n; ++i) {
+      const int ks = i % m.nk, vs = i % m.nv, key = key0 + i * kRows;
+      if (i >= m.nk) mbar_wait(bar(sm.k_empty[ks]), (i / m.nk - 1) & 1, dead);
+      __syncwarp();
+      if (lane == 0) mbar_expect(bar(sm.k_full[ks]), tile_bytes);
+      __syncwarp();
+      for (int p = 0; p < m.panels; ++p) {
+        const uint32_t dst = k_at + ks * tile_bytes + p * kPanel;
+        if (p < m.nope_panels) tma_box3(leader, dst, &m.k, p * 64, h, key, bar(sm.k_full[ks]));
+        else tma_box(leader, dst, &m.tail, 0, key, bar(sm.k_full[ks]));
+      }
+      if (i >= m.nv) mbar_wait(bar(sm.v_empty[vs]), (i / m.nv - 1) & 1, dead);
+      __syncwarp();
+      if (lane == 0) mbar_expect(bar(sm.v_full[vs]), v_bytes);
+      __syncwarp();
+      for (int p = 0; p < m.v_panels; ++p)
+        tma_box3(leader, v_at + vs * v_bytes + p * kPanel, &m.v, p * 64, h, key, bar(sm.v_full[vs]));
+      __syncwarp();
+    }
+    if (n > 0)
+      for (int j = 0; j < m.nsub; ++j) mbar_drain(bar(sm.q_full[j]), 0);
+    for (int i = max(0, n - 2); i < n; ++i) {
+      if (i >= n - m.nk) mbar_drain(bar(sm.k_full[i % m.nk]), (i / m.nk) & 1);
+      if (i >= n - m.nv) mbar_drain(bar(sm.v_full[i % m.nv]), (i / m.nv) & 1);
+    }
+  }
+  __syncthreads();
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+// The smallest request of stages and sub-tiles that fits, largest first.
+bool layout(const ExpandedArgs &a, ExpandedMma &m, int &smem) {
+  m.nope_panels = (a.dn + 63) / 64;
+  m.panels = m.nope_panels + (a.dr > 0 ? 1 : 0);
+  m.v_panels = (a.dv + 63) / 64;
+  const int limit = 227 * 1024;
+  for (m.nsub = 2; m.nsub >= 1; --m.nsub)
+    for (int s = 3; s >= 1; --s) {
+      m.nk = s >= 2 ? 2 : 1;
+      m.nv = s >= 3 ? 2 : 1;
+      smem = (m.nsub + m.nk) * m.panels * kPanel + m.nv * m.v_panels * kPanel + kSmall;
+      if (smem <= limit) return true;
+    }
+  return false;
+}
+
+bool rows_aligned(const void *p, int64_t n, int64_t ld, int64_t H, int64_t ld_h) {
+  return aligned16(p) && (n <= 1 || ld % 8 == 0) && (H <= 1 || ld_h % 8 == 0);
+}
+
+template <class E>
+int launch(const ExpandedMma &m, int smem, cudaStream_t stream) {
+  const ExpandedArgs &a = m.a;
+  if (!allow_smem(expanded_attend_mma_kernel<E>, smem)) return SATK_ECUDA;
+  const int64_t grid = (a.T / (m.nsub * kRows) + a.R + 1ll) * a.H;
+  if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
+  expanded_attend_mma_kernel<E><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(m);
+  return launch_status();
+}
+
+}  // namespace
+
+bool expanded_attend_mma_fits(const ExpandedArgs &a) {
+  ExpandedMma m;
+  int smem;
+  return a.S > 0 && a.scale_log2 > 0.f && a.dn % 16 == 0 && a.dr % 16 == 0 && a.dv % 16 == 0 &&
+         a.dr <= 64 && rows_aligned(a.q, a.T, a.ld_q_t, a.H, a.ld_q_h) &&
+         rows_aligned(a.k, a.S, a.ld_k_s, a.H, a.ld_k_h) &&
+         rows_aligned(a.v, a.S, a.ld_v_s, a.H, a.ld_v_h) &&
+         (a.dr == 0 || rows_aligned(a.tail, a.S, a.ld_tail, 1, 0)) && layout(a, m, smem);
+}
+
+int expanded_attend_mma(const ExpandedArgs &a, int dtype, cudaStream_t stream) {
+  ExpandedMma m;
+  int smem;
+  m.a = a;
+  if (!layout(a, m, smem)) return SATK_EUNSUPPORTED;
+  m.vec = rows_aligned(a.out, a.T, a.ld_out_t, a.H, a.ld_out_h);
+  const bool bf16 = dtype == SATK_BF16;
+  // Strides of dimensions of one are free: any multiple of 16 bytes.
+  auto map = [&](CUtensorMap *to, const void *p, int cols, int64_t n, int64_t ld, int64_t ld_h) {
+    return tensor_map_16bit(to, bf16, p, cols, a.H, a.H == 1 ? 1024 : ld_h, 1, n, n == 1 ? 1024 : ld,
+                            kRows);
+  };
+  if (!map(&m.q, a.q, a.dn + a.dr, a.T, a.ld_q_t, a.ld_q_h) ||
+      !map(&m.k, a.k, a.dn, a.S, a.ld_k_s, a.ld_k_h) ||
+      !map(&m.v, a.v, a.dv, a.S, a.ld_v_s, a.ld_v_h) ||
+      (a.dr > 0 && !tensor_map_16bit(&m.tail, bf16, a.tail, a.dr, a.S, a.S == 1 ? 1024 : a.ld_tail,
+                                     kRows)))
+    return SATK_ECUDA;
+  return bf16 ? launch<__nv_bfloat16>(m, smem, stream) : launch<__half>(m, smem, stream);
+}
+
+}  // namespace satk

@@ -226,6 +226,16 @@ __device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, 
       : "memory");
 }
 
+// The same with A in tensor memory: lane = row, a column holds two K values.
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t desc, bool accumulate) {
+  asm volatile(
+      "{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u), "r"(leader)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -253,6 +263,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
       "%13,%14,%15};" ::SATK_I8(v, 0),
       SATK_I8(v, 8), "r"(addr)
+      : "memory");
+}
+// The same for 32 columns, from v[o] on.
+template <int LEN>
+__device__ __forceinline__ void tmem_ld32(uint32_t (&v)[LEN], const int o, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : SATK_R8(v, o), SATK_R8(v, o + 8), SATK_R8(v, o + 16), SATK_R8(v, o + 24)
+      : "r"(addr)
+      : "memory");
+}
+template <int LEN>
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[LEN], const int o) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SATK_I8(v, o),
+      SATK_I8(v, o + 8), SATK_I8(v, o + 16), SATK_I8(v, o + 24), "r"(addr)
       : "memory");
 }
 // 16 lanes x 2 C columns: lanes 0-15 of the warp get columns [0, C) of their
