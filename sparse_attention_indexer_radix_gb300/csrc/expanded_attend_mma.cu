@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx = -INFINITY;
       if (work) {
         mbar_wait(bar(sm.s_full[sub]), i & 1, dead);
+        if (i > 0) mbar_wait(bar(sm.o_done[sub]), (i - 1) & 1, dead);
         __syncwarp();
         tc_fence_after();
 #pragma unroll
@@ -213,7 +214,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (k0 + kRows > low) {
         // Some token does not see some key.  Two threads look over each value
-        // row; rows that are not finite are cleared and remembered.
+        // row; rows that are not finite are cleared and remembered.  (Threads
+        // without a token wait here for those with one: only then has the
+        // stage's earlier use come and gone.)
+        named_sync(1, 256);
         mbar_wait(bar(sm.v_full[i % m.nv]), (i / m.nv) & 1, dead);
         unsigned char *v = smem + (v_at - base) + (i % m.nv) * v_bytes + row * 128;
         const int half = m.v_panels * 4;  // 16-byte chunks of half a row
@@ -259,7 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= f;
         ref = now;
         if (i > 0) {
-          // s_full came after this sub-tile's last P V
           for (int c = 0; c < a.dv; c += 16) {
             uint32_t o[16];
             tmem_ld16(o, o_at + c);

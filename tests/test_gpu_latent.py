@@ -561,6 +561,25 @@ def test_expanded_layouts(pad):
     assert torch.all(o[outside] == 0) and torch.all(torch.isneginf(lse[outside]))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_expanded_with_garbage_left_in_shared_memory(dtype, dv):
+    """Last tiles of few tokens over several key tiles, right after a kernel
+    that fills shared memory with NaN: nothing is read before it has arrived."""
+    g = gen(36)
+    new, context = [300, 260, 40, 1], [0, 100, 600, 900]
+    q, k, tail, v, ts, ks, ends = expanded_case(g, dtype, 4, 64, 32, dv, new, context)
+    nan = torch.full((4096, 544), float("nan"), dtype=dtype, device=DEV)
+    fill = torch.randint(0, 4096, (256, 512), generator=g, device=DEV).int()
+    fq = torch.zeros(256, 64, 544, dtype=dtype, device=DEV)
+    args = (q, k, tail, v, i32(ts), i32(ks), i32(ends))
+    for _ in range(4):
+        satk.latent_attend_rows(fq, nan, fill, latent_dim=512, scale=1.0)
+        o, lse = satk.latent_attend_expanded(*args, scale=0.2)
+        assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    expanded_check(q, k, tail, v, ts, ks, ends, o, lse, 0.2)
+
+
 def test_expanded_many_requests_and_graph():
     g = gen(35)
     new = [1 + (i * 7) % 23 for i in range(150)]
