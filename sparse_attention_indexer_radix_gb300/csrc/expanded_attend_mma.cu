@@ -10,19 +10,22 @@
 // sum need no exchange between threads; O is rescaled only when a score passes
 // the reference by 2^8.  P_j replaces S_j in tensor memory and is the A operand
 // of the second product from there; S_0, S_1, O_0, O_1 fill the 512 columns.
-// Keys, tail and values come by TMA in 128-byte-swizzled panels of 64 columns;
-// K panels are read K-major, V panels MN-major.
+// Keys, tail and values come by TMA in 128-byte-swizzled panels of 64 columns x
+// 128 keys, through one ring of panels in the order of their use (K of tile 0,
+// V 0, K 1, V 1, ...); K panels are read K-major, V panels MN-major.
 //
 // Bounded by the tensor core: per 256 x 128 tile at 192 query/key and 128 value
-// columns it takes 2560 cycles, the softmax about half of that.
+// columns it takes 2560 cycles.  A sub-tile's own chain (scores, softmax,
+// values) has to stay below that: the first half of the weights is handed over
+// while the second is still computed.
 //
 // Keys past a request's end, or that only some tokens see, are masked by value.
-// In tiles with such keys the value rows are looked over first: one that is not
-// finite would turn a 0 weight into NaN, so it is cleared and the weights of
-// the tokens that see it become NaN.
+// In tiles with such keys two warps look over the value rows first: one that is
+// not finite would turn a 0 weight into NaN, so it is cleared, and the tokens
+// that do see it get NaN.
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax and results of the sub-tiles,
-// warp 8 issues the MMAs, warp 9 the loads (10-11 only give their registers).
+// warp 8 issues the MMAs, warp 9 the loads, warps 10-11 look over value rows.
 // Tiles of the last tokens, which see most keys, start first.
 #include <cuda.h>
 #include <type_traits>
@@ -37,7 +40,11 @@ constexpr int kRows = 128;             // tokens of a sub-tile, keys of a tile
 constexpr int kPanel = kRows * 128;    // bytes of 64 columns of a tile
 constexpr int kThreads = 384;
 constexpr int kSmall = 2048;
-constexpr int kMaxStages = 2;
+constexpr int kMaxSlots = 12;
+// Arrival barriers for the keys and the values of that many tiles: the ring holds
+// fewer tiles (two panels each at least), so a barrier's last use is over before
+// its next one.
+constexpr int kTiles = 8;
 constexpr float kUnset = -1e30f;
 constexpr float kLag = 8.f;
 
@@ -45,22 +52,36 @@ struct ExpandedMma {
   ExpandedArgs a;
   int nsub;          // sub-tiles: 2, or 1 where two do not fit
   int nope_panels, panels, v_panels;
-  int nk, nv;        // stages
+  int slots;         // of the ring
   int vec;           // 16-byte aligned output rows
   CUtensorMap q, k, tail, v;
 };
 
 struct Small {
-  uint64_t q_full[2], k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages],
-      v_empty[kMaxStages];
-  uint64_t s_full[2], p_full[2], o_done[2], issued;
-  uint32_t bad[4];       // value rows of the tile that are not finite
+  uint64_t q_full[2], k_full[kTiles], v_full[kTiles], empty[kMaxSlots];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], v_ready[kTiles], issued;
+  int bad_key;           // the first key with a value row that is not finite
   int scan[12], low[8], high[8];
   int place[4];          // request's first key, its keys, first token, tokens
   uint32_t tmem;
   int dead;
 };
 static_assert(sizeof(Small) <= kSmall, "small shared arrays");
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A place in the ring of panels.
+struct Ring {
+  int slot = 0, use = 0;
+  __device__ void step(int n, int slots) {
+    slot += n;
+    while (slot >= slots) slot -= slots, ++use;
+  }
+};
 
 // Which tokens the CTA's tile has: tiles count through the requests in order.
 __device__ void find_tile(const ExpandedArgs &a, int tile, int tokens, Small &sm) {
@@ -130,9 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   const ExpandedArgs &a = m.a;
   const uint32_t base = smem_addr(smem);
-  const int tile_bytes = m.panels * kPanel, v_bytes = m.v_panels * kPanel;
-  const uint32_t k_at = base + m.nsub * tile_bytes, v_at = k_at + m.nk * tile_bytes;
-  Small &sm = *reinterpret_cast<Small *>(smem + (v_at - base) + m.nv * v_bytes);
+  const int q_bytes = m.panels * kPanel;
+  const uint32_t ring_at = base + m.nsub * q_bytes;
+  Small &sm = *reinterpret_cast<Small *>(smem + m.nsub * q_bytes + m.slots * kPanel);
   volatile int *dead = &sm.dead;
   auto bar = [&](uint64_t &b) { return smem_addr(&b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -161,21 +182,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && warp < 8) sm.low[warp] = lo, sm.high[warp] = hi;
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
+    for (int s = 0; s < kMaxSlots; ++s) mbar_init(bar(sm.empty[s]), 1);
+    for (int s = 0; s < kTiles; ++s) {
       mbar_init(bar(sm.k_full[s]), 1);
-      mbar_init(bar(sm.k_empty[s]), 1);
       mbar_init(bar(sm.v_full[s]), 1);
-      mbar_init(bar(sm.v_empty[s]), 1);
+      mbar_init(bar(sm.v_ready[s]), 64);
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(bar(sm.q_full[j]), 1);
       mbar_init(bar(sm.s_full[j]), 1);
+      mbar_init(bar(sm.p_half[j]), kRows);
       mbar_init(bar(sm.p_full[j]), kRows);
       mbar_init(bar(sm.o_done[j]), 1);
     }
     mbar_init(bar(sm.issued), 1);
     sm.dead = 0;
-    for (int x = 0; x < 4; ++x) sm.bad[x] = 0;
+    sm.bad_key = INT32_MAX;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) tmem_alloc(smem_addr(&sm.tmem), 512);
@@ -198,65 +220,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = tmem + sub * kRows + lanes, o_at = tmem + 256 + sub * kRows + lanes;
     const int my_tiles = sub < m.nsub ? n_sub[sub] : 0;
     float l = 0.f, ref = kUnset;
-    for (int i = 0; i < n; ++i) {
+    const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+    for (int i = 0; i < my_tiles; ++i) {
       const int k0 = i * kRows;
-      const bool work = i < my_tiles;
       uint32_t raw[kRows];
-      float mx = -INFINITY;
-      if (work) {
-        mbar_wait(bar(sm.s_full[sub]), i & 1, dead);
-        if (i > 0) mbar_wait(bar(sm.o_done[sub]), (i - 1) & 1, dead);
-        __syncwarp();
-        tc_fence_after();
+      mbar_wait(bar(sm.s_full[sub]), i & 1, dead);
+      if (i > 0) mbar_wait(bar(sm.o_done[sub]), (i - 1) & 1, dead);
+      __syncwarp();
+      tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(raw, c * 32, s_at + c * 32);
-        tmem_wait_ld();
+      for (int c = 0; c < 4; ++c) tmem_ld32(raw, c * 32, s_at + c * 32);
+      tmem_wait_ld();
+      if (__any_sync(~0u, k0 + kRows > end)) {
+#pragma unroll
+        for (int x = 0; x < kRows; ++x)
+          if (k0 + x >= end) raw[x] = 0xff800000u;  // -inf
       }
-      if (k0 + kRows > low) {
-        // Some token does not see some key.  Two threads look over each value
-        // row; rows that are not finite are cleared and remembered.  (Threads
-        // without a token wait here for those with one: only then has the
-        // stage's earlier use come and gone.)
-        named_sync(1, 256);
-        mbar_wait(bar(sm.v_full[i % m.nv]), (i / m.nv) & 1, dead);
-        unsigned char *v = smem + (v_at - base) + (i % m.nv) * v_bytes + row * 128;
-        const int half = m.v_panels * 4;  // 16-byte chunks of half a row
-        bool odd = false;
-        for (int x = sub * half; x < (sub + 1) * half; ++x) {
-          Pack8<E> p;
-          p.u = *reinterpret_cast<const uint4 *>(v + (x >> 3) * kPanel + ((x & 7) << 4));
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float2 f = Elem<E>::to2(p.h[y]);
-            odd |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
-          }
-        }
-        if (odd) atomicOr(&sm.bad[row >> 5], 1u << (row & 31));
-        named_sync(1, 256);
-        const uint32_t bad = sm.bad[row >> 5];
-        if ((bad >> (row & 31)) & 1) {
-          for (int x = sub * half; x < (sub + 1) * half; ++x)
-            *reinterpret_cast<uint4 *>(v + (x >> 3) * kPanel + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_shared();
-        const bool any = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;
-        if (work) {
-#pragma unroll
-          for (int x = 0; x < kRows; ++x) {
-            if (k0 + x >= end) raw[x] = 0xff800000u;  // -inf
-            else if (any && ((sm.bad[x >> 5] >> (x & 31)) & 1)) raw[x] = 0x7fc00000u;
-          }
-        }
-        named_sync(1, 256);
-        if (threadIdx.x < 4) sm.bad[threadIdx.x] = 0;
-        // the next tile's scan writes after another pair of barriers has passed
-        named_sync(1, 256);
-      }
-      if (!work) continue;
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int x = 0; x < kRows; ++x) m4[x & 3] = fmaxf(m4[x & 3], __uint_as_float(raw[x]));
-      mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+      for (int x = 0; x < kRows; x += 2)
+        m4[x >> 1 & 3] = max3(m4[x >> 1 & 3], __uint_as_float(raw[x]), __uint_as_float(raw[x + 1]));
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
       if (__any_sync(~0u, mx - ref > kLag)) {
         const float now = fmaxf(ref, mx);
         const float f = exp2_fast(ref - now);
@@ -273,29 +257,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 less = make_float2(-ref, -ref);
+      float2 l2[2] = {};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t p[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
           const int at = c * 64 + 2 * x;
-          const float p0 = exp2_fast(fmaf(__uint_as_float(raw[at]), a.scale_log2, -ref));
-          const float p1 = exp2_fast(fmaf(__uint_as_float(raw[at + 1]), a.scale_log2, -ref));
-          l4[x & 3] += p0 + p1;
+          float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[at]), __uint_as_float(raw[at + 1])),
+                                scale2, less);
+          e.x = exp2_fast(e.x);
+          e.y = exp2_fast(e.y);
+          l2[x & 1] = __fadd2_rn(l2[x & 1], e);
           union {
             typename Elem<E>::T2 h;
             uint32_t u;
           } pk;
-          pk.h = Elem<E>::from2(p0, p1);
+          pk.h = Elem<E>::from2(e.x, e.y);
           p[x] = pk.u;
         }
         tmem_st32(s_at + c * 32, p, 0);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(c == 0 ? sm.p_half[sub] : sm.p_full[sub]));
       }
-      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(sm.p_full[sub]));
+      l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     }
     if (sub < m.nsub) {
       if (my_tiles > 0) {
@@ -303,7 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_after();
       }
-      if (*dead != 0) l = NAN;  // a wait was given up: no result
+      // A wait was given up, or a value row that the token sees is not finite
+      // (found before the MMAs that o_done stands for).
+      if (*dead != 0 || *static_cast<volatile int *>(&sm.bad_key) < end) l = NAN;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       E *out = static_cast<E *>(a.out) + t * a.ld_out_t + h * a.ld_out_h;
       for (int c = 0; c < a.dv; c += 16) {
@@ -337,116 +326,170 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
-    constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
-    constexpr uint32_t ds = mma_desc(bf16, false, false, kRows, kRows);
-    const uint32_t dp = mma_desc(bf16, false, true, kRows, a.dv);
-    const uint32_t leader = elect_leader();
-    const uint64_t q_desc = tile_desc(base, 16, 1024), k_desc = tile_desc(k_at, 16, 1024);
-    const uint64_t v_desc = tile_desc(v_at, kPanel, 1024);
-    auto scores = [&](int j, int i) {
-      uint64_t qd = q_desc + ((j * tile_bytes) >> 4), kd = k_desc + (((i % m.nk) * tile_bytes) >> 4);
-      const uint32_t d = tmem + j * kRows;
-      bool more = false;
-      for (int p = 0; p < m.panels; ++p, qd += kPanel >> 4, kd += kPanel >> 4) {
-        const int cols = p < m.nope_panels ? a.dn - p * 64 : a.dr;
-        if (cols >= 64) {
-          mma_ss(leader, d, qd, kd, ds, more);
-          mma_ss(leader, d, qd + 2, kd + 2, ds, true);
-          mma_ss(leader, d, qd + 4, kd + 4, ds, true);
-          mma_ss(leader, d, qd + 6, kd + 6, ds, true);
-        } else {
-          for (int x = 0; x < cols >> 4; ++x)
-            mma_ss(leader, d, qd + 2 * x, kd + 2 * x, ds, more || x > 0);
+    if (elect_leader()) {
+      constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
+      constexpr uint32_t ds = mma_desc(bf16, false, false, kRows, kRows);
+      const uint32_t dp_full = mma_desc(bf16, false, true, kRows, 64);
+      const uint32_t dp_last = mma_desc(bf16, false, true, kRows, a.dv - (m.v_panels - 1) * 64);
+      const uint64_t q_desc = tile_desc(base, 16, 1024), k_desc = tile_desc(ring_at, 16, 1024);
+      const uint64_t v_desc = tile_desc(ring_at, kPanel, 1024);
+      const int per_tile = m.panels + m.v_panels;
+      Ring kr, vr;  // of the next scores' and the next values' tile
+      vr.step(m.panels, m.slots);
+      auto scores = [&](int j) {
+        uint64_t qd = q_desc + ((j * q_bytes) >> 4);
+        const uint32_t d = tmem + j * kRows;
+        Ring r = kr;
+        for (int p = 0; p < m.panels; ++p, qd += kPanel >> 4, r.step(1, m.slots)) {
+          const uint64_t kd = k_desc + (r.slot * kPanel >> 4);
+          const int cols = p < m.nope_panels ? a.dn - p * 64 : a.dr;
+          if (cols >= 64) {
+            mma_ss(d, qd, kd, ds, p > 0);
+            mma_ss(d, qd + 2, kd + 2, ds, true);
+            mma_ss(d, qd + 4, kd + 4, ds, true);
+            mma_ss(d, qd + 6, kd + 6, ds, true);
+          } else {
+            for (int x = 0; x < cols >> 4; ++x)
+              mma_ss(d, qd + 2 * x, kd + 2 * x, ds, p > 0 || x > 0);
+          }
         }
-        more = true;
-      }
-      tc_commit(leader, bar(sm.s_full[j]));
-    };
-    auto values = [&](int j, int i) {
-      const uint64_t vd = v_desc + (((i % m.nv) * v_bytes) >> 4);
-      const uint32_t d = tmem + 256 + j * kRows, p = tmem + j * kRows;
+        tc_commit(bar(sm.s_full[j]));
+      };
+      // One half of the keys of a tile: weights x values, a panel's columns at a
+      // time (the ring may have the two panels apart).
+      auto values = [&](int j, int i, int half) {
+        Ring r = vr;
+        for (int p = 0; p < m.v_panels; ++p, r.step(1, m.slots)) {
+          const uint64_t vd = v_desc + (r.slot * kPanel >> 4) + half * 512;
+          const uint32_t d = tmem + 256 + j * kRows + p * 64, w = tmem + j * kRows + half * 32;
+          const uint32_t dp = p == m.v_panels - 1 ? dp_last : dp_full;
 #pragma unroll
-      for (int x = 0; x < kRows / 16; ++x)
-        mma_ts(leader, d, p + x * 8, vd + x * 128, dp, i > 0 || x > 0);
-      tc_commit(leader, bar(sm.o_done[j]));
-    };
-    for (int i = -1; i < n; ++i) {
-      // values of tile i, scores of tile i + 1, the sub-tiles in turn
-      for (int j = 0; j < m.nsub; ++j) {
-        if (i >= 0 && i < n_sub[j]) {
-          mbar_wait(bar(sm.v_full[i % m.nv]), (i / m.nv) & 1, dead);
-          mbar_wait(bar(sm.p_full[j]), i & 1, dead);
-          __syncwarp();
-          tc_fence_after();
-          values(j, i);
+          for (int x = 0; x < 4; ++x)
+            mma_ts(d, w + x * 8, vd + x * 128, dp, i > 0 || half > 0 || x > 0);
         }
-        if (i + 1 < n_sub[j]) {
-          if (i < 0) mbar_wait(bar(sm.q_full[j]), 0, dead);
-          mbar_wait(bar(sm.k_full[(i + 1) % m.nk]), ((i + 1) / m.nk) & 1, dead);
-          __syncwarp();
-          tc_fence_after();
-          scores(j, i + 1);
+      };
+      auto give_back = [&](Ring r, int panels) {
+        for (int p = 0; p < panels; ++p, r.step(1, m.slots)) tc_commit(bar(sm.empty[r.slot]));
+      };
+      for (int i = -1; i < n; ++i) {
+        // values of tile i, scores of tile i + 1, the sub-tiles in turn
+        for (int j = 0; j < m.nsub; ++j) {
+          if (i >= 0 && i < n_sub[j]) {
+            mbar_wait(bar(sm.p_half[j]), i & 1, dead);
+            if (j == 0 || i >= n_sub[0]) mbar_wait(bar(sm.v_ready[i % kTiles]), (i / kTiles) & 1, dead);
+            tc_fence_after();
+            values(j, i, 0);
+            mbar_wait(bar(sm.p_full[j]), i & 1, dead);
+            tc_fence_after();
+            values(j, i, 1);
+            tc_commit(bar(sm.o_done[j]));
+          }
+          if (i + 1 < n_sub[j]) {
+            if (i < 0) mbar_wait(bar(sm.q_full[j]), 0, dead);
+            mbar_wait(bar(sm.k_full[(i + 1) % kTiles]), ((i + 1) / kTiles) & 1, dead);
+            tc_fence_after();
+            scores(j);
+          }
+        }
+        if (i >= 0) {
+          give_back(vr, m.v_panels);
+          vr.step(per_tile, m.slots);
+        }
+        if (i + 1 < n) {
+          give_back(kr, m.panels);
+          kr.step(per_tile, m.slots);
         }
       }
-      if (i >= 0) tc_commit(leader, bar(sm.v_empty[i % m.nv]));
-      if (i + 1 < n) tc_commit(leader, bar(sm.k_empty[(i + 1) % m.nk]));
+      tc_commit(bar(sm.issued));
+      mbar_drain(bar(sm.issued), 0);
     }
-    tc_commit(leader, bar(sm.issued));
-    mbar_drain(bar(sm.issued), 0);
+    __syncwarp();
   } else if (warp == 9) {
     // -------------------------------------------------------------------- loads
     const uint32_t leader = elect_leader();
     if (n > 0)
       for (int j = 0; j < m.nsub; ++j) {
-        if (lane == 0) mbar_expect(bar(sm.q_full[j]), tile_bytes);
+        if (lane == 0) mbar_expect(bar(sm.q_full[j]), q_bytes);
         __syncwarp();
         for (int p = 0; p < m.panels; ++p)
-          tma_box3(leader, base + j * tile_bytes + p * kPanel, &m.q,
+          tma_box3(leader, base + j * q_bytes + p * kPanel, &m.q,
                    p < m.nope_panels ? p * 64 : a.dn, h, t0 + j * kRows, bar(sm.q_full[j]));
       }
+    Ring r;
     for (int i = 0; i < n; ++i) {
-      const int ks = i % m.nk, vs = i % m.nv, key = key0 + i * kRows;
-      if (i >= m.nk) mbar_wait(bar(sm.k_empty[ks]), (i / m.nk - 1) & 1, dead);
-      __syncwarp();
-      if (lane == 0) mbar_expect(bar(sm.k_full[ks]), tile_bytes);
-      __syncwarp();
-      for (int p = 0; p < m.panels; ++p) {
-        const uint32_t dst = k_at + ks * tile_bytes + p * kPanel;
-        if (p < m.nope_panels) tma_box3(leader, dst, &m.k, p * 64, h, key, bar(sm.k_full[ks]));
-        else tma_box(leader, dst, &m.tail, 0, key, bar(sm.k_full[ks]));
+      const int key = key0 + i * kRows;
+      const uint32_t k_full = bar(sm.k_full[i % kTiles]), v_full = bar(sm.v_full[i % kTiles]);
+      for (int p = 0; p < m.panels + m.v_panels; ++p, r.step(1, m.slots)) {
+        if (r.use > 0) mbar_wait(bar(sm.empty[r.slot]), (r.use - 1) & 1, dead);
+        __syncwarp();
+        const uint32_t dst = ring_at + r.slot * kPanel;
+        if (lane == 0) {
+          if (p == 0) mbar_expect(k_full, m.panels * kPanel);
+          if (p == m.panels) mbar_expect(v_full, m.v_panels * kPanel);
+        }
+        __syncwarp();
+        if (p < m.nope_panels) tma_box3(leader, dst, &m.k, p * 64, h, key, k_full);
+        else if (p < m.panels) tma_box(leader, dst, &m.tail, 0, key, k_full);
+        else tma_box3(leader, dst, &m.v, (p - m.panels) * 64, h, key, v_full);
       }
-      if (i >= m.nv) mbar_wait(bar(sm.v_empty[vs]), (i / m.nv - 1) & 1, dead);
-      __syncwarp();
-      if (lane == 0) mbar_expect(bar(sm.v_full[vs]), v_bytes);
-      __syncwarp();
-      for (int p = 0; p < m.v_panels; ++p)
-        tma_box3(leader, v_at + vs * v_bytes + p * kPanel, &m.v, p * 64, h, key, bar(sm.v_full[vs]));
-      __syncwarp();
     }
     if (n > 0)
       for (int j = 0; j < m.nsub; ++j) mbar_drain(bar(sm.q_full[j]), 0);
-    for (int i = max(0, n - 2); i < n; ++i) {
-      if (i >= n - m.nk) mbar_drain(bar(sm.k_full[i % m.nk]), (i / m.nk) & 1);
-      if (i >= n - m.nv) mbar_drain(bar(sm.v_full[i % m.nv]), (i / m.nv) & 1);
+    for (int i = max(0, n - kTiles); i < n; ++i) {
+      mbar_drain(bar(sm.k_full[i % kTiles]), (i / kTiles) & 1);
+      mbar_drain(bar(sm.v_full[i % kTiles]), (i / kTiles) & 1);
+    }
+  } else {
+    // --------------------------------------------------------------- value rows
+    Ring r;
+    for (int i = 0; i < n; ++i) {
+      r.step(m.panels, m.slots);
+      const int k0 = i * kRows;
+      mbar_wait(bar(sm.v_full[i % kTiles]), (i / kTiles) & 1, dead);
+      for (int p = 0; p < m.v_panels; ++p, r.step(1, m.slots)) {
+        if (k0 + kRows > low) {
+          // Some token does not see some key.  A row's chunks are read from
+          // another one on for every lane, clear of bank conflicts.
+          for (int y = threadIdx.x - 320; y < kRows; y += 64) {
+            unsigned char *v = smem + (ring_at - base) + r.slot * kPanel + y * 128;
+            typename Elem<E>::T2 sum = Elem<E>::from2(0.f, 0.f), zero = sum;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              Pack8<E> c;
+              c.u = *reinterpret_cast<const uint4 *>(v + ((x ^ (y & 7)) << 4));
+#pragma unroll
+              for (int z = 0; z < 4; ++z) sum = __hfma2(c.h[z], zero, sum);  // NaN: not finite
+            }
+            const float2 f = Elem<E>::to2(sum);
+            if (!(f.x == 0.f && f.y == 0.f)) {
+              for (int x = 0; x < 8; ++x)
+                *reinterpret_cast<uint4 *>(v + (x << 4)) = make_uint4(0, 0, 0, 0);
+              atomicMin(&sm.bad_key, k0 + y);
+            }
+          }
+          fence_async_shared();
+        }
+      }
+      mbar_arrive(bar(sm.v_ready[i % kTiles]));
     }
   }
   __syncthreads();
   if (warp == 8) tmem_free(tmem, 512);
 }
 
-// The smallest request of stages and sub-tiles that fits, largest first.
+// Sub-tiles and ring that fit into shared memory.
 bool layout(const ExpandedArgs &a, ExpandedMma &m, int &smem) {
   m.nope_panels = (a.dn + 63) / 64;
   m.panels = m.nope_panels + (a.dr > 0 ? 1 : 0);
   m.v_panels = (a.dv + 63) / 64;
   const int limit = 227 * 1024;
-  for (m.nsub = 2; m.nsub >= 1; --m.nsub)
-    for (int s = 3; s >= 1; --s) {
-      m.nk = s >= 2 ? 2 : 1;
-      m.nv = s >= 3 ? 2 : 1;
-      smem = (m.nsub + m.nk) * m.panels * kPanel + m.nv * m.v_panels * kPanel + kSmall;
-      if (smem <= limit) return true;
-    }
+  for (m.nsub = 2; m.nsub >= 1; --m.nsub) {
+    m.slots = (limit - kSmall) / kPanel - m.nsub * m.panels;
+    if (m.slots > kMaxSlots) m.slots = kMaxSlots;
+    smem = (m.nsub * m.panels + m.slots) * kPanel + kSmall;
+    // the values of a tile and the keys of the next one are in use together
+    if (m.slots >= m.panels + m.v_panels) return true;
+  }
   return false;
 }
 

@@ -569,82 +569,84 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
     }
   } else if (warp == 4) {
     // -------------------------------------------------------------- MMA issue
-    const uint32_t leader = elect_leader();
-    constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
-    constexpr uint32_t dq = mma_desc(bf16, false, false, kTile, N);
-    constexpr uint32_t dp = mma_desc(bf16, true, true, 128, N);
-    const int ksteps = (a.D + 15) / 16;
-    // Descriptors hold addresses in units of 16 bytes: steps are added to them.
-    const uint64_t k_desc = tile_desc(base, 16, 1024), q_desc = tile_desc(q_at, 16, 1024);
-    const uint64_t v_desc = tile_desc(base, kPanel, 1024), p_desc = tile_desc(p_at, kPanel, 1024);
-    Cursor cq(w), cp(w);  // the next tile of the scores and of the values
-    const int ksteps0 = min(m.np0 * 4, ksteps), nb0 = m.np0 < m.np ? m.np0 / 2 : m.nb;
-    int iq = 0, ip = 0, q_stage = 0, q_use = 0, p_stage = 0, seg = 0;
-    bool q_half = false;  // the scores' first half is issued
-    uint64_t kd = 0, qd = 0;
-    auto scores = [&](int ks, int end) {
-      const uint32_t s_at = tmem + (iq & 1) * N;
-      for (; ks + 4 <= end; ks += 4, kd += kPanel >> 4, qd += q_panel >> 4) {
-        mma_ss(leader, s_at, kd, qd, dq, ks > 0);
-        mma_ss(leader, s_at, kd + 2, qd + 2, dq, true);
-        mma_ss(leader, s_at, kd + 4, qd + 4, dq, true);
-        mma_ss(leader, s_at, kd + 6, qd + 6, dq, true);
-      }
-      for (; ks < end; ++ks, kd += 2, qd += 2) mma_ss(leader, s_at, kd, qd, dq, ks > 0);
-    };
-    long long t0 = clock64();
-    while (cp.more()) {
-      bool moved = false;
-      if (cq.more() && !q_half && warp_poll(bar(sm.full[q_stage][0]), q_use & 1) &&
-          (iq < 2 || warp_poll(bar(sm.s_empty[iq & 1]), ((iq >> 1) - 1) & 1)) &&
-          (!cq.first() || warp_poll(bar(sm.q_full), seg & 1))) {
-        tc_fence_after();
-        kd = k_desc + ((q_stage * stage_bytes) >> 4);
-        qd = q_desc;
-        scores(0, ksteps0);
-        q_half = moved = true;
-      }
-      if (q_half && (m.np0 == m.np || warp_poll(bar(sm.full[q_stage][1]), q_use & 1))) {
-        tc_fence_after();
-        scores(ksteps0, ksteps);
-        tc_commit(leader, bar(sm.s_full[iq & 1]));
-        if (cq.last()) {
-          tc_commit(leader, bar(sm.q_empty));
-          ++seg;
+    if (elect_leader()) {
+      constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
+      constexpr uint32_t dq = mma_desc(bf16, false, false, kTile, N);
+      constexpr uint32_t dp = mma_desc(bf16, true, true, 128, N);
+      const int ksteps = (a.D + 15) / 16;
+      // Descriptors hold addresses in units of 16 bytes: steps are added to them.
+      const uint64_t k_desc = tile_desc(base, 16, 1024), q_desc = tile_desc(q_at, 16, 1024);
+      const uint64_t v_desc = tile_desc(base, kPanel, 1024), p_desc = tile_desc(p_at, kPanel, 1024);
+      Cursor cq(w), cp(w);  // the next tile of the scores and of the values
+      const int ksteps0 = min(m.np0 * 4, ksteps), nb0 = m.np0 < m.np ? m.np0 / 2 : m.nb;
+      int iq = 0, ip = 0, q_stage = 0, q_use = 0, p_stage = 0, seg = 0;
+      bool q_half = false;  // the scores' first half is issued
+      uint64_t kd = 0, qd = 0;
+      auto scores = [&](int ks, int end) {
+        const uint32_t s_at = tmem + (iq & 1) * N;
+        for (; ks + 4 <= end; ks += 4, kd += kPanel >> 4, qd += q_panel >> 4) {
+          mma_ss(s_at, kd, qd, dq, ks > 0);
+          mma_ss(s_at, kd + 2, qd + 2, dq, true);
+          mma_ss(s_at, kd + 4, qd + 4, dq, true);
+          mma_ss(s_at, kd + 6, qd + 6, dq, true);
         }
-        cq.step(piece);
-        ++iq;
-        if (++q_stage == m.nst) q_stage = 0, ++q_use;
-        q_half = false;
-        moved = true;
-      }
-      if (ip < iq && warp_poll(bar(sm.p_full), ip & 1)) {
-        tc_fence_after();
-        uint64_t vd = v_desc + ((p_stage * stage_bytes) >> 4);
-        const bool more = !cp.first();
-        for (int b = 0; b < m.nb; ++b, vd += (2 * kPanel) >> 4) {
-          mma_ss(leader, o_at + b * N, vd, p_desc, dp, more);
-          mma_ss(leader, o_at + b * N, vd + 128, p_desc + 128, dp, true);
-          mma_ss(leader, o_at + b * N, vd + 256, p_desc + 256, dp, true);
-          mma_ss(leader, o_at + b * N, vd + 384, p_desc + 384, dp, true);
-          if (b + 1 == nb0) tc_commit(leader, bar(sm.empty[p_stage][0]));
+        for (; ks < end; ++ks, kd += 2, qd += 2) mma_ss(s_at, kd, qd, dq, ks > 0);
+      };
+      long long t0 = clock64();
+      while (cp.more()) {
+        bool moved = false;
+        if (cq.more() && !q_half && mbar_poll(bar(sm.full[q_stage][0]), q_use & 1) &&
+            (iq < 2 || mbar_poll(bar(sm.s_empty[iq & 1]), ((iq >> 1) - 1) & 1)) &&
+            (!cq.first() || mbar_poll(bar(sm.q_full), seg & 1))) {
+          tc_fence_after();
+          kd = k_desc + ((q_stage * stage_bytes) >> 4);
+          qd = q_desc;
+          scores(0, ksteps0);
+          q_half = moved = true;
         }
-        if (m.np0 < m.np) tc_commit(leader, bar(sm.empty[p_stage][1]));
-        tc_commit(leader, bar(sm.o_done));
-        cp.step(piece);
-        ++ip;
-        if (++p_stage == m.nst) p_stage = 0;
-        moved = true;
+        if (q_half && (m.np0 == m.np || mbar_poll(bar(sm.full[q_stage][1]), q_use & 1))) {
+          tc_fence_after();
+          scores(ksteps0, ksteps);
+          tc_commit(bar(sm.s_full[iq & 1]));
+          if (cq.last()) {
+            tc_commit(bar(sm.q_empty));
+            ++seg;
+          }
+          cq.step(piece);
+          ++iq;
+          if (++q_stage == m.nst) q_stage = 0, ++q_use;
+          q_half = false;
+          moved = true;
+        }
+        if (ip < iq && mbar_poll(bar(sm.p_full), ip & 1)) {
+          tc_fence_after();
+          uint64_t vd = v_desc + ((p_stage * stage_bytes) >> 4);
+          const bool more = !cp.first();
+          for (int b = 0; b < m.nb; ++b, vd += (2 * kPanel) >> 4) {
+            mma_ss(o_at + b * N, vd, p_desc, dp, more);
+            mma_ss(o_at + b * N, vd + 128, p_desc + 128, dp, true);
+            mma_ss(o_at + b * N, vd + 256, p_desc + 256, dp, true);
+            mma_ss(o_at + b * N, vd + 384, p_desc + 384, dp, true);
+            if (b + 1 == nb0) tc_commit(bar(sm.empty[p_stage][0]));
+          }
+          if (m.np0 < m.np) tc_commit(bar(sm.empty[p_stage][1]));
+          tc_commit(bar(sm.o_done));
+          cp.step(piece);
+          ++ip;
+          if (++p_stage == m.nst) p_stage = 0;
+          moved = true;
+        }
+        if (moved) {
+          t0 = clock64();
+        } else if (*dead != 0 || clock64() - t0 > kWaitClocks) {
+          *dead = 1;
+          break;
+        }
       }
-      if (moved) {
-        t0 = clock64();
-      } else if (__any_sync(~0u, *dead != 0 || clock64() - t0 > kWaitClocks)) {
-        *dead = 1;
-        break;
-      }
+      tc_commit(bar(sm.issued));
+      mbar_drain(bar(sm.issued), 0);
     }
-    tc_commit(leader, bar(sm.issued));
-    mbar_drain(bar(sm.issued), 0);
+    __syncwarp();
   } else if (BOX && warp < 7) {
     // ------------------------------------------------------ key rows, in boxes
     // Warp 5 fills the stages' first halves, warp 6 the second ones.

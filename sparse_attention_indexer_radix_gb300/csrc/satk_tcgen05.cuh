@@ -53,9 +53,6 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity) {
-  return __all_sync(~0u, mbar_poll(bar, parity));
-}
 // Waits until the barrier's phase of this parity has completed.
 __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
   if (mbar_test(bar, parity)) return;
@@ -182,11 +179,11 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// The MMAs and their commits are written for a whole, converged warp of which
-// one lane issues (`leader`, the same one every time): under warp-uniform
-// control flow the descriptors stay in uniform registers, where the instruction
-// wants them.  Issued from a branch of one lane instead, each MMA cost about 90
-// cycles of moving its operands there.
+// One lane of a whole converged warp, the same one every time.  MMAs and their
+// commits are issued from a branch on it: the compiler knows that such a branch
+// has one lane and keeps descriptors in uniform registers, where the instruction
+// wants them.  (From a branch on a lane number each MMA costs 20 to 60 cycles
+// of moving its operands there.)
 __device__ __forceinline__ uint32_t elect_leader() {
   uint32_t leader;
   asm volatile(
@@ -195,13 +192,10 @@ __device__ __forceinline__ uint32_t elect_leader() {
   return leader;
 }
 
-// The barrier's phase gets one arrival when the elected lane's MMAs so far are done.
-__device__ __forceinline__ void tc_commit(uint32_t leader, uint32_t bar) {
+// The barrier's phase gets one arrival when this thread's MMAs so far are done.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile(
-      "{\n.reg .pred e;\nsetp.ne.u32 e, %1, 0;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          bar),
-      "r"(leader)
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
       : "memory");
 }
 
@@ -217,22 +211,21 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lbo, uint3
   return (static_cast<uint64_t>(addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lbo >> 4) << 16) |
          (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b,
-                                       uint32_t desc, bool accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
+                                       bool accumulate) {
   asm volatile(
-      "{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 e, %5, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u), "r"(leader)
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
-
 // The same with A in tensor memory: lane = row, a column holds two K values.
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b,
-                                       uint32_t desc, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc,
+                                       bool accumulate) {
   asm volatile(
-      "{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 e, %5, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u), "r"(leader)
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(desc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 
