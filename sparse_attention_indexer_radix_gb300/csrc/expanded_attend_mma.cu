@@ -25,7 +25,9 @@
 // that do see it get NaN.
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax and results of the sub-tiles,
-// warp 8 issues the MMAs, warp 9 the loads, warps 10-11 look over value rows.
+// warps 8 and 9 issue the MMAs of one sub-tile each (what one of them does
+// between MMAs would otherwise leave the tensor core idle: 250 us against 186 for
+// the 4096 x 8192 chunk), warp 10 the loads, warp 11 looks over value rows.
 // Tiles of the last tokens, which see most keys, start first.
 #include <cuda.h>
 #include <type_traits>
@@ -58,8 +60,8 @@ struct ExpandedMma {
 };
 
 struct Small {
-  uint64_t q_full[2], k_full[kTiles], v_full[kTiles], empty[kMaxSlots];
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], v_ready[kTiles], issued;
+  uint64_t q_full[2], k_full[kTiles], v_full[kTiles], k_empty[kTiles], v_empty[kTiles];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], v_ready[kTiles], issued[2];
   int bad_key;           // the first key with a value row that is not finite
   int scan[12], low[8], high[8];
   int place[4];          // request's first key, its keys, first token, tokens
@@ -73,15 +75,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-
-// A place in the ring of panels.
-struct Ring {
-  int slot = 0, use = 0;
-  __device__ void step(int n, int slots) {
-    slot += n;
-    while (slot >= slots) slot -= slots, ++use;
-  }
-};
 
 // Which tokens the CTA's tile has: tiles count through the requests in order.
 __device__ void find_tile(const ExpandedArgs &a, int tile, int tokens, Small &sm) {
@@ -182,11 +175,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && warp < 8) sm.low[warp] = lo, sm.high[warp] = hi;
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxSlots; ++s) mbar_init(bar(sm.empty[s]), 1);
     for (int s = 0; s < kTiles; ++s) {
+      mbar_init(bar(sm.k_empty[s]), m.nsub);
+      mbar_init(bar(sm.v_empty[s]), m.nsub);
       mbar_init(bar(sm.k_full[s]), 1);
       mbar_init(bar(sm.v_full[s]), 1);
-      mbar_init(bar(sm.v_ready[s]), 64);
+      mbar_init(bar(sm.v_ready[s]), 32);
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(bar(sm.q_full[j]), 1);
@@ -195,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(sm.p_full[j]), kRows);
       mbar_init(bar(sm.o_done[j]), 1);
     }
-    mbar_init(bar(sm.issued), 1);
+    mbar_init(bar(sm.issued[0]), 1);
+    mbar_init(bar(sm.issued[1]), 1);
     sm.dead = 0;
     sm.bad_key = INT32_MAX;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -324,87 +319,95 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mine && a.lse != nullptr)
         a.lse[static_cast<int64_t>(t) * a.H + h] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
     }
-  } else if (warp == 8) {
+  } else if (warp < 10) {
     // ---------------------------------------------------------------- MMA issue
-    if (elect_leader()) {
+    const int j = warp - 8;
+    if (j < m.nsub && elect_leader()) {
       constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
       constexpr uint32_t ds = mma_desc(bf16, false, false, kRows, kRows);
       const uint32_t dp_full = mma_desc(bf16, false, true, kRows, 64);
       const uint32_t dp_last = mma_desc(bf16, false, true, kRows, a.dv - (m.v_panels - 1) * 64);
-      const uint64_t q_desc = tile_desc(base, 16, 1024), k_desc = tile_desc(ring_at, 16, 1024);
-      const uint64_t v_desc = tile_desc(ring_at, kPanel, 1024);
-      const int per_tile = m.panels + m.v_panels;
-      Ring kr, vr;  // of the next scores' and the next values' tile
-      vr.step(m.panels, m.slots);
-      auto scores = [&](int j) {
-        uint64_t qd = q_desc + ((j * q_bytes) >> 4);
-        const uint32_t d = tmem + j * kRows;
-        Ring r = kr;
-        for (int p = 0; p < m.panels; ++p, qd += kPanel >> 4, r.step(1, m.slots)) {
-          const uint64_t kd = k_desc + (r.slot * kPanel >> 4);
+      const uint64_t q_desc = tile_desc(base + j * q_bytes, 16, 1024);
+      const uint64_t k_desc = tile_desc(ring_at, 16, 1024), v_desc = tile_desc(ring_at, kPanel, 1024);
+      const uint32_t s_col = tmem + j * kRows, o_col = tmem + 256 + j * kRows;
+      const int per_tile = m.panels + m.v_panels, mine_n = n_sub[j];
+      const uint32_t s_full = bar(sm.s_full[j]), o_done = bar(sm.o_done[j]);
+      const uint32_t p_half = bar(sm.p_half[j]), p_full = bar(sm.p_full[j]);
+      int k_slot = 0, v_slot = m.panels;  // of the next scores' and the next values' tile
+      auto scores = [&]() {
+        uint64_t qd = q_desc;
+        int slot = k_slot;
+        for (int p = 0; p < m.panels; ++p, qd += kPanel >> 4) {
+          const uint64_t kd = k_desc + (slot * kPanel >> 4);
           const int cols = p < m.nope_panels ? a.dn - p * 64 : a.dr;
           if (cols >= 64) {
-            mma_ss(d, qd, kd, ds, p > 0);
-            mma_ss(d, qd + 2, kd + 2, ds, true);
-            mma_ss(d, qd + 4, kd + 4, ds, true);
-            mma_ss(d, qd + 6, kd + 6, ds, true);
+            mma_ss(s_col, qd, kd, ds, p > 0);
+            mma_ss(s_col, qd + 2, kd + 2, ds, true);
+            mma_ss(s_col, qd + 4, kd + 4, ds, true);
+            mma_ss(s_col, qd + 6, kd + 6, ds, true);
           } else {
             for (int x = 0; x < cols >> 4; ++x)
-              mma_ss(d, qd + 2 * x, kd + 2 * x, ds, p > 0 || x > 0);
+              mma_ss(s_col, qd + 2 * x, kd + 2 * x, ds, p > 0 || x > 0);
           }
+          if (++slot == m.slots) slot = 0;
         }
-        tc_commit(bar(sm.s_full[j]));
       };
       // One half of the keys of a tile: weights x values, a panel's columns at a
       // time (the ring may have the two panels apart).
-      auto values = [&](int j, int i, int half) {
-        Ring r = vr;
-        for (int p = 0; p < m.v_panels; ++p, r.step(1, m.slots)) {
-          const uint64_t vd = v_desc + (r.slot * kPanel >> 4) + half * 512;
-          const uint32_t d = tmem + 256 + j * kRows + p * 64, w = tmem + j * kRows + half * 32;
+      auto values = [&](int half, bool more) {
+        int slot = v_slot;
+        for (int p = 0; p < m.v_panels; ++p) {
+          const uint64_t vd = v_desc + (slot * kPanel >> 4) + half * 512;
+          const uint32_t d = o_col + p * 64, w = s_col + half * 32;
           const uint32_t dp = p == m.v_panels - 1 ? dp_last : dp_full;
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            mma_ts(d, w + x * 8, vd + x * 128, dp, i > 0 || half > 0 || x > 0);
+          mma_ts(d, w, vd, dp, more);
+          mma_ts(d, w + 8, vd + 128, dp, true);
+          mma_ts(d, w + 16, vd + 256, dp, true);
+          mma_ts(d, w + 24, vd + 384, dp, true);
+          if (++slot == m.slots) slot = 0;
         }
       };
-      auto give_back = [&](Ring r, int panels) {
-        for (int p = 0; p < panels; ++p, r.step(1, m.slots)) tc_commit(bar(sm.empty[r.slot]));
-      };
+      if (mine_n > 0) mbar_wait(bar(sm.q_full[j]), 0, dead);
       for (int i = -1; i < n; ++i) {
-        // values of tile i, scores of tile i + 1, the sub-tiles in turn
-        for (int j = 0; j < m.nsub; ++j) {
-          if (i >= 0 && i < n_sub[j]) {
-            mbar_wait(bar(sm.p_half[j]), i & 1, dead);
-            if (j == 0 || i >= n_sub[0]) mbar_wait(bar(sm.v_ready[i % kTiles]), (i / kTiles) & 1, dead);
-            tc_fence_after();
-            values(j, i, 0);
-            mbar_wait(bar(sm.p_full[j]), i & 1, dead);
-            tc_fence_after();
-            values(j, i, 1);
-            tc_commit(bar(sm.o_done[j]));
-          }
-          if (i + 1 < n_sub[j]) {
-            if (i < 0) mbar_wait(bar(sm.q_full[j]), 0, dead);
-            mbar_wait(bar(sm.k_full[(i + 1) % kTiles]), ((i + 1) / kTiles) & 1, dead);
-            tc_fence_after();
-            scores(j);
-          }
-        }
+        // values of tile i, scores of tile i + 1
+        const int now = i & (kTiles - 1), next = (i + 1) & (kTiles - 1);
+        // (A sub-tile that is done waits for the tile too before it gives it back.)
         if (i >= 0) {
-          give_back(vr, m.v_panels);
-          vr.step(per_tile, m.slots);
+          mbar_wait(bar(sm.v_ready[now]), (i / kTiles) & 1, dead);
+          if (i < mine_n) {
+            mbar_wait(p_half, i & 1, dead);
+            tc_fence_after();
+            values(0, i > 0);
+            mbar_wait(p_full, i & 1, dead);
+            tc_fence_after();
+            values(1, true);
+            tc_commit(o_done);
+            tc_commit(bar(sm.v_empty[now]));
+          } else {
+            mbar_arrive(bar(sm.v_empty[now]));
+          }
+          v_slot += per_tile;
+          if (v_slot >= m.slots) v_slot -= m.slots;
         }
         if (i + 1 < n) {
-          give_back(kr, m.panels);
-          kr.step(per_tile, m.slots);
+          mbar_wait(bar(sm.k_full[next]), ((i + 1) / kTiles) & 1, dead);
+          if (i + 1 < mine_n) {
+            tc_fence_after();
+            scores();
+            tc_commit(s_full);
+            tc_commit(bar(sm.k_empty[next]));
+          } else {
+            mbar_arrive(bar(sm.k_empty[next]));
+          }
+          k_slot += per_tile;
+          if (k_slot >= m.slots) k_slot -= m.slots;
         }
       }
-      tc_commit(bar(sm.issued));
-      mbar_drain(bar(sm.issued), 0);
+      tc_commit(bar(sm.issued[j]));
+      mbar_drain(bar(sm.issued[j]), 0);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 10) {
     // -------------------------------------------------------------------- loads
     const uint32_t leader = elect_leader();
     if (n > 0)
@@ -415,14 +418,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_box3(leader, base + j * q_bytes + p * kPanel, &m.q,
                    p < m.nope_panels ? p * 64 : a.dn, h, t0 + j * kRows, bar(sm.q_full[j]));
       }
-    Ring r;
+    // The panel that had a slot before: `last` counts through them in order.
+    const int per_tile = m.panels + m.v_panels;
+    int slot = 0, last_tile = 0, last = -m.slots;
     for (int i = 0; i < n; ++i) {
       const int key = key0 + i * kRows;
       const uint32_t k_full = bar(sm.k_full[i % kTiles]), v_full = bar(sm.v_full[i % kTiles]);
-      for (int p = 0; p < m.panels + m.v_panels; ++p, r.step(1, m.slots)) {
-        if (r.use > 0) mbar_wait(bar(sm.empty[r.slot]), (r.use - 1) & 1, dead);
+      for (int p = 0; p < per_tile; ++p) {
+        if (last == 0 || last == m.panels)
+          mbar_wait(bar(last == 0 ? sm.k_empty[last_tile % kTiles] : sm.v_empty[last_tile % kTiles]),
+                    (last_tile / kTiles) & 1, dead);
+        if (++last == per_tile) last = 0, ++last_tile;
         __syncwarp();
-        const uint32_t dst = ring_at + r.slot * kPanel;
+        const uint32_t dst = ring_at + slot * kPanel;
+        if (++slot == m.slots) slot = 0;
         if (lane == 0) {
           if (p == 0) mbar_expect(k_full, m.panels * kPanel);
           if (p == m.panels) mbar_expect(v_full, m.v_panels * kPanel);
@@ -441,17 +450,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // --------------------------------------------------------------- value rows
-    Ring r;
+    int slot = 0;
     for (int i = 0; i < n; ++i) {
-      r.step(m.panels, m.slots);
+      slot += m.panels;
+      if (slot >= m.slots) slot -= m.slots;
       const int k0 = i * kRows;
       mbar_wait(bar(sm.v_full[i % kTiles]), (i / kTiles) & 1, dead);
-      for (int p = 0; p < m.v_panels; ++p, r.step(1, m.slots)) {
+      for (int p = 0; p < m.v_panels; ++p) {
+        unsigned char *panel = smem + (ring_at - base) + slot * kPanel;
+        if (++slot == m.slots) slot = 0;
         if (k0 + kRows > low) {
           // Some token does not see some key.  A row's chunks are read from
           // another one on for every lane, clear of bank conflicts.
-          for (int y = threadIdx.x - 320; y < kRows; y += 64) {
-            unsigned char *v = smem + (ring_at - base) + r.slot * kPanel + y * 128;
+          for (int y = lane; y < kRows; y += 32) {
+            unsigned char *v = panel + y * 128;
             typename Elem<E>::T2 sum = Elem<E>::from2(0.f, 0.f), zero = sum;
 #pragma unroll
             for (int x = 0; x < 8; ++x) {

@@ -580,6 +580,18 @@ def test_expanded_with_garbage_left_in_shared_memory(dtype, dv):
     expanded_check(q, k, tail, v, ts, ks, ends, o, lse, 0.2)
 
 
+def test_expanded_long_keys_and_few_tokens():
+    """One sub-tile or one token over more key tiles than the panels' ring and
+    its barriers hold, next to two full sub-tiles that end apart."""
+    g = gen(37)
+    for dn, dr, dv in ((32, 16, 32), (64, 0, 64), (128, 64, 128), (192, 64, 96)):
+        new, context = [3, 1, 256, 129], [4000, 2500, 1500, 3000]
+        q, k, tail, v, ts, ks, ends = expanded_case(g, BF16, 2, dn, dr, dv, new, context)
+        ends[4:132] = np.minimum(ends[4:132], 100)  # the first sub-tile ends early
+        o, lse = satk.latent_attend_expanded(q, k, tail, v, i32(ts), i32(ks), i32(ends), scale=0.1)
+        expanded_check(q, k, tail, v, ts, ks, ends, o, lse, 0.1, skip=lambda t: t % 9 > 1)
+
+
 def test_expanded_many_requests_and_graph():
     g = gen(35)
     new = [1 + (i * 7) % 23 for i in range(150)]
