@@ -389,54 +389,96 @@ def dcp_emit_rows(ids: torch.Tensor, W: int, dcp_rank: int, req_id: torch.Tensor
     return rows_out, valid_out
 
 
+# The latent-cache operators are called once a layer and step with little work
+# each, so their marshalling reads every tensor property once (a handful of
+# 0.1 us calls) and hands plain integers to ctypes.
+
+_DTYPE16 = {torch.bfloat16: SATK_BF16, torch.float16: SATK_F16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _dtype16(t, name: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return SATK_BF16
-    if t.dtype == torch.float16:
-        return SATK_F16
-    raise SatkError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    code = _DTYPE16.get(t.dtype)
+    if code is None:
+        raise SatkError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return code
 
 
-def _int32_vec(t, n: int, name: str):
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
-        raise SatkError(f"{name} must be contiguous int32 with {n} entries")
+def _stream_on(device: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-def _same_device(*ts):
-    """Every tensor on one CUDA device."""
+def _device_of(*ts) -> int:
+    """The CUDA device that holds every tensor."""
     dev = None
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise SatkError("every tensor must live on a CUDA device")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise SatkError(f"tensors on two devices: {dev} and {t.device}")
+            dev = d
+        elif d != dev:
+            raise SatkError(f"tensors on two devices: {dev} and {d}")
+    return dev
 
 
-def _unit_last(t, name: str, dims: int):
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise SatkError(f"{name} must be {dims}-D with unit stride in its last dimension, got "
-                        f"{tuple(t.shape)} {t.stride()}")
+def _addr(t):
+    """A tensor's address for ctypes: None stays NULL, a tensor without
+    elements gets the stand-in that is checked and never dereferenced."""
+    if t is None:
+        return None
+    return t.data_ptr() or _EMPTY_BATCH_PTR
 
 
-def _lse_out(lse, T: int, H: int, device):
+def _int32_vec(t, n: int, name: str):
+    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous():
+        raise SatkError(f"{name} must be contiguous int32 with {n} entries")
+
+
+def _bad_layout(t, name: str, dims: int):
+    raise SatkError(f"{name} must be {dims}-D with unit stride in its last dimension, got "
+                    f"{tuple(t.shape)} {t.stride()}")
+
+
+def _matrix(t, name: str):
+    """(rows, cols, row stride) of a 2-D tensor with unit column stride."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
+        _bad_layout(t, name, 2)
+    rows, cols = shape
+    return rows, cols, stride[0] if rows > 1 else (cols or 1)
+
+
+def _heads(t, name: str):
+    """(rows, heads, width, row stride, head stride) of a 3-D tensor with unit
+    stride inside; strides of dimensions of one as if it were contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (shape[2] > 1 and stride[2] != 1):
+        _bad_layout(t, name, 3)
+    n, h, w = shape
+    return n, h, w, stride[0] if n > 1 else h * w, stride[1] if h > 1 else w
+
+
+def _lse_out(lse, T: int, H: int, like):
     if lse is None:
-        return torch.empty((T, H), dtype=torch.float32, device=device)
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+        return torch.empty((T, H), dtype=torch.float32, device=like.device)
+    if lse.dtype is not torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
         raise SatkError(f"lse must be contiguous float32 [{T}, {H}]")
     return lse
 
 
-def _heads_out(out, T: int, H: int, width: int, like, name: str = "out"):
+def _heads_out(out, T: int, H: int, width: int, like):
+    """The output tensor, with its row and head strides."""
     if out is None:
-        return torch.empty((T, H, width), dtype=like.dtype, device=like.device)
-    _unit_last(out, name, 3)
-    if out.dtype != like.dtype or tuple(out.shape) != (T, H, width):
-        raise SatkError(f"{name} must be {like.dtype} [{T}, {H}, {width}]")
-    return out
+        return (torch.empty((T, H, width), dtype=like.dtype, device=like.device), H * width, width)
+    n, h, w, ld_t, ld_h = _heads(out, "out")
+    if out.dtype is not like.dtype or (n, h, w) != (T, H, width):
+        raise SatkError(f"out must be {like.dtype} [{T}, {H}, {width}]")
+    return out, ld_t, ld_h
 
 
 class StepTables(NamedTuple):
@@ -463,35 +505,38 @@ def step_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks:
     latent_attend take.  ``tokens`` is their capacity; entries past the last
     new token are padding (row_end 0, slot -1).  ``drafted`` gives every new
     token its request's context as row_end."""
-    _same_device(context_lens, new_lens, free_blocks, block_table, status,
-                 *(out if out is not None else ()))
-    _rowmajor_2d(block_table, "block_table")
-    if block_table.dtype != torch.int32:
+    dev = _device_of(context_lens, new_lens, free_blocks, block_table, status)
+    R, width, ld = _matrix(block_table, "block_table")
+    if block_table.dtype is not torch.int32:
         raise SatkError("block_table must be int32")
-    R, width = block_table.shape
     _int32_vec(context_lens, R, "context_lens")
     _int32_vec(new_lens, R, "new_lens")
     _int32_vec(free_blocks, 0, "free_blocks")
-    max_blocks = width if max_blocks is None else max_blocks
     if tokens < 0:
         raise SatkError("tokens must not be negative")
     sizes = (R + 1, R, tokens, tokens, tokens, tokens, 1)
     if out is None:
-        # one allocation; each array starts on its own 16-byte boundary
-        room = [(n + 3) // 4 * 4 for n in sizes]
-        buf = torch.empty(sum(room), dtype=torch.int32, device=block_table.device)
-        out = StepTables(*(part[:n] for part, n in zip(buf.split(room), sizes)))
-    for name, t, n in zip(StepTables._fields, out, sizes):
-        _int32_vec(t, n, name)
+        # one allocation, one after the other
+        buf = torch.empty(2 * R + 4 * tokens + 2, dtype=torch.int32, device=block_table.device)
+        out = StepTables(*buf.split(sizes))
+        base = buf.data_ptr()
+        at = [base, base + 4 * (R + 1), base + 4 * (2 * R + 1)]
+        for _ in range(4):
+            at.append(at[-1] + 4 * tokens)
+    else:
+        _device_of(block_table, *out)
+        for name, t, n in zip(StepTables._fields, out, sizes):
+            _int32_vec(t, n, name)
+        at = [_addr(t) for t in out]
     if status is not None:
         _int32_vec(status, 1, "status")
-    ld = block_table.stride(0) if R > 1 else max(width, 1)
-    p = [_ptr(t, True) for t in out]
     rc = lib().satk_step_tables(
-        _ptr(context_lens, True), _ptr(new_lens, True), R, W, dcp_rank, block_size, stride_rows,
-        _ptr(free_blocks, True), free_blocks.numel(), _ptr(block_table, True), ld, max_blocks,
-        int(drafted), tokens, *p, _ptr(status), _stream(block_table.device))
-    _check(rc, "satk_step_tables")
+        _addr(context_lens), _addr(new_lens), R, W, dcp_rank, block_size, stride_rows,
+        _addr(free_blocks), free_blocks.numel(), _addr(block_table), ld,
+        width if max_blocks is None else max_blocks, 1 if drafted else 0, tokens, *at,
+        _addr(status), _stream_on(dev))
+    if rc:
+        _check(rc, "satk_step_tables")
     return out
 
 
@@ -504,41 +549,37 @@ def latent_store(latent: torch.Tensor, tail: torch.Tensor | None, slots: torch.T
     (int32 [T], negative: skipped).  ``weight`` float32 [dl] or None (no
     norm); ``cos_sin`` float32 [P, dr] (cosines, then sines) with
     ``positions`` int32 [T], or None (no rotation).  Returns ``cache``."""
-    _same_device(latent, tail, slots, cache, weight, cos_sin, positions, status)
-    _rowmajor_2d(latent, "latent")
-    _rowmajor_2d(cache, "cache")
+    dev = _device_of(latent, tail, slots, cache, weight, cos_sin, positions, status)
+    T, dl, ld = _matrix(latent, "latent")
+    rows, width, ld_cache = _matrix(cache, "cache")
     dt = _dtype16(cache, "cache")
-    T, dl = latent.shape
-    dr = 0
+    dr = ld_tail = 0
     if tail is not None:
-        _rowmajor_2d(tail, "tail")
-        dr = tail.shape[1]
-        if tail.dtype != cache.dtype or tail.shape[0] != T:
+        n, dr, ld_tail = _matrix(tail, "tail")
+        if tail.dtype is not cache.dtype or n != T:
             raise SatkError(f"tail must be {cache.dtype} [{T}, dr]")
-    if latent.dtype != cache.dtype or cache.shape[1] < dl + dr:
+    if latent.dtype is not cache.dtype or width < dl + dr:
         raise SatkError(f"latent must be {cache.dtype} and cache at least {dl + dr} wide")
     _int32_vec(slots, T, "slots")
-    if weight is not None and (weight.dtype != torch.float32 or not weight.is_contiguous()
-                               or weight.numel() != dl):
+    if weight is not None and (weight.dtype is not torch.float32 or weight.numel() != dl
+                               or not weight.is_contiguous()):
         raise SatkError(f"weight must be contiguous float32 [{dl}]")
     P = 0
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or \
-                cos_sin.dim() != 2 or cos_sin.shape[1] != dr:
+        shape = cos_sin.shape
+        if cos_sin.dtype is not torch.float32 or len(shape) != 2 or shape[1] != dr or \
+                not cos_sin.is_contiguous():
             raise SatkError(f"cos_sin must be contiguous float32 [P, {dr}]")
         if positions is None:
             raise SatkError("cos_sin needs positions")
         _int32_vec(positions, T, "positions")
-        P = cos_sin.shape[0]
-    rows = cache.shape[0]
-    ld_cache = cache.stride(0) if rows > 1 else cache.shape[1]
-    e = T == 0
+        P = shape[0]
     rc = lib().satk_latent_store(
-        _ptr(latent, e), latent.stride(0) if T > 1 else dl, _ptr(tail if dr else None, e),
-        tail.stride(0) if dr and T > 1 else dr, dt, T, dl, dr, _ptr(weight), eps,
-        _ptr(cos_sin if dr else None, True), P, _ptr(positions, e), int(interleaved),
-        _ptr(slots, e), _ptr(cache, True), rows, ld_cache, _ptr(status), _stream(cache.device))
-    _check(rc, "satk_latent_store")
+        _addr(latent), ld, _addr(tail) if dr else None, ld_tail, dt, T, dl, dr, _addr(weight),
+        eps, _addr(cos_sin) if dr else None, P, _addr(positions), 1 if interleaved else 0,
+        _addr(slots), _addr(cache), rows, ld_cache, _addr(status), _stream_on(dev))
+    if rc:
+        _check(rc, "satk_latent_store")
     return cache
 
 
@@ -548,33 +589,27 @@ def latent_workspace_bytes(heads: int, latent_dim: int) -> int:
 
 
 def _latent_call(q, cache, latent_dim, out, lse, workspace):
-    """Shared checks of the two attentions over cache rows."""
-    _unit_last(q, "q", 3)
-    _rowmajor_2d(cache, "cache")
+    """Shared checks of the two attentions over cache rows: the tokens, the
+    arguments before and after the keys', and the results."""
+    T, H, D, ld_t, ld_h = _heads(q, "q")
+    rows, width, ld_cache = _matrix(cache, "cache")
     dt = _dtype16(q, "q")
-    T, H, D = q.shape
-    if cache.dtype != q.dtype or cache.shape[1] < D:
+    if cache.dtype is not q.dtype or width < D:
         raise SatkError(f"cache must be {q.dtype} and at least {D} wide")
     if not 0 < latent_dim <= D:
         raise SatkError(f"latent_dim must be in 1..{D}")
-    out = _heads_out(out, T, H, latent_dim, q)
-    lse = _lse_out(lse, T, H, q.device)
-    need = lib().satk_latent_workspace_bytes(H, latent_dim)
+    out, lo_t, lo_h = _heads_out(out, T, H, latent_dim, q)
+    lse = _lse_out(lse, T, H, q)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    if not workspace.is_contiguous():
-        raise SatkError("workspace must be contiguous")
-    ld_t = q.stride(0) if T > 1 else H * D
-    ld_h = q.stride(1) if H > 1 else D
-    lo_t = out.stride(0) if T > 1 else H * latent_dim
-    lo_h = out.stride(1) if H > 1 else latent_dim
-    rows = cache.shape[0]
-    ld_cache = cache.stride(0) if rows > 1 else cache.shape[1]
-    e = T == 0
-    head = (_ptr(q, e), dt, T, H, latent_dim, D - latent_dim, ld_t, ld_h, _ptr(cache, True), rows,
+        size = max(lib().satk_latent_workspace_bytes(H, latent_dim), 16)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    else:
+        if not workspace.is_contiguous():
+            raise SatkError("workspace must be contiguous")
+        size = workspace.numel() * workspace.element_size()
+    head = (_addr(q), dt, T, H, latent_dim, D - latent_dim, ld_t, ld_h, _addr(cache), rows,
             ld_cache)
-    end = (_ptr(out, e), lo_t, lo_h, _ptr(lse, e), _ptr(workspace),
-           workspace.numel() * workspace.element_size())
+    end = (_addr(out), lo_t, lo_h, _addr(lse), _addr(workspace), size)
     return T, head, end, out, lse
 
 
@@ -590,27 +625,26 @@ def latent_attend(q: torch.Tensor, cache: torch.Tensor, req_id: torch.Tensor,
     row_ends[t] + b for each set bit b.  Keys are whole cache rows, values
     their first ``latent_dim`` columns.  Returns (out [T, H, latent_dim], lse
     float32 [T, H])."""
-    _same_device(q, cache, req_id, block_table, row_ends, tree, out, lse, workspace, status)
+    dev = _device_of(q, cache, req_id, block_table, row_ends, tree, out, lse, workspace, status)
     T, head, end, out, lse = _latent_call(q, cache, latent_dim, out, lse, workspace)
-    _rowmajor_2d(block_table, "block_table")
-    if block_table.dtype != torch.int32:
+    R, width, ld_table = _matrix(block_table, "block_table")
+    if block_table.dtype is not torch.int32:
         raise SatkError("block_table must be int32")
     _int32_vec(req_id, T, "req_id")
     _int32_vec(row_ends, T, "row_ends")
     words = 0
     if tree is not None:
-        if tree.dtype != torch.int32 or tree.dim() != 2 or tree.shape[0] != T or \
-                not tree.is_contiguous() or tree.shape[1] < 1:
+        shape = tree.shape
+        if tree.dtype is not torch.int32 or len(shape) != 2 or shape[0] != T or shape[1] < 1 or \
+                not tree.is_contiguous():
             raise SatkError(f"tree must be contiguous int32 [{T}, >= 1]")
-        words = tree.shape[1]
-    R, width = block_table.shape
-    max_blocks = width if max_blocks is None else max_blocks
-    e = T == 0
+        words = shape[1]
     rc = lib().satk_latent_attend(
-        *head, _ptr(req_id, e), _ptr(block_table, True), R,
-        block_table.stride(0) if R > 1 else max(width, 1), max_blocks, block_size, stride_rows,
-        _ptr(row_ends, e), _ptr(tree, e), words, scale, *end, _ptr(status), _stream(q.device))
-    _check(rc, "satk_latent_attend")
+        *head, _addr(req_id), _addr(block_table), R, ld_table,
+        width if max_blocks is None else max_blocks, block_size, stride_rows, _addr(row_ends),
+        _addr(tree), words, scale, *end, _addr(status), _stream_on(dev))
+    if rc:
+        _check(rc, "satk_latent_attend")
     return out, lse
 
 
@@ -623,19 +657,19 @@ def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, rows: torch.Tensor,
     ``rows`` int32 [T, >= k] and ``counts`` int32 [T] as dcp_emit_rows writes
     them (negative entries and those past the count are skipped).  Returns
     (out [T, H, latent_dim], lse float32 [T, H])."""
-    _same_device(q, cache, rows, counts, out, lse, workspace, status)
+    dev = _device_of(q, cache, rows, counts, out, lse, workspace, status)
     T, head, end, out, lse = _latent_call(q, cache, latent_dim, out, lse, workspace)
-    _rowmajor_2d(rows, "rows")
-    k = rows.shape[1] if k is None else k
-    if rows.dtype != torch.int32 or rows.shape[0] != T or rows.shape[1] < k:
+    n, width, ld_rows = _matrix(rows, "rows")
+    k = width if k is None else k
+    if rows.dtype is not torch.int32 or n != T or width < k:
         raise SatkError(f"rows must be int32 [{T}, >= {k}]")
     if counts is not None:
         _int32_vec(counts, T, "counts")
-    e = T == 0
     rc = lib().satk_latent_attend_rows(
-        *head, _ptr(rows, e), rows.stride(0) if T > 1 else rows.shape[1], k, _ptr(counts, e),
-        scale, *end, _ptr(status), _stream(q.device))
-    _check(rc, "satk_latent_attend_rows")
+        *head, _addr(rows), ld_rows, k, _addr(counts), scale, *end, _addr(status),
+        _stream_on(dev))
+    if rc:
+        _check(rc, "satk_latent_attend_rows")
     return out, lse
 
 
@@ -648,22 +682,19 @@ def latent_attend_expanded(q: torch.Tensor, k: torch.Tensor, tail: torch.Tensor 
     [S, H, dv]; request r owns tokens token_starts[r:r+2] and keys
     key_starts[r:r+2]; token t sees its request's first row_ends[t] keys.
     Returns (out [T, H, dv], lse float32 [T, H])."""
-    _same_device(q, k, tail, v, token_starts, key_starts, row_ends, out, lse)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _unit_last(t, name, 3)
-        if t.dtype != q.dtype:
-            raise SatkError(f"{name} must be {q.dtype}")
+    dev = _device_of(q, k, tail, v, token_starts, key_starts, row_ends, out, lse)
+    T, H, D, q_t, q_h = _heads(q, "q")
+    S, hk, dn, k_s, k_h = _heads(k, "k")
+    sv, hv, dv, v_s, v_h = _heads(v, "v")
     dt = _dtype16(q, "q")
-    T, H, D = q.shape
-    S, _, dn = k.shape
-    dv = v.shape[2]
-    dr = 0
+    if k.dtype is not q.dtype or v.dtype is not q.dtype:
+        raise SatkError(f"k and v must be {q.dtype}")
+    dr = ld_tail = 0
     if tail is not None:
-        _rowmajor_2d(tail, "tail")
-        dr = tail.shape[1]
-        if tail.dtype != q.dtype or tail.shape[0] != S:
+        n, dr, ld_tail = _matrix(tail, "tail")
+        if tail.dtype is not q.dtype or n != S:
             raise SatkError(f"tail must be {q.dtype} [{S}, dr]")
-    if k.shape[1] != H or tuple(v.shape[:2]) != (S, H) or D != dn + dr:
+    if hk != H or (sv, hv) != (S, H) or D != dn + dr:
         raise SatkError(f"k, v and q must be [{S}, {H}, dn], [{S}, {H}, dv] and [T, {H}, dn + dr]")
     R = token_starts.numel() - 1
     if R < 0:
@@ -671,22 +702,14 @@ def latent_attend_expanded(q: torch.Tensor, k: torch.Tensor, tail: torch.Tensor 
     _int32_vec(token_starts, R + 1, "token_starts")
     _int32_vec(key_starts, R + 1, "key_starts")
     _int32_vec(row_ends, T, "row_ends")
-    out = _heads_out(out, T, H, dv, q)
-    lse = _lse_out(lse, T, H, q.device)
-
-    def strides(t, rows, width):
-        return (t.stride(0) if rows > 1 else H * width, t.stride(1) if H > 1 else width)
-    e = T == 0
-    q_t, q_h = strides(q, T, D)
-    k_s, k_h = strides(k, S, dn)
-    v_s, v_h = strides(v, S, dv)
-    o_t, o_h = strides(out, T, dv)
+    out, o_t, o_h = _heads_out(out, T, H, dv, q)
+    lse = _lse_out(lse, T, H, q)
     rc = lib().satk_latent_attend_expanded(
-        _ptr(q, e), dt, T, H, dn, dr, q_t, q_h, _ptr(k, True), S, k_s, k_h,
-        _ptr(tail if dr else None, True), tail.stride(0) if dr and S > 1 else dr, _ptr(v, True),
-        dv, v_s, v_h, _ptr(token_starts), _ptr(key_starts), R, _ptr(row_ends, e), scale,
-        _ptr(out, e), o_t, o_h, _ptr(lse, e), _stream(q.device))
-    _check(rc, "satk_latent_attend_expanded")
+        _addr(q), dt, T, H, dn, dr, q_t, q_h, _addr(k), S, k_s, k_h, _addr(tail) if dr else None,
+        ld_tail, _addr(v), dv, v_s, v_h, _addr(token_starts), _addr(key_starts), R,
+        _addr(row_ends), scale, _addr(out), o_t, o_h, _addr(lse), _stream_on(dev))
+    if rc:
+        _check(rc, "satk_latent_attend_expanded")
     return out, lse
 
 
@@ -695,19 +718,20 @@ def latent_merge(parts: torch.Tensor, lse: torch.Tensor, *, out: torch.Tensor | 
     """Joins W partial attention results over disjoint keys: ``parts``
     [W, T, H, dv] bfloat16 or float16, ``lse`` float32 [W, T, H] contiguous.
     Returns (out [T, H, dv], lse float32 [T, H])."""
-    _same_device(parts, lse, out, lse_out)
-    _unit_last(parts, "parts", 4)
+    dev = _device_of(parts, lse, out, lse_out)
+    shape, stride = parts.shape, parts.stride()
+    if len(shape) != 4 or (shape[3] > 1 and stride[3] != 1):
+        _bad_layout(parts, "parts", 4)
+    W, T, H, dv = shape
     dt = _dtype16(parts, "parts")
-    W, T, H, dv = parts.shape
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (W, T, H) or not lse.is_contiguous():
+    if lse.dtype is not torch.float32 or lse.shape != (W, T, H) or not lse.is_contiguous():
         raise SatkError(f"lse must be contiguous float32 [{W}, {T}, {H}]")
-    out = _heads_out(out, T, H, dv, parts)
-    lse_out = _lse_out(lse_out, T, H, parts.device)
-    e = T == 0
+    out, o_t, o_h = _heads_out(out, T, H, dv, parts)
+    lse_out = _lse_out(lse_out, T, H, parts)
     rc = lib().satk_latent_merge(
-        _ptr(parts, e), dt, W, T, H, dv, parts.stride(0) if W > 1 else T * H * dv,
-        parts.stride(1) if T > 1 else H * dv, parts.stride(2) if H > 1 else dv, _ptr(lse, e),
-        _ptr(out, e), out.stride(0) if T > 1 else H * dv, out.stride(1) if H > 1 else dv,
-        _ptr(lse_out, e), _stream(parts.device))
-    _check(rc, "satk_latent_merge")
+        _addr(parts), dt, W, T, H, dv, stride[0] if W > 1 else T * H * dv,
+        stride[1] if T > 1 else H * dv, stride[2] if H > 1 else dv, _addr(lse), _addr(out), o_t,
+        o_h, _addr(lse_out), _stream_on(dev))
+    if rc:
+        _check(rc, "satk_latent_merge")
     return out, lse_out
