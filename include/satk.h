@@ -527,7 +527,8 @@ int satk_latent_attend_expanded(const void *q, int dtype, int64_t T, int32_t H,
  * lse_out = log sum_w exp(lse_w), out = sum_w exp(lse_w - lse_out) parts_w.
  *
  * parts : [W, T, H, dv] of `dtype`, strides ld_w, ld_t, ld_h, unit inside.
- * lse   : float [W, T, H] contiguous.  A part whose lse is -inf is not read.
+ * lse   : float [W, T, H] contiguous.  What a part with lse -inf
+ *         holds does not count, whatever it is.
  * out   : [T, H, dv] of `dtype`, strides ld_out_t, ld_out_h; lse_out: nullable
  *         float [T, H].  All parts empty: zeros and -inf.
  * Errors: SATK_EINVAL for NULL parts/lse/out, W < 1, T < 0, T * H >= 2**31,

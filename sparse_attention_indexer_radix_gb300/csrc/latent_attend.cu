@@ -6,13 +6,6 @@
 namespace satk {
 namespace {
 
-int log2_or(int v) {
-  if (v <= 0 || (v & (v - 1)) != 0) return -1;
-  int s = 0;
-  while ((1 << s) < v) ++s;
-  return s;
-}
-
 // The checks both entry points share; SATK_OK when the call may go on.
 int check(const LatentArgs &a, int dtype, int64_t T, int64_t dr, float scale,
           const void *workspace, size_t workspace_bytes) {

@@ -1,11 +1,11 @@
 // latent_merge.cu -- satk_latent_merge: W partial attention results over
 // disjoint keys joined by their log-sum-exps.
 //
-// One thread per eight output columns of a (token, head): it reads the W lse
-// values (broadcast within the row), then the W parts with independent
-// 16-byte loads.  Each part is read once and the result written once:
-// memory-bound.  Rows that are not 16-byte aligned take one column per
-// thread.
+// One thread per eight output columns of a (token, head).  Ranks go in groups of
+// eight whose lse values and 16-byte parts are all asked for together; further
+// groups rescale by the running maximum.  Each part is read once and the result
+// written once: memory-bound.  Rows that are not 16-byte aligned take one column
+// per thread.
 #include "latent_common.cuh"
 
 namespace satk {
@@ -35,33 +35,49 @@ __global__ void __launch_bounds__(kMergeBlock) latent_merge_kernel(MergeArgs a) 
   const int h = static_cast<int>(row - t * a.H);
   const E *part = static_cast<const E *>(a.parts) + t * a.ld_t + h * a.ld_h + c;
   const float *lse = a.lse + row;
-  float m = -INFINITY;
-  bool nan = false;
-  for (int w = 0; w < a.W; ++w) {
-    const float x = __ldg(lse + w * a.rows);
-    nan |= x != x;
-    m = fmaxf(m, x);
-  }
-  const float ref = m == -INFINITY ? 0.f : m;
+  constexpr int kGroup = 8;
+  float ref = -INFINITY, sum = 0.f;
   float acc[VEC] = {};
-  float sum = nan ? NAN : 0.f;
-#pragma unroll 4
-  for (int w = 0; w < a.W; ++w) {
-    const float x = __ldg(lse + w * a.rows);
-    if (x == -INFINITY) continue;
-    const float p = exp2_fast((x - ref) * kLog2e);
-    sum += p;
-    if constexpr (VEC == 8) {
-      Pack8<E> v;
-      v.u = __ldg(reinterpret_cast<const uint4 *>(part + w * a.ld_w));
+  for (int w0 = 0; w0 < a.W; w0 += kGroup) {
+    float x[kGroup];
+    Pack8<E> v[kGroup];
+    E one[kGroup];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = Elem<E>::to2(v.h[j]);
-        acc[2 * j] = fmaf(p, f.x, acc[2 * j]);
-        acc[2 * j + 1] = fmaf(p, f.y, acc[2 * j + 1]);
+    for (int i = 0; i < kGroup; ++i) {
+      if (w0 + i < a.W) {
+        x[i] = __ldg(lse + (w0 + i) * a.rows);
+        if constexpr (VEC == 8) v[i].u = __ldg(reinterpret_cast<const uint4 *>(part + (w0 + i) * a.ld_w));
+        else one[i] = part[(w0 + i) * a.ld_w];
+      } else {
+        x[i] = -INFINITY;
       }
-    } else {
-      acc[0] = fmaf(p, Elem<E>::to(part[w * a.ld_w]), acc[0]);
+    }
+    float top = ref;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) top = fmaxf(top, x[i]);
+    const float base = top == -INFINITY ? 0.f : top;
+    const float keep = exp2_fast((ref - base) * kLog2e);
+    ref = top;
+    if (w0 > 0) {
+      sum *= keep;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) acc[j] *= keep;
+    }
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      if (x[i] == -INFINITY) continue;  // nothing of an empty part counts
+      const float p = exp2_fast((x[i] - base) * kLog2e);
+      sum += p;
+      if constexpr (VEC == 8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = Elem<E>::to2(v[i].h[j]);
+          acc[2 * j] = fmaf(p, f.x, acc[2 * j]);
+          acc[2 * j + 1] = fmaf(p, f.y, acc[2 * j + 1]);
+        }
+      } else {
+        acc[0] = fmaf(p, Elem<E>::to(one[i]), acc[0]);
+      }
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -36,18 +36,18 @@ __global__ void __launch_bounds__(kStoreWarps * 32) latent_store_kernel(StoreArg
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kStoreWarps + (threadIdx.x >> 5);
   if (t >= a.T) return;
+  // The row is asked for together with its slot and position.
   const int slot = a.slots[t];
-  if (slot < 0) return;
   const int pos = a.cos_sin != nullptr ? a.positions[t] : 0;
-  const bool row_ok = slot < a.cache_rows;
-  const bool pos_ok = a.cos_sin == nullptr || (pos >= 0 && pos < a.n_positions);
-  if (!row_ok || !pos_ok) {
-    if (lane == 0 && a.status != nullptr)
-      atomicOr(a.status, row_ok ? SATK_STATUS_BAD_POSITION : SATK_STATUS_BAD_ROW);
-    return;
-  }
   const E *x = static_cast<const E *>(a.latent) + t * a.ld_latent;
-  E *out = static_cast<E *>(a.cache) + slot * a.ld_cache;
+  const int half = a.dr / 2;  // the tail: lane i holds pair i (dr / 2 <= 32 pairs)
+  const int i0 = a.interleaved ? 2 * lane : lane, i1 = a.interleaved ? i0 + 1 : lane + half;
+  float y0 = 0.f, y1 = 0.f;
+  if (lane < half) {
+    const E *y = static_cast<const E *>(a.tail) + t * a.ld_tail;
+    y0 = Elem<E>::to(y[i0]);
+    y1 = Elem<E>::to(y[i1]);
+  }
   float v[kPer];
   float sum = 0.f;
 #pragma unroll
@@ -66,6 +66,21 @@ __global__ void __launch_bounds__(kStoreWarps * 32) latent_store_kernel(StoreArg
     } else {
       v[i] = c < a.dl ? Elem<E>::to(x[c]) : 0.f;
     }
+  }
+  if (slot < 0) return;
+  const bool row_ok = slot < a.cache_rows;
+  const bool pos_ok = a.cos_sin == nullptr || (pos >= 0 && pos < a.n_positions);
+  if (!row_ok || !pos_ok) {
+    if (lane == 0 && a.status != nullptr)
+      atomicOr(a.status, row_ok ? SATK_STATUS_BAD_POSITION : SATK_STATUS_BAD_ROW);
+    return;
+  }
+  E *out = static_cast<E *>(a.cache) + slot * a.ld_cache;
+  float co = 0.f, si = 0.f;
+  if (a.cos_sin != nullptr && lane < half) {
+    const float *cs = a.cos_sin + static_cast<int64_t>(pos) * a.dr;
+    co = __ldg(cs + lane);
+    si = __ldg(cs + half + lane);
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) sum = fmaf(v[i], v[i], sum);
@@ -96,21 +111,14 @@ __global__ void __launch_bounds__(kStoreWarps * 32) latent_store_kernel(StoreArg
       }
     }
   }
-  // the tail: lane i holds pair i (dr / 2 <= 32 pairs)
-  const int half = a.dr / 2;
   if (lane < half) {
-    const E *y = static_cast<const E *>(a.tail) + t * a.ld_tail;
-    const int i0 = a.interleaved ? 2 * lane : lane, i1 = a.interleaved ? i0 + 1 : lane + half;
-    float u = Elem<E>::to(y[i0]), w = Elem<E>::to(y[i1]);
     if (a.cos_sin != nullptr) {
-      const float *cs = a.cos_sin + static_cast<int64_t>(pos) * a.dr;
-      const float co = __ldg(cs + lane), si = __ldg(cs + half + lane);
-      const float r0 = u * co - w * si, r1 = u * si + w * co;
-      u = r0;
-      w = r1;
+      const float r0 = y0 * co - y1 * si, r1 = y0 * si + y1 * co;
+      y0 = r0;
+      y1 = r1;
     }
-    out[a.dl + i0] = Elem<E>::from(u);
-    out[a.dl + i1] = Elem<E>::from(w);
+    out[a.dl + i0] = Elem<E>::from(y0);
+    out[a.dl + i1] = Elem<E>::from(y1);
   }
 }
 

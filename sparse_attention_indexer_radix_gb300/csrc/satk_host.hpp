@@ -13,6 +13,14 @@ inline cudaStream_t as_stream(satk_stream_t s) { return reinterpret_cast<cudaStr
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// log2 of a power of two, else -1.
+inline int log2_or(int v) {
+  if (v <= 0 || (v & (v - 1)) != 0) return -1;
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
 // Maps the result of the launches just issued to an SATK return code.
 inline int launch_status() {
   const cudaError_t e = cudaGetLastError();

@@ -8,7 +8,8 @@
 // takes its share of the tokens and of the new blocks.  A token whose block
 // is new this step reads its id from the free list, not from the table, so no
 // CTA waits for another's table writes.  Latency-bound: one launch, about two
-// dependent rounds of loads.
+// dependent rounds of loads; W and block_size are divided by with shifts where
+// they are powers of two (64-bit divisions took half of the time).
 #include "satk_host.hpp"
 #include "satk_device.cuh"
 
@@ -16,7 +17,7 @@ namespace satk {
 namespace {
 
 constexpr int kTablesBlock = 512;
-constexpr int kTablesTokens = 1024;  // tokens per CTA
+constexpr int kTablesTokens = 512;  // tokens per CTA
 
 struct TablesArgs {
   const int32_t *context_lens, *new_lens;
@@ -29,7 +30,15 @@ struct TablesArgs {
   int max_blocks, drafted;
   int64_t T;
   int32_t *token_starts, *lens, *req_id, *positions, *row_ends, *slots, *blocks_used, *status;
+  int w_shift, b_shift;  // log2 of W and block_size when powers of two, else -1
 };
+
+__device__ __forceinline__ int64_t by_ranks(const TablesArgs &a, int64_t p) {
+  return a.w_shift >= 0 ? p >> a.w_shift : p / a.W;
+}
+__device__ __forceinline__ int64_t by_block(const TablesArgs &a, int64_t p) {
+  return a.b_shift >= 0 ? p >> a.b_shift : p / a.block_size;
+}
 
 struct Request {
   int64_t ctx, fresh;  // tokens before the step, new tokens
@@ -37,7 +46,7 @@ struct Request {
 };
 
 __device__ __forceinline__ int64_t local_count(const TablesArgs &a, int64_t p) {
-  return (p + a.W - 1 - a.rank) / a.W;
+  return by_ranks(a, p + a.W - 1 - a.rank);
 }
 
 __device__ __forceinline__ Request request(const TablesArgs &a, int r) {
@@ -45,7 +54,7 @@ __device__ __forceinline__ Request request(const TablesArgs &a, int r) {
   q.ctx = max(a.context_lens[r], 0);
   q.fresh = max(a.new_lens[r], 0);
   auto blocks = [&](int64_t p) {
-    const int64_t b = (local_count(a, p) + a.block_size - 1) / a.block_size;
+    const int64_t b = by_block(a, local_count(a, p) + a.block_size - 1);
     return static_cast<int>(b < a.max_blocks ? b : a.max_blocks);
   };
   q.have = blocks(q.ctx);
@@ -137,8 +146,9 @@ __global__ void __launch_bounds__(kTablesBlock) step_tables_kernel(TablesArgs a)
       const Request q = request(a, req);
       pos = q.ctx + (i - tok[req]);
       end = local_count(a, a.drafted ? q.ctx : pos + 1);
-      if (pos % a.W == a.rank) {
-        const int64_t l = pos / a.W, col = l / a.block_size;
+      const int64_t l = by_ranks(a, pos);
+      if (pos - l * a.W == a.rank) {
+        const int64_t col = by_block(a, l);
         int32_t id = -1;
         if (col < q.have) {
           id = a.table[req * a.ld_table + col];
@@ -149,7 +159,7 @@ __global__ void __launch_bounds__(kTablesBlock) step_tables_kernel(TablesArgs a)
         if (id < 0) {
           bad |= SATK_STATUS_NO_BLOCK;
         } else {
-          const int64_t row = id * a.stride_rows + l % a.block_size;
+          const int64_t row = id * a.stride_rows + (l - col * a.block_size);
           if (row > INT32_MAX) bad |= SATK_STATUS_BAD_ROW;
           else slot = static_cast<int>(row);
         }
@@ -187,7 +197,7 @@ extern "C" int satk_step_tables(const int32_t *context_lens, const int32_t *new_
   TablesArgs a{context_lens, new_lens,    R,           W,          dcp_rank,  block_size,
                stride_rows,  free_blocks, n_free,      block_table, ld_block_table, max_blocks,
                drafted,      T,           token_starts, lens,      req_id,    positions,
-               row_ends,     slots,       blocks_used, status};
+               row_ends,     slots,       blocks_used, status,     log2_or(W), log2_or(block_size)};
   const size_t smem = sizeof(int32_t) * 2 * static_cast<size_t>(R);
   if (!allow_smem(step_tables_kernel, smem)) return SATK_ECUDA;
   const int64_t grid = T > kTablesTokens ? (T + kTablesTokens - 1) / kTablesTokens : 1;
