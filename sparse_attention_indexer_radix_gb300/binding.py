@@ -465,7 +465,7 @@ def _heads(t, name: str):
 
 def _lse_out(lse, T: int, H: int, like):
     if lse is None:
-        return like.new_empty((T, H), dtype=torch.float32)
+        return torch.empty((T, H), dtype=torch.float32, device=like.device)
     if lse.dtype is not torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
         raise SatkError(f"lse must be contiguous float32 [{T}, {H}]")
     return lse
@@ -474,7 +474,7 @@ def _lse_out(lse, T: int, H: int, like):
 def _heads_out(out, T: int, H: int, width: int, like):
     """The output tensor, with its row and head strides."""
     if out is None:
-        return like.new_empty((T, H, width)), H * width, width
+        return (torch.empty((T, H, width), dtype=like.dtype, device=like.device), H * width, width)
     n, h, w, ld_t, ld_h = _heads(out, "out")
     if out.dtype is not like.dtype or (n, h, w) != (T, H, width):
         raise SatkError(f"out must be {like.dtype} [{T}, {H}, {width}]")
@@ -517,7 +517,7 @@ def step_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks:
     sizes = (R + 1, R, tokens, tokens, tokens, tokens, 1)
     if out is None:
         # one allocation, one after the other
-        buf = block_table.new_empty(2 * R + 4 * tokens + 2)
+        buf = torch.empty(2 * R + 4 * tokens + 2, dtype=torch.int32, device=block_table.device)
         out = StepTables(*buf.split(sizes))
         base = buf.data_ptr()
         at = [base, base + 4 * (R + 1), base + 4 * (2 * R + 1)]
@@ -602,7 +602,7 @@ def _latent_call(q, cache, latent_dim, out, lse, workspace):
     lse = _lse_out(lse, T, H, q)
     if workspace is None:
         size = max(lib().satk_latent_workspace_bytes(H, latent_dim), 16)
-        workspace = q.new_empty(size, dtype=torch.uint8)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     else:
         if not workspace.is_contiguous():
             raise SatkError("workspace must be contiguous")
