@@ -69,7 +69,9 @@ struct Group {
 
 struct Plan {
   int64_t tiles, per;  // on the line, per CTA
-  int ngroups, pad[3];
+  int ngroups;
+  int whole;           // one item (group, head chunk) per CTA: nothing is cut
+  int pad[2];
   __device__ Group *groups() { return reinterpret_cast<Group *>(this + 1); }
 };
 constexpr size_t plan_bytes(int groups) { return (sizeof(Plan) + sizeof(Group) * groups + 15) / 16 * 16; }
@@ -85,6 +87,7 @@ struct MmaArgs {
   }
   int nh, hc;    // head chunks and heads per chunk
   int tpg;       // tokens per group
+  int columns;   // N
   int np, nst;   // 64-column panels of a key row, stages
   int np0;       // panels of a stage's first half (all of them: there is no second)
   int nb;        // 128-column blocks of a value
@@ -105,9 +108,16 @@ __device__ __forceinline__ int64_t per_cta(int64_t tiles, int ctas) {
   return per < kMinTiles ? kMinTiles : per;
 }
 
+// What cutting groups costs a CTA, in tiles: two partial results written (12.5 K
+// cycles each for 64 columns x 512 values, where a tile takes 3.8 K) and the join
+// of its share.  Where every item can have a CTA of its own and the longest is
+// longer than an equal piece by no more than that, nothing is cut (128 tokens of
+// 2048 rows, 64 heads: 89 us cut, 8x us whole).
+__device__ __forceinline__ int cut_cost(int columns) { return 2 + 10 * columns / 64; }
+
 struct PlanScratch {
   int64_t tiles[32];
-  int groups[32];
+  int groups[32], longest[32];
 };
 
 // Groups in token order, and the prefix sum of their tiles, by one CTA of up to
@@ -138,11 +148,12 @@ __device__ void make_plan(const MmaArgs &m, int ctas, Plan *plan, PlanScratch &s
   };
   Group g = {};
   int64_t tiles = 0;
-  int groups = 0;
+  int groups = 0, longest = 0;
   for (int t = b; t < e; ++t)
     if (leader(t)) {
       g = group(t);
       tiles += static_cast<int64_t>(group_tiles(g) + kItemTiles) * m.nh;
+      longest = max(longest, group_tiles(g) + kItemTiles);
       ++groups;
     }
   int64_t st = tiles;
@@ -152,12 +163,14 @@ __device__ void make_plan(const MmaArgs &m, int ctas, Plan *plan, PlanScratch &s
     const int64_t x = __shfl_up_sync(~0u, st, d);
     const int y = __shfl_up_sync(~0u, sg, d);
     if (lane >= d) st += x, sg += y;
+    longest = max(longest, __shfl_xor_sync(~0u, longest, d));
   }
-  if (lane == 31) wt[warp] = st, wg[warp] = sg;
+  if (lane == 31) wt[warp] = st, wg[warp] = sg, scratch.longest[warp] = longest;
   __syncthreads();
   int64_t all = 0;
   int n = 0;
   for (int w = 0; w < threads / 32; ++w) {
+    longest = max(longest, scratch.longest[w]);
     if (w < warp) st += wt[w], sg += wg[w];
     all += wt[w];
     n += wg[w];
@@ -176,6 +189,8 @@ __device__ void make_plan(const MmaArgs &m, int ctas, Plan *plan, PlanScratch &s
     plan->tiles = all;
     plan->per = per_cta(all, ctas);
     plan->ngroups = n;
+    plan->whole = static_cast<int64_t>(n) * m.nh <= ctas &&
+                  longest <= plan->per + cut_cost(m.columns);
   }
 }
 
@@ -275,6 +290,35 @@ __device__ __forceinline__ void store4(E *out, float4 v, int left, bool vec) {
   }
 }
 
+// A reduction over the 16 keys (lanes of a half warp) of C columns at once: each
+// step halves the columns a lane still has.  Afterwards a lane's v[0 .. C / 16)
+// (v[0] at least) are the columns from `first` on.
+struct Maximum {
+  static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
+};
+struct Sum {
+  static __device__ __forceinline__ float of(float a, float b) { return a + b; }
+};
+template <class Op, int HAVE, int D, int C>
+__device__ __forceinline__ void reduce_keys(float (&v)[C], int lane, int &first) {
+  if constexpr (D > 0) {
+    if constexpr (HAVE > 1) {
+      const bool upper = lane & D;
+#pragma unroll
+      for (int x = 0; x < HAVE / 2; ++x) {
+        const float give = upper ? v[x] : v[x + HAVE / 2];
+        const float keep = upper ? v[x + HAVE / 2] : v[x];
+        v[x] = Op::of(keep, __shfl_xor_sync(~0u, give, D));
+      }
+      if (upper) first += HAVE / 2;
+      reduce_keys<Op, HAVE / 2, D / 2>(v, lane, first);
+    } else {
+      v[0] = Op::of(v[0], __shfl_xor_sync(~0u, v[0], D));
+      reduce_keys<Op, 1, D / 2>(v, lane, first);
+    }
+  }
+}
+
 struct Small {
   float red[4][64];
   float ref[64];
@@ -302,7 +346,17 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
     __syncthreads();
   }
   const int64_t per = plan->per, total = plan->tiles;
-  const int64_t u0 = min(blockIdx.x * per, total), u1 = min(u0 + per, total);
+  int64_t u0 = min(blockIdx.x * per, total), u1 = min(u0 + per, total);
+  if (plan->whole) {
+    const int gi = blockIdx.x / m.nh;
+    u0 = u1 = 0;
+    if (gi < plan->ngroups) {
+      const Group g = plan->groups()[gi];
+      const int length = group_tiles(g) + kItemTiles;
+      u0 = g.start + (blockIdx.x - gi * m.nh) * length;
+      u1 = u0 + length;
+    }
+  }
   const Piece piece{plan->groups(), m.nh, static_cast<int>(u1 - u0)};
   Walk w;
   w.k0 = w.k1 = 0;
@@ -451,24 +505,43 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
         for (int x = 0; x < C; ++x) pass |= s[x] > kLag;
         if (named_any(1, kSoftmax, pass)) {
           // Move the references to the running maxima.
+          {
+            float mx[C];
 #pragma unroll
-          for (int x = 0; x < C; ++x) {
-            float mx = s[x] == -INFINITY ? s[x] : __uint_as_float(raw[x]) * a.scale_log2;
+            for (int x = 0; x < C; ++x)
+              mx[x] = s[x] == -INFINITY ? s[x] : __uint_as_float(raw[x]) * a.scale_log2;
+            int at = c0;
+            reduce_keys<Maximum, C, 8>(mx, lane, at);
 #pragma unroll
-            for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-            if ((lane & 15) == 0) sm.red[warp][c0 + x] = mx;
+            for (int x = 0; x < (C + 15) / 16; ++x) sm.red[warp][at + x] = mx[x];
           }
           named_sync(1, kSoftmax);
 #pragma unroll
-          for (int x = 0; x < C; ++x) {
-            const int n = c0 + x;
-            const float now = fmaxf(fmaxf(fmaxf(sm.red[0][n], sm.red[1][n]),
-                                          fmaxf(sm.red[2][n], sm.red[3][n])), ref[x]);
-            const float f = exp2_fast(ref[x] - now);
-            l[x] *= f;
-            ref[x] = now;
-            if (s[x] != -INFINITY) s[x] = fmaf(__uint_as_float(raw[x]), a.scale_log2, -now);
-            if (warp == 0 && (lane & 15) == 0) sm.factor[n] = f, sm.ref[n] = now;
+          for (int x = 0; x < C; x += 4) {
+            float4 now = make_float4(ref[x], ref[x + 1], ref[x + 2], ref[x + 3]), f;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float4 r = *reinterpret_cast<const float4 *>(&sm.red[y][c0 + x]);
+              now.x = fmaxf(now.x, r.x);
+              now.y = fmaxf(now.y, r.y);
+              now.z = fmaxf(now.z, r.z);
+              now.w = fmaxf(now.w, r.w);
+            }
+            auto move = [&](int at, float to) {
+              const float factor = exp2_fast(ref[at] - to);
+              l[at] *= factor;
+              ref[at] = to;
+              if (s[at] != -INFINITY) s[at] = fmaf(__uint_as_float(raw[at]), a.scale_log2, -to);
+              return factor;
+            };
+            f.x = move(x, now.x);
+            f.y = move(x + 1, now.y);
+            f.z = move(x + 2, now.z);
+            f.w = move(x + 3, now.w);
+            if (warp == 0 && (lane & 15) == 0) {
+              *reinterpret_cast<float4 *>(&sm.factor[c0 + x]) = f;
+              *reinterpret_cast<float4 *>(&sm.ref[c0 + x]) = now;
+            }
           }
           named_sync(1, kSoftmax);
           if (!first) {
@@ -509,11 +582,11 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
         if (++stage == m.nst) stage = 0, ++use;
       }
       // Sums over the keys, then O.
+      {
+        int at = c0;
+        reduce_keys<Sum, C, 8>(l, lane, at);
 #pragma unroll
-      for (int x = 0; x < C; ++x) {
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) l[x] += __shfl_xor_sync(~0u, l[x], d);
-        if ((lane & 15) == 0) sm.red[warp][c0 + x] = l[x];
+        for (int x = 0; x < (C + 15) / 16; ++x) sm.red[warp][at + x] = l[x];
       }
       named_sync(1, kSoftmax);
       float *part = m.parts + (blockIdx.x * 2 + slot) * m.part_stride;
@@ -540,28 +613,46 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
       // (stored as they come, a lane a value, 64 columns x 512 took 14 us).
       float *turn = reinterpret_cast<float *>(p_ptr) + warp * 512;
       const int y0 = lane >> 3, d0 = warp * 32 + (lane & 7) * 4;
-      for (int col = 0; col < m.nb * N; col += 16) {
-        const int n0 = col & (N - 1), d = (col / N) * 128 + d0;
-        if (n0 >= ncol) continue;
-        uint32_t o[16];
-        tmem_ld16(o, o_at + col + (static_cast<uint32_t>(warp * 32) << 16));
-        tmem_wait_ld();
+      // Of the 16-column steps of each block only those with a column in use; the
+      // next step's values are on their way while one is stored.
+      const int steps = (ncol + 15) >> 4, total = m.nb * steps;
+      auto fetch = [&](uint32_t (&o)[16], int step) {
+        const int b = step / steps;
+        tmem_ld16(o, o_at + b * N + (step - b * steps) * 16 + (static_cast<uint32_t>(warp * 32) << 16));
+      };
+      auto store = [&](const uint32_t (&o)[16], int step) {
+        const int b = step / steps, n0 = (step - b * steps) * 16, d = b * 128 + d0;
         __syncwarp();
 #pragma unroll
         for (int y = 0; y < 16; ++y) turn[y * 32 + lane] = __uint_as_float(o[y]);
         __syncwarp();
+        float4 v[4];
 #pragma unroll
-        for (int y = 0; y < 16; y += 4) {
-          const int n = n0 + y + y0;
-          const float4 v = *reinterpret_cast<const float4 *>(turn + (y + y0) * 32 + (lane & 7) * 4);
+        for (int y = 0; y < 4; ++y)
+          v[y] = *reinterpret_cast<const float4 *>(turn + (4 * y + y0) * 32 + (lane & 7) * 4);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int n = n0 + 4 * y + y0;
           if (!whole) {
             if (d < m.part_ld)
-              __stcg(reinterpret_cast<float4 *>(part + static_cast<int64_t>(n) * m.part_ld + d), v);
+              __stcg(reinterpret_cast<float4 *>(part + static_cast<int64_t>(n) * m.part_ld + d), v[y]);
           } else if (n < ncol) {
             const float f = sm.factor[n];
             store4<E>(static_cast<E *>(a.out) + static_cast<int64_t>(sm.sees[n]) + d,
-                      make_float4(v.x * f, v.y * f, v.z * f, v.w * f), a.dl - d, m.out_vec);
+                      make_float4(v[y].x * f, v[y].y * f, v[y].z * f, v[y].w * f), a.dl - d, m.out_vec);
           }
+        }
+      };
+      uint32_t even[16], odd[16];
+      fetch(even, 0);
+      for (int step = 0; step < total; step += 2) {
+        tmem_wait_ld();
+        if (step + 1 < total) fetch(odd, step + 1);
+        store(even, step);
+        if (step + 1 < total) {
+          tmem_wait_ld();
+          if (step + 2 < total) fetch(even, step + 2);
+          store(odd, step + 1);
         }
       }
       tc_fence_before();
@@ -592,32 +683,10 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
         }
         for (; ks < end; ++ks, kd += 2, qd += 2) mma_ss(s_at, kd, qd, dq, ks > 0);
       };
-      long long t0 = clock64();
-      while (cp.more()) {
-        bool moved = false;
-        if (cq.more() && !q_half && mbar_poll(bar(sm.full[q_stage][0]), q_use & 1) &&
-            (iq < 2 || mbar_poll(bar(sm.s_empty[iq & 1]), ((iq >> 1) - 1) & 1)) &&
-            (!cq.first() || mbar_poll(bar(sm.q_full), seg & 1))) {
-          tc_fence_after();
-          kd = k_desc + ((q_stage * stage_bytes) >> 4);
-          qd = q_desc;
-          scores(0, ksteps0);
-          q_half = moved = true;
-        }
-        if (q_half && (m.np0 == m.np || mbar_poll(bar(sm.full[q_stage][1]), q_use & 1))) {
-          tc_fence_after();
-          scores(ksteps0, ksteps);
-          tc_commit(bar(sm.s_full[iq & 1]));
-          if (cq.last()) {
-            tc_commit(bar(sm.q_empty));
-            ++seg;
-          }
-          cq.step(piece);
-          ++iq;
-          if (++q_stage == m.nst) q_stage = 0, ++q_use;
-          q_half = false;
-          moved = true;
-        }
+      bool moved = false;
+      // A tile's values give its stage back, so they go between the two halves of
+      // the next tile's scores (34 MMAs, 1450 cycles) as soon as they can.
+      auto values = [&]() {
         if (ip < iq && mbar_poll(bar(sm.p_full), ip & 1)) {
           tc_fence_after();
           uint64_t vd = v_desc + ((p_stage * stage_bytes) >> 4);
@@ -634,6 +703,35 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
           cp.step(piece);
           ++ip;
           if (++p_stage == m.nst) p_stage = 0;
+          moved = true;
+        }
+      };
+      long long t0 = clock64();
+      while (cp.more()) {
+        moved = false;
+        values();
+        if (cq.more() && !q_half && mbar_poll(bar(sm.full[q_stage][0]), q_use & 1) &&
+            (iq < 2 || mbar_poll(bar(sm.s_empty[iq & 1]), ((iq >> 1) - 1) & 1)) &&
+            (!cq.first() || mbar_poll(bar(sm.q_full), seg & 1))) {
+          tc_fence_after();
+          kd = k_desc + ((q_stage * stage_bytes) >> 4);
+          qd = q_desc;
+          scores(0, ksteps0);
+          q_half = moved = true;
+        }
+        values();
+        if (q_half && (m.np0 == m.np || mbar_poll(bar(sm.full[q_stage][1]), q_use & 1))) {
+          tc_fence_after();
+          scores(ksteps0, ksteps);
+          tc_commit(bar(sm.s_full[iq & 1]));
+          if (cq.last()) {
+            tc_commit(bar(sm.q_empty));
+            ++seg;
+          }
+          cq.step(piece);
+          ++iq;
+          if (++q_stage == m.nst) q_stage = 0, ++q_use;
+          q_half = false;
           moved = true;
         }
         if (moved) {
@@ -1012,6 +1110,7 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
   m.tpg = tokens_per_request < room ? (tokens_per_request < 1 ? 1 : tokens_per_request) : room;
   const int N = columns_for(m.hc, m.tpg);
   m.tpg = N / m.hc < m.tpg ? N / m.hc : m.tpg;
+  m.columns = N;
   m.np = (args.D + 63) / 64;
   m.nb = (args.dl + 127) / 128;
   m.np0 = (m.nb + 1) / 2 * 2;
