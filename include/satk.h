@@ -340,8 +340,8 @@ int satk_dcp_emit_rows(const int32_t *ids, int64_t T, int32_t k, int64_t ld_ids,
  *  - a token that sees no key gets an output of zeros and an lse of -inf;
  *  - lse (nullable, float [T, H] contiguous) is the natural logarithm of the
  *    sum of exp(score), what satk_latent_merge takes;
- *  - keys that no token of a call's row group sees are not read; infinities
- *    and NaN in keys that a token does not see do not reach its output.  A
+ *  - what cache rows hold that a token does not see, infinities and NaN
+ *    included, does not reach its output (rows near them may be read).  A
  *    non-finite key row that it does see may make its whole output row NaN.
  */
 

@@ -112,7 +112,7 @@ __device__ __forceinline__ int64_t per_cta(int64_t tiles, int ctas) {
 // cycles each for 64 columns x 512 values, where a tile takes 3.8 K) and the join
 // of its share.  Where every item can have a CTA of its own and the longest is
 // longer than an equal piece by no more than that, nothing is cut (128 tokens of
-// 2048 rows, 64 heads: 89 us cut, 8x us whole).
+// 2048 rows, 64 heads: 89 us cut, 86 us whole).
 __device__ __forceinline__ int cut_cost(int columns) { return 2 + 10 * columns / 64; }
 
 struct PlanScratch {
@@ -616,43 +616,54 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
       // Of the 16-column steps of each block only those with a column in use; the
       // next step's values are on their way while one is stored.
       const int steps = (ncol + 15) >> 4, total = m.nb * steps;
-      auto fetch = [&](uint32_t (&o)[16], int step) {
-        const int b = step / steps;
-        tmem_ld16(o, o_at + b * N + (step - b * steps) * 16 + (static_cast<uint32_t>(warp * 32) << 16));
+      int fetched = 0, fetch_at = 0;  // the step's column in tensor memory
+      auto fetch = [&](uint32_t (&o)[16]) {
+        tmem_ld16(o, o_at + fetch_at + (static_cast<uint32_t>(warp * 32) << 16));
+        fetch_at += 16;
+        if (++fetched == steps) fetched = 0, fetch_at += N - steps * 16;
       };
-      auto store = [&](const uint32_t (&o)[16], int step) {
-        const int b = step / steps, n0 = (step - b * steps) * 16, d = b * 128 + d0;
+      int n0 = 0, d = d0;
+      auto store = [&](const uint32_t (&o)[16]) {
         __syncwarp();
 #pragma unroll
         for (int y = 0; y < 16; ++y) turn[y * 32 + lane] = __uint_as_float(o[y]);
         __syncwarp();
+        // All of shared memory's part first: stores to memory could alias it.
         float4 v[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          v[y] = *reinterpret_cast<const float4 *>(turn + (4 * y + y0) * 32 + (lane & 7) * 4);
+        float f[4];
+        long long off[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const int n = n0 + 4 * y + y0;
-          if (!whole) {
-            if (d < m.part_ld)
-              __stcg(reinterpret_cast<float4 *>(part + static_cast<int64_t>(n) * m.part_ld + d), v[y]);
-          } else if (n < ncol) {
-            const float f = sm.factor[n];
-            store4<E>(static_cast<E *>(a.out) + static_cast<int64_t>(sm.sees[n]) + d,
-                      make_float4(v[y].x * f, v[y].y * f, v[y].z * f, v[y].w * f), a.dl - d, m.out_vec);
-          }
+          v[y] = *reinterpret_cast<const float4 *>(turn + (4 * y + y0) * 32 + (lane & 7) * 4);
+          f[y] = sm.factor[n0 + 4 * y + y0];
+          off[y] = static_cast<long long>(sm.sees[n0 + 4 * y + y0]);
         }
+        if (whole) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (n0 + 4 * y + y0 < ncol)
+              store4<E>(static_cast<E *>(a.out) + off[y] + d,
+                        make_float4(v[y].x * f[y], v[y].y * f[y], v[y].z * f[y], v[y].w * f[y]),
+                        a.dl - d, m.out_vec);
+        } else if (d < m.part_ld) {
+          float *to = part + (n0 + y0) * m.part_ld + d;
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            __stcg(reinterpret_cast<float4 *>(to + 4 * y * m.part_ld), v[y]);
+        }
+        n0 += 16;
+        if (n0 >= steps * 16) n0 = 0, d += 128;
       };
       uint32_t even[16], odd[16];
-      fetch(even, 0);
+      fetch(even);
       for (int step = 0; step < total; step += 2) {
         tmem_wait_ld();
-        if (step + 1 < total) fetch(odd, step + 1);
-        store(even, step);
+        if (step + 1 < total) fetch(odd);
+        store(even);
         if (step + 1 < total) {
           tmem_wait_ld();
-          if (step + 2 < total) fetch(even, step + 2);
-          store(odd, step + 1);
+          if (step + 2 < total) fetch(even);
+          store(odd);
         }
       }
       tc_fence_before();
