@@ -88,6 +88,7 @@ struct MmaArgs {
   int nh, hc;    // head chunks and heads per chunk
   int tpg;       // tokens per group
   int columns;   // N
+  int may_cut;   // 0: the sizes alone rule out that a group is cut
   int np, nst;   // 64-column panels of a key row, stages
   int np0;       // panels of a stage's first half (all of them: there is no second)
   int nb;        // 128-column blocks of a value
@@ -113,7 +114,7 @@ __device__ __forceinline__ int64_t per_cta(int64_t tiles, int ctas) {
 // of its share.  Where every item can have a CTA of its own and the longest is
 // longer than an equal piece by no more than that, nothing is cut (128 tokens of
 // 2048 rows, 64 heads: 89 us cut, 86 us whole).
-__device__ __forceinline__ int cut_cost(int columns) { return 2 + 10 * columns / 64; }
+__host__ __device__ __forceinline__ int cut_cost(int columns) { return 2 + 10 * columns / 64; }
 
 struct PlanScratch {
   int64_t tiles[32];
@@ -1078,7 +1079,8 @@ int launch(const MmaArgs &m, int ctas, int smem, cudaStream_t stream) {
   int rc = SATK_OK;
   if (launch_early(latent_attend_mma_kernel<E, N, BOX>, dim3(ctas), threads_of(BOX), smem, stream,
                    m) != cudaSuccess ||
-      launch_early(latent_join_kernel<E>, dim3(ctas, kJoinY), 256, 0, stream, m, N) != cudaSuccess)
+      (m.may_cut && launch_early(latent_join_kernel<E>, dim3(ctas, kJoinY), 256, 0, stream, m, N) !=
+                        cudaSuccess))
     rc = SATK_ECUDA;
   return rc;
 }
@@ -1171,6 +1173,9 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
                                      a.T, args.T == 1 ? 1024 : a.ld_q_t, m.tpg))
       m.q_box = 0;
     m.inline_plan = a.T <= kInline;
+    // (per_cta() is kMinTiles at least, so this is make_plan()'s rule.)
+    m.may_cut = a.rows == nullptr || static_cast<int64_t>(a.T) * m.nh > ctas ||
+                (a.k + kTile - 1) / kTile + kItemTiles > kMinTiles + cut_cost(N);
     if (!m.inline_plan) latent_plan_kernel<<<1, 1024, 0, stream>>>(m, ctas);
     const int rc = dtype == SATK_BF16 ? launch_all<__nv_bfloat16>(m, N, ctas, smem, stream)
                                       : launch_all<__half>(m, N, ctas, smem, stream);
