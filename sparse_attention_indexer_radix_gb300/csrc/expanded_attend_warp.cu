@@ -2,7 +2,9 @@
 // one pass over the token's visible keys with the running maximum and sum,
 // query and accumulator in registers, one element of every 32 per lane.  Any
 // width, stride and alignment; every warp reads its keys again, so it is L2-
-// and instruction-bound.
+// and instruction-bound.  It serves widths that are not multiples of 16, rows
+// that are not 16-byte aligned and scales that are not positive: 4096 tokens x
+// 8192 keys x 16 heads take 104 ms here and 0.19 ms on the tensor cores.
 #include "expanded_attend.cuh"
 
 namespace satk {

@@ -6,7 +6,10 @@
 // every 32 per lane), takes a key's dot product by a warp reduction and keeps
 // the running maximum and sum.  Every element is its own 2-byte access, so any
 // width, stride and alignment works; each key row is read again by every
-// head's warp, which makes it L2- and instruction-bound.
+// head's warp, which makes it L2- and instruction-bound.  It serves what the
+// tensor-core kernel's 16-byte loads do not fit (widths or row strides that are
+// not multiples of eight, unaligned caches): 64 requests x up to 16384 keys x 32
+// heads take 23.8 ms here and 0.11 ms there.
 #include "latent_attend.cuh"
 
 namespace satk {

