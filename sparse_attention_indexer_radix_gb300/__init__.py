@@ -13,7 +13,8 @@ tensors into it.
 from .binding import (EXPANDED_MAX_QK, EXPANDED_MAX_V, LATENT_MAX, LATENT_MAX_RANKS,
                       LATENT_TAIL_MAX, MERGE_MAX_CANDIDATES, STATUS_BAD_POSITION,
                       STATUS_BAD_REQUEST, STATUS_BAD_ROW, STATUS_DUPLICATE_KEYS,
-                      STATUS_NO_BLOCK, STATUS_SLOTS_EXCEEDED, STATUS_TOO_MANY_TOKENS,
+                      STATUS_NO_BLOCK, STATUS_SLOTS_EXCEEDED, STATUS_STALLED,
+                      STATUS_TOO_MANY_TOKENS,
                       TABLES_MAX_REQUESTS, TOPK_MAX_K, SatkError, StepTables, dcp_emit_rows,
                       dcp_merge_select, dcp_pack, dcp_rescue_select, dcp_topk_pack,
                       latent_attend, latent_attend_expanded, latent_attend_rows, latent_merge,
@@ -26,5 +27,5 @@ __all__ = ["topk_rows", "dcp_pack", "dcp_topk_pack", "dcp_merge_select", "dcp_re
            "MERGE_MAX_CANDIDATES", "step_tables", "StepTables", "latent_store", "latent_attend",
            "latent_attend_rows", "latent_attend_expanded", "latent_merge",
            "latent_workspace_bytes", "STATUS_NO_BLOCK", "STATUS_TOO_MANY_TOKENS",
-           "STATUS_BAD_ROW", "STATUS_BAD_POSITION", "TABLES_MAX_REQUESTS", "LATENT_MAX",
+           "STATUS_BAD_ROW", "STATUS_BAD_POSITION", "STATUS_STALLED", "TABLES_MAX_REQUESTS", "LATENT_MAX",
            "LATENT_TAIL_MAX", "LATENT_MAX_RANKS", "EXPANDED_MAX_QK", "EXPANDED_MAX_V"]

@@ -28,6 +28,7 @@ STATUS_NO_BLOCK = 8
 STATUS_TOO_MANY_TOKENS = 16
 STATUS_BAD_ROW = 32
 STATUS_BAD_POSITION = 64
+STATUS_STALLED = 128
 TOPK_MAX_K = 4096
 MERGE_MAX_CANDIDATES = 32768
 TABLES_MAX_REQUESTS = 8192

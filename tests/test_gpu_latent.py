@@ -456,6 +456,82 @@ def test_more_tokens_than_one_plan():
         assert_close(lse[t], w[1], w[3], f"lse, token {t}")
 
 
+@pytest.mark.parametrize("scale", [-0.15, 0.0])
+def test_scales_of_any_sign(scale):
+    g, rng = gen(61), np.random.RandomState(61)
+    pg = Paged(g, rng, [200, 65], 96, 16, BF16)
+    q = torch.randn(2, 16, 96, generator=g, device=DEV).to(BF16)
+    o, lse, _ = run_paged(q, pg, [0, 1], [200, 65], 64, scale)
+    rows = torch.stack([pg.rows(0, np.arange(65)), pg.rows(1, np.arange(65))]).int().to(DEV)
+    o2, lse2 = satk.latent_attend_rows(q, pg.cache, rows, latent_dim=64, scale=scale)
+    for t, n in ((0, 200), (1, 65)):
+        w = one_token(q[t], pg.keys(t, np.arange(n)), 64, scale, U[BF16])
+        assert_close(o[t], w[0], w[2], f"paged out, token {t}")
+        assert_close(lse[t], w[1], w[3], f"paged lse, token {t}")
+        w = one_token(q[t], pg.keys(t, np.arange(65)), 64, scale, U[BF16])
+        assert_close(o2[t], w[0], w[2], f"rows out, token {t}")
+        assert_close(lse2[t], w[1], w[3], f"rows lse, token {t}")
+    case = expanded_case(g, BF16, 2, 64, 32, 64, [40, 3], [0, 9])
+    q, k, tail, v, ts, ks, ends = case
+    o, lse = satk.latent_attend_expanded(q, k, tail, v, i32(ts), i32(ks), i32(ends), scale=scale)
+    expanded_check(q, k, tail, v, ts, ks, ends, o, lse, scale)
+
+
+@pytest.mark.parametrize("block", [64, 16, 8, 4])
+def test_page_cut_by_the_cache_end(block):
+    """A block whose last rows lie past the cache: they are not seen, the bit
+    is raised, and what a box brings in their place does not matter."""
+    g = gen(63)
+    rows = 4 * block - 3
+    cache = latent_rows(g, rows, 96, F16)
+    table, ends = i32([[1, 3], [0, 2]]), [2 * block, 2 * block - 1]
+    q = torch.randn(2, 16, 96, generator=g, device=DEV).to(F16)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o, lse = satk.latent_attend(q, cache, i32([0, 1]), table, i32(ends), block_size=block,
+                                stride_rows=block, latent_dim=64, scale=0.2, status=status)
+    assert int(status.item()) == satk.STATUS_BAD_ROW
+    for t, at in ((0, list(range(block, 2 * block)) + list(range(3 * block, rows))),
+                  (1, list(range(block)) + list(range(2 * block, 3 * block - 1)))):
+        w = one_token(q[t], cache[torch.tensor(at, device=DEV)], 64, 0.2, U[F16])
+        assert_close(o[t], w[0], w[2], f"out, token {t}")
+        assert_close(lse[t], w[1], w[3], f"lse, token {t}")
+
+
+@pytest.mark.parametrize("selected", [False, True])
+def test_nan_next_to_what_is_seen(selected):
+    """Rows between a request's keys and its block's end, row 0 of the cache
+    (what stands in for skipped entries) and other requests' rows are NaN, in
+    every tile of a long context; heads of one token see one NaN query alone."""
+    g, rng = gen(65), np.random.RandomState(65)
+    ends = [1000, 7, 0, 64, 129]
+    pg = Paged(g, rng, ends, 160, 64, BF16)
+    q = torch.randn(5, 24, 160, generator=g, device=DEV).to(BF16)
+    q[0, 3, 5] = float("nan")
+    if selected:
+        rows = np.full((5, 1100), -1, dtype=np.int32)
+        for t, n in enumerate(ends):
+            rows[t, np.sort(rng.permutation(1100)[:n])] = pg.rows(t, np.arange(n)).numpy()
+        free = sorted(set(range(pg.cache.shape[0])) - set(rows.ravel().tolist()))
+        pg.cache[torch.tensor(free, device=DEV)] = float("inf")
+        o, lse = satk.latent_attend_rows(q, pg.cache, i32(rows), latent_dim=128, scale=0.1)
+    else:
+        o, lse, _ = run_paged(q, pg, range(5), ends, 128, 0.1)
+    assert torch.isnan(o[0, 3]).all() and torch.isnan(lse[0, 3])
+    for t in range(5):
+        heads = [h for h in range(24) if (t, h) != (0, 3)]
+        w = one_token(q[t, heads], pg.keys(t, np.arange(ends[t])), 128, 0.1, U[BF16])
+        assert_close(o[t, heads], w[0], w[2], f"out, token {t}")
+        assert_close(lse[t, heads], w[1], w[3], f"lse, token {t}")
+
+
+def test_step_tables_without_requests():
+    e = torch.zeros(0, dtype=torch.int32, device=DEV)
+    t = satk.step_tables(e, e, i32([1, 2]), torch.zeros(0, 4, dtype=torch.int32, device=DEV),
+                         tokens=3, block_size=16, stride_rows=16)
+    assert t.token_starts.tolist() == [0] and t.blocks_used.tolist() == [0]
+    assert t.slots.tolist() == [-1] * 3 and t.row_ends.tolist() == [0] * 3
+
+
 def test_attend_empty_calls():
     cache = torch.zeros(0, 96, dtype=BF16, device=DEV)
     q = torch.randn(2, 4, 96, device=DEV).to(BF16)
