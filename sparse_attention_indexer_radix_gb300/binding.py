@@ -162,6 +162,11 @@ def _need_cuda(*ts):
             raise SatkError("every tensor must live on a CUDA device")
 
 
+def _int32_or_none(t, name):
+    if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+        raise SatkError(f"{name} must be contiguous int32")
+
+
 def _rowmajor_2d(t, name):
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise SatkError(f"{name} must be 2-D with unit column stride, got "
@@ -297,9 +302,8 @@ def dcp_merge_select(cand: torch.Tensor, k: int, *, packed: bool,
     _rowmajor_2d(ids_out, "ids_out")
     if ids_out.dtype != torch.int32 or ids_out.shape[0] != T or ids_out.shape[1] < k:
         raise SatkError(f"ids_out must be int32 [{T}, >= {k}]")
-    for name, t in (("sat_word", sat_word), ("status", status)):
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
-            raise SatkError(f"{name} must be contiguous int32")
+    _int32_or_none(sat_word, "sat_word")
+    _int32_or_none(status, "status")
     if sat_word is not None and sat_word.numel() < T:
         raise SatkError("sat_word must hold T words")
     ld_out = ids_out.stride(0) if T > 1 else ids_out.shape[1]
@@ -331,6 +335,7 @@ def dcp_rescue_select(packed: torch.Tensor, logits: torch.Tensor, sat_word: torc
     ld = logits.stride(1) if T > 1 else (logits.stride(0) if W > 1 else max(S, 1))
     if W > 1 and T > 1 and logits.stride(0) != ld * T:
         raise SatkError("logits rows must sit at one common stride (rank-major)")
+    _int32_or_none(status, "status")
     words_needed = rescue_recv_words(T, n, k)
     if recv is None:
         recv = torch.zeros(max(words_needed, 1), dtype=torch.int32, device=packed.device)
@@ -378,6 +383,7 @@ def dcp_emit_rows(ids: torch.Tensor, W: int, dcp_rank: int, req_id: torch.Tensor
         raise SatkError(f"rows_out must be int32 [{T}, >= {k}]")
     if valid_out.dtype != torch.int32 or not valid_out.is_contiguous() or valid_out.numel() < T:
         raise SatkError("valid_out must be contiguous int32 with T entries")
+    _int32_or_none(status, "status")
     ld_ids = ids.stride(0) if T > 1 else ids.shape[1]
     ld_rows = rows_out.stride(0) if T > 1 else rows_out.shape[1]
     ld_table = block_table.stride(0) if R > 1 else max(width, 1)
@@ -438,6 +444,14 @@ def _addr(t):
 def _int32_vec(t, n: int, name: str):
     if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous():
         raise SatkError(f"{name} must be contiguous int32 with {n} entries")
+
+
+def _status_addr(status):
+    """The address of the nullable status word: kernels OR bits into four bytes."""
+    if status is None:
+        return None
+    _int32_vec(status, 1, "status")
+    return status.data_ptr()
 
 
 def _bad_layout(t, name: str, dims: int):
@@ -529,13 +543,11 @@ def step_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks:
         for name, t, n in zip(StepTables._fields, out, sizes):
             _int32_vec(t, n, name)
         at = [_addr(t) for t in out]
-    if status is not None:
-        _int32_vec(status, 1, "status")
     rc = lib().satk_step_tables(
         _addr(context_lens), _addr(new_lens), R, W, dcp_rank, block_size, stride_rows,
         _addr(free_blocks), free_blocks.numel(), _addr(block_table), ld,
         width if max_blocks is None else max_blocks, 1 if drafted else 0, tokens, *at,
-        _addr(status), _stream_on(dev))
+        _status_addr(status), _stream_on(dev))
     if rc:
         _check(rc, "satk_step_tables")
     return out
@@ -578,7 +590,7 @@ def latent_store(latent: torch.Tensor, tail: torch.Tensor | None, slots: torch.T
     rc = lib().satk_latent_store(
         _addr(latent), ld, _addr(tail) if dr else None, ld_tail, dt, T, dl, dr, _addr(weight),
         eps, _addr(cos_sin) if dr else None, P, _addr(positions), 1 if interleaved else 0,
-        _addr(slots), _addr(cache), rows, ld_cache, _addr(status), _stream_on(dev))
+        _addr(slots), _addr(cache), rows, ld_cache, _status_addr(status), _stream_on(dev))
     if rc:
         _check(rc, "satk_latent_store")
     return cache
@@ -643,7 +655,7 @@ def latent_attend(q: torch.Tensor, cache: torch.Tensor, req_id: torch.Tensor,
     rc = lib().satk_latent_attend(
         *head, _addr(req_id), _addr(block_table), R, ld_table,
         width if max_blocks is None else max_blocks, block_size, stride_rows, _addr(row_ends),
-        _addr(tree), words, scale, *end, _addr(status), _stream_on(dev))
+        _addr(tree), words, scale, *end, _status_addr(status), _stream_on(dev))
     if rc:
         _check(rc, "satk_latent_attend")
     return out, lse
@@ -667,7 +679,7 @@ def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, rows: torch.Tensor,
     if counts is not None:
         _int32_vec(counts, T, "counts")
     rc = lib().satk_latent_attend_rows(
-        *head, _addr(rows), ld_rows, k, _addr(counts), scale, *end, _addr(status),
+        *head, _addr(rows), ld_rows, k, _addr(counts), scale, *end, _status_addr(status),
         _stream_on(dev))
     if rc:
         _check(rc, "satk_latent_attend_rows")

@@ -1,0 +1,99 @@
+"""What the binding checks before it calls the library, on CPU tensors: the
+queries for devices and streams are stubbed and the calls go to a stand-in
+that records them."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import sparse_attention_indexer_radix_gb300 as satk
+from sparse_attention_indexer_radix_gb300 import binding
+
+BF16 = torch.bfloat16
+
+
+class Library:
+    """Takes any entry point's call, records its name and arguments, returns 0
+    (a size from the workspace query)."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            self.calls.append((name, args))
+            return 64 if name == "satk_latent_workspace_bytes" else 0
+        return entry
+
+
+@pytest.fixture
+def library(monkeypatch):
+    L = Library()
+    monkeypatch.setattr(binding, "lib", lambda: L)
+    monkeypatch.setattr(binding, "_device_of", lambda *ts: 0)
+    monkeypatch.setattr(binding, "_need_cuda", lambda *ts: 0)
+    monkeypatch.setattr(binding, "_stream", lambda device: 0)
+    monkeypatch.setattr(binding, "_stream_on", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return L
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def step_tables(table=None, **kw):
+    return satk.step_tables(i32(4), i32(4), i32(8), i32(4, 6) if table is None else table,
+                            tokens=4, block_size=4, stride_rows=4, **kw)
+
+
+def latent_store(**kw):
+    return satk.latent_store(torch.zeros(4, 32, dtype=BF16), None, i32(4),
+                             torch.zeros(16, 32, dtype=BF16), **kw)
+
+
+def latent_attend(table=None, **kw):
+    return satk.latent_attend(torch.zeros(4, 2, 32, dtype=BF16), torch.zeros(16, 32, dtype=BF16),
+                              i32(4), i32(4, 6) if table is None else table, i32(4), block_size=4,
+                              stride_rows=4, latent_dim=16, scale=1.0, **kw)
+
+
+def latent_attend_rows(**kw):
+    return satk.latent_attend_rows(torch.zeros(4, 2, 32, dtype=BF16),
+                                   torch.zeros(16, 32, dtype=BF16), i32(4, 6), latent_dim=16,
+                                   scale=1.0, **kw)
+
+
+def dcp_rescue_select(**kw):
+    return satk.dcp_rescue_select(i32(2, 4, 33), torch.zeros(2, 4, 64, dtype=BF16), i32(4),
+                                  i32(4, 16), 16, recv=i32(64), **kw)
+
+
+def dcp_emit_rows(table=None, **kw):
+    return satk.dcp_emit_rows(i32(4, 6), 1, 0, i32(4), i32(4, 6) if table is None else table, 4, 4,
+                              **kw)
+
+
+CALLS = [step_tables, latent_store, latent_attend, latent_attend_rows, dcp_rescue_select,
+         dcp_emit_rows]
+
+
+@pytest.mark.parametrize("call", CALLS, ids=lambda f: f.__name__)
+def test_status_is_a_whole_word(call, library, monkeypatch):
+    """Kernels OR bits into four bytes of it: no other type, and not the
+    stand-in address of a tensor without elements."""
+    monkeypatch.setattr(binding, "rescue_recv_words", lambda T, n, k: 64)
+    word = i32(1)
+    call(status=word)
+    assert any(getattr(a, "value", a) == word.data_ptr() for a in library.calls[-1][1])
+    library.calls.clear()
+    for bad in (torch.zeros(1, dtype=torch.uint8), torch.zeros(8, dtype=torch.bool)[1:],
+                torch.zeros(2, dtype=torch.float32)):
+        with pytest.raises(satk.SatkError, match="status"):
+            call(status=bad)
+    assert not [c for c in library.calls if c[0] != "satk_latent_workspace_bytes"]
+    try:
+        call(status=i32(0))
+    except satk.SatkError:
+        return
+    assert binding._EMPTY_BATCH_PTR not in [getattr(a, "value", a) for a in library.calls[-1][1]]
