@@ -173,6 +173,16 @@ def _rowmajor_2d(t, name):
                         f"{tuple(t.shape)} {t.stride()}")
 
 
+def _table_columns(max_blocks, width: int) -> int:
+    """How many columns of a block table count: of the tensor's own at most,
+    although the library would take any number below the row stride."""
+    if max_blocks is None:
+        return width
+    if max_blocks > width:
+        raise SatkError(f"max_blocks {max_blocks} is more than block_table's {width} columns")
+    return max_blocks
+
+
 def topk_rows(logits: torch.Tensor, k: int, row_ends: torch.Tensor | None = None,
               out: torch.Tensor | None = None, *, sorted: bool = False) -> torch.Tensor:
     """Exact top-k column ids of each row of ``logits`` ([rows, cols] float32
@@ -373,7 +383,7 @@ def dcp_emit_rows(ids: torch.Tensor, W: int, dcp_rank: int, req_id: torch.Tensor
     if not req_id.is_contiguous() or req_id.numel() < T:
         raise SatkError("req_id must be contiguous int32 with T entries")
     R, width = block_table.shape
-    max_blocks = width if max_blocks is None else max_blocks
+    max_blocks = _table_columns(max_blocks, width)
     if rows_out is None:
         rows_out = torch.empty((T, k), dtype=torch.int32, device=ids.device)
     if valid_out is None:
@@ -546,7 +556,7 @@ def step_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks:
     rc = lib().satk_step_tables(
         _addr(context_lens), _addr(new_lens), R, W, dcp_rank, block_size, stride_rows,
         _addr(free_blocks), free_blocks.numel(), _addr(block_table), ld,
-        width if max_blocks is None else max_blocks, 1 if drafted else 0, tokens, *at,
+        _table_columns(max_blocks, width), 1 if drafted else 0, tokens, *at,
         _status_addr(status), _stream_on(dev))
     if rc:
         _check(rc, "satk_step_tables")
@@ -654,7 +664,7 @@ def latent_attend(q: torch.Tensor, cache: torch.Tensor, req_id: torch.Tensor,
         words = shape[1]
     rc = lib().satk_latent_attend(
         *head, _addr(req_id), _addr(block_table), R, ld_table,
-        width if max_blocks is None else max_blocks, block_size, stride_rows, _addr(row_ends),
+        _table_columns(max_blocks, width), block_size, stride_rows, _addr(row_ends),
         _addr(tree), words, scale, *end, _status_addr(status), _stream_on(dev))
     if rc:
         _check(rc, "satk_latent_attend")

@@ -97,3 +97,18 @@ def test_status_is_a_whole_word(call, library, monkeypatch):
     except satk.SatkError:
         return
     assert binding._EMPTY_BATCH_PTR not in [getattr(a, "value", a) for a in library.calls[-1][1]]
+
+
+@pytest.mark.parametrize("call", [step_tables, latent_attend, dcp_emit_rows],
+                         ids=lambda f: f.__name__)
+def test_max_blocks_stays_within_the_table(call, library):
+    """Columns past a table that is a slice of a wider one belong to others, and
+    past the last row's they may not exist."""
+    table = i32(4, 10)[:, 2:8]
+    for ok in (None, 0, 5, 6):
+        call(table=table, max_blocks=ok)
+    library.calls.clear()
+    for bad in (7, 8, 10):
+        with pytest.raises(satk.SatkError, match="max_blocks"):
+            call(table=table, max_blocks=bad)
+    assert not [c for c in library.calls if c[0] != "satk_latent_workspace_bytes"]
