@@ -156,10 +156,21 @@ def _check(rc: int, name: str):
         raise SatkError(f"{name} returned {rc}: {msg}")
 
 
-def _need_cuda(*ts):
+def _need_cuda(*ts) -> int:
+    """The CUDA device of the first tensor; every one must live on a CUDA device."""
     for t in ts:
         if t is not None and not t.is_cuda:
             raise SatkError("every tensor must live on a CUDA device")
+    return ts[0].get_device()
+
+
+def _on(device: int, f, *args):
+    """f(*args) with `device` current: launches, a kernel's attributes and the
+    number of SMs go by the current device, not by the tensors'."""
+    if device == torch.cuda.current_device():
+        return f(*args)
+    with torch.cuda.device(device):
+        return f(*args)
 
 
 def _int32_or_none(t, name):
@@ -191,7 +202,7 @@ def topk_rows(logits: torch.Tensor, k: int, row_ends: torch.Tensor | None = None
     written.  ``sorted`` orders them by descending score, ties by ascending
     column (satk_topk_rows_sorted).  Returns ``out`` (allocated [rows, k]
     when not given)."""
-    _need_cuda(logits, row_ends, out)
+    dev = _need_cuda(logits, row_ends, out)
     _rowmajor_2d(logits, "logits")
     if logits.dtype == torch.float32:
         dt = SATK_F32
@@ -212,8 +223,8 @@ def topk_rows(logits: torch.Tensor, k: int, row_ends: torch.Tensor | None = None
     ld_out = out.stride(0) if rows > 1 else out.shape[1]
     f = lib().satk_topk_rows_sorted if sorted else lib().satk_topk_rows
     e = rows == 0
-    rc = f(_ptr(logits, e), dt, rows, cols, ld, _ptr(row_ends, e), k, _ptr(out, e), ld_out,
-           _stream(logits.device))
+    rc = _on(dev, f, _ptr(logits, e), dt, rows, cols, ld, _ptr(row_ends, e), k, _ptr(out, e),
+             ld_out, _stream(logits.device))
     _check(rc, "satk_topk_rows_sorted" if sorted else "satk_topk_rows")
     return out
 
@@ -236,7 +247,7 @@ def dcp_pack(logits: torch.Tensor, local_idx: torch.Tensor,
     """Pack a local top-n (``local_idx`` int32 [rows, n], -1 padded) of the
     bf16 ``logits`` [rows, S] into B' rows ``out`` (int32 [rows, n + n/32],
     contiguous)."""
-    _need_cuda(logits, local_idx, row_ends, out)
+    dev = _need_cuda(logits, local_idx, row_ends, out)
     _rowmajor_2d(logits, "logits")
     _rowmajor_2d(local_idx, "local_idx")
     if logits.dtype != torch.bfloat16 or local_idx.dtype != torch.int32:
@@ -251,8 +262,9 @@ def dcp_pack(logits: torch.Tensor, local_idx: torch.Tensor,
     ld = logits.stride(0) if rows > 1 else max(S, 1)
     ld_idx = local_idx.stride(0) if rows > 1 else n
     e = rows == 0
-    rc = lib().satk_dcp_pack(_ptr(logits, e), rows, S, ld, _ptr(local_idx, e), ld_idx, n,
-                             _ptr(row_ends, e), _ptr(out, e), _stream(logits.device))
+    rc = _on(dev, lib().satk_dcp_pack,
+             _ptr(logits, e), rows, S, ld, _ptr(local_idx, e), ld_idx, n, _ptr(row_ends, e),
+             _ptr(out, e), _stream(logits.device))
     _check(rc, "satk_dcp_pack")
     return out
 
@@ -262,7 +274,7 @@ def dcp_topk_pack(logits: torch.Tensor, n: int, row_ends: torch.Tensor | None = 
     """The local top-n of each bf16 row of ``logits`` [rows, S] written
     straight as B' rows ``out`` (int32 [rows, n + n/32], contiguous): what
     dcp_pack makes of topk_rows(logits, n)."""
-    _need_cuda(logits, row_ends, out)
+    dev = _need_cuda(logits, row_ends, out)
     _rowmajor_2d(logits, "logits")
     if logits.dtype != torch.bfloat16:
         raise SatkError("dcp_topk_pack takes bfloat16 logits")
@@ -276,8 +288,9 @@ def dcp_topk_pack(logits: torch.Tensor, n: int, row_ends: torch.Tensor | None = 
         raise SatkError("row_ends must be contiguous int32")
     ld = logits.stride(0) if rows > 1 else max(S, 1)
     e = rows == 0
-    rc = lib().satk_dcp_topk_pack(_ptr(logits, e), rows, S, ld, _ptr(row_ends, e), n,
-                                  _ptr(out, e), _stream(logits.device))
+    rc = _on(dev, lib().satk_dcp_topk_pack,
+             _ptr(logits, e), rows, S, ld, _ptr(row_ends, e), n, _ptr(out, e),
+             _stream(logits.device))
     _check(rc, "satk_dcp_topk_pack")
     return out
 
@@ -291,7 +304,7 @@ def dcp_merge_select(cand: torch.Tensor, k: int, *, packed: bool,
     packed=False: ``cand`` is [W, T, n, 2] int32 (float32 score bits, global
     id).  packed=True: ``cand`` is int32 [W, T, n + n/32] B' rows; then
     ``sat_word`` (int32 [T]) may receive the saturation words."""
-    _need_cuda(cand, ids_out, sat_word, status)
+    dev = _need_cuda(cand, ids_out, sat_word, status)
     if cand.dtype != torch.int32 or not cand.is_contiguous():
         raise SatkError("cand must be contiguous int32")
     if packed:
@@ -318,8 +331,9 @@ def dcp_merge_select(cand: torch.Tensor, k: int, *, packed: bool,
         raise SatkError("sat_word must hold T words")
     ld_out = ids_out.stride(0) if T > 1 else ids_out.shape[1]
     e = T == 0
-    rc = lib().satk_dcp_merge_select(_ptr(cand, e), fmt, W, T, n, k, _ptr(ids_out, e), ld_out,
-                                     _ptr(sat_word, e), _ptr(status), _stream(cand.device))
+    rc = _on(dev, lib().satk_dcp_merge_select,
+             _ptr(cand, e), fmt, W, T, n, k, _ptr(ids_out, e), ld_out, _ptr(sat_word, e),
+             _ptr(status), _stream(cand.device))
     _check(rc, "satk_dcp_merge_select")
     return ids_out
 
@@ -332,7 +346,7 @@ def dcp_rescue_select(packed: torch.Tensor, logits: torch.Tensor, sat_word: torc
     ``recv`` and the re-select of the saturated rows of ``ids_out`` (in
     place).  ``logits`` is bf16 [W, T, S] (unit column stride, rows at a
     common stride); ``row_ends`` int32 [W, T].  Returns ``recv``."""
-    _need_cuda(packed, logits, sat_word, ids_out, recv, row_ends, status)
+    dev = _need_cuda(packed, logits, sat_word, ids_out, recv, row_ends, status)
     if packed.dtype != torch.int32 or packed.dim() != 3 or not packed.is_contiguous():
         raise SatkError("packed must be contiguous int32 [W, T, n + n/32]")
     W, T, words = packed.shape
@@ -354,10 +368,10 @@ def dcp_rescue_select(packed: torch.Tensor, logits: torch.Tensor, sat_word: torc
     _rowmajor_2d(ids_out, "ids_out")
     ld_out = ids_out.stride(0) if T > 1 else ids_out.shape[1]
     e = T == 0
-    rc = lib().satk_dcp_rescue_select(_ptr(packed, e), W, T, n, k, _ptr(logits, e), S, ld,
-                                      _ptr(row_ends, e), _ptr(sat_word, e), _ptr(recv, e),
-                                      _ptr(ids_out, e), ld_out, _ptr(status),
-                                      _stream(packed.device))
+    rc = _on(dev, lib().satk_dcp_rescue_select,
+             _ptr(packed, e), W, T, n, k, _ptr(logits, e), S, ld, _ptr(row_ends, e),
+             _ptr(sat_word, e), _ptr(recv, e), _ptr(ids_out, e), ld_out, _ptr(status),
+             _stream(packed.device))
     _check(rc, "satk_dcp_rescue_select")
     return recv
 
@@ -373,7 +387,7 @@ def dcp_emit_rows(ids: torch.Tensor, W: int, dcp_rank: int, req_id: torch.Tensor
     [R, width] (unit column stride; ``max_blocks`` defaults to its width),
     ``req_id`` int32 [T].  Returns (rows_out [T, >= k] int32, valid_out [T]
     int32)."""
-    _need_cuda(ids, req_id, block_table, rows_out, valid_out, status)
+    dev = _need_cuda(ids, req_id, block_table, rows_out, valid_out, status)
     _rowmajor_2d(ids, "ids")
     _rowmajor_2d(block_table, "block_table")
     if ids.dtype != torch.int32 or req_id.dtype != torch.int32 or block_table.dtype != torch.int32:
@@ -398,10 +412,10 @@ def dcp_emit_rows(ids: torch.Tensor, W: int, dcp_rank: int, req_id: torch.Tensor
     ld_rows = rows_out.stride(0) if T > 1 else rows_out.shape[1]
     ld_table = block_table.stride(0) if R > 1 else max(width, 1)
     e = T == 0
-    rc = lib().satk_dcp_emit_rows(_ptr(ids, e), T, k, ld_ids, W, dcp_rank, _ptr(req_id, e),
-                                  _ptr(block_table, e), R, ld_table, max_blocks, block_size,
-                                  stride_rows, _ptr(rows_out, e), ld_rows, _ptr(valid_out, e),
-                                  _ptr(status), _stream(ids.device))
+    rc = _on(dev, lib().satk_dcp_emit_rows,
+             _ptr(ids, e), T, k, ld_ids, W, dcp_rank, _ptr(req_id, e), _ptr(block_table, e), R,
+             ld_table, max_blocks, block_size, stride_rows, _ptr(rows_out, e), ld_rows,
+             _ptr(valid_out, e), _ptr(status), _stream(ids.device))
     _check(rc, "satk_dcp_emit_rows")
     return rows_out, valid_out
 
@@ -553,7 +567,8 @@ def step_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks:
         for name, t, n in zip(StepTables._fields, out, sizes):
             _int32_vec(t, n, name)
         at = [_addr(t) for t in out]
-    rc = lib().satk_step_tables(
+    rc = _on(
+        dev, lib().satk_step_tables,
         _addr(context_lens), _addr(new_lens), R, W, dcp_rank, block_size, stride_rows,
         _addr(free_blocks), free_blocks.numel(), _addr(block_table), ld,
         _table_columns(max_blocks, width), 1 if drafted else 0, tokens, *at,
@@ -597,7 +612,8 @@ def latent_store(latent: torch.Tensor, tail: torch.Tensor | None, slots: torch.T
             raise SatkError("cos_sin needs positions")
         _int32_vec(positions, T, "positions")
         P = shape[0]
-    rc = lib().satk_latent_store(
+    rc = _on(
+        dev, lib().satk_latent_store,
         _addr(latent), ld, _addr(tail) if dr else None, ld_tail, dt, T, dl, dr, _addr(weight),
         eps, _addr(cos_sin) if dr else None, P, _addr(positions), 1 if interleaved else 0,
         _addr(slots), _addr(cache), rows, ld_cache, _status_addr(status), _stream_on(dev))
@@ -607,11 +623,12 @@ def latent_store(latent: torch.Tensor, tail: torch.Tensor | None, slots: torch.T
 
 
 def latent_workspace_bytes(heads: int, latent_dim: int) -> int:
-    """Bytes of the scratch of latent_attend and latent_attend_rows."""
+    """Bytes of the scratch of latent_attend and latent_attend_rows on the
+    current device."""
     return int(lib().satk_latent_workspace_bytes(heads, latent_dim))
 
 
-def _latent_call(q, cache, latent_dim, out, lse, workspace):
+def _latent_call(dev, q, cache, latent_dim, out, lse, workspace):
     """Shared checks of the two attentions over cache rows: the tokens, the
     arguments before and after the keys', and the results."""
     T, H, D, ld_t, ld_h = _heads(q, "q")
@@ -624,7 +641,7 @@ def _latent_call(q, cache, latent_dim, out, lse, workspace):
     out, lo_t, lo_h = _heads_out(out, T, H, latent_dim, q)
     lse = _lse_out(lse, T, H, q)
     if workspace is None:
-        size = max(lib().satk_latent_workspace_bytes(H, latent_dim), 16)
+        size = max(_on(dev, lib().satk_latent_workspace_bytes, H, latent_dim), 16)
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     else:
         if not workspace.is_contiguous():
@@ -649,7 +666,7 @@ def latent_attend(q: torch.Tensor, cache: torch.Tensor, req_id: torch.Tensor,
     their first ``latent_dim`` columns.  Returns (out [T, H, latent_dim], lse
     float32 [T, H])."""
     dev = _device_of(q, cache, req_id, block_table, row_ends, tree, out, lse, workspace, status)
-    T, head, end, out, lse = _latent_call(q, cache, latent_dim, out, lse, workspace)
+    T, head, end, out, lse = _latent_call(dev, q, cache, latent_dim, out, lse, workspace)
     R, width, ld_table = _matrix(block_table, "block_table")
     if block_table.dtype is not torch.int32:
         raise SatkError("block_table must be int32")
@@ -662,7 +679,8 @@ def latent_attend(q: torch.Tensor, cache: torch.Tensor, req_id: torch.Tensor,
                 not tree.is_contiguous():
             raise SatkError(f"tree must be contiguous int32 [{T}, >= 1]")
         words = shape[1]
-    rc = lib().satk_latent_attend(
+    rc = _on(
+        dev, lib().satk_latent_attend,
         *head, _addr(req_id), _addr(block_table), R, ld_table,
         _table_columns(max_blocks, width), block_size, stride_rows, _addr(row_ends),
         _addr(tree), words, scale, *end, _status_addr(status), _stream_on(dev))
@@ -681,14 +699,15 @@ def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, rows: torch.Tensor,
     them (negative entries and those past the count are skipped).  Returns
     (out [T, H, latent_dim], lse float32 [T, H])."""
     dev = _device_of(q, cache, rows, counts, out, lse, workspace, status)
-    T, head, end, out, lse = _latent_call(q, cache, latent_dim, out, lse, workspace)
+    T, head, end, out, lse = _latent_call(dev, q, cache, latent_dim, out, lse, workspace)
     n, width, ld_rows = _matrix(rows, "rows")
     k = width if k is None else k
     if rows.dtype is not torch.int32 or n != T or width < k:
         raise SatkError(f"rows must be int32 [{T}, >= {k}]")
     if counts is not None:
         _int32_vec(counts, T, "counts")
-    rc = lib().satk_latent_attend_rows(
+    rc = _on(
+        dev, lib().satk_latent_attend_rows,
         *head, _addr(rows), ld_rows, k, _addr(counts), scale, *end, _status_addr(status),
         _stream_on(dev))
     if rc:
@@ -727,7 +746,8 @@ def latent_attend_expanded(q: torch.Tensor, k: torch.Tensor, tail: torch.Tensor 
     _int32_vec(row_ends, T, "row_ends")
     out, o_t, o_h = _heads_out(out, T, H, dv, q)
     lse = _lse_out(lse, T, H, q)
-    rc = lib().satk_latent_attend_expanded(
+    rc = _on(
+        dev, lib().satk_latent_attend_expanded,
         _addr(q), dt, T, H, dn, dr, q_t, q_h, _addr(k), S, k_s, k_h, _addr(tail) if dr else None,
         ld_tail, _addr(v), dv, v_s, v_h, _addr(token_starts), _addr(key_starts), R,
         _addr(row_ends), scale, _addr(out), o_t, o_h, _addr(lse), _stream_on(dev))
@@ -751,7 +771,8 @@ def latent_merge(parts: torch.Tensor, lse: torch.Tensor, *, out: torch.Tensor | 
         raise SatkError(f"lse must be contiguous float32 [{W}, {T}, {H}]")
     out, o_t, o_h = _heads_out(out, T, H, dv, parts)
     lse_out = _lse_out(lse_out, T, H, parts)
-    rc = lib().satk_latent_merge(
+    rc = _on(
+        dev, lib().satk_latent_merge,
         _addr(parts), dt, W, T, H, dv, stride[0] if W > 1 else T * H * dv,
         stride[1] if T > 1 else H * dv, stride[2] if H > 1 else dv, _addr(lse), _addr(out), o_t,
         o_h, _addr(lse_out), _stream_on(dev))

@@ -17,11 +17,12 @@ class Library:
     (a size from the workspace query)."""
 
     def __init__(self):
-        self.calls = []
+        self.calls, self.devices = [], []
 
     def __getattr__(self, name):
         def entry(*args):
             self.calls.append((name, args))
+            self.devices.append(torch.cuda.current_device())
             return 64 if name == "satk_latent_workspace_bytes" else 0
         return entry
 
@@ -112,3 +113,61 @@ def test_max_blocks_stays_within_the_table(call, library):
         with pytest.raises(satk.SatkError, match="max_blocks"):
             call(table=table, max_blocks=bad)
     assert not [c for c in library.calls if c[0] != "satk_latent_workspace_bytes"]
+
+
+def topk_rows(**kw):
+    return satk.topk_rows(torch.zeros(4, 32), 8, **kw)
+
+
+def dcp_pack():
+    return satk.dcp_pack(torch.zeros(4, 64, dtype=BF16), i32(4, 32))
+
+
+def dcp_topk_pack():
+    return satk.dcp_topk_pack(torch.zeros(4, 64, dtype=BF16), 32)
+
+
+def dcp_merge_select():
+    return satk.dcp_merge_select(i32(2, 4, 33), 16, packed=True)
+
+
+def latent_attend_expanded():
+    x = torch.zeros(4, 2, 32, dtype=BF16)
+    return satk.latent_attend_expanded(x, x, None, x, i32(2), i32(2), i32(4), scale=1.0)
+
+
+def latent_merge():
+    return satk.latent_merge(torch.zeros(2, 4, 2, 32, dtype=BF16), torch.zeros(2, 4, 2))
+
+
+@pytest.mark.parametrize("call", [*CALLS, topk_rows, dcp_pack, dcp_topk_pack, dcp_merge_select,
+                                  latent_attend_expanded, latent_merge], ids=lambda f: f.__name__)
+def test_calls_run_on_their_tensors_device(call, library, monkeypatch):
+    """Tensors on device 1 while device 0 is current: the library (launches,
+    kernel attributes, the SM count behind the workspace's size) is entered
+    with device 1 current, and device 0 is current again afterwards."""
+    current = [0]
+
+    class device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *error):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(binding, "_device_of", lambda *ts: 1)
+    monkeypatch.setattr(binding, "_need_cuda", lambda *ts: 1)
+    monkeypatch.setattr(binding, "rescue_recv_words", lambda T, n, k: 64)
+    call()
+    assert library.devices and set(library.devices) == {1}
+    assert current == [0]
+    library.devices.clear()
+    monkeypatch.setattr(binding, "_device_of", lambda *ts: 0)
+    monkeypatch.setattr(binding, "_need_cuda", lambda *ts: 0)
+    call()
+    assert set(library.devices) == {0}
