@@ -51,12 +51,20 @@ bool tensor_map_16bit(void *map, bool bf16, const void *base, int64_t cols, int6
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows),
                              static_cast<cuuint32_t>(box_outer)};
   const cuuint32_t step[3] = {1, 1, 1};
-  return encode(static_cast<CUtensorMap *>(map),
-                bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                outer > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
+  const auto make = [&] {
+    return encode(static_cast<CUtensorMap *>(map),
+                  bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  outer > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (make()) return true;
+  // A host thread without a CUDA context (this may be its first call: the
+  // runtime gives it one when it launches) is refused by the driver's function.
+  // Setting the current device makes its context current.
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && make();
 }
 
 }  // namespace satk

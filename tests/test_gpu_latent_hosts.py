@@ -1,0 +1,82 @@
+"""Host-side conditions of the latent-cache calls on the GPU: several threads
+that call at once, and batch sizes at the edges of shared memory."""
+from __future__ import annotations
+
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_indexer_radix_gb300 as satk
+from test_gpu_latent import BF16, DEV, expanded_case, gen, i32, latent_rows, tables_oracle
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sparse_attention_indexer_radix_gb300 import build as satk_build
+    satk_build.build()
+
+
+def selected(seed, D, latent):
+    g = gen(seed)
+    cache = latent_rows(g, 256, D, BF16)
+    q = torch.randn(2, 64, D, generator=g, device=DEV).to(BF16)
+    rows = torch.randint(0, 256, (2, 70), generator=g, device=DEV).int()
+    size = satk.latent_workspace_bytes(64, latent)
+    kw = dict(workspace=torch.empty(size, dtype=torch.uint8, device=DEV),
+              out=torch.empty(2, 64, latent, dtype=BF16, device=DEV),
+              lse=torch.empty(2, 64, device=DEV))
+    return lambda: satk.latent_attend_rows(q, cache, rows, latent_dim=latent, scale=0.1, **kw)
+
+
+def expanded(seed, dn, dr, dv):
+    g = gen(seed)
+    q, k, tail, v, ts, ks, ends = expanded_case(g, BF16, 2, dn, dr, dv, [70], [30])
+    args = (q, k, tail, v, i32(ts), i32(ks), i32(ends))
+    kw = dict(out=torch.empty(70, 2, dv, dtype=BF16, device=DEV),
+              lse=torch.empty(70, 2, device=DEV))
+    return lambda: satk.latent_attend_expanded(*args, scale=0.1, **kw)
+
+
+def tables(requests):
+    zero, one = i32(np.zeros(requests)), i32(np.ones(requests))
+    free, table = i32(np.arange(requests)), i32(np.full((requests, 2), -1))
+    out = satk.StepTables(*(i32(np.zeros(n)) for n in (requests + 1, requests, *[requests] * 4, 1)))
+    return lambda: tuple(satk.step_tables(zero, one, free, table, tokens=requests, block_size=4,
+                                          stride_rows=4, out=out))
+
+
+def paged(seed, D, latent):
+    g = gen(seed)
+    cache = latent_rows(g, 256, D, BF16)
+    q = torch.randn(2, 16, D, generator=g, device=DEV).to(BF16)
+    req, table, ends = i32([0, 1]), i32([[0, 2], [1, 3]]), i32([100, 37])
+    return lambda: satk.latent_attend(q, cache, req, table, ends, block_size=64, stride_rows=64,
+                                      latent_dim=latent, scale=0.1)
+
+
+@pytest.mark.parametrize("make,args", [(selected, (3, 576, 512)), (paged, (7, 160, 128)),
+                                       (expanded, (5, 128, 64, 128)), (tables, (8192,))])
+def test_first_call_of_a_thread(make, args):
+    """A call that is a host thread's first use of CUDA."""
+    call = make(*args)
+    want = tuple(x.clone() for x in call())
+    torch.cuda.synchronize()
+    got, errors = [], []
+
+    def work():
+        try:
+            got.extend(call())
+        except satk.SatkError as e:
+            errors.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
