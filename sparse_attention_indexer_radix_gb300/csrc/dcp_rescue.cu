@@ -94,8 +94,11 @@ int launch_push(const uint16_t *logits, int64_t S, int64_t ld, int W, int64_t T,
                 const int32_t *row_ends, const int32_t *sat_word, int32_t *recv,
                 int32_t *status, cudaStream_t st) {
   auto kern = rescue_push_kernel<SUB, ALIGN>;
-  const size_t smem = sizeof(ListSmem<kPushBlock, SUB>) + sizeof(uint32_t) * (size_t)(K + K / 32);
-  if (!allow_smem(kern, smem)) return SATK_ECUDA;
+  const auto size = [](int k) {
+    return sizeof(ListSmem<kPushBlock, SUB>) + sizeof(uint32_t) * (size_t)(k + k / 32);
+  };
+  const size_t smem = size(K);
+  if (!allow_smem(kern, smem, size(SATK_TOPK_MAX_K))) return SATK_ECUDA;
   kern<<<dim3(static_cast<unsigned>(T * slots)), kPushBlock, smem, st>>>(
       logits, S, ld, W, T, K, slots, row_ends, sat_word, recv, status);
   return launch_status();

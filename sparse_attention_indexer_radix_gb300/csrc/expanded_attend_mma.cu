@@ -496,9 +496,8 @@ bool layout(const ExpandedArgs &a, ExpandedMma &m, int &smem) {
   m.nope_panels = (a.dn + 63) / 64;
   m.panels = m.nope_panels + (a.dr > 0 ? 1 : 0);
   m.v_panels = (a.dv + 63) / 64;
-  const int limit = 227 * 1024;
   for (m.nsub = 2; m.nsub >= 1; --m.nsub) {
-    m.slots = (limit - kSmall) / kPanel - m.nsub * m.panels;
+    m.slots = (kSmemLimit - kSmall) / kPanel - m.nsub * m.panels;
     if (m.slots > kMaxSlots) m.slots = kMaxSlots;
     smem = (m.nsub * m.panels + m.slots) * kPanel + kSmall;
     // the values of a tile and the keys of the next one are in use together
@@ -514,7 +513,7 @@ bool rows_aligned(const void *p, int64_t n, int64_t ld, int64_t H, int64_t ld_h)
 template <class E>
 int launch(const ExpandedMma &m, int smem, cudaStream_t stream) {
   const ExpandedArgs &a = m.a;
-  if (!allow_smem(expanded_attend_mma_kernel<E>, smem)) return SATK_ECUDA;
+  if (!allow_smem(expanded_attend_mma_kernel<E>, smem, kSmemLimit)) return SATK_ECUDA;
   const int64_t grid = (a.T / (m.nsub * kRows) + a.R + 1ll) * a.H;
   if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
   expanded_attend_mma_kernel<E><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(m);

@@ -1081,7 +1081,7 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, int smem, c
 
 template <class E, int N, bool BOX>
 int launch(const MmaArgs &m, int ctas, int smem, cudaStream_t stream) {
-  if (!allow_smem(latent_attend_mma_kernel<E, N, BOX>, smem)) return SATK_ECUDA;
+  if (!allow_smem(latent_attend_mma_kernel<E, N, BOX>, smem, kSmemLimit)) return SATK_ECUDA;
   int rc = SATK_OK;
   if (launch_early(latent_attend_mma_kernel<E, N, BOX>, dim3(ctas), threads_of(BOX), smem, stream,
                    m) != cudaSuccess ||
@@ -1136,8 +1136,8 @@ int latent_attend_mma(const LatentArgs &args, int dtype, int tokens_per_request,
   if (m.np0 > m.np) m.np0 = m.np;
   m.part_ld = (args.dl + 3) & ~3;
   m.part_stride = static_cast<int64_t>(N) * m.part_ld + 2 * N;
-  const int fixed = m.np * N * 128 + kPanel + kSmall, limit = 227 * 1024;
-  m.nst = (limit - fixed) / (m.np * kPanel);
+  const int fixed = m.np * N * 128 + kPanel + kSmall;
+  m.nst = (kSmemLimit - fixed) / (m.np * kPanel);
   if (m.nst > kMaxStages) m.nst = kMaxStages;
   const int smem = fixed + m.nst * m.np * kPanel;
   m.q_vec = aligned16(args.q) && (args.T == 1 || args.ld_q_t % 8 == 0) &&

@@ -27,13 +27,20 @@ inline int launch_status() {
   return e == cudaSuccess ? SATK_OK : SATK_ECUDA;
 }
 
-// Raises the dynamic shared-memory limit of a kernel once per process.
+// Lets a launch of `kernel` take `bytes` of dynamic shared memory.  `most` is
+// the largest size that any call of this kernel takes (0: it always takes
+// `bytes`).  The limit set is `most` every time, never a call's own size: it is
+// the kernel's for the whole process, and another thread may be about to launch
+// with more.
 template <class K>
-inline bool allow_smem(K kernel, size_t bytes) {
+inline bool allow_smem(K kernel, size_t bytes, size_t most = 0) {
   if (bytes <= 48 * 1024) return true;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes)) == cudaSuccess;
+                              static_cast<int>(most > bytes ? most : bytes)) == cudaSuccess;
 }
+
+// All the shared memory that a block may have.
+constexpr int kSmemLimit = 227 * 1024;
 
 // CTAs of `kernel` (block threads, smem dynamic bytes) the current device
 // holds at once: SMs x resident CTAs per SM, computed once per kernel and

@@ -200,7 +200,8 @@ extern "C" int satk_step_tables(const int32_t *context_lens, const int32_t *new_
                drafted,      T,           token_starts, lens,      req_id,    positions,
                row_ends,     slots,       blocks_used, status,     log2_or(W), log2_or(block_size)};
   const size_t smem = sizeof(int32_t) * 2 * static_cast<size_t>(R);
-  if (!allow_smem(step_tables_kernel, smem)) return SATK_ECUDA;
+  constexpr size_t kMost = sizeof(int32_t) * 2 * SATK_TABLES_MAX_REQUESTS;
+  if (!allow_smem(step_tables_kernel, smem, kMost)) return SATK_ECUDA;
   const int64_t grid = T > kTablesTokens ? (T + kTablesTokens - 1) / kTablesTokens : 1;
   step_tables_kernel<<<static_cast<unsigned>(grid), kTablesBlock, smem, as_stream(stream)>>>(a);
   return launch_status();

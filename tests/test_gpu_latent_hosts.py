@@ -2,6 +2,7 @@
 that call at once, and batch sizes at the edges of shared memory."""
 from __future__ import annotations
 
+import sys
 import threading
 
 import numpy as np
@@ -9,6 +10,7 @@ import pytest
 import torch
 
 import sparse_attention_indexer_radix_gb300 as satk
+from sparse_attention_indexer_radix_gb300 import binding
 from test_gpu_latent import BF16, DEV, expanded_case, gen, i32, latent_rows, tables_oracle
 
 pytestmark = pytest.mark.gpu
@@ -80,3 +82,59 @@ def test_first_call_of_a_thread(make, args):
     assert not errors, errors
     for x, y in zip(want, got):
         assert torch.equal(x, y)
+
+
+class Recorder:
+    """Passes calls on to the library and keeps the last one."""
+
+    def __init__(self, library):
+        self.library = library
+
+    def __getattr__(self, name):
+        f = getattr(self.library, name)
+
+        def entry(*args):
+            self.last = f, args
+            return f(*args)
+        return entry
+
+
+@pytest.mark.parametrize("make,wide,narrow", [
+    (selected, (3, 576, 512), (4, 64, 64)),
+    (expanded, (5, 192, 64, 128), (6, 32, 0, 32)),
+    (tables, (8192,), (6200,))])
+def test_threads_with_wide_and_narrow_calls(make, wide, narrow):
+    """Two host threads, each on its own stream and buffers, call one kernel
+    with much and with little shared memory, over and over: neither takes it
+    from the other between its setting and the launch."""
+    calls = [make(*wide), make(*narrow)]
+    want = [tuple(x.clone() for x in f()) for f in calls]
+    torch.cuda.synchronize()
+    begin, failed, got = threading.Barrier(2), [0, 0], [None, None]
+
+    def work(i):
+        stream, recorder = torch.cuda.Stream(), Recorder(binding.lib())
+        with torch.cuda.stream(stream):
+            with binding.routed_to(recorder):
+                got[i] = calls[i]()
+            f, args = recorder.last
+            begin.wait()
+            for _ in range(20000):
+                failed[i] += f(*args) != 0
+            stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-5)
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(before)
+    torch.cuda.synchronize()
+    assert failed == [0, 0]
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
