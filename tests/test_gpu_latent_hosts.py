@@ -138,3 +138,19 @@ def test_threads_with_wide_and_narrow_calls(make, wide, narrow):
     for a, b in zip(want, got):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("R", [4096, 4097, 6112, 6113, 6144, 6145, 8192])
+def test_tables_at_the_edges_of_shared_memory(R):
+    """The scan's arrays (8 bytes a request) next to the kernel's fixed ones:
+    below, at and above what a block gets without asking for more."""
+    rng = np.random.RandomState(R)
+    ctx, new = rng.randint(0, 9, R), rng.randint(0, 3, R)
+    free, table = rng.permutation(R * 3)[:2 * R].astype(np.int32), np.zeros((R, 3), np.int32)
+    want = tables_oracle(ctx, new, free, table, 2 * R, 4, 4, 1, 0, False)
+    dt = i32(table)
+    got = satk.step_tables(i32(ctx), i32(new), i32(free), dt, tokens=2 * R, block_size=4,
+                           stride_rows=4)
+    assert np.array_equal(dt.cpu().numpy(), want[0])
+    for name, x, y in zip(satk.StepTables._fields, got, want[1:8]):
+        assert x.cpu().tolist() == list(y), name
