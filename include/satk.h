@@ -74,9 +74,8 @@ enum satk_rc {
                                         the cos/sin table; token skipped    */
 #define SATK_STATUS_STALLED 128      /* an attention kernel gave up a wait
                                         inside the GPU (about two seconds):
-                                        its outputs are not to be used (the
-                                        expanded form, which has no status
-                                        word, writes NaN)                    */
+                                        results that it may have touched are
+                                        NaN, with or without a status word   */
 
 /* Largest K of satk_topk_rows and of the rescue push. */
 #define SATK_TOPK_MAX_K 4096
@@ -551,7 +550,10 @@ int satk_latent_merge(const void *parts, int dtype, int32_t W, int64_t T,
  * position, 4 histogram bin, 8 scratch or plane-word index) instead of
  * trapping.  This call waits for the device, returns the word and, when
  * `clear` is non-zero, zeroes it; 0xffffffff if the device could not be
- * read.  The normal build checks nothing and returns 0.  Not part of the
+ * read.  With `clear` = 2 it leaves 256 there instead of 0: until the next
+ * clearing, each CTA of satk_latent_attend and satk_latent_attend_rows treats
+ * the last of its results as if a wait inside the GPU had been given up
+ * (SATK_STATUS_STALLED).  The normal build checks nothing and returns 0.  Not part of the
  * pages' interface: a test aid of this library.
  */
 uint32_t satk_debug_flags(int clear);

@@ -80,7 +80,7 @@ extern "C" uint32_t satk_debug_flags(int clear) {
       cudaMemcpyFromSymbol(&h, satk::satk_debug_word, sizeof h) != cudaSuccess)
     return 0xffffffffu;
   if (clear) {
-    const unsigned int z = 0u;
+    const unsigned int z = (clear & 2) != 0 ? satk::kDbgStall : 0u;
     if (cudaMemcpyToSymbol(satk::satk_debug_word, &z, sizeof z) != cudaSuccess) return 0xffffffffu;
   }
   return h;

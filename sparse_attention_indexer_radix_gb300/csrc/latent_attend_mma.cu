@@ -597,24 +597,41 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
       }
       named_sync(1, kSoftmax);
       float *part = m.parts + (blockIdx.x * 2 + slot) * m.part_stride;
+      float sum = 0.f;
       if (threadIdx.x < N) {
         const int n = threadIdx.x;
-        const float sum = sm.red[0][n] + sm.red[1][n] + sm.red[2][n] + sm.red[3][n];
+        sum = sm.red[0][n] + sm.red[1][n] + sm.red[2][n] + sm.red[3][n];
         if (whole) {
           sm.factor[n] = sum == 0.f ? 0.f : 1.f / sum;
           sm.sees[n] = sm.token[n] * a.ld_out_t + (w.c * m.hc + n % m.hc) * a.ld_out_h;
-          if (a.lse != nullptr && n < ncol)
-            a.lse[static_cast<int64_t>(sm.token[n]) * a.H + w.c * m.hc + n % m.hc] =
-                sum == 0.f ? -INFINITY : (sm.ref[n] + log2f(sum)) * kLn2;
-        } else {
-          part[static_cast<int64_t>(N) * m.part_ld + n] = sm.ref[n];
-          part[static_cast<int64_t>(N) * m.part_ld + N + n] = sum;
         }
       }
       named_sync(1, kSoftmax);
       mbar_wait(bar(sm.o_done), (i - 1) & 1, dead);
       __syncwarp();
       tc_fence_after();
+      if (satk_stall_asked()) {  // debug build: after the last item nothing waits any more
+        Walk after = w;
+        after.next(piece);
+        if (after.done()) *dead = 1;
+      }
+      if (*dead != 0) {
+        // Some wait so far was given up: what there is may be anything.  The
+        // statistics of a part carry the NaN into the join.
+        sum = NAN;
+        for (int n = lane; n < N; n += 32) sm.factor[n] = NAN;
+        __syncwarp();
+      }
+      if (threadIdx.x < N) {
+        const int n = threadIdx.x;
+        if (!whole) {
+          part[static_cast<int64_t>(N) * m.part_ld + n] = sm.ref[n];
+          part[static_cast<int64_t>(N) * m.part_ld + N + n] = sum;
+        } else if (a.lse != nullptr && n < ncol) {
+          a.lse[static_cast<int64_t>(sm.token[n]) * a.H + w.c * m.hc + n % m.hc] =
+              sum == 0.f ? -INFINITY : (sm.ref[n] + log2f(sum)) * kLn2;
+        }
+      }
       // A warp turns its 32 lanes x 16 columns through its quarter of the weights'
       // buffer, so that eight lanes store 32 consecutive values of a column
       // (stored as they come, a lane a value, 64 columns x 512 took 14 us).

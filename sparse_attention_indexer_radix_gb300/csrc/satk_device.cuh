@@ -40,14 +40,19 @@ constexpr unsigned kDbgList = 1u;     // a shared-memory list index
 constexpr unsigned kDbgOut = 2u;      // an output position
 constexpr unsigned kDbgHist = 4u;     // a histogram bin
 constexpr unsigned kDbgScratch = 8u;  // a scratch or plane-word index
+constexpr unsigned kDbgStall = 256u;  // set by the host: act as if a wait had run out
 #ifdef SATK_DEBUG
 extern __device__ unsigned int satk_debug_word;
 __device__ __forceinline__ bool satk_check(bool ok, unsigned bit) {
   if (!ok) atomicOr(&satk_debug_word, bit);
   return ok;
 }
+__device__ __forceinline__ bool satk_stall_asked() {
+  return (*static_cast<volatile unsigned int *>(&satk_debug_word) & kDbgStall) != 0;
+}
 #else
 __device__ __forceinline__ constexpr bool satk_check(bool, unsigned) { return true; }
+__device__ __forceinline__ constexpr bool satk_stall_asked() { return false; }
 #endif
 
 // ------------------------------------------------------------------ keys --
