@@ -127,7 +127,8 @@ __device__ void find_tile(const ExpandedArgs &a, int tile, int tokens, Small &sm
 template <class E>
 __device__ void outside(const ExpandedArgs &a, int h) {
   const int b = a.R > 0 ? min(max(a.token_starts[0], 0), a.T) : a.T;
-  const int e = a.R > 0 ? max(a.token_starts[a.R], b) : a.T;
+  // (within the tokens: the steps below past the requests' tokens stay in 32 bits)
+  const int e = a.R > 0 ? min(max(a.token_starts[a.R], b), a.T) : a.T;
   for (int t = threadIdx.x >> 5; t < a.T; t += kThreads / 32) {
     if (t >= b && t < e) {
       t = ((e - 1 - t) / (kThreads / 32)) * (kThreads / 32) + t;  // the last such t below e
