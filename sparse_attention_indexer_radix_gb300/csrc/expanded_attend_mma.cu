@@ -49,7 +49,6 @@ constexpr int kMaxSlots = 12;
 // fewer tiles (two panels each at least), so a barrier's last use is over before
 // its next one.
 constexpr int kTiles = 8;
-constexpr float kUnset = -1e30f;
 constexpr float kLag = 8.f;
 
 struct ExpandedMma {
@@ -217,7 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + sub * kRows + lanes, o_at = tmem + 256 + sub * kRows + lanes;
     const int my_tiles = sub < m.nsub ? n_sub[sub] : 0;
-    float l = 0.f, ref = kUnset;
+    // A reference beyond kFine is looked at in every tile (`move`, the maximum that
+    // moves it, is then -inf), whose scores become far_exponent() / scale.
+    float l = 0.f, ref = kUnset, move = kUnset;
     const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
     for (int i = 0; i < my_tiles; ++i) {
       const int k0 = i * kRows;
@@ -239,11 +240,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < kRows; x += 2)
         m4[x >> 1 & 3] = max3(m4[x >> 1 & 3], __uint_as_float(raw[x]), __uint_as_float(raw[x + 1]));
       const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
-      if (__any_sync(~0u, mx - ref > kLag)) {
+      float less = -ref;
+      if (__any_sync(~0u, mx > move)) {
         const float now = fmaxf(ref, mx);
         const float f = exp2_fast(ref - now);
         l *= f;
         ref = now;
+        less = -now;
+        move = now + kLag;
+        if (__any_sync(~0u, fabsf(now) > kFine && now != kUnset)) {
+          // Exponents over the scale: the fmaf below, which then subtracts nothing,
+          // gives them back.
+          const float inverse = 1.f / a.scale_log2;
+#pragma unroll
+          for (int x = 0; x < kRows; ++x)
+            raw[x] = __float_as_uint(far_exponent(__uint_as_float(raw[x]), a.scale_log2, now) * inverse);
+          less = 0.f;
+          move = -INFINITY;
+        }
         if (i > 0) {
           for (int c = 0; c < a.dv; c += 16) {
             uint32_t o[16];
@@ -255,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const float2 less = make_float2(-ref, -ref);
+      const float2 less2 = make_float2(less, less);
       float2 l2[2] = {};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -264,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 32; ++x) {
           const int at = c * 64 + 2 * x;
           float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[at]), __uint_as_float(raw[at + 1])),
-                                scale2, less);
+                                scale2, less2);
           e.x = exp2_fast(e.x);
           e.y = exp2_fast(e.y);
           l2[x & 1] = __fadd2_rn(l2[x & 1], e);

@@ -63,7 +63,6 @@ constexpr int kInline = 512;             // tokens up to which CTAs plan for the
 constexpr int kJoinY = 8;                // CTAs that share a join, one warp a column
 constexpr int kItemTiles = 3;            // tiles that a group's own costs are worth
 constexpr int kMinTiles = 2;             // tiles per SM below which no group is cut
-constexpr float kUnset = -1e30f;         // reference of a column without a score
 constexpr float kLag = 8.f;              // log2 by which scores may pass m_n
 
 // One group: its tokens, the keys any of them may see, and where its tiles
@@ -444,7 +443,9 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
                                         w.k0 == 0 && end > piece.length
                                             ? static_cast<int>((end - 1) / per) + 1 : 0);
       }
-      bool first = true;
+      // near: every reference is at most kFine; else the references are looked at
+      // in every tile, which takes the exponents anew.
+      bool first = true, near = false;
       for (int k = w.k0; k < w.k1; ++k, ++i) {
         mbar_wait(bar(sm.s_full[i & 1]), (i >> 1) & 1, dead);
         mbar_wait(bar(sm.full[stage][0]), use & 1, dead);  // the stage's valid flags
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
                     make_uint4(0, 0, 0, 0);
           }
         }
-        bool pass = first;
+        bool pass = !near;
 #pragma unroll
         for (int x = 0; x < C; ++x) pass |= s[x] > kLag;
         if (named_any(1, kSoftmax, pass)) {
@@ -516,13 +517,14 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
             float mx[C];
 #pragma unroll
             for (int x = 0; x < C; ++x)
-              mx[x] = s[x] == -INFINITY ? s[x] : __uint_as_float(raw[x]) * a.scale_log2;
+              mx[x] = s[x] == -INFINITY ? s[x] : __fmul_rn(__uint_as_float(raw[x]), a.scale_log2);
             int at = c0;
             reduce_keys<Maximum, C, 8>(mx, lane, at);
 #pragma unroll
             for (int x = 0; x < (C + 15) / 16; ++x) sm.red[warp][at + x] = mx[x];
           }
           named_sync(1, kSoftmax);
+          near = true;
 #pragma unroll
           for (int x = 0; x < C; x += 4) {
             float4 now = make_float4(ref[x], ref[x + 1], ref[x + 2], ref[x + 3]), f;
@@ -538,7 +540,8 @@ __global__ void __launch_bounds__(threads_of(BOX), 1)
               const float factor = exp2_fast(ref[at] - to);
               l[at] *= factor;
               ref[at] = to;
-              if (s[at] != -INFINITY) s[at] = fmaf(__uint_as_float(raw[at]), a.scale_log2, -to);
+              near &= fabsf(to) <= kFine || to == kUnset;
+              if (s[at] != -INFINITY) s[at] = far_exponent(__uint_as_float(raw[at]), a.scale_log2, to);
               return factor;
             };
             f.x = move(x, now.x);

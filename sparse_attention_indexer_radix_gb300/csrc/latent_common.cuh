@@ -47,6 +47,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// References of a softmax in log2.  kUnset is that of a row without a score yet:
+// no finite score is below it.  A weight's exponent raw * scale - ref is one fmaf
+// while the reference is at most kFine: the reference is a rounded product, so
+// the fmaf is off from 0 at the largest score by that rounding, 2^-4 at kFine.
+// Beyond, where the rounding grows without bound (2^76 at 1e30: a weight of
+// infinity or of nothing), the product is rounded likewise before the subtraction.
+constexpr float kUnset = -3.402823466e38f;
+constexpr float kFine = 1048576.f;  // 2^20
+__device__ __forceinline__ float far_exponent(float raw, float scale, float ref) {
+  return __fsub_rn(__fmul_rn(raw, scale), ref);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
