@@ -341,7 +341,9 @@ int satk_dcp_emit_rows(const int32_t *ids, int64_t T, int32_t k, int64_t ld_ids,
  *    sum of exp(score), what satk_latent_merge takes;
  *  - what cache rows hold that a token does not see, infinities and NaN
  *    included, does not reach its output (rows near them may be read).  A
- *    non-finite key row that it does see may make its whole output row NaN.
+ *    non-finite key row that it does see may make its whole output row NaN,
+ *    and so may a non-finite value row of the expanded form, whose lse goes
+ *    by the keys alone.
  */
 
 /*

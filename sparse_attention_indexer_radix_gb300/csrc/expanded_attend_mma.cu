@@ -302,10 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_after();
       }
-      // A wait was given up, or a value row that the token sees is not finite
-      // (found before the MMAs that o_done stands for).
-      if (*dead != 0 || *static_cast<volatile int *>(&sm.bad_key) < end) l = NAN;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (*dead != 0) l = NAN;  // a wait was given up
+      // A value row that the token sees is not finite (found before the MMAs that
+      // o_done stands for): its sum of weights is as good as any.
+      const bool odd = *static_cast<volatile int *>(&sm.bad_key) < end;
+      const float inv = odd ? NAN : l == 0.f ? 0.f : 1.f / l;
       E *out = static_cast<E *>(a.out) + t * a.ld_out_t + h * a.ld_out_h;
       for (int c = 0; c < a.dv; c += 16) {
         uint32_t o[16];

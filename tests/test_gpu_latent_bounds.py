@@ -139,3 +139,33 @@ def test_causal_chunk_of_far_scores(new, context):
         assert ((o[t].double() - v.mean(0)).abs()
                 <= U[BF16] * v.mean(0).abs() + 1e-5 * v.abs().mean(0)).all()
         assert ((lse[t].double() - score).abs() <= 1e-6 * abs(score)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("dn", [64, 20])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+def test_expanded_lse_goes_by_the_keys_alone(what, dn, dtype):
+    """Values that are not finite, in tiles that every token sees whole and in
+    those that only some see: the lse of every token is that of its scores, and
+    only the outputs of tokens that see them are not finite."""
+    g = gen(87)
+    H, dv, T, context = 2, 32, 200, 300
+    q, k, _, v, ts, ks, ends = expanded_case(g, dtype, H, dn, 0, dv, [T], [context])
+    for key in (70, 330, 421):
+        clean, _ = satk.latent_attend_expanded(q, k, None, v, i32(ts), i32(ks), i32(ends),
+                                               scale=0.2)
+        odd = v.clone()
+        odd[key, 1, 7] = what
+        o, lse = satk.latent_attend_expanded(q, k, None, odd, i32(ts), i32(ks), i32(ends),
+                                             scale=0.2)
+        for t in range(T):
+            s = torch.einsum("hd,nhd->hn", q[t].double(), k[:ends[t]].double()) * 0.2
+            want = torch.logsumexp(s, 1)
+            ds = torch.einsum("hd,nhd->hn", q[t].double().abs(),
+                              k[:ends[t]].double().abs()).amax(1) * 0.2 * dn * 2.0**-23
+            assert ((lse[t].double() - want).abs() <= ds + 1e-5 + 1e-6 * want.abs()).all(), t
+            assert torch.equal(o[t, 0], clean[t, 0])
+            if ends[t] > key:
+                assert not torch.isfinite(o[t, 1, 7])
+            else:
+                assert torch.equal(o[t, 1], clean[t, 1])
