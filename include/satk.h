@@ -401,10 +401,12 @@ int satk_step_tables(const int32_t *context_lens, const int32_t *new_lens,
  *           sines; positions: int32 [T] (NULL cos_sin: stored as it is).
  *           Pair i is columns (i, i + dr/2), or (2i, 2i + 1) when
  *           `interleaved`; (a, b) becomes (a cos - b sin, a sin + b cos).
- * slots   : int32 [T]; a negative slot skips the token.
+ * slots   : int32 [T]; a negative slot skips the token, the others are
+ *           distinct (as satk_step_tables gives them): tokens that share a
+ *           slot are written at once, and the row may end up with parts of
+ *           each.
  * cache   : [cache_rows, ld_cache] of `dtype`, ld_cache >= dl + dr; only
- *           columns [0, dl + dr) of the slots' rows are written.  Two tokens
- *           with one slot: one of them is kept, unspecified which.
+ *           columns [0, dl + dr) of the slots' rows are written.
  * Errors  : SATK_EINVAL for NULL latent/slots/cache, NULL tail with dr > 0,
  *           NULL positions with cos_sin, T or cache_rows or n_positions < 0,
  *           T >= 2**31, dl < 1, dr < 0, dr odd, ld_latent < dl, ld_tail < dr,
