@@ -585,8 +585,9 @@ def latent_store(latent: torch.Tensor, tail: torch.Tensor | None, slots: torch.T
     """Writes rows [norm(latent) * weight | rotated tail] of new tokens into
     ``cache`` ([rows, >= dl + dr] bfloat16 or float16, in place) at ``slots``
     (int32 [T], negative: skipped, others distinct: tokens that share a slot
-    leave parts of each).  ``weight`` float32 [dl] or None (no norm); ``cos_sin`` float32 [P, dr] (cosines, then sines) with
-    ``positions`` int32 [T], or None (no rotation).  Returns ``cache``."""
+    leave parts of each).  ``weight`` float32 [dl] or None (no norm);
+    ``cos_sin`` float32 [P, dr] (cosines, then sines) with ``positions``
+    int32 [T], or None (no rotation).  Returns ``cache``."""
     dev = _device_of(latent, tail, slots, cache, weight, cos_sin, positions, status)
     T, dl, ld = _matrix(latent, "latent")
     rows, width, ld_cache = _matrix(cache, "cache")
