@@ -434,7 +434,10 @@ size_t satk_latent_workspace_bytes(int32_t H, int32_t dl);
  *
  * q        : [T, H, dl + dr] of `dtype`, token and head strides ld_q_t and
  *            ld_q_h, unit stride inside; already projected into the latent
- *            space.  Consecutive tokens with one req_id share their key reads.
+ *            space.  Consecutive tokens with one req_id share their key reads,
+ *            in groups of up to T / table_rows tokens (rounded up) and 64
+ *            score columns: a table of the requests that have tokens, rather
+ *            than of all slots, makes the largest groups.
  * cache    : [cache_rows, ld_cache] of `dtype`.
  * req_id   : int32 [T]; block_table [table_rows, ld_block_table], max_blocks,
  *            block_size, stride_rows: as in satk_dcp_emit_rows.
@@ -442,7 +445,8 @@ size_t satk_latent_workspace_bytes(int32_t H, int32_t dl);
  *            [0, row_ends[t]) (clamped to the table's max_blocks * block_size).
  * tree     : nullable, int32 [T, tree_words]: it also sees local token
  *            row_ends[t] + b for each set bit b (bit b % 32 of word b / 32) --
- *            the drafted tokens on its path, itself among them.
+ *            the drafted tokens on its path, itself among them.  With tokens
+ *            spread over W ranks the bits count this rank's drafted tokens.
  * out      : [T, H, dl] of `dtype`, strides ld_out_t and ld_out_h.
  * A req_id outside the table, and a row outside [0, cache_rows), raise
  * SATK_STATUS_BAD_REQUEST / SATK_STATUS_BAD_ROW; what they name is not seen.
@@ -547,7 +551,8 @@ int satk_latent_merge(const void *parts, int dtype, int32_t W, int64_t T,
 
 /*
  * satk_debug_flags -- the bounds-check bits of the debug build.  A library
- * built with -DSATK_DEBUG (libsatk_debug.so) checks, inside its kernels,
+ * built with -DSATK_DEBUG (libsatk_debug.so) checks, inside its selection
+ * kernels (the latent-cache ones test what they are given in every build),
  * every shared-memory list index, output position, histogram bin and
  * scratch index that the code relies on an invariant for; a failed check
  * skips the access and ORs a bit into a device word (1 list index, 2 output

@@ -4,7 +4,7 @@ parallel, then linked into one shared library next to this file.
     python -m sparse_attention_indexer_radix_gb300.build [--force] [--debug]
 
 --debug builds libsatk_debug.so instead: the same sources with -DSATK_DEBUG,
-whose kernels check the bounds of their shared-memory list indices, output
+whose selection kernels check the bounds of their shared-memory list indices, output
 positions, histogram bins and scratch indices and record a failed check in
 a device word (satk_debug_flags) rather than trapping.  It is compiled as
 relocatable device code so that every translation unit shares that word.

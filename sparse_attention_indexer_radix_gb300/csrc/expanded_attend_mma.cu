@@ -17,9 +17,14 @@
 // Bounded by the tensor core: per 256 x 128 tile at 192 query/key and 128 value
 // columns it takes 2560 cycles.  A sub-tile's own chain (scores, softmax,
 // values) has to stay below that: the first half of the weights is handed over
-// while the second is still computed.  4096 tokens over 8192 keys, 16 heads: 188
-// us, 1.37 PFLOP/s (72 % of the measured bf16 rate); 256 CTAs of unequal length
+// while the second is still computed.  4096 tokens over 8192 keys, 16 heads: 191
+// us, 1.35 PFLOP/s (71 % of the measured bf16 rate); 256 CTAs of unequal length
 // on 152 SMs leave 9 % idle, the rest are the CTAs' beginnings and ends.
+//
+// P_j is rounded to the values' type (both operands of a product have one): off by
+// half a step of itself at most (bf16 2^-8, fp16 2^-11), the output by that share
+// of sum p |v|, as much as its own rounding may be.  The sums take the weights
+// before the rounding and stay in fp32, like the scores, the maxima and O_j.
 //
 // Keys past a request's end, or that only some tokens see, are masked by value.
 // In tiles with such keys two warps look over the value rows first: one that is

@@ -16,6 +16,13 @@
 // the CTA), so most tiles need no cross-key reduction at all; l is summed per
 // thread and joined once at the end.
 //
+// The weights P are rounded to the cache's type, because both operands of a
+// product have one type and the values are the cache's: each is off by half a
+// step of itself at most (bf16 2^-8, fp16 2^-11), the output by that share of
+// sum p |v|, as much as its own rounding may be.  l sums them before the
+// rounding, so the lse is not touched; statistics, sums, O and partial results
+// are fp32.  In fp16 weights below 2^-25 vanish next to a largest of 1 to 2^8.
+//
 // Key rows reach shared memory in two ways, each its own instantiation:
 //  - BOX, where pages give runs of 8 or more keys that lie together: TMA boxes
 //    of a run x 64 columns.  256 threads: warps 0-3 softmax and results, warp 4
@@ -37,9 +44,9 @@
 // workspace that a second kernel joins in a fixed order.  Up to kInline tokens
 // every CTA works out the line for itself; a kernel before does it for more.
 //
-// Bound and measured: 643 thousand rows of 448 columns, 32 heads (576 MB): 110 us
-// with the join, 5.2 TB/s; 128 x 2048 selected rows of 544 columns, 64 heads (285
-// MB): 87 us, 3.3 TB/s.  A tile's chain (load, scores, softmax, values) is what
+// Bound and measured: 643 thousand rows of 448 columns, 32 heads (576 MB): 109 us
+// with the join, 5.3 TB/s; 128 x 2048 selected rows of 544 columns, 64 heads (285
+// MB): 84 us, 3.4 TB/s.  A tile's chain (load, scores, softmax, values) is what
 // two or three stages have to hide: of 227 KB, 64 heads' queries of 544 columns
 // take 72, and two stages of 72 remain.
 #include <cuda.h>
@@ -118,7 +125,7 @@ __device__ __forceinline__ int64_t per_cta(int64_t tiles, int ctas) {
 // cycles each for 64 columns x 512 values, where a tile takes 3.8 K) and the join
 // of its share.  Where every item can have a CTA of its own and the longest is
 // longer than an equal piece by no more than that, nothing is cut (128 tokens of
-// 2048 rows, 64 heads: 89 us cut, 86 us whole).
+// 2048 rows, 64 heads: 87 us cut, 84 us whole).
 __host__ __device__ __forceinline__ int cut_cost(int columns) { return 2 + 10 * columns / 64; }
 
 struct PlanScratch {

@@ -30,9 +30,9 @@ constexpr unsigned kFull = 0xffffffffu;
 
 // ----------------------------------------------------------- debug checks --
 //
-// Built with -DSATK_DEBUG (libsatk_debug.so), device code checks the bound
+// Built with -DSATK_DEBUG (libsatk_debug.so), the selection kernels check the bound
 // of every shared-memory list index, output position, histogram bin and
-// scratch index that it relies on an invariant for, before the access: a
+// scratch index that they rely on an invariant for, before the access: a
 // failed check skips the access and ORs a bit into the library's debug word
 // (read and cleared by satk_debug_flags), and never traps.  In the normal
 // build satk_check is the constant true and the checks compile away.
