@@ -46,6 +46,8 @@ typedef struct CUstream_st *satk_stream_t;
 
 enum satk_dtype { SATK_F32 = 0, SATK_BF16 = 1, SATK_F16 = 2 };
 enum satk_format { SATK_PAIRS_F32 = 0, SATK_PACKED_BF16 = 1 };
+enum satk_teacher { SATK_TEACHER_LOGITS = 0, SATK_TEACHER_WEIGHTS = 1, SATK_TEACHER_PROBS = 2 };
+enum satk_scope { SATK_DISTILL_ROW = 0, SATK_DISTILL_LISTED = 1 };
 
 enum satk_rc {
   SATK_OK = 0,
@@ -315,6 +317,74 @@ int satk_dcp_emit_rows(const int32_t *ids, int64_t T, int32_t k, int64_t ld_ids,
                        int32_t *valid_out, int32_t *status,
                        satk_stream_t stream);
 
+/*
+ * satk_distill_loss -- how far each row of scores is from a teacher that is
+ * known at a short list of columns: the divergence of the student's softmax
+ * from the teacher's shares, as an indexer is trained against the attention it
+ * selects for, or a model against the top entries of another.
+ *
+ * logits   : [rows, ld_logits] of `dtype` (any of satk_dtype), the student's
+ *            scores s; row i's visible columns are [0, end_i) as in
+ *            satk_topk_rows.  What the others hold does not count.
+ * ids      : int32 [rows, ld_ids], columns [0, k): a row's entries, in any order
+ *            (as satk_topk_rows writes them); one that is negative or not
+ *            visible does not count, a column named twice counts twice.
+ * teacher  : [rows, ld_teacher] of `teacher_dtype`, columns [0, k): the entries'
+ *            values x.  Their shares p by `kind`:
+ *            SATK_TEACHER_LOGITS   exp(x / temperature) over their sum;
+ *            SATK_TEACHER_WEIGHTS  x over the sum of x (satk_latent_rows_weights);
+ *            SATK_TEACHER_PROBS    x as it is (mass may be missing from the list).
+ *            A negative weight or probability counts as 0.
+ * scope    : what the student's shares q = exp(s / temperature - lse) are
+ *            normalised over: SATK_DISTILL_ROW the visible columns,
+ *            SATK_DISTILL_LISTED the entries that count.
+ * loss     : float [rows], sum over the entries of p (log p - log q), where p is
+ *            above 0; 0 for a row whose shares are all 0 (no entry counts).
+ * lse      : float [rows], log of the sum of exp(s / temperature) over the scope
+ *            (-inf when that is empty), what satk_distill_grad takes.
+ * Sums are kept in 32 bits.  An entry with p above 0 and a score of -inf makes
+ * its row's loss +inf; a NaN or +inf among the scope's scores or the entries'
+ * values makes the row's loss (and, among the scores, its lse) NaN.
+ * Errors   : SATK_EINVAL for NULL logits/ids/teacher/loss/lse, an unknown dtype,
+ *            kind or scope, rows or cols < 0 or >= 2**31, k outside
+ *            1..SATK_TOPK_MAX_K, ld_logits < cols, ld_ids < k or ld_teacher < k
+ *            (strides are not used with one row), a temperature that is not
+ *            positive and finite, or whose inverse is not.
+ */
+int satk_distill_loss(const void *logits, int dtype, int64_t rows, int64_t cols,
+                      int64_t ld_logits, const int32_t *row_ends,
+                      const int32_t *ids, int64_t ld_ids, int32_t k,
+                      const void *teacher, int teacher_dtype, int64_t ld_teacher,
+                      int kind, int scope, float temperature, float *loss,
+                      float *lse, satk_stream_t stream);
+
+/*
+ * satk_distill_grad -- the gradient of the scores of satk_distill_loss, whose
+ * arguments it takes again, with the lse that it wrote:
+ *   grad_v = dloss / temperature * (q_v sum p - sum of p over the entries at v),
+ * q_v counted once an entry of column v with SATK_DISTILL_LISTED.  The teacher
+ * is a constant.
+ *
+ * dloss    : float [rows], or one value for all rows with dloss_step 0 (else 1).
+ *            A row whose dloss is 0, or whose shares are all 0, gets zeros
+ *            whatever its scores hold.
+ * grad     : [rows, ld_grad] of `dtype`; columns [0, cols) are written, those
+ *            that are not visible with zeros.  It may be `logits` itself (with
+ *            one stride for both); any other overlap is not supported.
+ * One rounding to `dtype`; the same bits every time.
+ * Errors   : as satk_distill_loss; also SATK_EINVAL for NULL lse/dloss/grad,
+ *            dloss_step not 0 or 1, ld_grad < cols, or grad = logits with
+ *            another stride; SATK_EUNSUPPORTED when rows times the row's
+ *            32768-column pieces passes 2**31.
+ */
+int satk_distill_grad(const void *logits, int dtype, int64_t rows, int64_t cols,
+                      int64_t ld_logits, const int32_t *row_ends,
+                      const int32_t *ids, int64_t ld_ids, int32_t k,
+                      const void *teacher, int teacher_dtype, int64_t ld_teacher,
+                      int kind, int scope, float temperature, const float *lse,
+                      const float *dloss, int32_t dloss_step, void *grad,
+                      int64_t ld_grad, satk_stream_t stream);
+
 /* Largest request count of satk_step_tables. */
 #define SATK_TABLES_MAX_REQUESTS 8192
 /* Largest latent width and rotated tail of the latent operators, the widest
@@ -548,6 +618,88 @@ int satk_latent_merge(const void *parts, int dtype, int32_t W, int64_t T,
                       int64_t ld_h, const float *lse, void *out,
                       int64_t ld_out_t, int64_t ld_out_h, float *lse_out,
                       satk_stream_t stream);
+
+/*
+ * satk_latent_rows_weights -- how much weight the attention over selected rows
+ * gives to each of them, averaged over the heads (what an indexer is trained to
+ * rank by):
+ *   out[t][j] = 1/H sum_h exp(scale q_th . cache[rows[t][j]] - lse_th).
+ *
+ * q      : [T, H, D] of `dtype`, strides ld_q_t, ld_q_h: the D = dl + dr columns
+ *          of satk_latent_attend_rows, whose cache, rows, k and counts are taken
+ *          as there.
+ * lse    : float [T, H] contiguous, as satk_latent_attend_rows or (over all
+ *          ranks) satk_latent_merge gives it.  A head whose lse is -inf adds 0.
+ * out    : float [T, ld_out], columns [0, k): 0 for an entry that is skipped
+ *          (negative, past the token's count, or outside the cache, which raises
+ *          SATK_STATUS_BAD_ROW).  Columns [k, ld_out) are never written.
+ * Sums in 32 bits; a head's weight is at most 1.  A row that is not finite
+ * reaches its own entries only.
+ * Errors : SATK_EINVAL for NULL q/cache/rows/lse/out, T < 0, T >= 2**31, H < 1,
+ *          D < 1, k < 1, cache_rows < 0, a stride below its extent (ld_q_t,
+ *          ld_q_h, ld_cache, ld_rows, ld_out; not used at an extent of one), a
+ *          scale that is not finite, a dtype other than SATK_BF16 / SATK_F16;
+ *          SATK_EUNSUPPORTED for H > 1024 or D > SATK_LATENT_MAX +
+ *          SATK_LATENT_TAIL_MAX.
+ */
+int satk_latent_rows_weights(const void *q, int dtype, int64_t T, int32_t H,
+                             int32_t D, int64_t ld_q_t, int64_t ld_q_h,
+                             const void *cache, int64_t cache_rows,
+                             int64_t ld_cache, const int32_t *rows,
+                             int64_t ld_rows, int32_t k, const int32_t *counts,
+                             float scale, const float *lse, float *out,
+                             int64_t ld_out, int32_t *status,
+                             satk_stream_t stream);
+
+/* Bytes of the workspace of satk_latent_attend_expanded_grad: 8 T H + 4 S H dr
+ * and a little; 0 for invalid arguments.  It need not be initialised, belongs to
+ * one call at a time and holds nothing between calls. */
+size_t satk_latent_expanded_grad_workspace_bytes(int64_t T, int64_t S, int32_t R,
+                                                 int32_t H, int32_t dr);
+
+/*
+ * satk_latent_attend_expanded_grad -- the backward pass of
+ * satk_latent_attend_expanded: gradients of q, k, tail and v from that of out.
+ * The weights are computed again from lse:
+ *   P = exp(scale q . k - lse), dS = P (dout . v - delta),
+ *   delta = sum dout out - dlse,
+ *   grad_v = sum_t P dout, grad_k = scale sum_t dS q, grad_q = scale sum_j dS k,
+ *   grad_tail = the tail's part of grad_k summed over the heads.
+ *
+ * dout     : [T, H, dv] of `dtype`, strides ld_do_t, ld_do_h; dlse: nullable
+ *            float [T, H] contiguous, the gradient of lse.
+ * q, k, tail, v, token_starts, key_starts, row_ends, scale: those of the forward
+ *            call; out (strides ld_out_t, ld_out_h) and lse: what it wrote.
+ * grad_q   : [T, H, dn + dr], grad_k: [S, H, dn], grad_tail: [S, dr] (NULL when
+ *            dr is 0), grad_v: [S, H, dv], of `dtype` with their own strides;
+ *            written whole, zeros for rows that nothing sees or that no request
+ *            has.  They overlap nothing else.
+ * Sums and the rows' statistics are in 32 bits; P and dS are rounded to `dtype`
+ * before their products, the gradients once at the end.  (With SATK_F16 a dS
+ * beyond 65504 is infinite, one below 2**-25 nothing: scale dout accordingly.)
+ * A weight is at most 1, and relies on lse: it is off by about |lse| 2**-23 of
+ * itself.  The same bits every time: no sum depends on the order of arrival.
+ * What a token does not see does not reach its gradient, nor does a token that
+ * does not see a key reach that key's, infinities and NaN included; a token
+ * whose lse is -inf sees nothing.  A row that is not finite may make all of a
+ * gradient row that it does reach NaN.
+ * Errors   : as satk_latent_attend_expanded (lse is required); also SATK_EINVAL
+ *            for NULL dout/lse/grad_q/grad_k/grad_v/workspace, NULL grad_tail
+ *            with dr > 0, workspace not 16-byte aligned or smaller than
+ *            satk_latent_expanded_grad_workspace_bytes.
+ */
+int satk_latent_attend_expanded_grad(
+    const void *dout, int64_t ld_do_t, int64_t ld_do_h, const float *dlse,
+    const void *q, int dtype, int64_t T, int32_t H, int32_t dn, int32_t dr,
+    int64_t ld_q_t, int64_t ld_q_h, const void *k, int64_t S, int64_t ld_k_s,
+    int64_t ld_k_h, const void *tail, int64_t ld_tail, const void *v, int32_t dv,
+    int64_t ld_v_s, int64_t ld_v_h, const int32_t *token_starts,
+    const int32_t *key_starts, int32_t R, const int32_t *row_ends, float scale,
+    const void *out, int64_t ld_out_t, int64_t ld_out_h, const float *lse,
+    void *grad_q, int64_t ld_gq_t, int64_t ld_gq_h, void *grad_k,
+    int64_t ld_gk_s, int64_t ld_gk_h, void *grad_tail, int64_t ld_gtail,
+    void *grad_v, int64_t ld_gv_s, int64_t ld_gv_h, void *workspace,
+    size_t workspace_bytes, satk_stream_t stream);
 
 /*
  * satk_debug_flags -- the bounds-check bits of the debug build.  A library

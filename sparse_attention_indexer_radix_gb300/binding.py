@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libsatk.so")
 
 SATK_F32, SATK_BF16, SATK_F16 = 0, 1, 2
 SATK_PAIRS_F32, SATK_PACKED_BF16 = 0, 1
+SATK_TEACHER_LOGITS, SATK_TEACHER_WEIGHTS, SATK_TEACHER_PROBS = 0, 1, 2
+SATK_DISTILL_ROW, SATK_DISTILL_LISTED = 0, 1
 STATUS_SLOTS_EXCEEDED = 1
 STATUS_DUPLICATE_KEYS = 2
 STATUS_BAD_REQUEST = 4
@@ -44,7 +46,9 @@ EXPORTS = ("satk_topk_rows", "satk_dcp_pack", "satk_dcp_merge_select",
            "dcp_pack", "dcp_merge_select", "dcp_rescue_select", "dcp_emit_rows",
            "satk_dcp_topk_pack", "dcp_topk_pack", "satk_debug_flags", "satk_step_tables",
            "satk_latent_store", "satk_latent_workspace_bytes", "satk_latent_attend",
-           "satk_latent_attend_rows", "satk_latent_attend_expanded", "satk_latent_merge")
+           "satk_latent_attend_rows", "satk_latent_attend_expanded", "satk_latent_merge",
+           "satk_distill_loss", "satk_distill_grad", "satk_latent_rows_weights",
+           "satk_latent_expanded_grad_workspace_bytes", "satk_latent_attend_expanded_grad")
 
 _lock = threading.Lock()
 _lib = None
@@ -87,6 +91,16 @@ def load(path: str) -> ctypes.CDLL:
                                         vp, i64, i64, vp, vp],
         "satk_latent_merge": [vp, c_int, i32, i64, i32, i32, i64, i64, i64, vp, vp, i64, i64,
                               vp, vp],
+        "satk_distill_loss": [vp, c_int, i64, i64, i64, vp, vp, i64, i32, vp, c_int, i64, c_int,
+                              c_int, f32, vp, vp, vp],
+        "satk_distill_grad": [vp, c_int, i64, i64, i64, vp, vp, i64, i32, vp, c_int, i64, c_int,
+                              c_int, f32, vp, vp, i32, vp, i64, vp],
+        "satk_latent_rows_weights": [vp, c_int, i64, i32, i32, i64, i64, vp, i64, i64, vp, i64,
+                                     i32, vp, f32, vp, vp, i64, vp, vp],
+        "satk_latent_attend_expanded_grad": [vp, i64, i64, vp, vp, c_int, i64, i32, i32, i32, i64,
+                                             i64, vp, i64, i64, i64, vp, i64, vp, i32, i64, i64,
+                                             vp, vp, i32, vp, f32, vp, i64, i64, vp, vp, i64, i64,
+                                             vp, i64, i64, vp, i64, vp, i64, i64, vp, size, vp],
     }
     for name, args in sigs.items():
         f = getattr(L, name)
@@ -96,6 +110,8 @@ def load(path: str) -> ctypes.CDLL:
     L.satk_rescue_recv_words.restype = ctypes.c_size_t
     L.satk_latent_workspace_bytes.argtypes = [i32, i32]
     L.satk_latent_workspace_bytes.restype = size
+    L.satk_latent_expanded_grad_workspace_bytes.argtypes = [i64, i64, i32, i32, i32]
+    L.satk_latent_expanded_grad_workspace_bytes.restype = size
     L.satk_status_string.argtypes = [c_int]
     L.satk_status_string.restype = ctypes.c_char_p
     L.satk_debug_flags.argtypes = [c_int]
@@ -780,3 +796,213 @@ def latent_merge(parts: torch.Tensor, lse: torch.Tensor, *, out: torch.Tensor | 
     if rc:
         _check(rc, "satk_latent_merge")
     return out, lse_out
+
+
+# Training: the distillation of an indexer's scores and the backward pass of the
+# prompt attention.
+
+_DTYPE_ANY = {torch.float32: SATK_F32, **_DTYPE16}
+_KINDS = {"logits": SATK_TEACHER_LOGITS, "weights": SATK_TEACHER_WEIGHTS,
+          "probs": SATK_TEACHER_PROBS}
+_SCOPES = {"row": SATK_DISTILL_ROW, "listed": SATK_DISTILL_LISTED}
+
+
+def _float_vec(t, n: int, name: str):
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise SatkError(f"{name} must be contiguous float32 with {n} entries")
+
+
+def _distill_args(logits, ids, teacher, kind, scope, temperature, row_ends, k):
+    """Checks of the arguments that loss and gradient share, and those arguments."""
+    rows, cols, ld = _matrix(logits, "logits")
+    dt = _DTYPE_ANY.get(logits.dtype)
+    if dt is None:
+        raise SatkError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    n, width, ld_ids = _matrix(ids, "ids")
+    k = width if k is None else k
+    if ids.dtype is not torch.int32 or n != rows or width < k:
+        raise SatkError(f"ids must be int32 [{rows}, >= {k}]")
+    n, width, ld_teacher = _matrix(teacher, "teacher")
+    teacher_dt = _DTYPE_ANY.get(teacher.dtype)
+    if teacher_dt is None or n != rows or width < k:
+        raise SatkError(f"teacher must be float32, bfloat16 or float16 [{rows}, >= {k}]")
+    if kind not in _KINDS:
+        raise SatkError(f"kind must be one of {sorted(_KINDS)}, got {kind!r}")
+    if scope not in _SCOPES:
+        raise SatkError(f"scope must be one of {sorted(_SCOPES)}, got {scope!r}")
+    if row_ends is not None:
+        _int32_vec(row_ends, rows, "row_ends")
+    return rows, cols, (_addr(logits), dt, rows, cols, ld, _addr(row_ends), _addr(ids), ld_ids, k,
+                        _addr(teacher), teacher_dt, ld_teacher, _KINDS[kind], _SCOPES[scope],
+                        temperature)
+
+
+def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *,
+                 kind: str = "logits", scope: str = "row", temperature: float = 1.0,
+                 row_ends: torch.Tensor | None = None, k: int | None = None,
+                 loss: torch.Tensor | None = None, lse: torch.Tensor | None = None):
+    """How far each row of ``logits`` ([rows, cols] float32, bfloat16 or
+    float16) is from a teacher known at ``k`` columns: ``ids`` int32
+    [rows, >= k] (as topk_rows writes them, -1: none) with ``teacher``
+    [rows, >= k], which holds "logits", "weights" (shares of their sum) or
+    "probs" (shares as they are).  The student's softmax goes over the visible
+    columns of the "row" or over the "listed" ones.  Returns (loss, lse), float32
+    [rows]; lse is what distill_grad takes."""
+    dev = _device_of(logits, ids, teacher, row_ends, loss, lse)
+    rows, _, args = _distill_args(logits, ids, teacher, kind, scope, temperature, row_ends, k)
+    if loss is None:
+        loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    if lse is None:
+        lse = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _float_vec(loss, rows, "loss")
+    _float_vec(lse, rows, "lse")
+    rc = _on(dev, lib().satk_distill_loss, *args, _addr(loss), _addr(lse), _stream_on(dev))
+    if rc:
+        _check(rc, "satk_distill_loss")
+    return loss, lse
+
+
+def distill_grad(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
+                 lse: torch.Tensor, dloss: torch.Tensor, *, kind: str = "logits",
+                 scope: str = "row", temperature: float = 1.0,
+                 row_ends: torch.Tensor | None = None, k: int | None = None,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of distill_loss's ``logits`` (its arguments again, with the
+    ``lse`` it returned) for ``dloss``: float32 [rows], or one value for every
+    row.  ``out`` ([rows, cols] of the logits' type) may be ``logits`` itself.
+    Columns that are not visible get zeros, and so do rows whose dloss is 0."""
+    dev = _device_of(logits, ids, teacher, lse, dloss, row_ends, out)
+    rows, cols, args = _distill_args(logits, ids, teacher, kind, scope, temperature, row_ends, k)
+    _float_vec(lse, rows, "lse")
+    step = 0 if dloss.numel() == 1 or (dloss.dim() == 1 and dloss.stride(0) == 0) else 1
+    if dloss.dtype is not torch.float32 or dloss.numel() not in (1, rows) or \
+            (step == 1 and not dloss.is_contiguous()):
+        raise SatkError(f"dloss must be float32 with one or {rows} entries")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=logits.dtype, device=logits.device)
+    n, width, ld_out = _matrix(out, "out")
+    if out.dtype is not logits.dtype or (n, width) != (rows, cols):
+        raise SatkError(f"out must be {logits.dtype} [{rows}, {cols}]")
+    rc = _on(dev, lib().satk_distill_grad, *args, _addr(lse), _addr(dloss), step, _addr(out),
+             ld_out, _stream_on(dev))
+    if rc:
+        _check(rc, "satk_distill_grad")
+    return out
+
+
+def latent_rows_weights(q: torch.Tensor, cache: torch.Tensor, rows: torch.Tensor,
+                        lse: torch.Tensor, *, scale: float, counts: torch.Tensor | None = None,
+                        k: int | None = None, out: torch.Tensor | None = None,
+                        status: torch.Tensor | None = None) -> torch.Tensor:
+    """The weight that the attention of ``q`` [T, H, D] gives to each of its
+    selected ``cache`` rows, averaged over the heads: ``rows`` and ``counts`` as
+    latent_attend_rows takes them, ``lse`` float32 [T, H] as it (or latent_merge)
+    returns it.  Returns float32 [T, >= k]; skipped entries get 0."""
+    dev = _device_of(q, cache, rows, lse, counts, out, status)
+    T, H, D, ld_t, ld_h = _heads(q, "q")
+    cache_rows, width, ld_cache = _matrix(cache, "cache")
+    dt = _dtype16(q, "q")
+    if cache.dtype is not q.dtype or width < D:
+        raise SatkError(f"cache must be {q.dtype} and at least {D} wide")
+    n, width, ld_rows = _matrix(rows, "rows")
+    k = width if k is None else k
+    if rows.dtype is not torch.int32 or n != T or width < k:
+        raise SatkError(f"rows must be int32 [{T}, >= {k}]")
+    if counts is not None:
+        _int32_vec(counts, T, "counts")
+    lse = _lse_out(lse, T, H, q)
+    if out is None:
+        out = torch.empty((T, k), dtype=torch.float32, device=q.device)
+    n, width, ld_out = _matrix(out, "out")
+    if out.dtype is not torch.float32 or n != T or width < k:
+        raise SatkError(f"out must be float32 [{T}, >= {k}]")
+    rc = _on(
+        dev, lib().satk_latent_rows_weights,
+        _addr(q), dt, T, H, D, ld_t, ld_h, _addr(cache), cache_rows, ld_cache, _addr(rows),
+        ld_rows, k, _addr(counts), scale, _addr(lse), _addr(out), ld_out, _status_addr(status),
+        _stream_on(dev))
+    if rc:
+        _check(rc, "satk_latent_rows_weights")
+    return out
+
+
+def latent_expanded_grad_workspace_bytes(tokens: int, keys: int, requests: int, heads: int,
+                                         tail_dim: int) -> int:
+    """Bytes of the scratch of latent_attend_expanded_grad."""
+    return int(lib().satk_latent_expanded_grad_workspace_bytes(tokens, keys, requests, heads,
+                                                               tail_dim))
+
+
+def _expanded_input(t, n: int, H: int, width: int, like, name: str):
+    """Row and head strides of a [n, H, width] input of q's type."""
+    rows, heads, w, ld, ld_h = _heads(t, name)
+    if t.dtype is not like.dtype or (rows, heads, w) != (n, H, width):
+        raise SatkError(f"{name} must be {like.dtype} [{n}, {H}, {width}]")
+    return ld, ld_h
+
+
+def latent_attend_expanded_grad(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                                tail: torch.Tensor | None, v: torch.Tensor, out: torch.Tensor,
+                                lse: torch.Tensor, token_starts: torch.Tensor,
+                                key_starts: torch.Tensor, row_ends: torch.Tensor, *, scale: float,
+                                dlse: torch.Tensor | None = None, dq: torch.Tensor | None = None,
+                                dk: torch.Tensor | None = None, dtail: torch.Tensor | None = None,
+                                dv: torch.Tensor | None = None,
+                                workspace: torch.Tensor | None = None):
+    """The backward pass of latent_attend_expanded: its arguments, the ``out`` and
+    ``lse`` that it returned, and the gradients of those (``dout`` like out;
+    ``dlse`` float32 [T, H] or None).  Returns (dq, dk, dtail, dv) like q, k, tail
+    and v; dtail, summed over the heads, is None where tail is."""
+    dev = _device_of(dout, q, k, tail, v, out, lse, token_starts, key_starts, row_ends, dlse, dq,
+                     dk, dtail, dv, workspace)
+    T, H, D, q_t, q_h = _heads(q, "q")
+    S, _, dn, _, _ = _heads(k, "k")
+    width = _heads(v, "v")[2]
+    dt = _dtype16(q, "q")
+    k_s, k_h = _expanded_input(k, S, H, dn, q, "k")
+    v_s, v_h = _expanded_input(v, S, H, width, q, "v")
+    o_t, o_h = _expanded_input(out, T, H, width, q, "out")
+    do_t, do_h = _expanded_input(dout, T, H, width, q, "dout")
+    dr = ld_tail = ld_dtail = 0
+    if tail is not None:
+        n, dr, ld_tail = _matrix(tail, "tail")
+        if tail.dtype is not q.dtype or n != S:
+            raise SatkError(f"tail must be {q.dtype} [{S}, dr]")
+        if dtail is None:
+            dtail = torch.empty((S, dr), dtype=q.dtype, device=q.device)
+        n, w, ld_dtail = _matrix(dtail, "dtail")
+        if dtail.dtype is not q.dtype or (n, w) != (S, dr):
+            raise SatkError(f"dtail must be {q.dtype} [{S}, {dr}]")
+    elif dtail is not None:
+        raise SatkError("dtail without a tail")
+    if D != dn + dr:
+        raise SatkError(f"q must be [T, {H}, {dn} + {dr}]")
+    R = token_starts.numel() - 1
+    if R < 0:
+        raise SatkError("token_starts must have at least one entry")
+    _int32_vec(token_starts, R + 1, "token_starts")
+    _int32_vec(key_starts, R + 1, "key_starts")
+    _int32_vec(row_ends, T, "row_ends")
+    lse = _lse_out(lse, T, H, q)
+    if dlse is not None:
+        _lse_out(dlse, T, H, q)
+    dq, dq_t, dq_h = _heads_out(dq, T, H, D, q)
+    dk, dk_s, dk_h = _heads_out(dk, S, H, dn, q)
+    dv, dv_s, dv_h = _heads_out(dv, S, H, width, q)
+    if workspace is None:
+        size = max(latent_expanded_grad_workspace_bytes(T, S, R, H, dr), 16)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    else:
+        if not workspace.is_contiguous():
+            raise SatkError("workspace must be contiguous")
+        size = workspace.numel() * workspace.element_size()
+    rc = _on(
+        dev, lib().satk_latent_attend_expanded_grad,
+        _addr(dout), do_t, do_h, _addr(dlse), _addr(q), dt, T, H, dn, dr, q_t, q_h, _addr(k), S,
+        k_s, k_h, _addr(tail) if dr else None, ld_tail, _addr(v), width, v_s, v_h,
+        _addr(token_starts), _addr(key_starts), R, _addr(row_ends), scale, _addr(out), o_t, o_h,
+        _addr(lse), _addr(dq), dq_t, dq_h, _addr(dk), dk_s, dk_h, _addr(dtail) if dr else None,
+        ld_dtail, _addr(dv), dv_s, dv_h, _addr(workspace), size, _stream_on(dev))
+    if rc:
+        _check(rc, "satk_latent_attend_expanded_grad")
+    return dq, dk, dtail, dv
