@@ -1,0 +1,466 @@
+// expanded_grad_keys.cu -- gradients of keys, tail and values of the expanded
+// attention on the tensor cores.
+//
+// A CTA takes 128 keys of one request and head and goes over the tokens that see
+// any of them in tiles of 64:
+//   S[key, token]  = [K | tail] Q^T        dP[key, token] = V dO^T
+//   P  = exp2(scale S - lse)               dS = P (dP - delta)
+//   dV += P dO                             dK += dS Q
+// The keys are the M side throughout, so P and dS need no exchange between
+// threads: rounded to the inputs' type (as the forward pass rounds P: off by half
+// a step of themselves), they replace S in tensor memory and are the A operand of
+// the second products.  dV and dK stay in tensor memory for the whole call.  S has
+// two buffers where they fit (two of 64 columns, dP 64, dV 128, dK 192: 512), so
+// that the scores of the next tile are computed while P and dS of this one are.
+//
+// The tail's gradient is summed over the heads by a kernel of its own, from a part
+// of each head: no atomics, the same bits every time.
+//
+// Bounded by the tensor core: at 192 query/key and 128 value columns a 128 x 64
+// tile is 1280 cycles of products, of which the scores and dP read both operands
+// from shared memory (6 KB in 32 cycles: 1.5 times what it delivers).
+#include "expanded_grad_mma.cuh"
+
+namespace satk {
+namespace {
+
+constexpr int kTokens = kGradTokens;  // of a tile
+constexpr int kKeyPanel = kTile * 128, kTokenPanel = kTokens * 128;  // bytes
+constexpr int kMaxStages = 4;
+
+struct KeysMma {
+  ExpandedGradArgs a;
+  GradShape s;
+  int stages, score_buffers;
+  CUtensorMap q, dout, k, tail, v;
+};
+
+// A tile's tokens: -lse in log2, -delta, row ends (0 for one that sees nothing).
+struct Tokens {
+  float less[kTokens], delta[kTokens];
+  int end[kTokens];
+};
+
+struct Small {
+  uint64_t own, full[kMaxStages], empty[kMaxStages], tokens[kMaxStages], looked[kMaxStages];
+  uint64_t s_full[2], dp_full, dp_read, ready, done, issued;
+  int least[kMaxStages][2];  // smallest row end of each half of a tile
+  int odd_end;               // keys below it are seen by a token that is not finite
+  int place[6];              // first key (of all), first key of the request's, keys in the tile,
+                             // keys of the request, first token, tokens
+  int slots;                 // first tile of the request's tokens in the table of ends
+  int live;                  // tiles with a token that sees the keys
+  uint32_t tmem;
+  int dead;
+};
+
+// The tiles of tokens that see a key of this CTA's, in order, by a whole warp.
+struct LiveTiles {
+  const int2 *ends;
+  int count, first_key, base = -32;
+  unsigned mask = 0;
+  __device__ __forceinline__ int next() {
+    while (mask == 0) {
+      base += 32;
+      if (base >= count) return -1;
+      const int i = base + (threadIdx.x & 31);
+      mask = __ballot_sync(~0u, i < count && ends[i].y > first_key);
+    }
+    const int bit = __ffs(mask) - 1;
+    mask &= mask - 1;
+    return base + bit;
+  }
+};
+
+template <class E>
+__global__ void __launch_bounds__(kGradThreads, 1)
+    expanded_grad_keys_kernel(const __grid_constant__ KeysMma m) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const ExpandedGradArgs &a = m.a;
+  const ExpandedArgs &f = a.f;
+  const int panels = m.s.panels, v_panels = m.s.v_panels, stages = m.stages;
+  const uint32_t base = smem_addr(smem);
+  const int v_at = panels * kKeyPanel, ring_at = v_at + v_panels * kKeyPanel;
+  const int stage_bytes = (panels + v_panels) * kTokenPanel, do_at = panels * kTokenPanel;
+  Tokens *tokens = reinterpret_cast<Tokens *>(smem + ring_at + stages * stage_bytes);
+  Small &sm = *reinterpret_cast<Small *>(tokens + stages);
+  volatile int *dead = &sm.dead;
+  auto bar = [&](uint64_t &b) { return smem_addr(&b); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.x % f.H;
+  const int D = f.dn + f.dr;
+
+  if (blockIdx.x >= gridDim.x - f.H) {
+    rows_outside(f.key_starts, f.R, f.S, [&](int64_t s) {
+      E *k = static_cast<E *>(a.dk) + s * a.ld_dk_s + h * a.ld_dk_h;
+      E *v = static_cast<E *>(a.dv) + s * a.ld_dv_s + h * a.ld_dv_h;
+      float *tail = a.tails + (static_cast<int64_t>(h) * f.S + s) * f.dr;
+      for (int c = lane; c < f.dn; c += 32) k[c] = Elem<E>::from(0.f);
+      for (int c = lane; c < f.dv; c += 32) v[c] = Elem<E>::from(0.f);
+      for (int c = lane; c < f.dr; c += 32) tail[c] = 0.f;
+    });
+    return;
+  }
+  if (warp == 0) {
+    const int slot = blockIdx.x / f.H;
+    const int r = request_of_slot(f.key_starts, f.R, f.S, slot);
+    const Span keys = span_of(f.key_starts, r, f.S), mine = span_of(f.token_starts, r, f.T);
+    const int64_t first = static_cast<int64_t>(slot - keys.begin / kTile - r) * kTile;
+    if (lane == 0) {
+      sm.place[0] = static_cast<int>(keys.begin + first);
+      sm.place[1] = static_cast<int>(first);
+      sm.place[2] = static_cast<int>(
+          first < 0 ? 0 : max(static_cast<int64_t>(0), min(static_cast<int64_t>(kTile), keys.end - keys.begin - first)));
+      sm.place[3] = keys.end - keys.begin;
+      sm.place[4] = mine.begin;
+      sm.place[5] = mine.end - mine.begin;
+      sm.slots = mine.begin / kTokens + r;
+      sm.live = 0;
+    }
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(bar(sm.own), 1);
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(bar(sm.full[s]), 1);
+      mbar_init(bar(sm.empty[s]), 1);
+      mbar_init(bar(sm.tokens[s]), 64);
+      mbar_init(bar(sm.looked[s]), 64);
+    }
+    mbar_init(bar(sm.s_full[0]), 1);
+    mbar_init(bar(sm.s_full[1]), 1);
+    mbar_init(bar(sm.dp_full), 1);
+    mbar_init(bar(sm.dp_read), 256);
+    mbar_init(bar(sm.ready), 256);
+    mbar_init(bar(sm.done), 1);
+    mbar_init(bar(sm.issued), 1);
+    sm.dead = 0;
+    sm.odd_end = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  const int key_at = sm.place[0], key0 = sm.place[1], rows = sm.place[2], keys = sm.place[3];
+  const int token0 = sm.place[4], n_tokens = sm.place[5];
+  if (rows == 0) return;
+  LiveTiles tiles{a.ends + sm.slots, (n_tokens + kTokens - 1) / kTokens, key0};
+  {
+    int mine = 0;
+    for (int i = threadIdx.x; i < tiles.count; i += kGradThreads) mine += tiles.ends[i].y > key0;
+    mine = __reduce_add_sync(~0u, mine);
+    if (lane == 0 && mine > 0) atomicAdd(&sm.live, mine);
+  }
+  if (warp == 8) tmem_alloc(smem_addr(&sm.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int n = sm.live, buffers = m.score_buffers;
+  const uint32_t dp_at = tmem + buffers * kTokens, dv_at = dp_at + kTokens;
+  const uint32_t dk_at = dv_at + ((f.dv + 31) & ~31);
+
+  // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168.
+  if (warp < 8) regs_raise<208>(); else regs_lower<88>();
+  if (warp < 8) {
+    // ------------------------------------------------------- P and dS, results
+    // A thread has a key (its TMEM lane) and half of each tile's tokens.
+    const int half = warp >> 2, row = threadIdx.x & 127, key = key0 + row;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float2 scale2 = make_float2(f.scale_log2, f.scale_log2);
+    int stage = 0, around = 0;
+    for (int i = 0; i < n; ++i) {
+      const int buffer = buffers == 2 ? i & 1 : 0;
+      const uint32_t s_at = tmem + buffer * kTokens + half * 32 + lanes;
+      const Tokens &tk = tokens[stage];
+      uint32_t s[32], dp[32];
+      mbar_wait(bar(sm.tokens[stage]), around & 1, dead);
+      mbar_wait(bar(sm.s_full[buffer]), (buffers == 2 ? i >> 1 : i) & 1, dead);
+      __syncwarp();
+      tc_fence_after();
+      tmem_ld32(s, 0, s_at);
+      tmem_wait_ld();
+      const bool masked = sm.least[stage][half] < key0 + kTile;
+      const float2 *less = reinterpret_cast<const float2 *>(tk.less + half * 32);
+      const float2 *delta = reinterpret_cast<const float2 *>(tk.delta + half * 32);
+      const int *end = tk.end + half * 32;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
+                              scale2, less[x]);
+        asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as grad_weight)
+        asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.y));
+        s[2 * x] = __float_as_uint(exp2_fast(e.x));
+        s[2 * x + 1] = __float_as_uint(exp2_fast(e.y));
+      }
+      mbar_wait(bar(sm.dp_full), i & 1, dead);
+      __syncwarp();
+      tc_fence_after();
+      tmem_ld32(dp, 0, dp_at + half * 32 + lanes);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(bar(sm.dp_read));
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const float2 p = make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+        const float2 d = __fmul2_rn(
+            p, __fadd2_rn(make_float2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])), delta[x]));
+        dp[2 * x] = __float_as_uint(d.x);
+        dp[2 * x + 1] = __float_as_uint(d.y);
+      }
+      if (masked) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+          if (key >= end[x]) s[x] = dp[x] = 0;
+      }
+      uint32_t p16[16], d16[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        union {
+          typename Elem<E>::T2 h;
+          uint32_t u;
+        } pk;
+        pk.h = Elem<E>::from2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+        p16[x] = pk.u;
+        pk.h = Elem<E>::from2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]));
+        d16[x] = pk.u;
+      }
+      // This half's 32 columns of scores become 16 of P and 16 of dS.
+      tmem_st16(s_at, p16);
+      tmem_st16(s_at + 16, d16);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(sm.ready));
+      if (++stage == stages) stage = 0, ++around;
+    }
+    if (n > 0) {
+      mbar_wait(bar(sm.done), 0, dead);
+      __syncwarp();
+      tc_fence_after();
+    }
+    const bool nan = *dead != 0 || key < *static_cast<volatile int *>(&sm.odd_end);
+    const int64_t at = key_at + row;
+    E *to_k = static_cast<E *>(a.dk) + at * a.ld_dk_s + h * a.ld_dk_h;
+    E *to_v = static_cast<E *>(a.dv) + at * a.ld_dv_s + h * a.ld_dv_h;
+    float *to_tail = a.tails + (static_cast<int64_t>(h) * f.S + at) * f.dr;
+    for (int c = half * 16; c < f.dv + D; c += 32) {
+      const int ck = c - f.dv;
+      uint32_t x[16];
+      if (n > 0) {
+        tmem_ld16(x, (ck < 0 ? dv_at + c : dk_at + ck) + lanes);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int y = 0; y < 16; ++y) x[y] = 0;
+      }
+      if (row >= rows) {
+        // not one of this request's keys
+      } else if (ck < 0) {
+        store16<E>(to_v + c, x, nan ? NAN : 1.f, m.s.vec_v);
+      } else if (ck < f.dn) {
+        store16<E>(to_k + ck, x, nan ? NAN : a.scale, m.s.vec_k);
+      } else {
+        const float scale = nan ? NAN : a.scale;
+        float4 *to = reinterpret_cast<float4 *>(to_tail + ck - f.dn);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          to[y] = make_float4(__uint_as_float(x[4 * y]) * scale, __uint_as_float(x[4 * y + 1]) * scale,
+                              __uint_as_float(x[4 * y + 2]) * scale, __uint_as_float(x[4 * y + 3]) * scale);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- MMA issue
+    if (elect_leader()) {
+      constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
+      constexpr uint32_t d_s = mma_desc(bf16, false, false, kTile, kTokens);
+      const uint32_t d_v = mma_desc(bf16, false, true, kTile, f.dv);
+      const uint32_t d_k = mma_desc(bf16, false, true, kTile, m.s.one_product ? D : f.dn);
+      const uint32_t d_t = mma_desc(bf16, false, true, kTile, f.dr);
+      const uint64_t k_desc = tile_desc(base, 16, 1024), v_desc = tile_desc(base + v_at, 16, 1024);
+      const uint64_t q_cols = tile_desc(base + ring_at, 16, 1024);
+      const uint64_t q_rows = tile_desc(base + ring_at, kTokenPanel, 1024);
+      const int nope_last = m.s.nope_panels - 1, cut = f.dn - nope_last * 64;
+      const int q_last = f.dr > 0 ? f.dr : cut, v_last = f.dv - (v_panels - 1) * 64;
+      auto scores = [&](int i, int stage, int around) {
+        mbar_wait(bar(sm.full[stage]), around & 1, dead);
+        tc_fence_after();
+        const int buffer = buffers == 2 ? i & 1 : 0;
+        product_over_columns(tmem + buffer * kTokens, k_desc, kKeyPanel,
+                             q_cols + (stage * stage_bytes >> 4), kTokenPanel, d_s, panels, nope_last,
+                             cut, q_last);
+        tc_commit(bar(sm.s_full[buffer]));
+      };
+      auto dps = [&](int stage) {
+        product_over_columns(dp_at, v_desc, kKeyPanel, q_cols + ((stage * stage_bytes + do_at) >> 4),
+                             kTokenPanel, d_s, v_panels, v_panels, 64, v_last);
+        tc_commit(bar(sm.dp_full));
+      };
+      int stage = 0, around = 0;
+      if (n > 0) {
+        mbar_wait(bar(sm.own), 0, dead);
+        scores(0, 0, 0);
+        dps(0);
+      }
+      for (int i = 0; i < n; ++i) {
+        const int next = stage + 1 == stages ? 0 : stage + 1, next_around = around + (next == 0);
+        if (buffers == 2 && i + 1 < n) {
+          scores(i + 1, next, next_around);
+          mbar_wait(bar(sm.dp_read), i & 1, dead);
+          tc_fence_after();
+          dps(next);
+        }
+        mbar_wait(bar(sm.looked[stage]), around & 1, dead);
+        mbar_wait(bar(sm.ready), i & 1, dead);
+        tc_fence_after();
+        const uint32_t p_at = tmem + (buffers == 2 ? i & 1 : 0) * kTokens;
+        const uint64_t q = q_rows + (stage * stage_bytes >> 4), o = q + (do_at >> 4);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          mma_ts(dv_at, p_at + (x >> 1) * 32 + (x & 1) * 8, o + 128 * x, d_v, i > 0 || x > 0);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t ds_at = p_at + (x >> 1) * 32 + 16 + (x & 1) * 8;
+          mma_ts(dk_at, ds_at, q + 128 * x, d_k, i > 0 || x > 0);
+          if (!m.s.one_product)
+            mma_ts(dk_at + f.dn, ds_at, q + (m.s.nope_panels * kTokenPanel >> 4) + 128 * x, d_t, i > 0 || x > 0);
+        }
+        tc_commit(bar(sm.empty[stage]));
+        if (buffers == 1 && i + 1 < n) {
+          scores(i + 1, next, next_around);
+          dps(next);
+        }
+        stage = next;
+        around = next_around;
+      }
+      tc_commit(bar(sm.done));
+      tc_commit(bar(sm.issued));
+      mbar_drain(bar(sm.issued), 0);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // -------------------------------------------------------------------- loads
+    const uint32_t leader = elect_leader();
+    if (n > 0) {
+      if (lane == 0) mbar_expect(bar(sm.own), (panels + v_panels) * kKeyPanel);
+      __syncwarp();
+      for (int p = 0; p < m.s.nope_panels; ++p)
+        tma_box3(leader, base + p * kKeyPanel, &m.k, p * 64, h, key_at, bar(sm.own));
+      if (f.dr > 0)
+        tma_box(leader, base + m.s.nope_panels * kKeyPanel, &m.tail, 0, key_at, bar(sm.own));
+      for (int p = 0; p < v_panels; ++p)
+        tma_box3(leader, base + v_at + p * kKeyPanel, &m.v, p * 64, h, key_at, bar(sm.own));
+    }
+    int stage = 0, around = 0;
+    for (int i = 0; i < n; ++i) {
+      const int t = token0 + tiles.next() * kTokens;
+      if (around > 0) mbar_wait(bar(sm.empty[stage]), (around - 1) & 1, dead);
+      __syncwarp();
+      const uint32_t full = bar(sm.full[stage]), to = base + ring_at + stage * stage_bytes;
+      if (lane == 0) mbar_expect(full, stage_bytes);
+      __syncwarp();
+      for (int p = 0; p < panels; ++p)
+        tma_box3(leader, to + p * kTokenPanel, &m.q, p < m.s.nope_panels ? p * 64 : f.dn, h, t, full);
+      for (int p = 0; p < v_panels; ++p)
+        tma_box3(leader, to + do_at + p * kTokenPanel, &m.dout, p * 64, h, t, full);
+      if (++stage == stages) stage = 0, ++around;
+    }
+    if (n > 0) mbar_drain(bar(sm.own), 0);
+    for (int i = max(0, n - stages); i < n; ++i)
+      mbar_drain(bar(sm.full[i % stages]), (i / stages) & 1);
+  } else {
+    // ------------------------------------------------ the tokens' numbers and rows
+    // A lane has one token of each tile.  Where some token does not see some key, a
+    // row that is not finite would turn a 0 of P or dS into NaN: it is cleared, and
+    // the keys that do see it get NaN.
+    const int half = warp - 10, y = half * 32 + lane;
+    const float2 *stats = a.stats + static_cast<int64_t>(h) * f.T;
+    struct Numbers {
+      float2 st;
+      int end;
+    };
+    auto look_up = [&](int tile) {
+      Numbers x{make_float2(0.f, 0.f), 0};
+      const int64_t i = static_cast<int64_t>(tile) * kTokens + y;
+      if (tile >= 0 && i < n_tokens) {
+        x.st = stats[token0 + i];
+        x.end = min(max(f.row_ends[token0 + i], 0), keys);
+        if (x.st.x == -INFINITY) x = Numbers{make_float2(0.f, 0.f), 0};
+      }
+      return x;
+    };
+    Numbers now = look_up(n > 0 ? tiles.next() : -1);
+    int stage = 0, around = 0;
+    for (int i = 0; i < n; ++i) {
+      if (around > 0) mbar_wait(bar(sm.empty[stage]), (around - 1) & 1, dead);
+      tokens[stage].less[y] = -now.st.x;
+      tokens[stage].delta[y] = -now.st.y;
+      tokens[stage].end[y] = now.end;
+      const int least = __reduce_min_sync(~0u, now.end);
+      if (lane == 0) sm.least[stage][half] = least;
+      __syncwarp();
+      mbar_arrive(bar(sm.tokens[stage]));
+      const int end = now.end;
+      now = look_up(i + 1 < n ? tiles.next() : -1);
+      mbar_wait(bar(sm.full[stage]), around & 1, dead);
+      if (least < key0 + kTile) {
+        unsigned char *q = smem + ring_at + stage * stage_bytes;
+        if (row_is_odd<E>(q, y, panels + v_panels, kTokenPanel)) {
+          clear_row(q, y, panels + v_panels, kTokenPanel);
+          atomicMax(&sm.odd_end, end);
+        }
+        fence_async_shared();
+      }
+      mbar_arrive(bar(sm.looked[stage]));
+      if (++stage == stages) stage = 0, ++around;
+    }
+  }
+  __syncthreads();
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+// Stages and buffers that fit.
+bool layout(const ExpandedGradArgs &a, KeysMma &m, int &smem) {
+  const int D = a.f.dn + a.f.dr, stage = (m.s.panels + m.s.v_panels) * kTokenPanel;
+  const int own = (m.s.panels + m.s.v_panels) * kKeyPanel;
+  m.stages = (kSmemLimit - own - static_cast<int>(sizeof(Small))) / (stage + static_cast<int>(sizeof(Tokens)));
+  if (m.stages > kMaxStages) m.stages = kMaxStages;
+  smem = own + m.stages * (stage + static_cast<int>(sizeof(Tokens))) + static_cast<int>(sizeof(Small));
+  m.score_buffers = 3 * kTokens + ((a.f.dv + 31) & ~31) + D <= 512 ? 2 : 1;
+  return m.stages >= 2;
+}
+
+template <class E>
+int launch(const KeysMma &m, int smem, cudaStream_t stream) {
+  if (!allow_smem(expanded_grad_keys_kernel<E>, smem, kSmemLimit)) return SATK_ECUDA;
+  const int64_t grid = (tile_slots(m.a.f.S, m.a.f.R, kTile) + 1) * m.a.f.H;
+  if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
+  expanded_grad_keys_kernel<E><<<static_cast<unsigned>(grid), kGradThreads, smem, stream>>>(m);
+  return launch_status();
+}
+
+}  // namespace
+
+bool expanded_grad_keys_fits(const ExpandedGradArgs &a, const GradShape &s) {
+  KeysMma m;
+  m.s = s;
+  int smem;
+  return layout(a, m, smem);
+}
+
+int expanded_grad_keys(const ExpandedGradArgs &a, const GradShape &s, int dtype, cudaStream_t stream) {
+  KeysMma m;
+  m.a = a;
+  m.s = s;
+  int smem;
+  const ExpandedArgs &f = a.f;
+  const bool bf16 = dtype == SATK_BF16;
+  if (!layout(a, m, smem)) return SATK_EUNSUPPORTED;
+  if (!grad_map(&m.q, bf16, f.q, f.dn + f.dr, f.H, f.T, f.ld_q_t, f.ld_q_h, kTokens) ||
+      !grad_map(&m.dout, bf16, a.dout, f.dv, f.H, f.T, a.ld_do_t, a.ld_do_h, kTokens) ||
+      !grad_map(&m.k, bf16, f.k, f.dn, f.H, f.S, f.ld_k_s, f.ld_k_h, kTile) ||
+      !grad_map(&m.v, bf16, f.v, f.dv, f.H, f.S, f.ld_v_s, f.ld_v_h, kTile) ||
+      (f.dr > 0 && !tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kTile)))
+    return SATK_ECUDA;
+  return bf16 ? launch<__nv_bfloat16>(m, smem, stream) : launch<__half>(m, smem, stream);
+}
+
+}  // namespace satk

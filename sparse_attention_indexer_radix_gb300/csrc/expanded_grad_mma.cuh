@@ -1,0 +1,115 @@
+// expanded_grad_mma.cuh -- what the two tensor-core kernels of the expanded
+// attention's backward pass share.
+#pragma once
+
+#include <cuda.h>
+#include <type_traits>
+
+#include "expanded_grad.cuh"
+#include "satk_tcgen05.cuh"
+
+namespace satk {
+
+constexpr int kGradThreads = 384;  // warps 0-7 elementwise, 8 MMAs, 9 loads, 10 and 11 rows
+constexpr int kTile = 128;         // rows of the tile that a CTA owns
+constexpr int kMaxPanels = 5;      // 64-column panels of a query or key (dn, then the tail)
+
+// Widths in panels, and where a CTA's work lies.
+struct GradShape {
+  int nope_panels, panels, v_panels;
+  int one_product;  // keys' gradient: one product over all columns (no gap before the tail)
+  int vec_k, vec_v, vec_q;  // 16-byte aligned gradient rows
+};
+
+// The request whose tiles of kTile rows have this slot, by a whole warp: the last
+// one whose first slot, starts[r] / kTile + r, is at or before it.
+__device__ __forceinline__ int request_of_slot(const int32_t *starts, int R, int n, int slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = R;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, r = lo + lane * step;
+    const bool before = r < hi && (lane == 0 || span_of(starts, r, n).begin / kTile + r <= slot);
+    const int count = __popc(__ballot_sync(~0u, before));
+    lo += (count - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// One row of a tile in `panels` 128-byte-swizzled panels `stride` bytes apart:
+// whether a value is not finite, and zeros in its place.  A row's chunks are read
+// from another one on for every lane, clear of bank conflicts.
+template <class E>
+__device__ __forceinline__ bool row_is_odd(const unsigned char *tile, int row, int panels, int stride) {
+  typename Elem<E>::T2 sum = Elem<E>::from2(0.f, 0.f), zero = sum;
+  for (int p = 0; p < panels; ++p) {
+    const unsigned char *at = tile + p * stride + row * 128;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      Pack8<E> c;
+      c.u = *reinterpret_cast<const uint4 *>(at + ((x ^ (row & 7)) << 4));
+#pragma unroll
+      for (int z = 0; z < 4; ++z) sum = __hfma2(c.h[z], zero, sum);  // NaN: not finite
+    }
+  }
+  const float2 f = Elem<E>::to2(sum);
+  return !(f.x == 0.f && f.y == 0.f);
+}
+__device__ __forceinline__ void clear_row(unsigned char *tile, int row, int panels, int stride) {
+  for (int p = 0; p < panels; ++p)
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      *reinterpret_cast<uint4 *>(tile + p * stride + row * 128 + (x << 4)) = make_uint4(0, 0, 0, 0);
+}
+
+// Sixteen columns of a gradient row.
+template <class E>
+__device__ __forceinline__ void store16(E *to, const uint32_t (&x)[16], float scale, bool vec) {
+  Pack8<E> p[2];
+#pragma unroll
+  for (int y = 0; y < 8; ++y)
+    p[y >> 2].h[y & 3] = Elem<E>::from2(__uint_as_float(x[2 * y]) * scale,
+                                        __uint_as_float(x[2 * y + 1]) * scale);
+  if (vec) {
+    *reinterpret_cast<uint4 *>(to) = p[0].u;
+    *reinterpret_cast<uint4 *>(to + 8) = p[1].u;
+  } else {
+#pragma unroll
+    for (int y = 0; y < 16; ++y) to[y] = (y & 1) ? p[y >> 3].h[(y & 7) >> 1].y : p[y >> 3].h[(y & 7) >> 1].x;
+  }
+}
+
+// The rows of no request, of one head: zeros by whole warps.
+template <class F>
+__device__ __forceinline__ void rows_outside(const int32_t *starts, int R, int n, F zero) {
+  const int b = R > 0 ? min(max(starts[0], 0), n) : n;
+  const int e = R > 0 ? min(max(starts[R], b), n) : n;
+  const int warp = threadIdx.x >> 5, warps = kGradThreads / 32;
+  for (int64_t i = warp; i < b; i += warps) zero(i);
+  for (int64_t i = e + warp; i < n; i += warps) zero(i);
+}
+
+// Scores of one panel after another, 16 columns at a time: both operands K-major,
+// panels `a_stride` and `b_stride` bytes apart.
+__device__ __forceinline__ void product_over_columns(uint32_t d, uint64_t a, uint32_t a_stride,
+                                                     uint64_t b, uint32_t b_stride, uint32_t desc,
+                                                     int panels, int last_full, int cut, int last) {
+  // Panel `last_full` has `cut` columns, the last one `last`; the others 64.
+  for (int p = 0; p < panels; ++p, a += a_stride >> 4, b += b_stride >> 4) {
+    const int cols = p == panels - 1 ? last : p == last_full ? cut : 64;
+    for (int x = 0; x < cols >> 4; ++x) mma_ss(d, a + 2 * x, b + 2 * x, desc, p > 0 || x > 0);
+  }
+}
+
+// dk, dv and the heads' tails; dq.
+bool expanded_grad_keys_fits(const ExpandedGradArgs &a, const GradShape &s);
+int expanded_grad_keys(const ExpandedGradArgs &a, const GradShape &s, int dtype, cudaStream_t stream);
+bool expanded_grad_tokens_fits(const ExpandedGradArgs &a, const GradShape &s);
+int expanded_grad_tokens(const ExpandedGradArgs &a, const GradShape &s, int dtype, cudaStream_t stream);
+
+bool rows_of_16_bytes(const void *p, int64_t n, int64_t ld, int64_t H, int64_t ld_h);
+// The tensor map of [n, H, cols] read in boxes of 64 columns x `rows` rows of a head.
+bool grad_map(CUtensorMap *to, bool bf16, const void *p, int cols, int64_t H, int64_t n, int64_t ld,
+              int64_t ld_h, int rows);
+
+}  // namespace satk
