@@ -35,8 +35,8 @@ struct KeysMma {
   CUtensorMap q, dout, k, tail, v;
 };
 
-// A tile's tokens: -lse in log2, -delta, row ends (0 for one that sees nothing).
-struct Tokens {
+// A tile's tokens (rows of 16 bytes): -lse in log2, -delta, row ends (0 for one that sees nothing).
+struct alignas(16) Tokens {
   float less[kTokens], delta[kTokens];
   int end[kTokens];
 };
@@ -178,13 +178,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       tmem_ld32(s, 0, s_at);
       tmem_wait_ld();
       const bool masked = sm.least[stage][half] < key0 + kTile;
-      const float2 *less = reinterpret_cast<const float2 *>(tk.less + half * 32);
-      const float2 *delta = reinterpret_cast<const float2 *>(tk.delta + half * 32);
+      // (four tokens a load: every load takes a cycle from the products' operands)
+      const float4 *less = reinterpret_cast<const float4 *>(tk.less + half * 32);
+      const float4 *delta = reinterpret_cast<const float4 *>(tk.delta + half * 32);
       const int *end = tk.end + half * 32;
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
+        const float4 l4 = less[x >> 1];
         float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
-                              scale2, less[x]);
+                              scale2, (x & 1) != 0 ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
         asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as grad_weight)
         asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.y));
         s[2 * x] = __float_as_uint(exp2_fast(e.x));
@@ -200,8 +202,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         const float2 p = make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+        const float4 d4 = delta[x >> 1];
         const float2 d = __fmul2_rn(
-            p, __fadd2_rn(make_float2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])), delta[x]));
+            p, __fadd2_rn(make_float2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])),
+                          (x & 1) != 0 ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y)));
         dp[2 * x] = __float_as_uint(d.x);
         dp[2 * x + 1] = __float_as_uint(d.y);
       }
@@ -284,14 +288,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         mbar_wait(bar(sm.full[stage]), around & 1, dead);
         tc_fence_after();
         const int buffer = buffers == 2 ? i & 1 : 0;
-        product_over_columns(tmem + buffer * kTokens, k_desc, kKeyPanel,
-                             q_cols + (stage * stage_bytes >> 4), kTokenPanel, d_s, panels, nope_last,
-                             cut, q_last);
+        const uint32_t d = tmem + buffer * kTokens;
+        uint64_t k = k_desc, q = q_cols + (stage * stage_bytes >> 4);
+        for (int p = 0; p < panels; ++p, k += kKeyPanel >> 4, q += kTokenPanel >> 4)
+          panel_scores(d, k, q, d_s, p == panels - 1 ? q_last : p == nope_last ? cut : 64, p > 0);
         tc_commit(bar(sm.s_full[buffer]));
       };
       auto dps = [&](int stage) {
-        product_over_columns(dp_at, v_desc, kKeyPanel, q_cols + ((stage * stage_bytes + do_at) >> 4),
-                             kTokenPanel, d_s, v_panels, v_panels, 64, v_last);
+        const uint64_t o = q_cols + ((stage * stage_bytes + do_at) >> 4);
+        panel_scores(dp_at, v_desc, o, d_s, v_panels == 1 ? v_last : 64, false);
+        if (v_panels == 2)
+          panel_scores(dp_at, v_desc + (kKeyPanel >> 4), o + (kTokenPanel >> 4), d_s, v_last, true);
         tc_commit(bar(sm.dp_full));
       };
       int stage = 0, around = 0;

@@ -89,16 +89,41 @@ __device__ __forceinline__ void rows_outside(const int32_t *starts, int R, int n
   for (int64_t i = e + warp; i < n; i += warps) zero(i);
 }
 
-// Scores of one panel after another, 16 columns at a time: both operands K-major,
-// panels `a_stride` and `b_stride` bytes apart.
-__device__ __forceinline__ void product_over_columns(uint32_t d, uint64_t a, uint32_t a_stride,
-                                                     uint64_t b, uint32_t b_stride, uint32_t desc,
-                                                     int panels, int last_full, int cut, int last) {
-  // Panel `last_full` has `cut` columns, the last one `last`; the others 64.
-  for (int p = 0; p < panels; ++p, a += a_stride >> 4, b += b_stride >> 4) {
-    const int cols = p == panels - 1 ? last : p == last_full ? cut : 64;
-    for (int x = 0; x < cols >> 4; ++x) mma_ss(d, a + 2 * x, b + 2 * x, desc, p > 0 || x > 0);
+// One 64-column panel of scores, 16 columns at a time: both operands K-major.  The
+// descriptors are plain sums of what stays in uniform registers: a loop over steps
+// costs 60 cycles an MMA (a 128 x 64 tile's scores 780 cycles to issue).
+__device__ __forceinline__ void panel_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, int cols,
+                                             bool more) {
+  mma_ss(d, a, b, desc, more);
+  if (cols == 64) {
+    mma_ss(d, a + 2, b + 2, desc, true);
+    mma_ss(d, a + 4, b + 4, desc, true);
+    mma_ss(d, a + 6, b + 6, desc, true);
+  } else {
+    if (cols > 16) mma_ss(d, a + 2, b + 2, desc, true);
+    if (cols > 32) mma_ss(d, a + 4, b + 4, desc, true);
   }
+}
+
+// The same with A in tensor memory, eight columns of it a step.
+__device__ __forceinline__ void panel_scores_inside(uint32_t d, uint32_t a, uint64_t b, uint32_t desc,
+                                                    int cols, bool more) {
+  mma_ts(d, a, b, desc, more);
+  if (cols == 64) {
+    mma_ts(d, a + 8, b + 2, desc, true);
+    mma_ts(d, a + 16, b + 4, desc, true);
+    mma_ts(d, a + 24, b + 6, desc, true);
+  } else {
+    if (cols > 16) mma_ts(d, a + 8, b + 2, desc, true);
+    if (cols > 32) mma_ts(d, a + 16, b + 4, desc, true);
+  }
+}
+
+// 32 lanes x 8 columns of tensor memory.
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::SATK_I8(v, 0),
+               "r"(addr)
+               : "memory");
 }
 
 // dk, dv and the heads' tails; dq.

@@ -2,39 +2,41 @@
 // the tensor cores.
 //
 // A CTA takes 128 tokens of one request and head and goes over their keys in tiles
-// of 128:
+// of 64:
 //   S[token, key] = Q [K | tail]^T         dP[token, key] = dO V^T
 //   dS = exp2(scale S - lse) (dP - delta)  dQ += dS [K | tail]
-// A token is a TMEM lane and a thread.  dS, rounded to the inputs' type, is the A
-// operand of the second product from tensor memory; S 128, dP 128, dQ up to 192
-// and dS 64 columns fill it.  (Wider queries have dS in the place of S.)  While dS
-// of a tile is computed, the scores of the next one are.
+// A token is a TMEM lane and a thread.  dS, rounded to the inputs' type, replaces S
+// in tensor memory and is the A operand of the second product.  Q, and dO where
+// there is room too, are A operands in tensor memory as well: with a tile of 64
+// keys a product with both operands in shared memory takes 50 cycles a step of 16
+// columns, one with A in tensor memory 36.  At 192 query/key columns: S 2 x 64, dP
+// 64, Q 96, dQ 192 columns, dO in shared memory.
 //
 // S and dP are computed again, as in the kernel of the keys: seven products where
 // five would do, and no sum of dQ over CTAs, whose order would change the result.
 //
-// Bounded by the tensor core: 2048 cycles of products a 128 x 128 tile at 192
+// Bounded by the tensor core: 1225 cycles of products a 128 x 64 tile at 192
 // query/key and 128 value columns.
 #include "expanded_grad_mma.cuh"
 
 namespace satk {
 namespace {
 
-constexpr int kPanel = kTile * 128;  // bytes of 64 columns of a tile
-constexpr int kMaxBuffers = 2;
+constexpr int kKeys = 64;  // of a tile
+constexpr int kOwnPanel = kTile * 128, kPanel = kKeys * 128;  // bytes of 64 columns
+constexpr int kMaxStages = 4;
 
 struct TokensMma {
   ExpandedGradArgs a;
   GradShape s;
-  int k_buffers, v_buffers;
-  int early;  // the next tile's scores before this one's dQ
+  int stages;
+  int q_inside, do_inside;  // in tensor memory
   CUtensorMap q, dout, k, tail, v;
 };
 
 struct Small {
-  uint64_t own, k_full[kMaxBuffers][kMaxPanels], k_empty[kMaxBuffers][kMaxPanels];
-  uint64_t v_full[kMaxBuffers], v_empty[kMaxBuffers], looked[kMaxBuffers];
-  uint64_t s_full, s_read, dp_full, ready, dq_done, issued;
+  uint64_t own, full[kMaxStages], empty[kMaxStages], looked[kMaxStages];
+  uint64_t s_full[2], dp_full, dp_read, ready, done, issued;
   int low[8], high[8];
   int odd_key;   // the first key that is not finite
   int place[4];  // first key, keys, first token, tokens
@@ -42,17 +44,32 @@ struct Small {
   int dead;
 };
 
+// This thread's half of a row of `cols` 16-bit columns into tensor memory.
+template <class E>
+__device__ __forceinline__ void row_inside(uint32_t at, const E *row, int cols, int half, bool mine) {
+  for (int c = half * 16; c < cols; c += 32) {
+    uint32_t x[8] = {};
+    if (mine) {
+      const uint4 a = *reinterpret_cast<const uint4 *>(row + c), b = *reinterpret_cast<const uint4 *>(row + c + 8);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+    __syncwarp();
+    tmem_st8(at + c / 2, x);
+  }
+}
+
 template <class E>
 __global__ void __launch_bounds__(kGradThreads, 1)
     expanded_grad_tokens_kernel(const __grid_constant__ TokensMma m) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const ExpandedGradArgs &a = m.a;
   const ExpandedArgs &f = a.f;
-  const int panels = m.s.panels, v_panels = m.s.v_panels;
+  const int panels = m.s.panels, v_panels = m.s.v_panels, stages = m.stages;
   const uint32_t base = smem_addr(smem);
-  const int do_at = panels * kPanel, k_at = do_at + v_panels * kPanel;
-  const int v_at = k_at + m.k_buffers * panels * kPanel;
-  Small &sm = *reinterpret_cast<Small *>(smem + v_at + m.v_buffers * v_panels * kPanel);
+  const int do_at = m.q_inside ? 0 : panels * kOwnPanel;
+  const int ring_at = do_at + (m.do_inside ? 0 : v_panels * kOwnPanel);
+  const int stage_bytes = (panels + v_panels) * kPanel, v_at = panels * kPanel;
+  Small &sm = *reinterpret_cast<Small *>(smem + ring_at + stages * stage_bytes);
   volatile int *dead = &sm.dead;
   auto bar = [&](uint64_t &b) { return smem_addr(&b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -83,20 +100,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   }
   if (threadIdx.x == 0) {
     mbar_init(bar(sm.own), 1);
-    for (int b = 0; b < kMaxBuffers; ++b) {
-      for (int p = 0; p < kMaxPanels; ++p) {
-        mbar_init(bar(sm.k_full[b][p]), 1);
-        mbar_init(bar(sm.k_empty[b][p]), 1);
-      }
-      mbar_init(bar(sm.v_full[b]), 1);
-      mbar_init(bar(sm.v_empty[b]), 1);
-      mbar_init(bar(sm.looked[b]), 64);
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(bar(sm.full[s]), 1);
+      mbar_init(bar(sm.empty[s]), 1);
+      mbar_init(bar(sm.looked[s]), 64);
     }
-    mbar_init(bar(sm.s_full), 1);
-    mbar_init(bar(sm.s_read), 256);
+    mbar_init(bar(sm.s_full[0]), 1);
+    mbar_init(bar(sm.s_full[1]), 1);
     mbar_init(bar(sm.dp_full), 1);
+    mbar_init(bar(sm.dp_read), 256);
     mbar_init(bar(sm.ready), 256);
-    mbar_init(bar(sm.dq_done), 1);
+    mbar_init(bar(sm.done), 1);
     mbar_init(bar(sm.issued), 1);
     sm.dead = 0;
     sm.odd_key = INT32_MAX;
@@ -127,31 +141,39 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const uint32_t tmem = sm.tmem;
   int low = INT32_MAX, high = 0;
   for (int w = 0; w < 4; ++w) low = min(low, sm.low[w]), high = max(high, sm.high[w]);
-  const int n = (high + kTile - 1) / kTile;
-  const uint32_t dp_at = tmem + 128, dq_at = tmem + 256;
-  // dS: 32 columns of each half of the keys
-  const uint32_t ds_at = m.early ? dq_at + D : tmem, ds_half = m.early ? 32 : 64;
+  const int n = (high + kKeys - 1) / kKeys;
+  const int first_masked = low / kKeys;  // the first tile with a key that some token does not see
+  const uint32_t dp_at = tmem + 2 * kKeys, dq_at = dp_at + kKeys, q_in = dq_at + D;
+  const uint32_t do_in = q_in + (m.q_inside ? D / 2 : 0);
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  if (n > 0 && warp < 8) {
+    if (m.q_inside)
+      row_inside(q_in + lanes, static_cast<const E *>(f.q) + t * f.ld_q_t + h * f.ld_q_h, D, half, mine);
+    if (m.do_inside)
+      row_inside(do_in + lanes, static_cast<const E *>(a.dout) + t * a.ld_do_t + h * a.ld_do_h, f.dv, half, mine);
+    tmem_wait_st();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
 
   // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168.
   if (warp < 8) regs_raise<208>(); else regs_lower<88>();
   if (warp < 8) {
     // ------------------------------------------------------------- dS, results
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float2 scale2 = make_float2(f.scale_log2, f.scale_log2);
     const float2 less = make_float2(-st.x, -st.x), delta = make_float2(-st.y, -st.y);
     for (int i = 0; i < n; ++i) {
-      const int k0 = i * kTile + half * 64;
-      uint32_t s[64];
-      mbar_wait(bar(sm.s_full), i & 1, dead);
+      const int k0 = i * kKeys + half * 32, buffer = i & 1;
+      const uint32_t s_at = tmem + buffer * kKeys + half * 32 + lanes;
+      uint32_t s[32], dp[32], packed[16];
+      mbar_wait(bar(sm.s_full[buffer]), (i >> 1) & 1, dead);
       __syncwarp();
       tc_fence_after();
-      tmem_ld32(s, 0, tmem + half * 64 + lanes);
-      tmem_ld32(s, 32, tmem + half * 64 + 32 + lanes);
+      tmem_ld32(s, 0, s_at);
       tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(bar(sm.s_read));
 #pragma unroll
-      for (int x = 0; x < 32; ++x) {
+      for (int x = 0; x < 16; ++x) {
         float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
                               scale2, less);
         asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as grad_weight)
@@ -162,43 +184,39 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       mbar_wait(bar(sm.dp_full), i & 1, dead);
       __syncwarp();
       tc_fence_after();
-      uint32_t packed[32];
-      const bool masked = __any_sync(~0u, k0 + 64 > end);
+      tmem_ld32(dp, 0, dp_at + half * 32 + lanes);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(bar(sm.dp_read));
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t dp[32];
-        tmem_ld32(dp, 0, dp_at + half * 64 + c * 32 + lanes);
-        tmem_wait_ld();
+      for (int x = 0; x < 16; ++x) {
+        const float2 d = __fmul2_rn(
+            make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
+            __fadd2_rn(make_float2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])), delta));
+        dp[2 * x] = __float_as_uint(d.x);
+        dp[2 * x + 1] = __float_as_uint(d.y);
+      }
+      if (i >= first_masked) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int y = c * 32 + 2 * x;
-          float2 d = __fmul2_rn(
-              make_float2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])),
-              __fadd2_rn(make_float2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])), delta));
-          if (masked) {
-            if (k0 + y >= end) d.x = 0.f;
-            if (k0 + y + 1 >= end) d.y = 0.f;
-          }
-          union {
-            typename Elem<E>::T2 h;
-            uint32_t u;
-          } pk;
-          pk.h = Elem<E>::from2(d.x, d.y);
-          packed[c * 16 + x] = pk.u;
-        }
+        for (int x = 0; x < 32; ++x)
+          if (k0 + x >= end) dp[x] = 0;
       }
-      if (i > 0) {  // dS of the tile before has been used
-        mbar_wait(bar(sm.dq_done), (i - 1) & 1, dead);
-        __syncwarp();
-        tc_fence_after();
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        union {
+          typename Elem<E>::T2 h;
+          uint32_t u;
+        } pk;
+        pk.h = Elem<E>::from2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]));
+        packed[x] = pk.u;
       }
-      tmem_st32(ds_at + half * ds_half + lanes, packed, 0);
+      tmem_st16(s_at, packed);  // the first half of this thread's columns of S
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bar(sm.ready));
     }
     if (n > 0) {
-      mbar_wait(bar(sm.dq_done), (n - 1) & 1, dead);
+      mbar_wait(bar(sm.done), 0, dead);
       __syncwarp();
       tc_fence_after();
     }
@@ -221,66 +239,75 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     // ---------------------------------------------------------------- MMA issue
     if (elect_leader()) {
       constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
-      constexpr uint32_t d_s = mma_desc(bf16, false, false, kTile, kTile);
+      constexpr uint32_t d_s = mma_desc(bf16, false, false, kTile, kKeys);
+      const uint32_t d_q = mma_desc(bf16, false, true, kTile, m.s.one_product ? D : f.dn);
+      const uint32_t d_t = mma_desc(bf16, false, true, kTile, f.dr);
       const uint64_t q_desc = tile_desc(base, 16, 1024), o_desc = tile_desc(base + do_at, 16, 1024);
-      const uint64_t k_cols = tile_desc(base + k_at, 16, 1024), v_cols = tile_desc(base + v_at, 16, 1024);
-      const uint64_t k_rows = tile_desc(base + k_at, kPanel, 1024);
+      const uint64_t k_cols = tile_desc(base + ring_at, 16, 1024);
+      const uint64_t k_rows = tile_desc(base + ring_at, kPanel, 1024);
       const int nope_last = m.s.nope_panels - 1, cut = f.dn - nope_last * 64;
-      const int v_last = f.dv - (v_panels - 1) * 64;
-      auto columns = [&](int p) { return p > nope_last ? f.dr : p == nope_last ? cut : 64; };
-      auto scores = [&](int i) {
-        const int b = i % m.k_buffers;
-        uint64_t q = q_desc, k = k_cols + (b * panels * kPanel >> 4);
-        for (int p = 0; p < panels; ++p, q += kPanel >> 4, k += kPanel >> 4) {
-          mbar_wait(bar(sm.k_full[b][p]), (i / m.k_buffers) & 1, dead);
-          tc_fence_after();
-          const int steps = columns(p) >> 4;
-          for (int x = 0; x < steps; ++x) mma_ss(tmem, q + 2 * x, k + 2 * x, d_s, p > 0 || x > 0);
-        }
-        tc_commit(bar(sm.s_full));
-      };
-      auto dps = [&](int i) {
-        const int b = i % m.v_buffers;
-        mbar_wait(bar(sm.v_full[b]), (i / m.v_buffers) & 1, dead);
+      const int q_last = f.dr > 0 ? f.dr : cut, v_last = f.dv - (v_panels - 1) * 64;
+      auto scores = [&](int i, int stage, int around) {
+        mbar_wait(bar(sm.full[stage]), around & 1, dead);
         tc_fence_after();
-        product_over_columns(dp_at, o_desc, kPanel, v_cols + (b * v_panels * kPanel >> 4), kPanel, d_s,
-                             v_panels, v_panels, 64, v_last);
-        tc_commit(bar(sm.dp_full));
-        tc_commit(bar(sm.v_empty[b]));
+        const uint32_t d = tmem + (i & 1) * kKeys;
+        uint64_t k = k_cols + (stage * stage_bytes >> 4), q = q_desc;
+        uint32_t in = q_in;
+        for (int p = 0; p < panels; ++p, k += kPanel >> 4, q += kOwnPanel >> 4) {
+          const int cols = p == panels - 1 ? q_last : p == nope_last ? cut : 64;
+          if (m.q_inside) panel_scores_inside(d, in, k, d_s, cols, p > 0);
+          else panel_scores(d, q, k, d_s, cols, p > 0);
+          in += cols / 2;
+        }
+        tc_commit(bar(sm.s_full[i & 1]));
       };
+      auto dps = [&](int stage) {
+        const uint64_t v = k_cols + ((stage * stage_bytes + v_at) >> 4);
+        const int cols = v_panels == 1 ? v_last : 64;
+        if (m.do_inside) {
+          panel_scores_inside(dp_at, do_in, v, d_s, cols, false);
+          if (v_panels == 2) panel_scores_inside(dp_at, do_in + 32, v + (kPanel >> 4), d_s, v_last, true);
+        } else {
+          panel_scores(dp_at, o_desc, v, d_s, cols, false);
+          if (v_panels == 2)
+            panel_scores(dp_at, o_desc + (kOwnPanel >> 4), v + (kPanel >> 4), d_s, v_last, true);
+        }
+        tc_commit(bar(sm.dp_full));
+      };
+      int stage = 0, around = 0, looked = 0, looked_around = 0;
       if (n > 0) {
-        mbar_wait(bar(sm.own), 0, dead);
-        scores(0);
+        if (!m.q_inside || !m.do_inside) mbar_wait(bar(sm.own), 0, dead);
+        scores(0, 0, 0);
         dps(0);
       }
       for (int i = 0; i < n; ++i) {
-        if (m.early && i + 1 < n) {
-          mbar_wait(bar(sm.s_read), i & 1, dead);
+        const int next = stage + 1 == stages ? 0 : stage + 1, next_around = around + (next == 0);
+        if (i + 1 < n) {
+          scores(i + 1, next, next_around);
+          mbar_wait(bar(sm.dp_read), i & 1, dead);
           tc_fence_after();
-          scores(i + 1);
+          dps(next);
         }
-        const int b = i % m.k_buffers;
-        mbar_wait(bar(sm.looked[b]), (i / m.k_buffers) & 1, dead);
+        if (i >= first_masked) {
+          mbar_wait(bar(sm.looked[looked]), looked_around & 1, dead);
+          if (++looked == stages) looked = 0, ++looked_around;
+        }
         mbar_wait(bar(sm.ready), i & 1, dead);
         tc_fence_after();
-        // A panel's columns at a time, so that its place is free for the next tile's.
-        uint64_t k = k_rows + (b * panels * kPanel >> 4);
-        uint32_t d = dq_at;
-        for (int p = 0; p < panels; ++p, k += kPanel >> 4) {
-          const int cols = columns(p);
-          const uint32_t desc = mma_desc(bf16, false, true, kTile, cols);
+        const uint32_t ds_at = tmem + (i & 1) * kKeys;
+        const uint64_t k = k_rows + (stage * stage_bytes >> 4);
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            mma_ts(d, ds_at + (x >> 2) * ds_half + (x & 3) * 8, k + 128 * x, desc, i > 0 || x > 0);
-          d += cols;
-          tc_commit(bar(sm.k_empty[b][p]));
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t at = ds_at + (x >> 1) * 32 + (x & 1) * 8;
+          mma_ts(dq_at, at, k + 128 * x, d_q, i > 0 || x > 0);
+          if (!m.s.one_product)
+            mma_ts(dq_at + f.dn, at, k + (m.s.nope_panels * kPanel >> 4) + 128 * x, d_t, i > 0 || x > 0);
         }
-        tc_commit(bar(sm.dq_done));
-        if (i + 1 < n) {
-          if (!m.early) scores(i + 1);
-          dps(i + 1);
-        }
+        tc_commit(bar(sm.empty[stage]));
+        stage = next;
+        around = next_around;
       }
+      tc_commit(bar(sm.done));
       tc_commit(bar(sm.issued));
       mbar_drain(bar(sm.issued), 0);
     }
@@ -288,68 +315,65 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   } else if (warp == 9) {
     // -------------------------------------------------------------------- loads
     const uint32_t leader = elect_leader();
-    if (n > 0) {
-      if (lane == 0) mbar_expect(bar(sm.own), (panels + v_panels) * kPanel);
+    const int own = ((m.q_inside ? 0 : panels) + (m.do_inside ? 0 : v_panels)) * kOwnPanel;
+    if (n > 0 && own > 0) {
+      if (lane == 0) mbar_expect(bar(sm.own), own);
       __syncwarp();
-      for (int p = 0; p < panels; ++p)
-        tma_box3(leader, base + p * kPanel, &m.q, p < m.s.nope_panels ? p * 64 : f.dn, h, t0, bar(sm.own));
-      for (int p = 0; p < v_panels; ++p)
-        tma_box3(leader, base + do_at + p * kPanel, &m.dout, p * 64, h, t0, bar(sm.own));
+      if (!m.q_inside)
+        for (int p = 0; p < panels; ++p)
+          tma_box3(leader, base + p * kOwnPanel, &m.q, p < m.s.nope_panels ? p * 64 : f.dn, h, t0, bar(sm.own));
+      if (!m.do_inside)
+        for (int p = 0; p < v_panels; ++p)
+          tma_box3(leader, base + do_at + p * kOwnPanel, &m.dout, p * 64, h, t0, bar(sm.own));
     }
+    int stage = 0, around = 0;
     for (int i = 0; i < n; ++i) {
-      const int key = key0 + i * kTile, b = i % m.k_buffers, vb = i % m.v_buffers;
-      for (int p = 0; p < panels; ++p) {
-        if (i >= m.k_buffers) mbar_wait(bar(sm.k_empty[b][p]), (i / m.k_buffers - 1) & 1, dead);
-        __syncwarp();
-        const uint32_t full = bar(sm.k_full[b][p]), to = base + k_at + (b * panels + p) * kPanel;
-        if (lane == 0) mbar_expect(full, kPanel);
-        __syncwarp();
-        if (p < m.s.nope_panels) tma_box3(leader, to, &m.k, p * 64, h, key, full);
-        else tma_box(leader, to, &m.tail, 0, key, full);
-      }
-      if (i >= m.v_buffers) mbar_wait(bar(sm.v_empty[vb]), (i / m.v_buffers - 1) & 1, dead);
+      const int key = key0 + i * kKeys;
+      if (around > 0) mbar_wait(bar(sm.empty[stage]), (around - 1) & 1, dead);
       __syncwarp();
-      if (lane == 0) mbar_expect(bar(sm.v_full[vb]), v_panels * kPanel);
+      const uint32_t full = bar(sm.full[stage]), to = base + ring_at + stage * stage_bytes;
+      if (lane == 0) mbar_expect(full, stage_bytes);
       __syncwarp();
-      for (int p = 0; p < v_panels; ++p)
-        tma_box3(leader, base + v_at + (vb * v_panels + p) * kPanel, &m.v, p * 64, h, key, bar(sm.v_full[vb]));
+      for (int p = 0; p < m.s.nope_panels; ++p) tma_box3(leader, to + p * kPanel, &m.k, p * 64, h, key, full);
+      if (f.dr > 0) tma_box(leader, to + m.s.nope_panels * kPanel, &m.tail, 0, key, full);
+      for (int p = 0; p < v_panels; ++p) tma_box3(leader, to + v_at + p * kPanel, &m.v, p * 64, h, key, full);
+      if (++stage == stages) stage = 0, ++around;
     }
-    if (n > 0) mbar_drain(bar(sm.own), 0);
-    for (int i = max(0, n - m.k_buffers); i < n; ++i)
-      for (int p = 0; p < panels; ++p) mbar_drain(bar(sm.k_full[i % m.k_buffers][p]), (i / m.k_buffers) & 1);
-    for (int i = max(0, n - m.v_buffers); i < n; ++i)
-      mbar_drain(bar(sm.v_full[i % m.v_buffers]), (i / m.v_buffers) & 1);
+    if (n > 0 && own > 0) mbar_drain(bar(sm.own), 0);
+    for (int i = max(0, n - stages); i < n; ++i) mbar_drain(bar(sm.full[i % stages]), (i / stages) & 1);
   } else {
     // ----------------------------------------------------------------- key rows
     // Where some token does not see some key, a key that is not finite would turn a
     // 0 of dS into NaN: it is cleared, and the tokens that do see it get NaN.
-    for (int i = 0; i < n; ++i) {
-      const int b = i % m.k_buffers;
-      for (int p = 0; p < panels; ++p) mbar_wait(bar(sm.k_full[b][p]), (i / m.k_buffers) & 1, dead);
-      if (i * kTile + kTile > low) {
-        unsigned char *k = smem + k_at + b * panels * kPanel;
-        for (int y = (warp - 10) * 64 + lane; y < (warp - 9) * 64; y += 32)
-          if (row_is_odd<E>(k, y, panels, kPanel)) {
-            clear_row(k, y, panels, kPanel);
-            atomicMin(&sm.odd_key, i * kTile + y);
-          }
-        fence_async_shared();
+    const int y = (warp - 10) * 32 + lane;
+    for (int i = first_masked; i < n; ++i) {
+      const int stage = i % stages;
+      mbar_wait(bar(sm.full[stage]), (i / stages) & 1, dead);
+      unsigned char *k = smem + ring_at + stage * stage_bytes;
+      if (row_is_odd<E>(k, y, panels, kPanel)) {
+        clear_row(k, y, panels, kPanel);
+        atomicMin(&sm.odd_key, i * kKeys + y);
       }
-      mbar_arrive(bar(sm.looked[b]));
+      fence_async_shared();
+      mbar_arrive(bar(sm.looked[(i - first_masked) % stages]));
     }
   }
   __syncthreads();
   if (warp == 8) tmem_free(tmem, 512);
 }
 
+// What fits: Q in tensor memory first, it saves most; then dO.
 bool layout(const ExpandedGradArgs &a, TokensMma &m, int &smem) {
-  const int own = (m.s.panels + m.s.v_panels) * kPanel, small = static_cast<int>(sizeof(Small));
-  const int k = m.s.panels * kPanel, v = m.s.v_panels * kPanel, left = kSmemLimit - own - small;
-  m.k_buffers = left >= 2 * k + v ? 2 : 1;
-  m.v_buffers = left >= m.k_buffers * k + 2 * v ? 2 : 1;
-  m.early = m.k_buffers == 2 && 128 + 128 + a.f.dn + a.f.dr + 64 <= 512;
-  smem = own + m.k_buffers * k + m.v_buffers * v + small;
-  return smem <= kSmemLimit;
+  const int D = a.f.dn + a.f.dr, stage = (m.s.panels + m.s.v_panels) * kPanel;
+  int columns = 3 * kKeys + D;
+  m.q_inside = columns + D / 2 <= 512;
+  if (m.q_inside) columns += D / 2;
+  m.do_inside = columns + a.f.dv / 2 <= 512;
+  const int own = ((m.q_inside ? 0 : m.s.panels) + (m.do_inside ? 0 : m.s.v_panels)) * kOwnPanel;
+  m.stages = (kSmemLimit - own - static_cast<int>(sizeof(Small))) / stage;
+  if (m.stages > kMaxStages) m.stages = kMaxStages;
+  smem = own + m.stages * stage + static_cast<int>(sizeof(Small));
+  return m.stages >= 2;
 }
 
 template <class E>
@@ -390,9 +414,9 @@ int expanded_grad_tokens(const ExpandedGradArgs &a, const GradShape &s, int dtyp
   if (!layout(a, m, smem)) return SATK_EUNSUPPORTED;
   if (!grad_map(&m.q, bf16, f.q, f.dn + f.dr, f.H, f.T, f.ld_q_t, f.ld_q_h, kTile) ||
       !grad_map(&m.dout, bf16, a.dout, f.dv, f.H, f.T, a.ld_do_t, a.ld_do_h, kTile) ||
-      !grad_map(&m.k, bf16, f.k, f.dn, f.H, f.S, f.ld_k_s, f.ld_k_h, kTile) ||
-      !grad_map(&m.v, bf16, f.v, f.dv, f.H, f.S, f.ld_v_s, f.ld_v_h, kTile) ||
-      (f.dr > 0 && !tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kTile)))
+      !grad_map(&m.k, bf16, f.k, f.dn, f.H, f.S, f.ld_k_s, f.ld_k_h, kKeys) ||
+      !grad_map(&m.v, bf16, f.v, f.dv, f.H, f.S, f.ld_v_s, f.ld_v_h, kKeys) ||
+      (f.dr > 0 && !tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kKeys)))
     return SATK_ECUDA;
   return bf16 ? launch<__nv_bfloat16>(m, smem, stream) : launch<__half>(m, smem, stream);
 }
