@@ -279,64 +279,72 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const uint32_t d_v = mma_desc(bf16, false, true, kTile, f.dv);
       const uint32_t d_k = mma_desc(bf16, false, true, kTile, m.s.one_product ? D : f.dn);
       const uint32_t d_t = mma_desc(bf16, false, true, kTile, f.dr);
-      const uint64_t k_desc = tile_desc(base, 16, 1024), v_desc = tile_desc(base + v_at, 16, 1024);
-      const uint64_t q_cols = tile_desc(base + ring_at, 16, 1024);
-      const uint64_t q_rows = tile_desc(base + ring_at, kTokenPanel, 1024);
-      const int nope_last = m.s.nope_panels - 1, cut = f.dn - nope_last * 64;
-      const int q_last = f.dr > 0 ? f.dr : cut, v_last = f.dv - (v_panels - 1) * 64;
-      auto scores = [&](int i, int stage, int around) {
+      const uint32_t k_low = desc_low(base, 16), v_low = desc_low(base + v_at, 16);
+      const uint32_t stage_step = stage_bytes >> 4, do_step = do_at >> 4;
+      const uint32_t q_steps = panel_steps(panels, m.s.nope_panels, f.dn, f.dr);
+      const uint32_t v_steps = panel_steps(v_panels, v_panels, f.dv, 0);
+      const uint32_t tail_step = m.s.nope_panels * kTokenPanel >> 4;
+      // the tiles' rows as operands over columns, and over rows (panels apart)
+      const uint32_t cols_low = desc_low(base + ring_at, 16), rows_low = desc_low(base + ring_at, kTokenPanel);
+      auto scores = [&](int i, int stage, uint32_t at, int around) {
         mbar_wait(bar(sm.full[stage]), around & 1, dead);
         tc_fence_after();
         const int buffer = buffers == 2 ? i & 1 : 0;
-        const uint32_t d = tmem + buffer * kTokens;
-        uint64_t k = k_desc, q = q_cols + (stage * stage_bytes >> 4);
-        for (int p = 0; p < panels; ++p, k += kKeyPanel >> 4, q += kTokenPanel >> 4)
-          panel_scores(d, k, q, d_s, p == panels - 1 ? q_last : p == nope_last ? cut : 64, p > 0);
+        product_over_columns<false, kMaxPanels, kKeyPanel, kTokenPanel>(tmem + buffer * kTokens, k_low,
+                                                                        cols_low + at, d_s, q_steps);
         tc_commit(bar(sm.s_full[buffer]));
       };
-      auto dps = [&](int stage) {
-        const uint64_t o = q_cols + ((stage * stage_bytes + do_at) >> 4);
-        panel_scores(dp_at, v_desc, o, d_s, v_panels == 1 ? v_last : 64, false);
-        if (v_panels == 2)
-          panel_scores(dp_at, v_desc + (kKeyPanel >> 4), o + (kTokenPanel >> 4), d_s, v_last, true);
+      auto dps = [&](uint32_t at) {
+        product_over_columns<false, 2, kKeyPanel, kTokenPanel>(dp_at, v_low, cols_low + at + do_step, d_s,
+                                                               v_steps);
         tc_commit(bar(sm.dp_full));
       };
       int stage = 0, around = 0;
+      uint32_t at = 0;
       if (n > 0) {
         mbar_wait(bar(sm.own), 0, dead);
-        scores(0, 0, 0);
+        scores(0, 0, 0, 0);
         dps(0);
       }
       for (int i = 0; i < n; ++i) {
-        const int next = stage + 1 == stages ? 0 : stage + 1, next_around = around + (next == 0);
+        const bool wrap = stage + 1 == stages;
+        const int next = wrap ? 0 : stage + 1, next_around = around + (wrap ? 1 : 0);
+        const uint32_t next_at = wrap ? 0 : at + stage_step;
         if (buffers == 2 && i + 1 < n) {
-          scores(i + 1, next, next_around);
+          scores(i + 1, next, next_at, next_around);
           mbar_wait(bar(sm.dp_read), i & 1, dead);
           tc_fence_after();
-          dps(next);
+          dps(next_at);
         }
         mbar_wait(bar(sm.looked[stage]), around & 1, dead);
         mbar_wait(bar(sm.ready), i & 1, dead);
         tc_fence_after();
         const uint32_t p_at = tmem + (buffers == 2 ? i & 1 : 0) * kTokens;
-        const uint64_t q = q_rows + (stage * stage_bytes >> 4), o = q + (do_at >> 4);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          mma_ts(dv_at, p_at + (x >> 1) * 32 + (x & 1) * 8, o + 128 * x, d_v, i > 0 || x > 0);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t ds_at = p_at + (x >> 1) * 32 + 16 + (x & 1) * 8;
-          mma_ts(dk_at, ds_at, q + 128 * x, d_k, i > 0 || x > 0);
-          if (!m.s.one_product)
-            mma_ts(dk_at + f.dn, ds_at, q + (m.s.nope_panels * kTokenPanel >> 4) + 128 * x, d_t, i > 0 || x > 0);
+        const uint32_t q = rows_low + at, o = q + do_step;
+        const bool more = i > 0;
+        mma_ts_low(dv_at, p_at, o, d_v, more);
+        mma_ts_low(dv_at, p_at + 8, o + 128, d_v, true);
+        mma_ts_low(dv_at, p_at + 32, o + 256, d_v, true);
+        mma_ts_low(dv_at, p_at + 40, o + 384, d_v, true);
+        mma_ts_low(dk_at, p_at + 16, q, d_k, more);
+        mma_ts_low(dk_at, p_at + 24, q + 128, d_k, true);
+        mma_ts_low(dk_at, p_at + 48, q + 256, d_k, true);
+        mma_ts_low(dk_at, p_at + 56, q + 384, d_k, true);
+        if (!m.s.one_product) {
+          const uint32_t d = dk_at + f.dn, x = q + tail_step;
+          mma_ts_low(d, p_at + 16, x, d_t, more);
+          mma_ts_low(d, p_at + 24, x + 128, d_t, true);
+          mma_ts_low(d, p_at + 48, x + 256, d_t, true);
+          mma_ts_low(d, p_at + 56, x + 384, d_t, true);
         }
         tc_commit(bar(sm.empty[stage]));
         if (buffers == 1 && i + 1 < n) {
-          scores(i + 1, next, next_around);
-          dps(next);
+          scores(i + 1, next, next_at, next_around);
+          dps(next_at);
         }
         stage = next;
         around = next_around;
+        at = next_at;
       }
       tc_commit(bar(sm.done));
       tc_commit(bar(sm.issued));

@@ -89,33 +89,63 @@ __device__ __forceinline__ void rows_outside(const int32_t *starts, int R, int n
   for (int64_t i = e + warp; i < n; i += warps) zero(i);
 }
 
-// One 64-column panel of scores, 16 columns at a time: both operands K-major.  The
-// descriptors are plain sums of what stays in uniform registers: a loop over steps
-// costs 60 cycles an MMA (a 128 x 64 tile's scores 780 cycles to issue).
-__device__ __forceinline__ void panel_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, int cols,
-                                             bool more) {
-  mma_ss(d, a, b, desc, more);
-  if (cols == 64) {
-    mma_ss(d, a + 2, b + 2, desc, true);
-    mma_ss(d, a + 4, b + 4, desc, true);
-    mma_ss(d, a + 6, b + 6, desc, true);
-  } else {
-    if (cols > 16) mma_ss(d, a + 2, b + 2, desc, true);
-    if (cols > 32) mma_ss(d, a + 4, b + 4, desc, true);
-  }
+// MMAs with descriptors whose upper words are all the same (atoms of eight rows are
+// 1024 bytes apart): the lower words are what changes, a constant away from one
+// uniform register.  64-bit sums and loops over the steps cost 50 cycles an MMA to
+// issue, more than most of them take to run.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3fff) | (lbo >> 4) << 16;
+}
+__device__ __forceinline__ void mma_ss_low(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool more) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 x, y;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
+      "setp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(more ? 1u : 0u), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool more) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 y;\nmov.b64 y, {%2, %5};\n"
+      "setp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(more ? 1u : 0u), "r"(kDescHigh)
+      : "memory");
 }
 
-// The same with A in tensor memory, eight columns of it a step.
-__device__ __forceinline__ void panel_scores_inside(uint32_t d, uint32_t a, uint64_t b, uint32_t desc,
-                                                    int cols, bool more) {
-  mma_ts(d, a, b, desc, more);
-  if (cols == 64) {
-    mma_ts(d, a + 8, b + 2, desc, true);
-    mma_ts(d, a + 16, b + 4, desc, true);
-    mma_ts(d, a + 24, b + 6, desc, true);
-  } else {
-    if (cols > 16) mma_ts(d, a + 8, b + 2, desc, true);
-    if (cols > 32) mma_ts(d, a + 16, b + 4, desc, true);
+// Steps of 16 columns of each panel, four bits a panel.
+__device__ __forceinline__ uint32_t panel_steps(int panels, int nope_panels, int dn, int dr) {
+  uint32_t steps = 0;
+  for (int p = 0; p < panels; ++p) {
+    const int cols = p >= nope_panels ? dr : p == nope_panels - 1 ? dn - p * 64 : 64;
+    steps |= static_cast<uint32_t>(cols >> 4) << (4 * p);
+  }
+  return steps;
+}
+
+// A product over columns, both operands K-major in panels: A in shared memory
+// (panels A_PANEL bytes apart) or, INSIDE, in tensor memory without gaps.
+template <bool INSIDE, int PANELS, int A_PANEL, int B_PANEL>
+__device__ __forceinline__ void product_over_columns(uint32_t d, uint32_t a, uint32_t b, uint32_t desc,
+                                                     uint32_t steps) {
+  auto step = [&](uint32_t at, uint32_t bt, bool more) {
+    if (INSIDE) mma_ts_low(d, at, bt, desc, more); else mma_ss_low(d, at, bt, desc, more);
+  };
+  constexpr int kStep = INSIDE ? 8 : 2;
+#pragma unroll
+  for (int p = 0; p < PANELS; ++p) {
+    const uint32_t n = steps >> (4 * p) & 15u, bp = b + p * (B_PANEL >> 4);
+    if (n == 0) break;
+    step(a, bp, p > 0);
+    if (n == 4) {
+      step(a + kStep, bp + 2, true);
+      step(a + 2 * kStep, bp + 4, true);
+      step(a + 3 * kStep, bp + 6, true);
+    } else {
+      if (n > 1) step(a + kStep, bp + 2, true);
+      if (n > 2) step(a + 2 * kStep, bp + 4, true);
+    }
+    a += INSIDE ? n * 8 : A_PANEL >> 4;
   }
 }
 

@@ -242,51 +242,46 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       constexpr uint32_t d_s = mma_desc(bf16, false, false, kTile, kKeys);
       const uint32_t d_q = mma_desc(bf16, false, true, kTile, m.s.one_product ? D : f.dn);
       const uint32_t d_t = mma_desc(bf16, false, true, kTile, f.dr);
-      const uint64_t q_desc = tile_desc(base, 16, 1024), o_desc = tile_desc(base + do_at, 16, 1024);
-      const uint64_t k_cols = tile_desc(base + ring_at, 16, 1024);
-      const uint64_t k_rows = tile_desc(base + ring_at, kPanel, 1024);
-      const int nope_last = m.s.nope_panels - 1, cut = f.dn - nope_last * 64;
-      const int q_last = f.dr > 0 ? f.dr : cut, v_last = f.dv - (v_panels - 1) * 64;
-      auto scores = [&](int i, int stage, int around) {
+      const uint32_t q_low = desc_low(base, 16), o_low = desc_low(base + do_at, 16);
+      const uint32_t stage_step = stage_bytes >> 4, v_step = v_at >> 4;
+      const uint32_t q_steps = panel_steps(panels, m.s.nope_panels, f.dn, f.dr);
+      const uint32_t v_steps = panel_steps(v_panels, v_panels, f.dv, 0);
+      const uint32_t tail_step = m.s.nope_panels * kPanel >> 4;
+      // the tiles' rows as operands over columns, and over rows (panels apart)
+      const uint32_t cols_low = desc_low(base + ring_at, 16), rows_low = desc_low(base + ring_at, kPanel);
+      auto scores = [&](int i, int stage, uint32_t at, int around) {
         mbar_wait(bar(sm.full[stage]), around & 1, dead);
         tc_fence_after();
         const uint32_t d = tmem + (i & 1) * kKeys;
-        uint64_t k = k_cols + (stage * stage_bytes >> 4), q = q_desc;
-        uint32_t in = q_in;
-        for (int p = 0; p < panels; ++p, k += kPanel >> 4, q += kOwnPanel >> 4) {
-          const int cols = p == panels - 1 ? q_last : p == nope_last ? cut : 64;
-          if (m.q_inside) panel_scores_inside(d, in, k, d_s, cols, p > 0);
-          else panel_scores(d, q, k, d_s, cols, p > 0);
-          in += cols / 2;
-        }
+        if (m.q_inside)
+          product_over_columns<true, kMaxPanels, 0, kPanel>(d, q_in, cols_low + at, d_s, q_steps);
+        else
+          product_over_columns<false, kMaxPanels, kOwnPanel, kPanel>(d, q_low, cols_low + at, d_s, q_steps);
         tc_commit(bar(sm.s_full[i & 1]));
       };
-      auto dps = [&](int stage) {
-        const uint64_t v = k_cols + ((stage * stage_bytes + v_at) >> 4);
-        const int cols = v_panels == 1 ? v_last : 64;
-        if (m.do_inside) {
-          panel_scores_inside(dp_at, do_in, v, d_s, cols, false);
-          if (v_panels == 2) panel_scores_inside(dp_at, do_in + 32, v + (kPanel >> 4), d_s, v_last, true);
-        } else {
-          panel_scores(dp_at, o_desc, v, d_s, cols, false);
-          if (v_panels == 2)
-            panel_scores(dp_at, o_desc + (kOwnPanel >> 4), v + (kPanel >> 4), d_s, v_last, true);
-        }
+      auto dps = [&](uint32_t at) {
+        if (m.do_inside)
+          product_over_columns<true, 2, 0, kPanel>(dp_at, do_in, cols_low + at + v_step, d_s, v_steps);
+        else
+          product_over_columns<false, 2, kOwnPanel, kPanel>(dp_at, o_low, cols_low + at + v_step, d_s, v_steps);
         tc_commit(bar(sm.dp_full));
       };
       int stage = 0, around = 0, looked = 0, looked_around = 0;
+      uint32_t at = 0;
       if (n > 0) {
         if (!m.q_inside || !m.do_inside) mbar_wait(bar(sm.own), 0, dead);
-        scores(0, 0, 0);
+        scores(0, 0, 0, 0);
         dps(0);
       }
       for (int i = 0; i < n; ++i) {
-        const int next = stage + 1 == stages ? 0 : stage + 1, next_around = around + (next == 0);
+        const bool wrap = stage + 1 == stages;
+        const int next = wrap ? 0 : stage + 1, next_around = around + (wrap ? 1 : 0);
+        const uint32_t next_at = wrap ? 0 : at + stage_step;
         if (i + 1 < n) {
-          scores(i + 1, next, next_around);
+          scores(i + 1, next, next_at, next_around);
           mbar_wait(bar(sm.dp_read), i & 1, dead);
           tc_fence_after();
-          dps(next);
+          dps(next_at);
         }
         if (i >= first_masked) {
           mbar_wait(bar(sm.looked[looked]), looked_around & 1, dead);
@@ -294,18 +289,23 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
         mbar_wait(bar(sm.ready), i & 1, dead);
         tc_fence_after();
-        const uint32_t ds_at = tmem + (i & 1) * kKeys;
-        const uint64_t k = k_rows + (stage * stage_bytes >> 4);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t at = ds_at + (x >> 1) * 32 + (x & 1) * 8;
-          mma_ts(dq_at, at, k + 128 * x, d_q, i > 0 || x > 0);
-          if (!m.s.one_product)
-            mma_ts(dq_at + f.dn, at, k + (m.s.nope_panels * kPanel >> 4) + 128 * x, d_t, i > 0 || x > 0);
+        const uint32_t ds_at = tmem + (i & 1) * kKeys, k = rows_low + at;
+        const bool more = i > 0;
+        mma_ts_low(dq_at, ds_at, k, d_q, more);
+        mma_ts_low(dq_at, ds_at + 8, k + 128, d_q, true);
+        mma_ts_low(dq_at, ds_at + 32, k + 256, d_q, true);
+        mma_ts_low(dq_at, ds_at + 40, k + 384, d_q, true);
+        if (!m.s.one_product) {
+          const uint32_t d = dq_at + f.dn, x = k + tail_step;
+          mma_ts_low(d, ds_at, x, d_t, more);
+          mma_ts_low(d, ds_at + 8, x + 128, d_t, true);
+          mma_ts_low(d, ds_at + 32, x + 256, d_t, true);
+          mma_ts_low(d, ds_at + 40, x + 384, d_t, true);
         }
         tc_commit(bar(sm.empty[stage]));
         stage = next;
         around = next_around;
+        at = next_at;
       }
       tc_commit(bar(sm.done));
       tc_commit(bar(sm.issued));
