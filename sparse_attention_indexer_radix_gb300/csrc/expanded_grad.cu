@@ -1,6 +1,6 @@
 // expanded_grad.cu -- the backward pass of the expanded attention: entry points,
 // the rows' statistics before it and the tail's sum over the heads after it.
-#include "expanded_grad_mma.cuh"
+#include "expanded_grad.cuh"
 
 namespace satk {
 namespace {
@@ -65,26 +65,6 @@ __global__ void __launch_bounds__(256) grad_tail_kernel(ExpandedGradArgs a, int6
   float sum = 0.f;
   for (int h = 0; h < a.f.H; ++h) sum += a.tails[h * n + i];
   static_cast<E *>(a.dtail)[i / a.f.dr * a.ld_dtail + i % a.f.dr] = Elem<E>::from(sum);
-}
-
-// Whether the tensor-core kernels take a call, and its shape for them: widths in
-// steps of 16, rows of 16 bytes, something to see.
-bool mma_fits(const ExpandedGradArgs &a, GradShape &s) {
-  const ExpandedArgs &f = a.f;
-  s.nope_panels = (f.dn + 63) / 64;
-  s.panels = s.nope_panels + (f.dr > 0 ? 1 : 0);
-  s.v_panels = (f.dv + 63) / 64;
-  s.one_product = f.dr == 0 || f.dn % 64 == 0;
-  s.vec_k = rows_of_16_bytes(a.dk, f.S, a.ld_dk_s, f.H, a.ld_dk_h);
-  s.vec_v = rows_of_16_bytes(a.dv, f.S, a.ld_dv_s, f.H, a.ld_dv_h);
-  s.vec_q = rows_of_16_bytes(a.dq, f.T, a.ld_dq_t, f.H, a.ld_dq_h);
-  return f.T > 0 && f.S > 0 && f.R > 0 && f.dn % 16 == 0 && f.dr % 16 == 0 && f.dv % 16 == 0 &&
-         f.dr <= 64 && s.panels <= kMaxPanels && rows_of_16_bytes(f.q, f.T, f.ld_q_t, f.H, f.ld_q_h) &&
-         rows_of_16_bytes(a.dout, f.T, a.ld_do_t, f.H, a.ld_do_h) &&
-         rows_of_16_bytes(f.k, f.S, f.ld_k_s, f.H, f.ld_k_h) &&
-         rows_of_16_bytes(f.v, f.S, f.ld_v_s, f.H, f.ld_v_h) &&
-         (f.dr == 0 || rows_of_16_bytes(f.tail, f.S, f.ld_tail, 1, 0)) &&
-         expanded_grad_keys_fits(a, s) && expanded_grad_tokens_fits(a, s);
 }
 
 }  // namespace
@@ -171,13 +151,8 @@ extern "C" int satk_latent_attend_expanded_grad(
   a.tails = reinterpret_cast<float *>(at + w.tails);
   const cudaStream_t s = as_stream(stream);
   int rc = expanded_grad_prepare(a, dtype, s);
-  GradShape shape;
-  if (rc == SATK_OK && mma_fits(a, shape)) {
-    rc = expanded_grad_keys(a, shape, dtype, s);
-    if (rc == SATK_OK) rc = expanded_grad_tokens(a, shape, dtype, s);
-  } else if (rc == SATK_OK) {
-    rc = expanded_grad_warp(a, dtype, s);
-  }
+  if (rc == SATK_OK)
+    rc = expanded_grad_mma_fits(a) ? expanded_grad_mma(a, dtype, s) : expanded_grad_warp(a, dtype, s);
   if (rc == SATK_OK) rc = expanded_grad_tail(a, dtype, s);
   return rc;
 }

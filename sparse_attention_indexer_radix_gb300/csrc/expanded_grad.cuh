@@ -84,8 +84,11 @@ __device__ __forceinline__ float grad_weight(float raw, float scale_log2, float 
   return exp2_fast(x);
 }
 
-// stats and ends; then dk, dv and the heads' tails, and dq; then the tail's sum.
+// stats and ends; then dk, dv and the heads' tails, and dq, by the general kernels or
+// (where they take the call) on the tensor cores; then the tail's sum.
 int expanded_grad_prepare(const ExpandedGradArgs &a, int dtype, cudaStream_t stream);
+bool expanded_grad_mma_fits(const ExpandedGradArgs &a);
+int expanded_grad_mma(const ExpandedGradArgs &a, int dtype, cudaStream_t stream);
 int expanded_grad_warp(const ExpandedGradArgs &a, int dtype, cudaStream_t stream);
 int expanded_grad_tail(const ExpandedGradArgs &a, int dtype, cudaStream_t stream);
 

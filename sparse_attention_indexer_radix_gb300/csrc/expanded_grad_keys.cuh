@@ -1,4 +1,4 @@
-// expanded_grad_keys.cu -- gradients of keys, tail and values of the expanded
+// expanded_grad_keys.cuh -- gradients of keys, tail and values of the expanded
 // attention on the tensor cores.
 //
 // A CTA takes 128 keys of one request and head and goes over the tokens that see
@@ -19,18 +19,18 @@
 // Bounded by the tensor core: at 192 query/key and 128 value columns a 128 x 64
 // tile is 1280 cycles of products, of which the scores and dP read both operands
 // from shared memory (6 KB in 32 cycles: 1.5 times what it delivers).
+#pragma once
+
 #include "expanded_grad_mma.cuh"
 
 namespace satk {
-namespace {
+namespace grad_keys {
 
 constexpr int kTokens = kGradTokens;  // of a tile
 constexpr int kKeyPanel = kTile * 128, kTokenPanel = kTokens * 128;  // bytes
 constexpr int kMaxStages = 4;
 
-struct KeysMma {
-  ExpandedGradArgs a;
-  GradShape s;
+struct Plan {
   int stages, score_buffers;
   CUtensorMap q, dout, k, tail, v;
 };
@@ -43,7 +43,9 @@ struct alignas(16) Tokens {
 
 struct Small {
   uint64_t own, full[kMaxStages], empty[kMaxStages], tokens[kMaxStages], looked[kMaxStages];
-  uint64_t s_full[2], dp_full, dp_read, ready, done, issued;
+  // (ready: a warp may be a tile ahead of another, so its arrival must not count for
+  // the tile before)
+  uint64_t s_full[2], dp_full, dp_read, ready[2], done, issued;
   int least[kMaxStages][2];  // smallest row end of each half of a tile
   int odd_end;               // keys below it are seen by a token that is not finite
   int place[6];              // first key (of all), first key of the request's, keys in the tile,
@@ -72,13 +74,12 @@ struct LiveTiles {
   }
 };
 
+// CTA `block` of `blocks`.
 template <class E>
-__global__ void __launch_bounds__(kGradThreads, 1)
-    expanded_grad_keys_kernel(const __grid_constant__ KeysMma m) {
-  extern __shared__ __align__(1024) unsigned char smem[];
-  const ExpandedGradArgs &a = m.a;
+__device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &shape, const Plan &m,
+                                    unsigned char *smem, unsigned block, unsigned blocks) {
   const ExpandedArgs &f = a.f;
-  const int panels = m.s.panels, v_panels = m.s.v_panels, stages = m.stages;
+  const int panels = shape.panels, v_panels = shape.v_panels, stages = m.stages;
   const uint32_t base = smem_addr(smem);
   const int v_at = panels * kKeyPanel, ring_at = v_at + v_panels * kKeyPanel;
   const int stage_bytes = (panels + v_panels) * kTokenPanel, do_at = panels * kTokenPanel;
@@ -87,10 +88,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   volatile int *dead = &sm.dead;
   auto bar = [&](uint64_t &b) { return smem_addr(&b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x % f.H;
+  const int h = block % f.H;
   const int D = f.dn + f.dr;
 
-  if (blockIdx.x >= gridDim.x - f.H) {
+  if (block >= blocks - f.H) {
     rows_outside(f.key_starts, f.R, f.S, [&](int64_t s) {
       E *k = static_cast<E *>(a.dk) + s * a.ld_dk_s + h * a.ld_dk_h;
       E *v = static_cast<E *>(a.dv) + s * a.ld_dv_s + h * a.ld_dv_h;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     return;
   }
   if (warp == 0) {
-    const int slot = blockIdx.x / f.H;
+    const int slot = block / f.H;
     const int r = request_of_slot(f.key_starts, f.R, f.S, slot);
     const Span keys = span_of(f.key_starts, r, f.S), mine = span_of(f.token_starts, r, f.T);
     const int64_t first = static_cast<int64_t>(slot - keys.begin / kTile - r) * kTile;
@@ -130,7 +131,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     mbar_init(bar(sm.s_full[1]), 1);
     mbar_init(bar(sm.dp_full), 1);
     mbar_init(bar(sm.dp_read), 256);
-    mbar_init(bar(sm.ready), 256);
+    mbar_init(bar(sm.ready[0]), 256);
+    mbar_init(bar(sm.ready[1]), 256);
     mbar_init(bar(sm.done), 1);
     mbar_init(bar(sm.issued), 1);
     sm.dead = 0;
@@ -161,7 +163,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   if (warp < 8) regs_raise<208>(); else regs_lower<88>();
   if (warp < 8) {
     // ------------------------------------------------------- P and dS, results
-    // A thread has a key (its TMEM lane) and half of each tile's tokens.
+    // A warp has 32 keys (its TMEM lanes) and half of each tile's tokens; a thread
+    // two of every eight tokens of four keys, so that it needs few tokens' numbers: a
+    // load that all lanes share costs shared memory as much as any other, and the
+    // products need all that it delivers (one key and 32 tokens a thread: 451 cycles
+    // of loads a tile).
     const int half = warp >> 2, row = threadIdx.x & 127, key = key0 + row;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float2 scale2 = make_float2(f.scale_log2, f.scale_log2);
@@ -170,23 +176,25 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const int buffer = buffers == 2 ? i & 1 : 0;
       const uint32_t s_at = tmem + buffer * kTokens + half * 32 + lanes;
       const Tokens &tk = tokens[stage];
-      uint32_t s[32], dp[32];
+      uint32_t s[32], dp[32], p16[16], d16[16];
       mbar_wait(bar(sm.tokens[stage]), around & 1, dead);
+      const bool masked = sm.least[stage][half] < key0 + kTile;
+      float2 less[4], delta[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        less[j] = *reinterpret_cast<const float2 *>(tk.less + half * 32 + 8 * j + 2 * (lane & 3));
+        delta[j] = *reinterpret_cast<const float2 *>(tk.delta + half * 32 + 8 * j + 2 * (lane & 3));
+      }
       mbar_wait(bar(sm.s_full[buffer]), (buffers == 2 ? i >> 1 : i) & 1, dead);
       __syncwarp();
       tc_fence_after();
-      tmem_ld32(s, 0, s_at);
+      tmem_ld_pairs(s, 0, s_at);
+      tmem_ld_pairs(s, 16, s_at + (16u << 16));
       tmem_wait_ld();
-      const bool masked = sm.least[stage][half] < key0 + kTile;
-      // (four tokens a load: every load takes a cycle from the products' operands)
-      const float4 *less = reinterpret_cast<const float4 *>(tk.less + half * 32);
-      const float4 *delta = reinterpret_cast<const float4 *>(tk.delta + half * 32);
-      const int *end = tk.end + half * 32;
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
-        const float4 l4 = less[x >> 1];
         float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
-                              scale2, (x & 1) != 0 ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+                              scale2, less[x >> 1 & 3]);
         asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as grad_weight)
         asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.y));
         s[2 * x] = __float_as_uint(exp2_fast(e.x));
@@ -195,26 +203,29 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       mbar_wait(bar(sm.dp_full), i & 1, dead);
       __syncwarp();
       tc_fence_after();
-      tmem_ld32(dp, 0, dp_at + half * 32 + lanes);
+      tmem_ld_pairs(dp, 0, dp_at + half * 32 + lanes);
+      tmem_ld_pairs(dp, 16, dp_at + half * 32 + lanes + (16u << 16));
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(bar(sm.dp_read));
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
-        const float2 p = make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
-        const float4 d4 = delta[x >> 1];
         const float2 d = __fmul2_rn(
-            p, __fadd2_rn(make_float2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])),
-                          (x & 1) != 0 ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y)));
+            make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
+            __fadd2_rn(make_float2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])),
+                       delta[x >> 1 & 3]));
         dp[2 * x] = __float_as_uint(d.x);
         dp[2 * x + 1] = __float_as_uint(d.y);
       }
       if (masked) {
 #pragma unroll
-        for (int x = 0; x < 32; ++x)
-          if (key >= end[x]) s[x] = dp[x] = 0;
+        for (int x = 0; x < 16; ++x) {
+          const int2 end = *reinterpret_cast<const int2 *>(tk.end + half * 32 + 8 * (x >> 1 & 3) + 2 * (lane & 3));
+          const int key = key0 + (warp & 3) * 32 + (x >> 3) * 16 + (x & 1) * 8 + (lane >> 2);
+          if (key >= end.x) s[2 * x] = dp[2 * x] = 0;
+          if (key >= end.y) s[2 * x + 1] = dp[2 * x + 1] = 0;
+        }
       }
-      uint32_t p16[16], d16[16];
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         union {
@@ -227,11 +238,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         d16[x] = pk.u;
       }
       // This half's 32 columns of scores become 16 of P and 16 of dS.
-      tmem_st16(s_at, p16);
-      tmem_st16(s_at + 16, d16);
+      tmem_st_packed(s_at, p16, 0);
+      tmem_st_packed(s_at + (16u << 16), p16, 8);
+      tmem_st_packed(s_at + 16, d16, 0);
+      tmem_st_packed(s_at + 16 + (16u << 16), d16, 8);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bar(sm.ready));
+      mbar_arrive(bar(sm.ready[i & 1]));
       if (++stage == stages) stage = 0, ++around;
     }
     if (n > 0) {
@@ -257,9 +270,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (row >= rows) {
         // not one of this request's keys
       } else if (ck < 0) {
-        store16<E>(to_v + c, x, nan ? NAN : 1.f, m.s.vec_v);
+        store16<E>(to_v + c, x, nan ? NAN : 1.f, shape.vec_v);
       } else if (ck < f.dn) {
-        store16<E>(to_k + ck, x, nan ? NAN : a.scale, m.s.vec_k);
+        store16<E>(to_k + ck, x, nan ? NAN : a.scale, shape.vec_k);
       } else {
         const float scale = nan ? NAN : a.scale;
         float4 *to = reinterpret_cast<float4 *>(to_tail + ck - f.dn);
@@ -277,13 +290,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
       constexpr uint32_t d_s = mma_desc(bf16, false, false, kTile, kTokens);
       const uint32_t d_v = mma_desc(bf16, false, true, kTile, f.dv);
-      const uint32_t d_k = mma_desc(bf16, false, true, kTile, m.s.one_product ? D : f.dn);
+      const uint32_t d_k = mma_desc(bf16, false, true, kTile, shape.one_product ? D : f.dn);
       const uint32_t d_t = mma_desc(bf16, false, true, kTile, f.dr);
       const uint32_t k_low = desc_low(base, 16), v_low = desc_low(base + v_at, 16);
       const uint32_t stage_step = stage_bytes >> 4, do_step = do_at >> 4;
-      const uint32_t q_steps = panel_steps(panels, m.s.nope_panels, f.dn, f.dr);
+      const uint32_t q_steps = panel_steps(panels, shape.nope_panels, f.dn, f.dr);
       const uint32_t v_steps = panel_steps(v_panels, v_panels, f.dv, 0);
-      const uint32_t tail_step = m.s.nope_panels * kTokenPanel >> 4;
+      const uint32_t tail_step = shape.nope_panels * kTokenPanel >> 4;
       // the tiles' rows as operands over columns, and over rows (panels apart)
       const uint32_t cols_low = desc_low(base + ring_at, 16), rows_low = desc_low(base + ring_at, kTokenPanel);
       auto scores = [&](int i, int stage, uint32_t at, int around) {
@@ -317,7 +330,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           dps(next_at);
         }
         mbar_wait(bar(sm.looked[stage]), around & 1, dead);
-        mbar_wait(bar(sm.ready), i & 1, dead);
+        mbar_wait(bar(sm.ready[i & 1]), (i >> 1) & 1, dead);
         tc_fence_after();
         const uint32_t p_at = tmem + (buffers == 2 ? i & 1 : 0) * kTokens;
         const uint32_t q = rows_low + at, o = q + do_step;
@@ -330,7 +343,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         mma_ts_low(dk_at, p_at + 24, q + 128, d_k, true);
         mma_ts_low(dk_at, p_at + 48, q + 256, d_k, true);
         mma_ts_low(dk_at, p_at + 56, q + 384, d_k, true);
-        if (!m.s.one_product) {
+        if (!shape.one_product) {
           const uint32_t d = dk_at + f.dn, x = q + tail_step;
           mma_ts_low(d, p_at + 16, x, d_t, more);
           mma_ts_low(d, p_at + 24, x + 128, d_t, true);
@@ -357,10 +370,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (n > 0) {
       if (lane == 0) mbar_expect(bar(sm.own), (panels + v_panels) * kKeyPanel);
       __syncwarp();
-      for (int p = 0; p < m.s.nope_panels; ++p)
+      for (int p = 0; p < shape.nope_panels; ++p)
         tma_box3(leader, base + p * kKeyPanel, &m.k, p * 64, h, key_at, bar(sm.own));
       if (f.dr > 0)
-        tma_box(leader, base + m.s.nope_panels * kKeyPanel, &m.tail, 0, key_at, bar(sm.own));
+        tma_box(leader, base + shape.nope_panels * kKeyPanel, &m.tail, 0, key_at, bar(sm.own));
       for (int p = 0; p < v_panels; ++p)
         tma_box3(leader, base + v_at + p * kKeyPanel, &m.v, p * 64, h, key_at, bar(sm.own));
     }
@@ -373,7 +386,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (lane == 0) mbar_expect(full, stage_bytes);
       __syncwarp();
       for (int p = 0; p < panels; ++p)
-        tma_box3(leader, to + p * kTokenPanel, &m.q, p < m.s.nope_panels ? p * 64 : f.dn, h, t, full);
+        tma_box3(leader, to + p * kTokenPanel, &m.q, p < shape.nope_panels ? p * 64 : f.dn, h, t, full);
       for (int p = 0; p < v_panels; ++p)
         tma_box3(leader, to + do_at + p * kTokenPanel, &m.dout, p * 64, h, t, full);
       if (++stage == stages) stage = 0, ++around;
@@ -432,50 +445,25 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   if (warp == 8) tmem_free(tmem, 512);
 }
 
-// Stages and buffers that fit.
-bool layout(const ExpandedGradArgs &a, KeysMma &m, int &smem) {
-  const int D = a.f.dn + a.f.dr, stage = (m.s.panels + m.s.v_panels) * kTokenPanel;
-  const int own = (m.s.panels + m.s.v_panels) * kKeyPanel;
-  m.stages = (kSmemLimit - own - static_cast<int>(sizeof(Small))) / (stage + static_cast<int>(sizeof(Tokens)));
+// Stages and buffers that fit; shared memory in `smem`.
+inline bool plan(const ExpandedGradArgs &a, const GradShape &shape, Plan &m, int &smem) {
+  const int D = a.f.dn + a.f.dr, stage = (shape.panels + shape.v_panels) * kTokenPanel;
+  const int own = (shape.panels + shape.v_panels) * kKeyPanel, numbers = static_cast<int>(sizeof(Tokens));
+  m.stages = (kSmemLimit - own - static_cast<int>(sizeof(Small))) / (stage + numbers);
   if (m.stages > kMaxStages) m.stages = kMaxStages;
-  smem = own + m.stages * (stage + static_cast<int>(sizeof(Tokens))) + static_cast<int>(sizeof(Small));
+  smem = own + m.stages * (stage + numbers) + static_cast<int>(sizeof(Small));
   m.score_buffers = 3 * kTokens + ((a.f.dv + 31) & ~31) + D <= 512 ? 2 : 1;
   return m.stages >= 2;
 }
 
-template <class E>
-int launch(const KeysMma &m, int smem, cudaStream_t stream) {
-  if (!allow_smem(expanded_grad_keys_kernel<E>, smem, kSmemLimit)) return SATK_ECUDA;
-  const int64_t grid = (tile_slots(m.a.f.S, m.a.f.R, kTile) + 1) * m.a.f.H;
-  if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
-  expanded_grad_keys_kernel<E><<<static_cast<unsigned>(grid), kGradThreads, smem, stream>>>(m);
-  return launch_status();
-}
-
-}  // namespace
-
-bool expanded_grad_keys_fits(const ExpandedGradArgs &a, const GradShape &s) {
-  KeysMma m;
-  m.s = s;
-  int smem;
-  return layout(a, m, smem);
-}
-
-int expanded_grad_keys(const ExpandedGradArgs &a, const GradShape &s, int dtype, cudaStream_t stream) {
-  KeysMma m;
-  m.a = a;
-  m.s = s;
-  int smem;
+inline bool maps(const ExpandedGradArgs &a, bool bf16, Plan &m) {
   const ExpandedArgs &f = a.f;
-  const bool bf16 = dtype == SATK_BF16;
-  if (!layout(a, m, smem)) return SATK_EUNSUPPORTED;
-  if (!grad_map(&m.q, bf16, f.q, f.dn + f.dr, f.H, f.T, f.ld_q_t, f.ld_q_h, kTokens) ||
-      !grad_map(&m.dout, bf16, a.dout, f.dv, f.H, f.T, a.ld_do_t, a.ld_do_h, kTokens) ||
-      !grad_map(&m.k, bf16, f.k, f.dn, f.H, f.S, f.ld_k_s, f.ld_k_h, kTile) ||
-      !grad_map(&m.v, bf16, f.v, f.dv, f.H, f.S, f.ld_v_s, f.ld_v_h, kTile) ||
-      (f.dr > 0 && !tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kTile)))
-    return SATK_ECUDA;
-  return bf16 ? launch<__nv_bfloat16>(m, smem, stream) : launch<__half>(m, smem, stream);
+  return grad_map(&m.q, bf16, f.q, f.dn + f.dr, f.H, f.T, f.ld_q_t, f.ld_q_h, kTokens) &&
+         grad_map(&m.dout, bf16, a.dout, f.dv, f.H, f.T, a.ld_do_t, a.ld_do_h, kTokens) &&
+         grad_map(&m.k, bf16, f.k, f.dn, f.H, f.S, f.ld_k_s, f.ld_k_h, kTile) &&
+         grad_map(&m.v, bf16, f.v, f.dv, f.H, f.S, f.ld_v_s, f.ld_v_h, kTile) &&
+         (f.dr == 0 || tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kTile));
 }
 
+}  // namespace grad_keys
 }  // namespace satk

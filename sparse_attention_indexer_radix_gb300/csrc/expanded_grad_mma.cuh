@@ -156,15 +156,32 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&v)[8]) 
                : "memory");
 }
 
-// dk, dv and the heads' tails; dq.
-bool expanded_grad_keys_fits(const ExpandedGradArgs &a, const GradShape &s);
-int expanded_grad_keys(const ExpandedGradArgs &a, const GradShape &s, int dtype, cudaStream_t stream);
-bool expanded_grad_tokens_fits(const ExpandedGradArgs &a, const GradShape &s);
-int expanded_grad_tokens(const ExpandedGradArgs &a, const GradShape &s, int dtype, cudaStream_t stream);
+// 32 columns of 16 lanes, eight columns a step: a thread gets columns 2 (l % 4) and
+// the next one of lanes l / 4 and l / 4 + 8, for its lane l of the warp.
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t (&v)[32], const int o, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+      "[%16];"
+      : SATK_R8(v, o), SATK_R8(v, o + 8)
+      : "r"(addr)
+      : "memory");
+}
+// The same places of 16 columns that hold two 16-bit values each.
+__device__ __forceinline__ void tmem_st_packed(uint32_t addr, const uint32_t (&v)[16], const int o) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::SATK_I8(v, o),
+               "r"(addr)
+               : "memory");
+}
 
-bool rows_of_16_bytes(const void *p, int64_t n, int64_t ld, int64_t H, int64_t ld_h);
+// Rows of 16-byte chunks; strides of dimensions of one are free.
+inline bool rows_of_16_bytes(const void *p, int64_t n, int64_t ld, int64_t H, int64_t ld_h) {
+  return aligned16(p) && (n <= 1 || ld % 8 == 0) && (H <= 1 || ld_h % 8 == 0);
+}
+
 // The tensor map of [n, H, cols] read in boxes of 64 columns x `rows` rows of a head.
-bool grad_map(CUtensorMap *to, bool bf16, const void *p, int cols, int64_t H, int64_t n, int64_t ld,
-              int64_t ld_h, int rows);
+inline bool grad_map(CUtensorMap *to, bool bf16, const void *p, int cols, int64_t H, int64_t n, int64_t ld,
+                     int64_t ld_h, int rows) {
+  return tensor_map_16bit(to, bf16, p, cols, H, H == 1 ? 1024 : ld_h, 1, n, n == 1 ? 1024 : ld, rows);
+}
 
 }  // namespace satk

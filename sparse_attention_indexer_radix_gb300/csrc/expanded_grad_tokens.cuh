@@ -1,4 +1,4 @@
-// expanded_grad_tokens.cu -- gradient of the queries of the expanded attention on
+// expanded_grad_tokens.cuh -- gradient of the queries of the expanded attention on
 // the tensor cores.
 //
 // A CTA takes 128 tokens of one request and head and goes over their keys in tiles
@@ -17,18 +17,18 @@
 //
 // Bounded by the tensor core: 1225 cycles of products a 128 x 64 tile at 192
 // query/key and 128 value columns.
+#pragma once
+
 #include "expanded_grad_mma.cuh"
 
 namespace satk {
-namespace {
+namespace grad_tokens {
 
 constexpr int kKeys = 64;  // of a tile
 constexpr int kOwnPanel = kTile * 128, kPanel = kKeys * 128;  // bytes of 64 columns
 constexpr int kMaxStages = 4;
 
-struct TokensMma {
-  ExpandedGradArgs a;
-  GradShape s;
+struct Plan {
   int stages;
   int q_inside, do_inside;  // in tensor memory
   CUtensorMap q, dout, k, tail, v;
@@ -36,7 +36,9 @@ struct TokensMma {
 
 struct Small {
   uint64_t own, full[kMaxStages], empty[kMaxStages], looked[kMaxStages];
-  uint64_t s_full[2], dp_full, dp_read, ready, done, issued;
+  // (ready: a warp may be a tile ahead of another, so its arrival must not count for
+  // the tile before)
+  uint64_t s_full[2], dp_full, dp_read, ready[2], done, issued;
   int low[8], high[8];
   int odd_key;   // the first key that is not finite
   int place[4];  // first key, keys, first token, tokens
@@ -58,13 +60,12 @@ __device__ __forceinline__ void row_inside(uint32_t at, const E *row, int cols, 
   }
 }
 
+// CTA `block` of `blocks`.
 template <class E>
-__global__ void __launch_bounds__(kGradThreads, 1)
-    expanded_grad_tokens_kernel(const __grid_constant__ TokensMma m) {
-  extern __shared__ __align__(1024) unsigned char smem[];
-  const ExpandedGradArgs &a = m.a;
+__device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &shape, const Plan &m,
+                                    unsigned char *smem, unsigned block, unsigned blocks) {
   const ExpandedArgs &f = a.f;
-  const int panels = m.s.panels, v_panels = m.s.v_panels, stages = m.stages;
+  const int panels = shape.panels, v_panels = shape.v_panels, stages = m.stages;
   const uint32_t base = smem_addr(smem);
   const int do_at = m.q_inside ? 0 : panels * kOwnPanel;
   const int ring_at = do_at + (m.do_inside ? 0 : v_panels * kOwnPanel);
@@ -73,10 +74,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   volatile int *dead = &sm.dead;
   auto bar = [&](uint64_t &b) { return smem_addr(&b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x % f.H;
+  const int h = block % f.H;
   const int D = f.dn + f.dr;
 
-  if (blockIdx.x >= gridDim.x - f.H) {
+  if (block >= blocks - f.H) {
     rows_outside(f.token_starts, f.R, f.T, [&](int64_t t) {
       E *q = static_cast<E *>(a.dq) + t * a.ld_dq_t + h * a.ld_dq_h;
       for (int c = lane; c < D; c += 32) q[c] = Elem<E>::from(0.f);
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     return;
   }
   if (warp == 0) {
-    const int slot = blockIdx.x / f.H;
+    const int slot = block / f.H;
     const int r = request_of_slot(f.token_starts, f.R, f.T, slot);
     const Span keys = span_of(f.key_starts, r, f.S), mine = span_of(f.token_starts, r, f.T);
     const int n = mine.end - mine.begin, count = (n + kTile - 1) / kTile;
@@ -109,7 +110,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     mbar_init(bar(sm.s_full[1]), 1);
     mbar_init(bar(sm.dp_full), 1);
     mbar_init(bar(sm.dp_read), 256);
-    mbar_init(bar(sm.ready), 256);
+    mbar_init(bar(sm.ready[0]), 256);
+    mbar_init(bar(sm.ready[1]), 256);
     mbar_init(bar(sm.done), 1);
     mbar_init(bar(sm.issued), 1);
     sm.dead = 0;
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       tmem_st16(s_at, packed);  // the first half of this thread's columns of S
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bar(sm.ready));
+      mbar_arrive(bar(sm.ready[i & 1]));
     }
     if (n > 0) {
       mbar_wait(bar(sm.done), 0, dead);
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int y = 0; y < 16; ++y) x[y] = 0;
       }
-      if (mine) store16<E>(to + c, x, nan ? NAN : a.scale, m.s.vec_q);
+      if (mine) store16<E>(to + c, x, nan ? NAN : a.scale, shape.vec_q);
       __syncwarp();
     }
     tc_fence_before();
@@ -240,13 +242,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (elect_leader()) {
       constexpr bool bf16 = std::is_same<E, __nv_bfloat16>::value;
       constexpr uint32_t d_s = mma_desc(bf16, false, false, kTile, kKeys);
-      const uint32_t d_q = mma_desc(bf16, false, true, kTile, m.s.one_product ? D : f.dn);
+      const uint32_t d_q = mma_desc(bf16, false, true, kTile, shape.one_product ? D : f.dn);
       const uint32_t d_t = mma_desc(bf16, false, true, kTile, f.dr);
       const uint32_t q_low = desc_low(base, 16), o_low = desc_low(base + do_at, 16);
       const uint32_t stage_step = stage_bytes >> 4, v_step = v_at >> 4;
-      const uint32_t q_steps = panel_steps(panels, m.s.nope_panels, f.dn, f.dr);
+      const uint32_t q_steps = panel_steps(panels, shape.nope_panels, f.dn, f.dr);
       const uint32_t v_steps = panel_steps(v_panels, v_panels, f.dv, 0);
-      const uint32_t tail_step = m.s.nope_panels * kPanel >> 4;
+      const uint32_t tail_step = shape.nope_panels * kPanel >> 4;
       // the tiles' rows as operands over columns, and over rows (panels apart)
       const uint32_t cols_low = desc_low(base + ring_at, 16), rows_low = desc_low(base + ring_at, kPanel);
       auto scores = [&](int i, int stage, uint32_t at, int around) {
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           product_over_columns<false, 2, kOwnPanel, kPanel>(dp_at, o_low, cols_low + at + v_step, d_s, v_steps);
         tc_commit(bar(sm.dp_full));
       };
-      int stage = 0, around = 0, looked = 0, looked_around = 0;
+      int stage = 0, around = 0;
       uint32_t at = 0;
       if (n > 0) {
         if (!m.q_inside || !m.do_inside) mbar_wait(bar(sm.own), 0, dead);
@@ -283,11 +285,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           tc_fence_after();
           dps(next_at);
         }
-        if (i >= first_masked) {
-          mbar_wait(bar(sm.looked[looked]), looked_around & 1, dead);
-          if (++looked == stages) looked = 0, ++looked_around;
-        }
-        mbar_wait(bar(sm.ready), i & 1, dead);
+        mbar_wait(bar(sm.looked[stage]), around & 1, dead);
+        mbar_wait(bar(sm.ready[i & 1]), (i >> 1) & 1, dead);
         tc_fence_after();
         const uint32_t ds_at = tmem + (i & 1) * kKeys, k = rows_low + at;
         const bool more = i > 0;
@@ -295,7 +294,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         mma_ts_low(dq_at, ds_at + 8, k + 128, d_q, true);
         mma_ts_low(dq_at, ds_at + 32, k + 256, d_q, true);
         mma_ts_low(dq_at, ds_at + 40, k + 384, d_q, true);
-        if (!m.s.one_product) {
+        if (!shape.one_product) {
           const uint32_t d = dq_at + f.dn, x = k + tail_step;
           mma_ts_low(d, ds_at, x, d_t, more);
           mma_ts_low(d, ds_at + 8, x + 128, d_t, true);
@@ -321,7 +320,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       __syncwarp();
       if (!m.q_inside)
         for (int p = 0; p < panels; ++p)
-          tma_box3(leader, base + p * kOwnPanel, &m.q, p < m.s.nope_panels ? p * 64 : f.dn, h, t0, bar(sm.own));
+          tma_box3(leader, base + p * kOwnPanel, &m.q, p < shape.nope_panels ? p * 64 : f.dn, h, t0, bar(sm.own));
       if (!m.do_inside)
         for (int p = 0; p < v_panels; ++p)
           tma_box3(leader, base + do_at + p * kOwnPanel, &m.dout, p * 64, h, t0, bar(sm.own));
@@ -334,8 +333,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const uint32_t full = bar(sm.full[stage]), to = base + ring_at + stage * stage_bytes;
       if (lane == 0) mbar_expect(full, stage_bytes);
       __syncwarp();
-      for (int p = 0; p < m.s.nope_panels; ++p) tma_box3(leader, to + p * kPanel, &m.k, p * 64, h, key, full);
-      if (f.dr > 0) tma_box(leader, to + m.s.nope_panels * kPanel, &m.tail, 0, key, full);
+      for (int p = 0; p < shape.nope_panels; ++p) tma_box3(leader, to + p * kPanel, &m.k, p * 64, h, key, full);
+      if (f.dr > 0) tma_box(leader, to + shape.nope_panels * kPanel, &m.tail, 0, key, full);
       for (int p = 0; p < v_panels; ++p) tma_box3(leader, to + v_at + p * kPanel, &m.v, p * 64, h, key, full);
       if (++stage == stages) stage = 0, ++around;
     }
@@ -345,17 +344,22 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     // ----------------------------------------------------------------- key rows
     // Where some token does not see some key, a key that is not finite would turn a
     // 0 of dS into NaN: it is cleared, and the tokens that do see it get NaN.
+    // (Every tile is waited for and answered: a barrier waited for later than its
+    // next phase but one would look like one that has not come.)
     const int y = (warp - 10) * 32 + lane;
-    for (int i = first_masked; i < n; ++i) {
-      const int stage = i % stages;
-      mbar_wait(bar(sm.full[stage]), (i / stages) & 1, dead);
-      unsigned char *k = smem + ring_at + stage * stage_bytes;
-      if (row_is_odd<E>(k, y, panels, kPanel)) {
-        clear_row(k, y, panels, kPanel);
-        atomicMin(&sm.odd_key, i * kKeys + y);
+    int stage = 0, around = 0;
+    for (int i = 0; i < n; ++i) {
+      mbar_wait(bar(sm.full[stage]), around & 1, dead);
+      if (i >= first_masked) {
+        unsigned char *k = smem + ring_at + stage * stage_bytes;
+        if (row_is_odd<E>(k, y, panels, kPanel)) {
+          clear_row(k, y, panels, kPanel);
+          atomicMin(&sm.odd_key, i * kKeys + y);
+        }
+        fence_async_shared();
       }
-      fence_async_shared();
-      mbar_arrive(bar(sm.looked[(i - first_masked) % stages]));
+      mbar_arrive(bar(sm.looked[stage]));
+      if (++stage == stages) stage = 0, ++around;
     }
   }
   __syncthreads();
@@ -363,62 +367,27 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 }
 
 // What fits: Q in tensor memory first, it saves most; then dO.
-bool layout(const ExpandedGradArgs &a, TokensMma &m, int &smem) {
-  const int D = a.f.dn + a.f.dr, stage = (m.s.panels + m.s.v_panels) * kPanel;
+inline bool plan(const ExpandedGradArgs &a, const GradShape &shape, Plan &m, int &smem) {
+  const int D = a.f.dn + a.f.dr, stage = (shape.panels + shape.v_panels) * kPanel;
   int columns = 3 * kKeys + D;
   m.q_inside = columns + D / 2 <= 512;
   if (m.q_inside) columns += D / 2;
   m.do_inside = columns + a.f.dv / 2 <= 512;
-  const int own = ((m.q_inside ? 0 : m.s.panels) + (m.do_inside ? 0 : m.s.v_panels)) * kOwnPanel;
+  const int own = ((m.q_inside ? 0 : shape.panels) + (m.do_inside ? 0 : shape.v_panels)) * kOwnPanel;
   m.stages = (kSmemLimit - own - static_cast<int>(sizeof(Small))) / stage;
   if (m.stages > kMaxStages) m.stages = kMaxStages;
   smem = own + m.stages * stage + static_cast<int>(sizeof(Small));
   return m.stages >= 2;
 }
 
-template <class E>
-int launch(const TokensMma &m, int smem, cudaStream_t stream) {
-  if (!allow_smem(expanded_grad_tokens_kernel<E>, smem, kSmemLimit)) return SATK_ECUDA;
-  const int64_t grid = (tile_slots(m.a.f.T, m.a.f.R, kTile) + 1) * m.a.f.H;
-  if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
-  expanded_grad_tokens_kernel<E><<<static_cast<unsigned>(grid), kGradThreads, smem, stream>>>(m);
-  return launch_status();
-}
-
-}  // namespace
-
-bool rows_of_16_bytes(const void *p, int64_t n, int64_t ld, int64_t H, int64_t ld_h) {
-  return aligned16(p) && (n <= 1 || ld % 8 == 0) && (H <= 1 || ld_h % 8 == 0);
-}
-
-bool grad_map(CUtensorMap *to, bool bf16, const void *p, int cols, int64_t H, int64_t n, int64_t ld,
-              int64_t ld_h, int rows) {
-  // Strides of dimensions of one are free: any multiple of 16 bytes.
-  return tensor_map_16bit(to, bf16, p, cols, H, H == 1 ? 1024 : ld_h, 1, n, n == 1 ? 1024 : ld, rows);
-}
-
-bool expanded_grad_tokens_fits(const ExpandedGradArgs &a, const GradShape &s) {
-  TokensMma m;
-  m.s = s;
-  int smem;
-  return layout(a, m, smem);
-}
-
-int expanded_grad_tokens(const ExpandedGradArgs &a, const GradShape &s, int dtype, cudaStream_t stream) {
-  TokensMma m;
-  m.a = a;
-  m.s = s;
-  int smem;
+inline bool maps(const ExpandedGradArgs &a, bool bf16, Plan &m) {
   const ExpandedArgs &f = a.f;
-  const bool bf16 = dtype == SATK_BF16;
-  if (!layout(a, m, smem)) return SATK_EUNSUPPORTED;
-  if (!grad_map(&m.q, bf16, f.q, f.dn + f.dr, f.H, f.T, f.ld_q_t, f.ld_q_h, kTile) ||
-      !grad_map(&m.dout, bf16, a.dout, f.dv, f.H, f.T, a.ld_do_t, a.ld_do_h, kTile) ||
-      !grad_map(&m.k, bf16, f.k, f.dn, f.H, f.S, f.ld_k_s, f.ld_k_h, kKeys) ||
-      !grad_map(&m.v, bf16, f.v, f.dv, f.H, f.S, f.ld_v_s, f.ld_v_h, kKeys) ||
-      (f.dr > 0 && !tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kKeys)))
-    return SATK_ECUDA;
-  return bf16 ? launch<__nv_bfloat16>(m, smem, stream) : launch<__half>(m, smem, stream);
+  return grad_map(&m.q, bf16, f.q, f.dn + f.dr, f.H, f.T, f.ld_q_t, f.ld_q_h, kTile) &&
+         grad_map(&m.dout, bf16, a.dout, f.dv, f.H, f.T, a.ld_do_t, a.ld_do_h, kTile) &&
+         grad_map(&m.k, bf16, f.k, f.dn, f.H, f.S, f.ld_k_s, f.ld_k_h, kKeys) &&
+         grad_map(&m.v, bf16, f.v, f.dv, f.H, f.S, f.ld_v_s, f.ld_v_h, kKeys) &&
+         (f.dr == 0 || tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kKeys));
 }
 
+}  // namespace grad_tokens
 }  // namespace satk

@@ -424,6 +424,22 @@ def test_streams_graphs_and_the_same_bits(shape):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("shape", [3, 5, 9])
+def test_calls_in_a_row_with_cold_caches(shape):
+    """The same bits whatever the memory system makes of the order in which loads,
+    products and rows' checks arrive: caches full of NaN patterns in between."""
+    c = Case(gen(43), BF16, *SHAPES[shape])
+    c.forward()
+    want = c.grad()
+    close(want, definition(c), "first")
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    for i in range(40):
+        if i % 2:
+            flush.fill_(255)
+        for x, y in zip(c.grad(), want):
+            assert torch.equal(x, y), i
+
+
 def test_refusals():
     c = Case(gen(42), BF16, 2, 32, 16, 32, [10], [5])
     c.forward()
