@@ -89,30 +89,6 @@ __device__ __forceinline__ void rows_outside(const int32_t *starts, int R, int n
   for (int64_t i = e + warp; i < n; i += warps) zero(i);
 }
 
-// MMAs with descriptors whose upper words are all the same (atoms of eight rows are
-// 1024 bytes apart): the lower words are what changes, a constant away from one
-// uniform register.  64-bit sums and loops over the steps cost 50 cycles an MMA to
-// issue, more than most of them take to run.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-
-__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
-  return ((addr >> 4) & 0x3fff) | (lbo >> 4) << 16;
-}
-__device__ __forceinline__ void mma_ss_low(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool more) {
-  asm volatile(
-      "{\n.reg .pred p;\n.reg .b64 x, y;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
-      "setp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(desc), "r"(more ? 1u : 0u), "r"(kDescHigh)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool more) {
-  asm volatile(
-      "{\n.reg .pred p;\n.reg .b64 y;\nmov.b64 y, {%2, %5};\n"
-      "setp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(desc), "r"(more ? 1u : 0u), "r"(kDescHigh)
-      : "memory");
-}
-
 // Steps of 16 columns of each panel, four bits a panel.
 __device__ __forceinline__ uint32_t panel_steps(int panels, int nope_panels, int dn, int dr) {
   uint32_t steps = 0;
@@ -147,35 +123,6 @@ __device__ __forceinline__ void product_over_columns(uint32_t d, uint32_t a, uin
     }
     a += INSIDE ? n * 8 : A_PANEL >> 4;
   }
-}
-
-// 32 lanes x 8 columns of tensor memory.
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::SATK_I8(v, 0),
-               "r"(addr)
-               : "memory");
-}
-
-// 32 columns of 16 lanes, eight columns a step: a thread gets columns 2 (l % 4) and
-// the next one of lanes l / 4 and l / 4 + 8, for its lane l of the warp.
-__device__ __forceinline__ void tmem_ld_pairs(uint32_t (&v)[32], const int o, uint32_t addr) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
-      "[%16];"
-      : SATK_R8(v, o), SATK_R8(v, o + 8)
-      : "r"(addr)
-      : "memory");
-}
-// The same places of 16 columns that hold two 16-bit values each.
-__device__ __forceinline__ void tmem_st_packed(uint32_t addr, const uint32_t (&v)[16], const int o) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::SATK_I8(v, o),
-               "r"(addr)
-               : "memory");
-}
-
-// Rows of 16-byte chunks; strides of dimensions of one are free.
-inline bool rows_of_16_bytes(const void *p, int64_t n, int64_t ld, int64_t H, int64_t ld_h) {
-  return aligned16(p) && (n <= 1 || ld % 8 == 0) && (H <= 1 || ld_h % 8 == 0);
 }
 
 // The tensor map of [n, H, cols] read in boxes of 64 columns x `rows` rows of a head.

@@ -62,6 +62,11 @@ __device__ __forceinline__ float far_exponent(float raw, float scale, float ref)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Rows of 16-byte chunks; strides of dimensions of one are free.
+inline bool rows_of_16_bytes(const void *p, int64_t n, int64_t ld, int64_t H, int64_t ld_h) {
+  return aligned16(p) && (n <= 1 || ld % 8 == 0) && (H <= 1 || ld_h % 8 == 0);
+}
+
 inline bool is_16bit(int dtype) { return dtype == SATK_BF16 || dtype == SATK_F16; }
 
 }  // namespace satk

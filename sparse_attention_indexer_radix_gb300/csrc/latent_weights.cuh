@@ -47,6 +47,10 @@ __device__ __forceinline__ float head_weight(float raw, float scale_log2, float 
   return lse_log2 == -INFINITY ? 0.f : exp2_fast(x);
 }
 
+// The tensor-core kernel: whether it takes this call, and the call.
+bool latent_weights_mma_fits(const WeightsArgs &a);
+int latent_weights_mma(const WeightsArgs &a, int dtype, cudaStream_t stream);
+
 // The general kernel: any widths, strides and alignment.
 int latent_weights_warp(const WeightsArgs &a, int dtype, cudaStream_t stream);
 

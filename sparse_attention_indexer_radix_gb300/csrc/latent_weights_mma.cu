@@ -1,0 +1,385 @@
+// latent_weights_mma.cu -- attention weights over selected rows on the tensor cores.
+//
+// Per token and tile of 128 of its entries:
+//   S[entry, head] = K[entry, :] . Q[head, :]      M = 128 entries, N heads
+//   out[entry]     = 1/H sum_head exp2(scale S - lse)
+// The entries are the M side, so that what is summed, the heads, lies along the
+// columns of tensor memory.  There is no maximum to look for: lse is known.
+//
+// The rows arrive as 16-byte asynchronous copies in panels of 64 columns x 128
+// rows through one ring that holds as many panels as shared memory has room for; a
+// panel's products start when it is there.  Eight warps keep several panels each
+// in flight.  A unit of work is a token and a piece of its tiles, dealt out over
+// persistent CTAs; the next unit's queries replace this one's a panel at a time,
+// behind the last tile's products.
+//
+// Bounded by the copies: 512 tokens x 2048 rows of 544 columns, 64 heads, are 1.1
+// GB through shared memory (17 us of products at the bf16 rate).
+#include <cuda.h>
+#include <type_traits>
+
+#include "latent_weights.cuh"
+#include "satk_tcgen05.cuh"
+
+namespace satk {
+namespace {
+
+constexpr int kRows = 128;             // entries of a tile
+constexpr int kPanel = kRows * 128;    // bytes of 64 columns of a tile
+constexpr int kThreads = 512;          // warps 0-3 sums, 4 MMAs, 5 queries, 8-15 rows
+constexpr int kMaxWide = 9;            // panels of a row
+constexpr int kMaxSlots = 12;
+constexpr int kHeads = 128;            // of a chunk
+constexpr int kUnitTiles = 4;          // tiles worth a load of queries
+
+struct WeightsMma {
+  WeightsArgs a;
+  int panels, last_steps;    // steps of 16 columns of the last panel
+  int slots, heads, chunks;  // heads of a chunk (a multiple of 16), chunks
+  int tiles, pieces, per;    // tiles of k entries, pieces of a token's tiles, tiles of a piece
+  int64_t units;
+  CUtensorMap q;
+};
+
+struct Small {
+  uint64_t full[kMaxSlots], empty[kMaxSlots], q_full[kMaxWide], q_empty[kMaxWide];
+  uint64_t s_full[2], s_empty[2], issued;
+  uint32_t tmem;
+  int dead;
+};
+
+// A CTA's units in order.  The next one's count is on its way while one is worked
+// on.
+struct Units {
+  const WeightsMma &m;
+  int64_t u;
+  int t, first, count, next_count;
+  __device__ __forceinline__ Units(const WeightsMma &m) : m(m), u(blockIdx.x), next_count(0) {
+    if (more()) next_count = entry_count(m.a, static_cast<int>(u / m.pieces));
+    set();
+  }
+  __device__ __forceinline__ bool more() const { return u < m.units; }
+  __device__ __forceinline__ void set() {
+    if (!more()) return;
+    t = static_cast<int>(u / m.pieces);
+    first = static_cast<int>(u % m.pieces) * m.per;
+    count = next_count;
+    const int64_t v = u + gridDim.x;
+    if (v < m.units) next_count = entry_count(m.a, static_cast<int>(v / m.pieces));
+  }
+  __device__ __forceinline__ void next() {
+    u += gridDim.x;
+    set();
+  }
+  __device__ __forceinline__ int last() const { return min(first + m.per, m.tiles); }
+  // tiles of the piece with an entry that counts
+  __device__ __forceinline__ int tiles() const {
+    return max(0, min(last(), (count + kRows - 1) / kRows) - first);
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// DEPTH: panels that a row warp has in flight.
+template <class E, int DEPTH>
+__global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const __grid_constant__ WeightsMma m) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const WeightsArgs &a = m.a;
+  const uint32_t base = smem_addr(smem);
+  const int q_panel = m.heads * 128, ring_at = m.panels * q_panel;
+  Small &sm = *reinterpret_cast<Small *>(smem + ring_at + m.slots * kPanel);
+  volatile int *dead = &sm.dead;
+  auto bar = [&](uint64_t &b) { return smem_addr(&b); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t buffer = m.heads, columns = m.heads <= 16 ? 32 : m.heads <= 32 ? 64 : m.heads <= 64 ? 128 : 256;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < m.slots; ++s) {
+      mbar_init(bar(sm.full[s]), 8);
+      mbar_init(bar(sm.empty[s]), 1);
+    }
+    for (int p = 0; p < m.panels; ++p) {
+      mbar_init(bar(sm.q_full[p]), 1);
+      mbar_init(bar(sm.q_empty[p]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(sm.s_full[b]), 1);
+      mbar_init(bar(sm.s_empty[b]), 4);
+    }
+    mbar_init(bar(sm.issued), 1);
+    sm.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 4) tmem_alloc(smem_addr(&sm.tmem), columns);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp < 4) {
+    // --------------------------------------------------------------------- sums
+    // A thread has two of every eight heads of four entries.
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+    const float share = 1.f / a.H;
+    int done = 0;  // tiles so far
+    for (Units w(m); w.more(); w.next()) {
+      const int n = w.tiles();
+      float *out = a.out + w.t * a.ld_out;
+      for (int c = 0; n > 0 && c < m.chunks; ++c) {
+        // -lse in log2; a head that saw nothing, or that is not there, adds nothing
+        float2 less[kHeads / 8];
+#pragma unroll
+        for (int j = 0; j < kHeads / 8; ++j) {
+          const int h = c * m.heads + 8 * j + 2 * (lane & 3);
+          const float *lse = a.lse + static_cast<int64_t>(w.t) * a.H + h;
+          const float x = 8 * j < m.heads && h < a.H ? lse[0] * kLog2e : -INFINITY;
+          const float y = 8 * j < m.heads && h + 1 < a.H ? lse[1] * kLog2e : -INFINITY;
+          less[j] = make_float2(x == -INFINITY ? x : -x, y == -INFINITY ? y : -y);
+        }
+        for (int i = 0; i < n; ++i, ++done) {
+          const int b = done & 1;
+          const int entry0 = (w.first + i) * kRows + warp * 32 + (lane >> 2);
+          bool live[4];
+          if ((lane & 3) == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) live[r] = entry_row(a, w.t, entry0 + 8 * r, w.count) >= 0;
+          }
+          mbar_wait(bar(sm.s_full[b]), (done >> 1) & 1, dead);
+          __syncwarp();
+          tc_fence_after();
+          float2 sum[4] = {};
+#pragma unroll
+          for (int j = 0; j < kHeads / 32; ++j) {
+            if (32 * j >= m.heads) break;
+            uint32_t s[32];
+            const uint32_t at = tmem + b * buffer + 32 * j + lanes;
+            if (32 * j + 32 <= m.heads) {
+              tmem_ld_pairs(s, 0, at);
+              tmem_ld_pairs(s, 16, at + (16u << 16));
+            } else {
+              tmem_ld_pairs_half(s, 0, at);
+              tmem_ld_pairs_half(s, 16, at + (16u << 16));
+#pragma unroll
+              for (int x = 8; x < 16; ++x) s[x] = s[16 + x] = 0;
+            }
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
+                                    scale2, less[4 * j + (x >> 1 & 3)]);
+              asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as head_weight)
+              asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.y));
+              e.x = exp2_fast(e.x);
+              e.y = exp2_fast(e.y);
+              const int r = (x >> 3) * 2 + (x & 1);
+              sum[r] = __fadd2_rn(sum[r], e);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sm.s_empty[b]));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float x = sum[r].x + sum[r].y;
+            x += __shfl_xor_sync(~0u, x, 1);
+            x += __shfl_xor_sync(~0u, x, 2);
+            const int e = entry0 + 8 * r;
+            if ((lane & 3) == 0 && e < a.k) {
+              x = *dead != 0 ? NAN : live[r] ? x * share : 0.f;
+              out[e] = c == 0 ? x : out[e] + x;
+            }
+          }
+        }
+      }
+      // Entries behind the token's count.
+      const int end = min(w.last() * kRows, a.k);
+      for (int e = (w.first + n) * kRows + threadIdx.x; e < end; e += kRows) out[e] = 0.f;
+    }
+    if (threadIdx.x == 0 && *dead != 0 && a.status != nullptr) atomicOr(a.status, SATK_STATUS_STALLED);
+  } else if (warp == 4) {
+    // ---------------------------------------------------------------- MMA issue
+    if (elect_leader()) {
+      const uint32_t desc = mma_desc(std::is_same<E, __nv_bfloat16>::value, false, false, kRows, m.heads);
+      const uint32_t q_low = desc_low(base, 16), ring_low = desc_low(base + ring_at, 16);
+      int slot = 0, around = 0, done = 0, loads = 0;
+      for (Units w(m); w.more(); w.next()) {
+        const int n = w.tiles();
+        for (int c = 0; n > 0 && c < m.chunks; ++c, ++loads)
+          for (int i = 0; i < n; ++i, ++done) {
+            const int b = done & 1;
+            if (done >= 2) mbar_wait(bar(sm.s_empty[b]), ((done >> 1) - 1) & 1, dead);
+            uint32_t q = q_low;
+            for (int p = 0; p < m.panels; ++p, q += q_panel >> 4) {
+              if (i == 0) mbar_wait(bar(sm.q_full[p]), loads & 1, dead);
+              mbar_wait(bar(sm.full[slot]), around & 1, dead);
+              tc_fence_after();
+              const uint32_t d = tmem + b * buffer, k = ring_low + slot * (kPanel >> 4);
+              mma_ss_low(d, k, q, desc, p > 0);
+              if (p < m.panels - 1 || m.last_steps == 4) {
+                mma_ss_low(d, k + 2, q + 2, desc, true);
+                mma_ss_low(d, k + 4, q + 4, desc, true);
+                mma_ss_low(d, k + 6, q + 6, desc, true);
+              } else {
+                if (m.last_steps > 1) mma_ss_low(d, k + 2, q + 2, desc, true);
+                if (m.last_steps > 2) mma_ss_low(d, k + 4, q + 4, desc, true);
+              }
+              tc_commit(bar(sm.empty[slot]));
+              if (i == n - 1) tc_commit(bar(sm.q_empty[p]));
+              if (++slot == m.slots) slot = 0, ++around;
+            }
+            tc_commit(bar(sm.s_full[b]));
+          }
+      }
+      tc_commit(bar(sm.issued));
+      mbar_drain(bar(sm.issued), 0);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ------------------------------------------------------------------ queries
+    const uint32_t leader = elect_leader();
+    int loads = 0;
+    for (Units w(m); w.more(); w.next())
+      for (int c = 0; w.tiles() > 0 && c < m.chunks; ++c, ++loads)
+        for (int p = 0; p < m.panels; ++p) {
+          if (loads > 0) mbar_wait(bar(sm.q_empty[p]), (loads - 1) & 1, dead);
+          __syncwarp();
+          if (lane == 0) mbar_expect(bar(sm.q_full[p]), q_panel);
+          __syncwarp();
+          tma_box3(leader, base + p * q_panel, &m.q, p * 64, c * m.heads, w.t, bar(sm.q_full[p]));
+        }
+    if (loads > 0)
+      for (int p = 0; p < m.panels; ++p) mbar_drain(bar(sm.q_full[p]), (loads - 1) & 1);
+  } else if (warp >= 8) {
+    // --------------------------------------------------------------------- rows
+    // A warp has 16 rows of every panel, four rows x 128 bytes an instruction.
+    const int r0 = (warp - 8) * 16, ch = lane & 7;
+    const E *cache = static_cast<const E *>(a.cache);
+    uint32_t dst[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int r = r0 + 4 * g + (lane >> 3);
+      dst[g] = base + ring_at + r * 128 + ((ch ^ (r & 7)) << 4);
+    }
+    int slot = 0, around = 0, filled = 0, told = 0, told_slot = 0;
+    auto tell = [&]() {  // the oldest panel that has not been handed over
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sm.full[told_slot]));
+      if (++told_slot == m.slots) told_slot = 0;
+      ++told;
+    };
+    Units w(m);
+    int c = 0, i = 0;
+    while (w.more() && w.tiles() == 0) w.next();
+    auto rows_of = [&]() {  // of this lane: entry r0 + lane of the tile
+      const int64_t row = lane < 16 ? entry_row(a, w.t, (w.first + i) * kRows + r0 + lane, w.count) : -1;
+      return static_cast<int>(row);
+    };
+    int row = w.more() ? rows_of() : -1;
+    while (w.more()) {
+      const E *src[4];
+      bool live[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int at = __shfl_sync(~0u, row, 4 * g + (lane >> 3));
+        live[g] = at >= 0;
+        src[g] = cache + static_cast<int64_t>(live[g] ? at : 0) * a.ld_cache + ch * 8;
+      }
+      // the next tile's rows are looked up while this one's are copied
+      if (++i == w.tiles()) {
+        i = 0;
+        if (++c == m.chunks) {
+          c = 0;
+          do w.next();
+          while (w.more() && w.tiles() == 0);
+        }
+      }
+      if (w.more()) row = rows_of();
+      for (int p = 0; p < m.panels; ++p) {
+        if (around > 0) mbar_wait(bar(sm.empty[slot]), (around - 1) & 1, dead);
+        __syncwarp();
+        if (p < m.panels - 1 || ch < 2 * m.last_steps) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) cp_async16(dst[g] + slot * kPanel, src[g] + p * 64, live[g]);
+        }
+        cp_async_commit();
+        if (++slot == m.slots) slot = 0, ++around;
+        if (++filled >= DEPTH) {
+          cp_async_wait_but<DEPTH - 1>();
+          tell();
+        }
+      }
+    }
+    cp_async_wait_all();
+    while (told < filled) tell();
+  }
+  __syncthreads();
+  if (warp == 4) tmem_free(tmem, columns);
+}
+
+constexpr int kDeep = 8, kShallow = 3;
+
+bool plan(const WeightsArgs &a, WeightsMma &m, int &smem) {
+  m.panels = (a.D + 63) / 64;
+  m.last_steps = (a.D - (m.panels - 1) * 64) / 16;
+  m.chunks = (a.H + kHeads - 1) / kHeads;
+  m.heads = ((a.H + m.chunks - 1) / m.chunks + 15) & ~15;
+  m.chunks = (a.H + m.heads - 1) / m.heads;
+  const int q = m.panels * m.heads * 128;
+  m.slots = (kSmemLimit - q - static_cast<int>(sizeof(Small))) / kPanel;
+  if (m.slots > kMaxSlots) m.slots = kMaxSlots;
+  smem = q + m.slots * kPanel + static_cast<int>(sizeof(Small));
+  return m.slots >= kShallow;
+}
+
+template <class E, int DEPTH>
+int launch(WeightsMma &m, int smem, cudaStream_t stream) {
+  auto kernel = latent_weights_mma_kernel<E, DEPTH>;
+  if (!allow_smem(kernel, smem, kSmemLimit)) return SATK_ECUDA;
+  const int64_t ctas = resident_ctas(reinterpret_cast<const void *>(kernel), kThreads, kSmemLimit);
+  if (ctas == 0) return SATK_ECUDA;
+  // A token's tiles in pieces: one a CTA where there are fewer tokens than CTAs,
+  // else as long as six units a CTA even out their lengths or a piece is short.
+  m.tiles = (m.a.k + kRows - 1) / kRows;
+  m.pieces = 1;
+  while (m.pieces < m.tiles && (static_cast<int64_t>(m.a.T) * m.pieces < ctas ||
+                                (static_cast<int64_t>(m.a.T) * m.pieces < 6 * ctas &&
+                                 m.tiles / (m.pieces * 2) >= kUnitTiles)))
+    m.pieces *= 2;
+  if (m.pieces > m.tiles) m.pieces = m.tiles;
+  m.per = (m.tiles + m.pieces - 1) / m.pieces;
+  m.pieces = (m.tiles + m.per - 1) / m.per;
+  m.units = static_cast<int64_t>(m.a.T) * m.pieces;
+  kernel<<<static_cast<unsigned>(m.units < ctas ? m.units : ctas), kThreads, smem, stream>>>(m);
+  return launch_status();
+}
+
+}  // namespace
+
+// Widths in steps of 16, rows of 16 bytes.
+bool latent_weights_mma_fits(const WeightsArgs &a) {
+  WeightsMma m;
+  int smem;
+  return a.D % 16 == 0 && a.cache_rows > 0 && rows_of_16_bytes(a.q, a.T, a.ld_q_t, a.H, a.ld_q_h) &&
+         rows_of_16_bytes(a.cache, a.cache_rows, a.ld_cache, 1, 0) && plan(a, m, smem);
+}
+
+int latent_weights_mma(const WeightsArgs &a, int dtype, cudaStream_t stream) {
+  WeightsMma m;
+  int smem;
+  m.a = a;
+  if (!plan(a, m, smem)) return SATK_EUNSUPPORTED;
+  const bool bf16 = dtype == SATK_BF16;
+  if (!tensor_map_16bit(&m.q, bf16, a.q, a.D, a.H, a.H == 1 ? 1024 : a.ld_q_h, m.heads, a.T,
+                        a.T == 1 ? static_cast<int64_t>(a.H == 1 ? 1024 : a.ld_q_h) * a.H : a.ld_q_t))
+    return SATK_ECUDA;
+  if (m.slots >= kDeep)
+    return bf16 ? launch<__nv_bfloat16, kDeep>(m, smem, stream) : launch<__half, kDeep>(m, smem, stream);
+  return bf16 ? launch<__nv_bfloat16, kShallow>(m, smem, stream) : launch<__half, kShallow>(m, smem, stream);
+}
+
+}  // namespace satk
