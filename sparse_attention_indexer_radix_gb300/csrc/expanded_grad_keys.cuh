@@ -159,8 +159,6 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
   const uint32_t dp_at = tmem + buffers * kTokens, dv_at = dp_at + kTokens;
   const uint32_t dk_at = dv_at + ((f.dv + 31) & ~31);
 
-  // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168.
-  if (warp < 8) regs_raise<208>(); else regs_lower<88>();
   if (warp < 8) {
     // ------------------------------------------------------- P and dS, results
     // A warp has 32 keys (its TMEM lanes) and half of each tile's tokens; a thread
@@ -299,66 +297,84 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       const uint32_t tail_step = shape.nope_panels * kTokenPanel >> 4;
       // the tiles' rows as operands over columns, and over rows (panels apart)
       const uint32_t cols_low = desc_low(base + ring_at, 16), rows_low = desc_low(base + ring_at, kTokenPanel);
-      auto scores = [&](int i, int stage, uint32_t at, int around) {
-        mbar_wait(bar(sm.full[stage]), around & 1, dead);
-        tc_fence_after();
-        const int buffer = buffers == 2 ? i & 1 : 0;
-        product_over_columns<false, kMaxPanels, kKeyPanel, kTokenPanel>(tmem + buffer * kTokens, k_low,
-                                                                        cols_low + at, d_s, q_steps);
-        tc_commit(bar(sm.s_full[buffer]));
-      };
-      auto dps = [&](uint32_t at) {
-        product_over_columns<false, 2, kKeyPanel, kTokenPanel>(dp_at, v_low, cols_low + at + do_step, d_s,
-                                                               v_steps);
-        tc_commit(bar(sm.dp_full));
-      };
-      int stage = 0, around = 0;
-      uint32_t at = 0;
-      if (n > 0) {
-        mbar_wait(bar(sm.own), 0, dead);
-        scores(0, 0, 0, 0);
-        dps(0);
-      }
-      for (int i = 0; i < n; ++i) {
-        const bool wrap = stage + 1 == stages;
-        const int next = wrap ? 0 : stage + 1, next_around = around + (wrap ? 1 : 0);
-        const uint32_t next_at = wrap ? 0 : at + stage_step;
-        if (buffers == 2 && i + 1 < n) {
-          scores(i + 1, next, next_at, next_around);
-          mbar_wait(bar(sm.dp_read), i & 1, dead);
+      const uint32_t full = bar(sm.full[0]), empty = bar(sm.empty[0]), looked = bar(sm.looked[0]);
+      const uint32_t s_full = bar(sm.s_full[0]), dp_full = bar(sm.dp_full), dp_read = bar(sm.dp_read);
+      const uint32_t ready = bar(sm.ready[0]), gap = shape.gap;
+      const bool two = shape.one_product == 0;
+      if (n > 0) mbar_wait(bar(sm.own), 0, dead);
+      with_shape(panels, v_panels, shape.full != 0, [&](auto np, auto vp, auto all) {
+        // Tile i's place in the ring: its stage, the low words' distance, the phase.
+        struct At {
+          uint32_t stage = 0, low = 0, phase = 0;
+        };
+        auto following = [&](At x) {
+          const bool wrap = x.stage + 1 == static_cast<uint32_t>(stages);
+          x.stage = wrap ? 0 : x.stage + 1;
+          x.low = wrap ? 0 : x.low + stage_step;
+          x.phase ^= wrap ? 1 : 0;
+          return x;
+        };
+        auto scores = [&](uint32_t buffer, At x) {
+          mbar_wait(full + 8 * x.stage, x.phase, dead);
           tc_fence_after();
-          dps(next_at);
+          product_over_columns<false, np.value, all.value != 0, kKeyPanel, kTokenPanel>(
+              tmem + buffer * kTokens, k_low, cols_low + x.low, d_s, q_steps, gap);
+          tc_commit(s_full + 8 * buffer);
+        };
+        auto dps = [&](At x) {
+          product_over_columns<false, vp.value, all.value != 0, kKeyPanel, kTokenPanel>(
+              dp_at, v_low, cols_low + x.low + do_step, d_s, v_steps, 0);
+          tc_commit(dp_full);
+        };
+        // dV and dK of tile i from the buffer that holds its P and dS
+        auto gradients = [&](uint32_t i, uint32_t buffer, At x) {
+          mbar_wait(looked + 8 * x.stage, x.phase, dead);
+          mbar_wait(ready + 8 * (i & 1), i >> 1 & 1, dead);
+          tc_fence_after();
+          const uint32_t p_at = tmem + buffer * kTokens, q = rows_low + x.low, o = q + do_step;
+          const bool more = i > 0;
+          mma_ts_low(dv_at, p_at, o, d_v, more);
+          mma_ts_low(dv_at, p_at + 8, o + 128, d_v, true);
+          mma_ts_low(dv_at, p_at + 32, o + 256, d_v, true);
+          mma_ts_low(dv_at, p_at + 40, o + 384, d_v, true);
+          mma_ts_low(dk_at, p_at + 16, q, d_k, more);
+          mma_ts_low(dk_at, p_at + 24, q + 128, d_k, true);
+          mma_ts_low(dk_at, p_at + 48, q + 256, d_k, true);
+          mma_ts_low(dk_at, p_at + 56, q + 384, d_k, true);
+          if (all.value == 0 && two) {
+            const uint32_t d = dk_at + f.dn, t = q + tail_step;
+            mma_ts_low(d, p_at + 16, t, d_t, more);
+            mma_ts_low(d, p_at + 24, t + 128, d_t, true);
+            mma_ts_low(d, p_at + 48, t + 256, d_t, true);
+            mma_ts_low(d, p_at + 56, t + 384, d_t, true);
+          }
+          tc_commit(empty + 8 * x.stage);
+        };
+        if (n == 0) return;
+        At at;
+        scores(0, at);
+        dps(at);
+        if (buffers == 2) {
+          for (int i = 0; i + 1 < n; ++i) {
+            const At next = following(at);
+            scores(i + 1 & 1, next);
+            mbar_wait(dp_read, i & 1, dead);
+            tc_fence_after();
+            dps(next);
+            gradients(i, i & 1, at);
+            at = next;
+          }
+          gradients(n - 1, n - 1 & 1, at);
+        } else {
+          for (int i = 0; i + 1 < n; ++i) {
+            gradients(i, 0, at);
+            at = following(at);
+            scores(0, at);
+            dps(at);
+          }
+          gradients(n - 1, 0, at);
         }
-        mbar_wait(bar(sm.looked[stage]), around & 1, dead);
-        mbar_wait(bar(sm.ready[i & 1]), (i >> 1) & 1, dead);
-        tc_fence_after();
-        const uint32_t p_at = tmem + (buffers == 2 ? i & 1 : 0) * kTokens;
-        const uint32_t q = rows_low + at, o = q + do_step;
-        const bool more = i > 0;
-        mma_ts_low(dv_at, p_at, o, d_v, more);
-        mma_ts_low(dv_at, p_at + 8, o + 128, d_v, true);
-        mma_ts_low(dv_at, p_at + 32, o + 256, d_v, true);
-        mma_ts_low(dv_at, p_at + 40, o + 384, d_v, true);
-        mma_ts_low(dk_at, p_at + 16, q, d_k, more);
-        mma_ts_low(dk_at, p_at + 24, q + 128, d_k, true);
-        mma_ts_low(dk_at, p_at + 48, q + 256, d_k, true);
-        mma_ts_low(dk_at, p_at + 56, q + 384, d_k, true);
-        if (!shape.one_product) {
-          const uint32_t d = dk_at + f.dn, x = q + tail_step;
-          mma_ts_low(d, p_at + 16, x, d_t, more);
-          mma_ts_low(d, p_at + 24, x + 128, d_t, true);
-          mma_ts_low(d, p_at + 48, x + 256, d_t, true);
-          mma_ts_low(d, p_at + 56, x + 384, d_t, true);
-        }
-        tc_commit(bar(sm.empty[stage]));
-        if (buffers == 1 && i + 1 < n) {
-          scores(i + 1, next, next_at, next_around);
-          dps(next_at);
-        }
-        stage = next;
-        around = next_around;
-        at = next_at;
-      }
+      });
       tc_commit(bar(sm.done));
       tc_commit(bar(sm.issued));
       mbar_drain(bar(sm.issued), 0);

@@ -32,6 +32,8 @@ GradShape shape_of(const ExpandedGradArgs &a) {
   s.panels = s.nope_panels + (f.dr > 0 ? 1 : 0);
   s.v_panels = (f.dv + 63) / 64;
   s.one_product = f.dr == 0 || f.dn % 64 == 0;
+  s.full = f.dn % 64 == 0 && f.dr % 64 == 0 && f.dv % 64 == 0;
+  s.gap = f.dr > 0 ? (s.nope_panels * 64 - f.dn) / 2 : 0;
   s.vec_k = rows_of_16_bytes(a.dk, f.S, a.ld_dk_s, f.H, a.ld_dk_h);
   s.vec_v = rows_of_16_bytes(a.dv, f.S, a.ld_dv_s, f.H, a.ld_dv_h);
   s.vec_q = rows_of_16_bytes(a.dq, f.T, a.ld_dq_t, f.H, a.ld_dq_h);

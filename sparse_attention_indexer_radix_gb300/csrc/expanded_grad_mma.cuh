@@ -17,7 +17,9 @@ constexpr int kMaxPanels = 5;      // 64-column panels of a query or key (dn, th
 // Widths in panels, and where a CTA's work lies.
 struct GradShape {
   int nope_panels, panels, v_panels;
-  int one_product;  // keys' gradient: one product over all columns (no gap before the tail)
+  int one_product;  // one product gives all of the query's or key's columns (no gap before the tail)
+  int full;         // no panel has fewer than 64 columns
+  int gap;          // columns of tensor memory that the nope part's last panel lacks
   int vec_k, vec_v, vec_q;  // 16-byte aligned gradient rows
 };
 
@@ -89,40 +91,55 @@ __device__ __forceinline__ void rows_outside(const int32_t *starts, int R, int n
   for (int64_t i = e + warp; i < n; i += warps) zero(i);
 }
 
-// Steps of 16 columns of each panel, four bits a panel.
+// Which steps of 16 columns there are, four bits a panel.
 __device__ __forceinline__ uint32_t panel_steps(int panels, int nope_panels, int dn, int dr) {
   uint32_t steps = 0;
   for (int p = 0; p < panels; ++p) {
     const int cols = p >= nope_panels ? dr : p == nope_panels - 1 ? dn - p * 64 : 64;
-    steps |= static_cast<uint32_t>(cols >> 4) << (4 * p);
+    steps |= ((1u << (cols >> 4)) - 1) << (4 * p);
   }
   return steps;
 }
 
-// A product over columns, both operands K-major in panels: A in shared memory
-// (panels A_PANEL bytes apart) or, INSIDE, in tensor memory without gaps.
-template <bool INSIDE, int PANELS, int A_PANEL, int B_PANEL>
+// A product over columns, both operands K-major in PANELS panels: A in shared memory
+// (panels A_PANEL bytes apart) or, INSIDE, in tensor memory without gaps (`gap`: what
+// the last panel but one lacks there).  FULL: every panel has all its steps.
+template <bool INSIDE, int PANELS, bool FULL, int A_PANEL, int B_PANEL>
 __device__ __forceinline__ void product_over_columns(uint32_t d, uint32_t a, uint32_t b, uint32_t desc,
-                                                     uint32_t steps) {
-  auto step = [&](uint32_t at, uint32_t bt, bool more) {
-    if (INSIDE) mma_ts_low(d, at, bt, desc, more); else mma_ss_low(d, at, bt, desc, more);
-  };
-  constexpr int kStep = INSIDE ? 8 : 2;
+                                                     uint32_t steps, uint32_t gap) {
 #pragma unroll
   for (int p = 0; p < PANELS; ++p) {
-    const uint32_t n = steps >> (4 * p) & 15u, bp = b + p * (B_PANEL >> 4);
-    if (n == 0) break;
-    step(a, bp, p > 0);
-    if (n == 4) {
-      step(a + kStep, bp + 2, true);
-      step(a + 2 * kStep, bp + 4, true);
-      step(a + 3 * kStep, bp + 6, true);
-    } else {
-      if (n > 1) step(a + kStep, bp + 2, true);
-      if (n > 2) step(a + 2 * kStep, bp + 4, true);
+    uint32_t at = a + p * (INSIDE ? 32 : A_PANEL >> 4);
+    if (INSIDE && !FULL && p == PANELS - 1) at -= gap;
+    const uint32_t bt = b + p * (B_PANEL >> 4);
+    if (INSIDE) mma_ts_low(d, at, bt, desc, p > 0); else mma_ss_low(d, at, bt, desc, p > 0);
+#pragma unroll
+    for (int x = 1; x < 4; ++x) {
+      const bool on = FULL || (steps >> (4 * p + x) & 1u) != 0;
+      if (INSIDE) mma_ts_low_if(on, d, at + 8 * x, bt + 2 * x, desc);
+      else mma_ss_low_if(on, d, at + 2 * x, bt + 2 * x, desc);
     }
-    a += INSIDE ? n * 8 : A_PANEL >> 4;
   }
+}
+
+template <int N>
+using Const = std::integral_constant<int, N>;
+
+// issue(panels, panels of the values, whether all are full) with constants.
+template <class F>
+__device__ __forceinline__ void with_shape(int panels, int v_panels, bool full, F issue) {
+  auto values = [&](auto np) {
+    if (full) {
+      if (v_panels == 1) issue(np, Const<1>(), Const<1>()); else issue(np, Const<2>(), Const<1>());
+    } else {
+      if (v_panels == 1) issue(np, Const<1>(), Const<0>()); else issue(np, Const<2>(), Const<0>());
+    }
+  };
+  if (panels == 1) values(Const<1>());
+  else if (panels == 2) values(Const<2>());
+  else if (panels == 3) values(Const<3>());
+  else if (panels == 4) values(Const<4>());
+  else values(Const<5>());
 }
 
 // The tensor map of [n, H, cols] read in boxes of 64 columns x `rows` rows of a head.

@@ -159,8 +159,6 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
   __syncthreads();
   tc_fence_after();
 
-  // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168.
-  if (warp < 8) regs_raise<208>(); else regs_lower<88>();
   if (warp < 8) {
     // ------------------------------------------------------------- dS, results
     const float2 scale2 = make_float2(f.scale_log2, f.scale_log2);
@@ -251,61 +249,75 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       const uint32_t tail_step = shape.nope_panels * kPanel >> 4;
       // the tiles' rows as operands over columns, and over rows (panels apart)
       const uint32_t cols_low = desc_low(base + ring_at, 16), rows_low = desc_low(base + ring_at, kPanel);
-      auto scores = [&](int i, int stage, uint32_t at, int around) {
-        mbar_wait(bar(sm.full[stage]), around & 1, dead);
-        tc_fence_after();
-        const uint32_t d = tmem + (i & 1) * kKeys;
-        if (m.q_inside)
-          product_over_columns<true, kMaxPanels, 0, kPanel>(d, q_in, cols_low + at, d_s, q_steps);
-        else
-          product_over_columns<false, kMaxPanels, kOwnPanel, kPanel>(d, q_low, cols_low + at, d_s, q_steps);
-        tc_commit(bar(sm.s_full[i & 1]));
-      };
-      auto dps = [&](uint32_t at) {
-        if (m.do_inside)
-          product_over_columns<true, 2, 0, kPanel>(dp_at, do_in, cols_low + at + v_step, d_s, v_steps);
-        else
-          product_over_columns<false, 2, kOwnPanel, kPanel>(dp_at, o_low, cols_low + at + v_step, d_s, v_steps);
-        tc_commit(bar(sm.dp_full));
-      };
-      int stage = 0, around = 0;
-      uint32_t at = 0;
-      if (n > 0) {
-        if (!m.q_inside || !m.do_inside) mbar_wait(bar(sm.own), 0, dead);
-        scores(0, 0, 0, 0);
-        dps(0);
-      }
-      for (int i = 0; i < n; ++i) {
-        const bool wrap = stage + 1 == stages;
-        const int next = wrap ? 0 : stage + 1, next_around = around + (wrap ? 1 : 0);
-        const uint32_t next_at = wrap ? 0 : at + stage_step;
-        if (i + 1 < n) {
-          scores(i + 1, next, next_at, next_around);
-          mbar_wait(bar(sm.dp_read), i & 1, dead);
+      const uint32_t full = bar(sm.full[0]), empty = bar(sm.empty[0]), looked = bar(sm.looked[0]);
+      const uint32_t s_full = bar(sm.s_full[0]), dp_full = bar(sm.dp_full), dp_read = bar(sm.dp_read);
+      const uint32_t ready = bar(sm.ready[0]), gap = shape.gap;
+      const bool two = shape.one_product == 0, q_inside = m.q_inside != 0, do_inside = m.do_inside != 0;
+      if (n > 0 && (!q_inside || !do_inside)) mbar_wait(bar(sm.own), 0, dead);
+      with_shape(panels, v_panels, shape.full != 0, [&](auto np, auto vp, auto all) {
+        // Tile i's place in the ring: its stage, the low words' distance, the phase.
+        struct At {
+          uint32_t stage = 0, low = 0, phase = 0;
+        };
+        auto following = [&](At x) {
+          const bool wrap = x.stage + 1 == static_cast<uint32_t>(stages);
+          x.stage = wrap ? 0 : x.stage + 1;
+          x.low = wrap ? 0 : x.low + stage_step;
+          x.phase ^= wrap ? 1 : 0;
+          return x;
+        };
+        auto scores = [&](uint32_t buffer, At x) {
+          mbar_wait(full + 8 * x.stage, x.phase, dead);
           tc_fence_after();
-          dps(next_at);
+          const uint32_t d = tmem + buffer * kKeys, k = cols_low + x.low;
+          if (q_inside)
+            product_over_columns<true, np.value, all.value != 0, 0, kPanel>(d, q_in, k, d_s, q_steps, gap);
+          else
+            product_over_columns<false, np.value, all.value != 0, kOwnPanel, kPanel>(d, q_low, k, d_s, q_steps, gap);
+          tc_commit(s_full + 8 * buffer);
+        };
+        auto dps = [&](At x) {
+          const uint32_t v = cols_low + x.low + v_step;
+          if (do_inside)
+            product_over_columns<true, vp.value, all.value != 0, 0, kPanel>(dp_at, do_in, v, d_s, v_steps, 0);
+          else
+            product_over_columns<false, vp.value, all.value != 0, kOwnPanel, kPanel>(dp_at, o_low, v, d_s, v_steps, 0);
+          tc_commit(dp_full);
+        };
+        auto gradients = [&](uint32_t i, At x) {
+          mbar_wait(looked + 8 * x.stage, x.phase, dead);
+          mbar_wait(ready + 8 * (i & 1), i >> 1 & 1, dead);
+          tc_fence_after();
+          const uint32_t ds_at = tmem + (i & 1) * kKeys, k = rows_low + x.low;
+          const bool more = i > 0;
+          mma_ts_low(dq_at, ds_at, k, d_q, more);
+          mma_ts_low(dq_at, ds_at + 8, k + 128, d_q, true);
+          mma_ts_low(dq_at, ds_at + 32, k + 256, d_q, true);
+          mma_ts_low(dq_at, ds_at + 40, k + 384, d_q, true);
+          if (all.value == 0 && two) {
+            const uint32_t d = dq_at + f.dn, t = k + tail_step;
+            mma_ts_low(d, ds_at, t, d_t, more);
+            mma_ts_low(d, ds_at + 8, t + 128, d_t, true);
+            mma_ts_low(d, ds_at + 32, t + 256, d_t, true);
+            mma_ts_low(d, ds_at + 40, t + 384, d_t, true);
+          }
+          tc_commit(empty + 8 * x.stage);
+        };
+        if (n == 0) return;
+        At at;
+        scores(0, at);
+        dps(at);
+        for (int i = 0; i + 1 < n; ++i) {
+          const At next = following(at);
+          scores(i + 1 & 1, next);
+          mbar_wait(dp_read, i & 1, dead);
+          tc_fence_after();
+          dps(next);
+          gradients(i, at);
+          at = next;
         }
-        mbar_wait(bar(sm.looked[stage]), around & 1, dead);
-        mbar_wait(bar(sm.ready[i & 1]), (i >> 1) & 1, dead);
-        tc_fence_after();
-        const uint32_t ds_at = tmem + (i & 1) * kKeys, k = rows_low + at;
-        const bool more = i > 0;
-        mma_ts_low(dq_at, ds_at, k, d_q, more);
-        mma_ts_low(dq_at, ds_at + 8, k + 128, d_q, true);
-        mma_ts_low(dq_at, ds_at + 32, k + 256, d_q, true);
-        mma_ts_low(dq_at, ds_at + 40, k + 384, d_q, true);
-        if (!shape.one_product) {
-          const uint32_t d = dq_at + f.dn, x = k + tail_step;
-          mma_ts_low(d, ds_at, x, d_t, more);
-          mma_ts_low(d, ds_at + 8, x + 128, d_t, true);
-          mma_ts_low(d, ds_at + 32, x + 256, d_t, true);
-          mma_ts_low(d, ds_at + 40, x + 384, d_t, true);
-        }
-        tc_commit(bar(sm.empty[stage]));
-        stage = next;
-        around = next_around;
-        at = next_at;
-      }
+        gradients(n - 1, at);
+      });
       tc_commit(bar(sm.done));
       tc_commit(bar(sm.issued));
       mbar_drain(bar(sm.issued), 0);

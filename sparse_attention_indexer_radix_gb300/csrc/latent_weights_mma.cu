@@ -29,6 +29,8 @@ constexpr int kPanel = kRows * 128;    // bytes of 64 columns of a tile
 constexpr int kThreads = 512;          // warps 0-3 sums, 4 MMAs, 5 queries, 8-15 rows
 constexpr int kMaxWide = 9;            // panels of a row
 constexpr int kMaxSlots = 12;
+constexpr int kGroups = 4;             // of row warps
+constexpr int kGather = 1;             // of them by the TMA
 constexpr int kHeads = 128;            // of a chunk
 constexpr int kUnitTiles = 4;          // tiles worth a load of queries
 
@@ -37,8 +39,8 @@ struct WeightsMma {
   int panels, last_steps;    // steps of 16 columns of the last panel
   int slots, heads, chunks;  // heads of a chunk (a multiple of 16), chunks
   int tiles, pieces, per;    // tiles of k entries, pieces of a token's tiles, tiles of a piece
-  int64_t units;
-  CUtensorMap q;
+  int step_t, step_piece;    // from a CTA's unit to its next
+  CUtensorMap q, rows;
 };
 
 struct Small {
@@ -48,33 +50,31 @@ struct Small {
   int dead;
 };
 
-// A CTA's units in order.  The next one's count is on its way while one is worked
-// on.
+// A CTA's units in order: token t, piece of its tiles.  The next one's count is on
+// its way while one is worked on.
 struct Units {
   const WeightsMma &m;
-  int64_t u;
-  int t, first, count, next_count;
-  __device__ __forceinline__ Units(const WeightsMma &m) : m(m), u(blockIdx.x), next_count(0) {
-    if (more()) next_count = entry_count(m.a, static_cast<int>(u / m.pieces));
-    set();
+  int t, piece, next_t, next_piece, count, next_count;
+  __device__ __forceinline__ Units(const WeightsMma &m) : m(m) {
+    next_t = static_cast<int>(blockIdx.x) / m.pieces;
+    next_piece = static_cast<int>(blockIdx.x) - next_t * m.pieces;
+    next_count = next_t < m.a.T ? entry_count(m.a, next_t) : 0;
+    next();
   }
-  __device__ __forceinline__ bool more() const { return u < m.units; }
-  __device__ __forceinline__ void set() {
-    if (!more()) return;
-    t = static_cast<int>(u / m.pieces);
-    first = static_cast<int>(u % m.pieces) * m.per;
-    count = next_count;
-    const int64_t v = u + gridDim.x;
-    if (v < m.units) next_count = entry_count(m.a, static_cast<int>(v / m.pieces));
-  }
+  __device__ __forceinline__ bool more() const { return t < m.a.T; }
   __device__ __forceinline__ void next() {
-    u += gridDim.x;
-    set();
+    t = next_t, piece = next_piece, count = next_count;
+    if (t >= m.a.T) return;
+    next_t += m.step_t;
+    next_piece += m.step_piece;
+    if (next_piece >= m.pieces) next_piece -= m.pieces, ++next_t;
+    if (next_t < m.a.T) next_count = entry_count(m.a, next_t);
   }
-  __device__ __forceinline__ int last() const { return min(first + m.per, m.tiles); }
+  __device__ __forceinline__ int first() const { return piece * m.per; }
+  __device__ __forceinline__ int last() const { return min(first() + m.per, m.tiles); }
   // tiles of the piece with an entry that counts
   __device__ __forceinline__ int tiles() const {
-    return max(0, min(last(), (count + kRows - 1) / kRows) - first);
+    return max(0, min(last(), (count + kRows - 1) / kRows) - first());
   }
 };
 
@@ -83,7 +83,26 @@ __device__ __forceinline__ void cp_async_wait_but() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// DEPTH: panels that a row warp has in flight.
+template <int N>
+using Const = std::integral_constant<int, N>;
+
+// f(panels) with a constant.
+template <class F>
+__device__ __forceinline__ void with_panels(int panels, F f) {
+  switch (panels) {
+    case 1: return f(Const<1>());
+    case 2: return f(Const<2>());
+    case 3: return f(Const<3>());
+    case 4: return f(Const<4>());
+    case 5: return f(Const<5>());
+    case 6: return f(Const<6>());
+    case 7: return f(Const<7>());
+    case 8: return f(Const<8>());
+    default: return f(Const<9>());
+  }
+}
+
+// DEPTH: panels that a group of row warps has in flight.
 template <class E, int DEPTH>
 __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const __grid_constant__ WeightsMma m) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -98,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < m.slots; ++s) {
-      mbar_init(bar(sm.full[s]), 8);
+      mbar_init(bar(sm.full[s]), 2);
       mbar_init(bar(sm.empty[s]), 1);
     }
     for (int p = 0; p < m.panels; ++p) {
@@ -140,14 +159,22 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
           const float y = 8 * j < m.heads && h + 1 < a.H ? lse[1] * kLog2e : -INFINITY;
           less[j] = make_float2(x == -INFINITY ? x : -x, y == -INFINITY ? y : -y);
         }
+        // whether the next tile's entries count
+        int row[4];
+        auto look_up = [&](int i) {
+          const int e = (w.first() + i) * kRows + warp * 32 + (lane >> 2);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            row[r] = e + 8 * r < w.count ? a.rows[w.t * a.ld_rows + e + 8 * r] : -1;
+        };
+        look_up(0);
         for (int i = 0; i < n; ++i, ++done) {
           const int b = done & 1;
-          const int entry0 = (w.first + i) * kRows + warp * 32 + (lane >> 2);
+          const int entry0 = (w.first() + i) * kRows + warp * 32 + (lane >> 2);
           bool live[4];
-          if ((lane & 3) == 0) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) live[r] = entry_row(a, w.t, entry0 + 8 * r, w.count) >= 0;
-          }
+          for (int r = 0; r < 4; ++r) live[r] = row[r] >= 0 && row[r] < a.cache_rows;
+          if (i + 1 < n) look_up(i + 1);
           mbar_wait(bar(sm.s_full[b]), (done >> 1) & 1, dead);
           __syncwarp();
           tc_fence_after();
@@ -197,43 +224,52 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
       }
       // Entries behind the token's count.
       const int end = min(w.last() * kRows, a.k);
-      for (int e = (w.first + n) * kRows + threadIdx.x; e < end; e += kRows) out[e] = 0.f;
+      for (int e = (w.first() + n) * kRows + threadIdx.x; e < end; e += kRows) out[e] = 0.f;
     }
     if (threadIdx.x == 0 && *dead != 0 && a.status != nullptr) atomicOr(a.status, SATK_STATUS_STALLED);
   } else if (warp == 4) {
     // ---------------------------------------------------------------- MMA issue
     if (elect_leader()) {
       const uint32_t desc = mma_desc(std::is_same<E, __nv_bfloat16>::value, false, false, kRows, m.heads);
+      const uint32_t full = bar(sm.full[0]), empty = bar(sm.empty[0]), q_full = bar(sm.q_full[0]);
+      const uint32_t q_empty = bar(sm.q_empty[0]), s_full = bar(sm.s_full[0]), s_empty = bar(sm.s_empty[0]);
       const uint32_t q_low = desc_low(base, 16), ring_low = desc_low(base + ring_at, 16);
-      int slot = 0, around = 0, done = 0, loads = 0;
-      for (Units w(m); w.more(); w.next()) {
-        const int n = w.tiles();
-        for (int c = 0; n > 0 && c < m.chunks; ++c, ++loads)
-          for (int i = 0; i < n; ++i, ++done) {
-            const int b = done & 1;
-            if (done >= 2) mbar_wait(bar(sm.s_empty[b]), ((done >> 1) - 1) & 1, dead);
-            uint32_t q = q_low;
-            for (int p = 0; p < m.panels; ++p, q += q_panel >> 4) {
-              if (i == 0) mbar_wait(bar(sm.q_full[p]), loads & 1, dead);
-              mbar_wait(bar(sm.full[slot]), around & 1, dead);
-              tc_fence_after();
-              const uint32_t d = tmem + b * buffer, k = ring_low + slot * (kPanel >> 4);
-              mma_ss_low(d, k, q, desc, p > 0);
-              if (p < m.panels - 1 || m.last_steps == 4) {
-                mma_ss_low(d, k + 2, q + 2, desc, true);
-                mma_ss_low(d, k + 4, q + 4, desc, true);
-                mma_ss_low(d, k + 6, q + 6, desc, true);
-              } else {
-                if (m.last_steps > 1) mma_ss_low(d, k + 2, q + 2, desc, true);
-                if (m.last_steps > 2) mma_ss_low(d, k + 4, q + 4, desc, true);
-              }
-              tc_commit(bar(sm.empty[slot]));
-              if (i == n - 1) tc_commit(bar(sm.q_empty[p]));
-              if (++slot == m.slots) slot = 0, ++around;
-            }
-            tc_commit(bar(sm.s_full[b]));
+      const uint32_t q_step = q_panel >> 4, slots = m.slots, last_steps = m.last_steps;
+      uint32_t slot = 0, phase = 0, done = 0, loads = 0;
+      with_panels(m.panels, [&](auto panels) {
+        // One tile; the first of a unit waits for its queries, behind the last one's
+        // products their places are free.
+        auto tile = [&](auto first, bool last) {
+          const uint32_t b = done & 1, d = tmem + b * buffer;
+          mbar_wait(s_empty + 8 * b, (done >> 1 & 1) ^ 1, dead);
+#pragma unroll
+          for (int p = 0; p < panels.value; ++p) {
+            if (first.value != 0) mbar_wait(q_full + 8 * p, loads & 1, dead);
+            mbar_wait(full + 8 * slot, phase, dead);
+            tc_fence_after();
+            const uint32_t k = ring_low + slot * (kPanel >> 4), q = q_low + p * q_step;
+            const bool whole = p < panels.value - 1;
+            mma_ss_low(d, k, q, desc, p > 0);
+            mma_ss_low_if(whole || last_steps > 1, d, k + 2, q + 2, desc);
+            mma_ss_low_if(whole || last_steps > 2, d, k + 4, q + 4, desc);
+            mma_ss_low_if(whole || last_steps > 3, d, k + 6, q + 6, desc);
+            tc_commit(empty + 8 * slot);
+            tc_commit_if(last, q_empty + 8 * p);
+            const bool wrap = slot + 1 == slots;
+            slot = wrap ? 0 : slot + 1;
+            phase ^= wrap ? 1 : 0;
           }
-      }
+          tc_commit(s_full + 8 * b);
+          ++done;
+        };
+        for (Units w(m); w.more(); w.next()) {
+          const int n = w.tiles();
+          for (int c = 0; n > 0 && c < m.chunks; ++c, ++loads) {
+            tile(Const<1>(), n == 1);
+            for (int i = 1; i < n; ++i) tile(Const<0>(), i == n - 1);
+          }
+        }
+      });
       tc_commit(bar(sm.issued));
       mbar_drain(bar(sm.issued), 0);
     }
@@ -255,40 +291,53 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
       for (int p = 0; p < m.panels; ++p) mbar_drain(bar(sm.q_full[p]), (loads - 1) & 1);
   } else if (warp >= 8) {
     // --------------------------------------------------------------------- rows
-    // A warp has 16 rows of every panel, four rows x 128 bytes an instruction.
-    const int r0 = (warp - 8) * 16, ch = lane & 7;
-    const E *cache = static_cast<const E *>(a.cache);
-    uint32_t dst[4];
+    // Two warps share a panel, 64 rows each, four rows x 128 bytes an instruction;
+    // four such groups take panels in turn, DEPTH of them in flight each.
+    const int group = (warp - 8) >> 1, r0 = (warp & 1) * 64, ch = lane & 7;
+    const E *cache = static_cast<const E *>(a.cache) + ch * 8;
+    // (row r0 + 4 g + lane / 8; the swizzle repeats every eight rows)
+    uint32_t dst[2];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < 2; ++g) {
       const int r = r0 + 4 * g + (lane >> 3);
       dst[g] = base + ring_at + r * 128 + ((ch ^ (r & 7)) << 4);
     }
-    int slot = 0, around = 0, filled = 0, told = 0, told_slot = 0;
+    int last_slot = -1, last_phase = 0;  // (the last panel: by then all before it are there)
+    int slot = group % m.slots, around = group / m.slots, filled = 0, told = 0, told_slot = slot;
+    auto advance = [&](int &at) {
+      at += kGroups;
+      const bool wrap = at >= m.slots;
+      if (wrap) at -= m.slots;
+      return wrap;
+    };
     auto tell = [&]() {  // the oldest panel that has not been handed over
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sm.full[told_slot]));
-      if (++told_slot == m.slots) told_slot = 0;
+      advance(told_slot);
       ++told;
     };
     Units w(m);
-    int c = 0, i = 0;
+    int c = 0, i = 0, p = group;  // the next panel of the tile for this group
     while (w.more() && w.tiles() == 0) w.next();
-    auto rows_of = [&]() {  // of this lane: entry r0 + lane of the tile
-      const int64_t row = lane < 16 ? entry_row(a, w.t, (w.first + i) * kRows + r0 + lane, w.count) : -1;
-      return static_cast<int>(row);
+    // The groups copy in two ways at once, each with a limit of its own on what is
+    // under way: four rows x 128 bytes a request of the TMA (a skipped entry gets row
+    // 0, which nothing looks at), or 16 bytes a lane.
+    const bool gather = group >= kGroups - kGather;
+    int2 row = make_int2(-1, -1);  // of this lane: entries r0 + lane and r0 + 32 + lane
+    int4 four = make_int4(0, 0, 0, 0);  // or four from r0 + 4 lane on
+    auto look_up = [&]() {
+      const int e = (w.first() + i) * kRows + r0;
+      auto at = [&](int x) { return static_cast<int>(entry_row(a, w.t, x, w.count)); };
+      if (!gather) row = make_int2(at(e + lane), at(e + lane + 32));
+      else if (lane < 16)
+        four = make_int4(max(at(e + 4 * lane), 0), max(at(e + 4 * lane + 1), 0),
+                         max(at(e + 4 * lane + 2), 0), max(at(e + 4 * lane + 3), 0));
     };
-    int row = w.more() ? rows_of() : -1;
+    if (w.more()) look_up();
     while (w.more()) {
-      const E *src[4];
-      bool live[4];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int at = __shfl_sync(~0u, row, 4 * g + (lane >> 3));
-        live[g] = at >= 0;
-        src[g] = cache + static_cast<int64_t>(live[g] ? at : 0) * a.ld_cache + ch * 8;
-      }
+      const int2 now = row;
+      const int4 now4 = four;
       // the next tile's rows are looked up while this one's are copied
       if (++i == w.tiles()) {
         i = 0;
@@ -298,22 +347,38 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
           while (w.more() && w.tiles() == 0);
         }
       }
-      if (w.more()) row = rows_of();
-      for (int p = 0; p < m.panels; ++p) {
-        if (around > 0) mbar_wait(bar(sm.empty[slot]), (around - 1) & 1, dead);
+      if (w.more()) look_up();
+      for (; p < m.panels; p += kGroups) {
+        mbar_wait(bar(sm.empty[slot]), (around & 1) ^ 1, dead);
         __syncwarp();
-        if (p < m.panels - 1 || ch < 2 * m.last_steps) {
+        const uint32_t to = slot * kPanel;
+        if (gather) {
+          if (lane == 0) mbar_expect(bar(sm.full[slot]), kPanel / 2);
+          __syncwarp();
+          if (lane < 16)
+            tma_gather4(base + ring_at + to + (r0 + 4 * lane) * 128, &m.rows, p * 64, now4, bar(sm.full[slot]));
+        } else {
+          const bool wide = p < m.panels - 1 || ch < 2 * m.last_steps;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) cp_async16(dst[g] + slot * kPanel, src[g] + p * 64, live[g]);
+          for (int g = 0; g < 16; ++g) {
+            const int at = __shfl_sync(~0u, g < 8 ? now.x : now.y, (4 * g & 31) + (lane >> 3));
+            const bool live = at >= 0;
+            const E *src = cache + static_cast<int64_t>(live ? at : 0) * a.ld_cache + p * 64;
+            if (wide) cp_async16(dst[g & 1] + to + (g >> 1) * 1024, src, live);
+          }
+          cp_async_commit();
+          if (++filled >= DEPTH) {
+            cp_async_wait_but<DEPTH - 1>();
+            tell();
+          }
         }
-        cp_async_commit();
-        if (++slot == m.slots) slot = 0, ++around;
-        if (++filled >= DEPTH) {
-          cp_async_wait_but<DEPTH - 1>();
-          tell();
-        }
+        last_slot = slot;
+        last_phase = around & 1;
+        if (advance(slot)) ++around;
       }
+      p -= m.panels;
     }
+    if (gather && last_slot >= 0) mbar_drain(bar(sm.full[last_slot]), last_phase);
     cp_async_wait_all();
     while (told < filled) tell();
   }
@@ -321,7 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
   if (warp == 4) tmem_free(tmem, columns);
 }
 
-constexpr int kDeep = 8, kShallow = 3;
+// Panels in flight of a group: the oldest panel not handed over waits for one
+// kGroups (DEPTH - 1) further on to find room.
+constexpr int kDeep = 2, kShallow = 1;
+static_assert(kMaxSlots >= kGroups, "a group's next slot is less than a round further");
 
 bool plan(const WeightsArgs &a, WeightsMma &m, int &smem) {
   m.panels = (a.D + 63) / 64;
@@ -333,7 +401,7 @@ bool plan(const WeightsArgs &a, WeightsMma &m, int &smem) {
   m.slots = (kSmemLimit - q - static_cast<int>(sizeof(Small))) / kPanel;
   if (m.slots > kMaxSlots) m.slots = kMaxSlots;
   smem = q + m.slots * kPanel + static_cast<int>(sizeof(Small));
-  return m.slots >= kShallow;
+  return m.slots >= kGroups;
 }
 
 template <class E, int DEPTH>
@@ -353,8 +421,11 @@ int launch(WeightsMma &m, int smem, cudaStream_t stream) {
   if (m.pieces > m.tiles) m.pieces = m.tiles;
   m.per = (m.tiles + m.pieces - 1) / m.pieces;
   m.pieces = (m.tiles + m.per - 1) / m.per;
-  m.units = static_cast<int64_t>(m.a.T) * m.pieces;
-  kernel<<<static_cast<unsigned>(m.units < ctas ? m.units : ctas), kThreads, smem, stream>>>(m);
+  const int64_t units = static_cast<int64_t>(m.a.T) * m.pieces;
+  const int grid = static_cast<int>(units < ctas ? units : ctas);
+  m.step_t = grid / m.pieces;
+  m.step_piece = grid % m.pieces;
+  kernel<<<grid, kThreads, smem, stream>>>(m);
   return launch_status();
 }
 
@@ -377,7 +448,9 @@ int latent_weights_mma(const WeightsArgs &a, int dtype, cudaStream_t stream) {
   if (!tensor_map_16bit(&m.q, bf16, a.q, a.D, a.H, a.H == 1 ? 1024 : a.ld_q_h, m.heads, a.T,
                         a.T == 1 ? static_cast<int64_t>(a.H == 1 ? 1024 : a.ld_q_h) * a.H : a.ld_q_t))
     return SATK_ECUDA;
-  if (m.slots >= kDeep)
+  if (!tensor_map_16bit(&m.rows, bf16, a.cache, a.D, a.cache_rows, a.cache_rows == 1 ? 1024 : a.ld_cache, 1))
+    return SATK_ECUDA;
+  if (m.slots > kGroups * (kDeep - 1))
     return bf16 ? launch<__nv_bfloat16, kDeep>(m, smem, stream) : launch<__half, kDeep>(m, smem, stream);
   return bf16 ? launch<__nv_bfloat16, kShallow>(m, smem, stream) : launch<__half, kShallow>(m, smem, stream);
 }

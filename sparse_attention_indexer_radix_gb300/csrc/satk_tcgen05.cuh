@@ -145,6 +145,17 @@ __device__ __forceinline__ void tma_box3(uint32_t leader, uint32_t dst, const vo
       : "memory");
 }
 
+// Four rows of a matrix, 64 columns from `col` on (a multiple of 64), into
+// consecutive 128-byte rows; the map's box is one row high.  By each thread that
+// calls it.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void *map, int col, int4 rows, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(col), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
+      : "memory");
+}
+
 // 16 bytes global -> shared; zeros, and no read, when !live.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -338,8 +349,11 @@ __device__ __forceinline__ void tmem_st_packed(uint32_t addr, const uint32_t (&v
 
 // MMAs with descriptors whose upper words are all the same (atoms of eight rows are
 // 1024 bytes apart): the lower words are what changes, a constant away from one
-// uniform register.  64-bit sums and loops over the steps cost 50 cycles an MMA to
-// issue, more than most of them take to run.
+// uniform register.  What the one issuing thread does between MMAs counts: 64-bit
+// sums cost 50 cycles an MMA, a branch 40 to 60, a satisfied barrier wait 90, a
+// commit or a fence nothing, while an MMA of 64 columns runs for 32 to 50.  So the
+// issuing loops are straight lines: panel counts are constants, what not every
+// shape has is predicated, rings wrap by selects.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
@@ -350,6 +364,30 @@ __device__ __forceinline__ void mma_ss_low(uint32_t d, uint32_t a, uint32_t b, u
       "{\n.reg .pred p;\n.reg .b64 x, y;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
       "setp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
       "r"(a), "r"(b), "r"(desc), "r"(more ? 1u : 0u), "r"(kDescHigh)
+      : "memory");
+}
+// The same only where `on`: a predicate, not a branch.
+__device__ __forceinline__ void mma_ss_low_if(bool on, uint32_t d, uint32_t a, uint32_t b, uint32_t desc) {
+  asm volatile(
+      "{\n.reg .pred p, e;\n.reg .b64 x, y;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
+      "setp.ne.u32 e, %4, 0;\nsetp.eq.u32 p, 0, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(on ? 1u : 0u), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_low_if(bool on, uint32_t d, uint32_t a, uint32_t b, uint32_t desc) {
+  asm volatile(
+      "{\n.reg .pred p, e;\n.reg .b64 y;\nmov.b64 y, {%2, %5};\n"
+      "setp.ne.u32 e, %4, 0;\nsetp.eq.u32 p, 0, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(on ? 1u : 0u), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_if(bool on, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %1, 0;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(on ? 1u : 0u)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool more) {
