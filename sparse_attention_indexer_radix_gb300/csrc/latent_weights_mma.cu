@@ -30,7 +30,6 @@ constexpr int kThreads = 512;          // warps 0-3 sums, 4 MMAs, 5 queries, 8-1
 constexpr int kMaxWide = 9;            // panels of a row
 constexpr int kMaxSlots = 12;
 constexpr int kGroups = 4;             // of row warps
-constexpr int kGather = 1;             // of them by the TMA
 constexpr int kHeads = 128;            // of a chunk
 constexpr int kUnitTiles = 4;          // tiles worth a load of queries
 
@@ -102,7 +101,8 @@ __device__ __forceinline__ void with_panels(int panels, F f) {
   }
 }
 
-// DEPTH: panels that a group of row warps has in flight.
+// DEPTH: panels that a group of row warps has in flight by copies; 0: by the TMA's
+// gathers, as many as the ring holds.
 template <class E, int DEPTH>
 __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const __grid_constant__ WeightsMma m) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -320,10 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
     Units w(m);
     int c = 0, i = 0, p = group;  // the next panel of the tile for this group
     while (w.more() && w.tiles() == 0) w.next();
-    // The groups copy in two ways at once, each with a limit of its own on what is
-    // under way: four rows x 128 bytes a request of the TMA (a skipped entry gets row
-    // 0, which nothing looks at), or 16 bytes a lane.
-    const bool gather = group >= kGroups - kGather;
+    // A gather brings four rows x 128 bytes (a skipped entry gets row 0, which nothing
+    // looks at): 7.0 TB/s at most, but nobody waits for it, so it is what a short ring
+    // wants.
+    constexpr bool gather = DEPTH == 0;
     int2 row = make_int2(-1, -1);  // of this lane: entries r0 + lane and r0 + 32 + lane
     int4 four = make_int4(0, 0, 0, 0);  // or four from r0 + 4 lane on
     auto look_up = [&]() {
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
           }
           cp_async_commit();
           if (++filled >= DEPTH) {
-            cp_async_wait_but<DEPTH - 1>();
+            cp_async_wait_but<(DEPTH > 0 ? DEPTH - 1 : 0)>();
             tell();
           }
         }
@@ -386,9 +386,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
   if (warp == 4) tmem_free(tmem, columns);
 }
 
-// Panels in flight of a group: the oldest panel not handed over waits for one
-// kGroups (DEPTH - 1) further on to find room.
-constexpr int kDeep = 2, kShallow = 1;
+// Copies in flight: the oldest panel of a group that has not been handed over waits
+// until one kGroups (DEPTH - 1) further on has found room.  512 tokens x 2048 rows of
+// 544 columns: 64 heads (a ring of 9 panels) 131 us with copies two deep, 163 with
+// gathers; 128 heads (a ring of 4) 192 with gathers, 284 with copies one deep.
+constexpr int kDepth = 2;
 static_assert(kMaxSlots >= kGroups, "a group's next slot is less than a round further");
 
 bool plan(const WeightsArgs &a, WeightsMma &m, int &smem) {
@@ -450,9 +452,9 @@ int latent_weights_mma(const WeightsArgs &a, int dtype, cudaStream_t stream) {
     return SATK_ECUDA;
   if (!tensor_map_16bit(&m.rows, bf16, a.cache, a.D, a.cache_rows, a.cache_rows == 1 ? 1024 : a.ld_cache, 1))
     return SATK_ECUDA;
-  if (m.slots > kGroups * (kDeep - 1))
-    return bf16 ? launch<__nv_bfloat16, kDeep>(m, smem, stream) : launch<__half, kDeep>(m, smem, stream);
-  return bf16 ? launch<__nv_bfloat16, kShallow>(m, smem, stream) : launch<__half, kShallow>(m, smem, stream);
+  if (m.slots >= kGroups * kDepth)
+    return bf16 ? launch<__nv_bfloat16, kDepth>(m, smem, stream) : launch<__half, kDepth>(m, smem, stream);
+  return bf16 ? launch<__nv_bfloat16, 0>(m, smem, stream) : launch<__half, 0>(m, smem, stream);
 }
 
 }  // namespace satk
