@@ -852,10 +852,12 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     rows, _, args = _distill_args(logits, ids, teacher, kind, scope, temperature, row_ends, k)
     if loss is None:
         loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    else:
+        _float_vec(loss, rows, "loss")
     if lse is None:
         lse = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _float_vec(loss, rows, "loss")
-    _float_vec(lse, rows, "lse")
+    else:
+        _float_vec(lse, rows, "lse")
     rc = _on(dev, lib().satk_distill_loss, *args, _addr(loss), _addr(lse), _stream_on(dev))
     if rc:
         _check(rc, "satk_distill_loss")

@@ -1,39 +1,18 @@
 // expanded_grad.cu -- the backward pass of the expanded attention: entry points,
 // the rows' statistics before it and the tail's sum over the heads after it.
 #include "expanded_grad.cuh"
+#include "satk_tcgen05.cuh"
 
 namespace satk {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kRowLanes = SATK_EXPANDED_MAX_V / 8;  // lanes of a row, eight values each
 
-// A warp a token and head: delta, and the normaliser in log2, head by head side by
-// side (what the tiles read).  A token whose lse is -inf saw nothing: its row end
-// counts as 0 wherever this is read, so a NaN of its own cannot get out.
-template <class E>
-__global__ void __launch_bounds__(kWarps * 32) grad_stats_kernel(ExpandedGradArgs a) {
+// The range of row ends of one tile of tokens, ends cut to the request's keys, by a
+// warp.
+__device__ void tile_ends(const ExpandedGradArgs &a, int slot) {
   const int lane = threadIdx.x & 31;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (id >= static_cast<int64_t>(a.f.T) * a.f.H) return;
-  const int64_t t = id / a.f.H;
-  const int h = static_cast<int>(id % a.f.H);
-  const E *dout = static_cast<const E *>(a.dout) + t * a.ld_do_t + h * a.ld_do_h;
-  const E *out = static_cast<const E *>(a.f.out) + t * a.f.ld_out_t + h * a.f.ld_out_h;
-  float sum = 0.f;
-  for (int c = lane; c < a.f.dv; c += 32)
-    sum = fmaf(Elem<E>::to(dout[c]), Elem<E>::to(out[c]), sum);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  if (lane == 0)
-    a.stats[static_cast<int64_t>(h) * a.f.T + t] =
-        make_float2(a.f.lse[id] * kLog2e, sum - (a.dlse != nullptr ? a.dlse[id] : 0.f));
-}
-
-// The range of row ends of each tile of tokens, ends cut to the request's keys.
-__global__ void __launch_bounds__(kWarps * 32) grad_ends_kernel(ExpandedGradArgs a, int slots) {
-  const int lane = threadIdx.x & 31;
-  const int slot = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (slot >= slots) return;
   int lo = 0, hi = a.f.R;  // the last request whose first slot is at or before this one
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -49,49 +28,108 @@ __global__ void __launch_bounds__(kWarps * 32) grad_ends_kernel(ExpandedGradArgs
       most = max(most, end);
     }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    least = min(least, __shfl_xor_sync(~0u, least, d));
-    most = max(most, __shfl_xor_sync(~0u, most, d));
-  }
+  least = __reduce_min_sync(~0u, least);
+  most = __reduce_max_sync(~0u, most);
   if (lane == 0) a.ends[slot] = make_int2(least, most);
 }
 
-// The heads' tails in one order.
-template <class E>
-__global__ void __launch_bounds__(256) grad_tail_kernel(ExpandedGradArgs a, int64_t n) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n) return;
+// Half a warp a token and head: delta, and the normaliser in log2, head by head side
+// by side (what the tiles read); the last CTAs: the tiles' row ends.  A token whose
+// lse is -inf saw nothing: its row end counts as 0 wherever this is read, so a NaN of
+// its own cannot get out.  VEC: rows of whole 16-byte chunks.
+template <class E, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32) grad_stats_kernel(ExpandedGradArgs a, unsigned row_blocks, int slots) {
+  let_next_kernel_start();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x >= row_blocks) {
+    const int slot = static_cast<int>(blockIdx.x - row_blocks) * kWarps + warp;
+    if (slot < slots) tile_ends(a, slot);
+    return;
+  }
+  const int64_t id = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * 2 + lane / kRowLanes;
+  const int at = lane % kRowLanes;
   float sum = 0.f;
-  for (int h = 0; h < a.f.H; ++h) sum += a.tails[h * n + i];
-  static_cast<E *>(a.dtail)[i / a.f.dr * a.ld_dtail + i % a.f.dr] = Elem<E>::from(sum);
+  if (id < static_cast<int64_t>(a.f.T) * a.f.H) {
+    const int64_t t = id / a.f.H;
+    const int h = static_cast<int>(id - t * a.f.H);
+    const E *dout = static_cast<const E *>(a.dout) + t * a.ld_do_t + h * a.ld_do_h;
+    const E *out = static_cast<const E *>(a.f.out) + t * a.f.ld_out_t + h * a.f.ld_out_h;
+    if (VEC) {
+      if (at * 8 < a.f.dv) {
+        Pack8<E> x, y;
+        x.u = *reinterpret_cast<const uint4 *>(dout + at * 8);
+        y.u = *reinterpret_cast<const uint4 *>(out + at * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 u = Elem<E>::to2(x.h[i]), v = Elem<E>::to2(y.h[i]);
+          sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
+        }
+      }
+    } else {
+      for (int c = at; c < a.f.dv; c += kRowLanes) sum = fmaf(Elem<E>::to(dout[c]), Elem<E>::to(out[c]), sum);
+    }
+#pragma unroll
+    for (int d = kRowLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(__activemask(), sum, d);
+    if (at == 0)
+      a.stats[static_cast<int64_t>(h) * a.f.T + t] =
+          make_float2(a.f.lse[id] * kLog2e, sum - (a.dlse != nullptr ? a.dlse[id] : 0.f));
+  }
+}
+
+// The heads' tails in one order, N values a thread.
+template <class E, int N>
+__global__ void __launch_bounds__(256) grad_tail_kernel(ExpandedGradArgs a, int64_t n) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * N;
+  wait_for_previous_kernel();
+  if (i >= n) return;
+  float sum[N] = {};
+#pragma unroll 4
+  for (int h = 0; h < a.f.H; ++h) {
+    const float *from = a.tails + h * n + i;
+    if (N == 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(from);
+      sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+    } else {
+      sum[0] += *from;
+    }
+  }
+  E *to = static_cast<E *>(a.dtail) + i / a.f.dr * a.ld_dtail + i % a.f.dr;
+#pragma unroll
+  for (int x = 0; x < N; ++x) to[x] = Elem<E>::from(sum[x]);
+}
+
+template <class E>
+int launch_stats(const ExpandedGradArgs &a, cudaStream_t stream) {
+  const int64_t rows = (static_cast<int64_t>(a.f.T) * a.f.H + 2 * kWarps - 1) / (2 * kWarps);
+  const int slots = static_cast<int>(tile_slots(a.f.T, a.f.R, kGradTokens));
+  const int64_t grid = rows + (slots + kWarps - 1) / kWarps;
+  if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
+  const bool vec = a.f.dv % 8 == 0 && rows_of_16_bytes(a.dout, a.f.T, a.ld_do_t, a.f.H, a.ld_do_h) &&
+                   rows_of_16_bytes(a.f.out, a.f.T, a.f.ld_out_t, a.f.H, a.f.ld_out_h);
+  const auto kernel = vec ? grad_stats_kernel<E, true> : grad_stats_kernel<E, false>;
+  kernel<<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(a, static_cast<unsigned>(rows), slots);
+  return launch_status();
+}
+
+template <class E>
+int launch_tail(const ExpandedGradArgs &a, cudaStream_t stream) {
+  const int64_t n = static_cast<int64_t>(a.f.S) * a.f.dr;
+  const int each = a.f.dr % 4 == 0 ? 4 : 1;
+  const int64_t grid = (n / each + 255) / 256;
+  if (n == 0) return SATK_OK;
+  if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
+  return launch_early(each == 4 ? grad_tail_kernel<E, 4> : grad_tail_kernel<E, 1>, static_cast<unsigned>(grid),
+                      256, 0, stream, a, n);
 }
 
 }  // namespace
 
 int expanded_grad_prepare(const ExpandedGradArgs &a, int dtype, cudaStream_t stream) {
-  const int64_t grid = (static_cast<int64_t>(a.f.T) * a.f.H + kWarps - 1) / kWarps;
-  if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
-  if (grid > 0) {
-    if (dtype == SATK_BF16)
-      grad_stats_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(a);
-    else
-      grad_stats_kernel<__half><<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(a);
-  }
-  const int slots = static_cast<int>(tile_slots(a.f.T, a.f.R, kGradTokens));
-  grad_ends_kernel<<<(slots + kWarps - 1) / kWarps, kWarps * 32, 0, stream>>>(a, slots);
-  return launch_status();
+  return dtype == SATK_BF16 ? launch_stats<__nv_bfloat16>(a, stream) : launch_stats<__half>(a, stream);
 }
 
 int expanded_grad_tail(const ExpandedGradArgs &a, int dtype, cudaStream_t stream) {
-  const int64_t n = static_cast<int64_t>(a.f.S) * a.f.dr, grid = (n + 255) / 256;
-  if (n == 0) return SATK_OK;
-  if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
-  if (dtype == SATK_BF16)
-    grad_tail_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a, n);
-  else
-    grad_tail_kernel<__half><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a, n);
-  return launch_status();
+  return dtype == SATK_BF16 ? launch_tail<__nv_bfloat16>(a, stream) : launch_tail<__half>(a, stream);
 }
 
 }  // namespace satk

@@ -27,12 +27,12 @@ namespace satk {
 namespace grad_keys {
 
 constexpr int kTokens = kGradTokens;  // of a tile
+static_assert(kTokens == kBoxRows && kTile == 2 * kBoxRows, "boxes");
 constexpr int kKeyPanel = kTile * 128, kTokenPanel = kTokens * 128;  // bytes
 constexpr int kMaxStages = 4;
 
 struct Plan {
   int stages, score_buffers;
-  CUtensorMap q, dout, k, tail, v;
 };
 
 // A tile's tokens (rows of 16 bytes): -lse in log2, -delta, row ends (0 for one that sees nothing).
@@ -76,7 +76,7 @@ struct LiveTiles {
 
 // CTA `block` of `blocks`.
 template <class E>
-__device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &shape, const Plan &m,
+__device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &shape, const Plan &m, const GradMaps &maps,
                                     unsigned char *smem, unsigned block, unsigned blocks) {
   const ExpandedArgs &f = a.f;
   const int panels = shape.panels, v_panels = shape.v_panels, stages = m.stages;
@@ -386,12 +386,15 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
     if (n > 0) {
       if (lane == 0) mbar_expect(bar(sm.own), (panels + v_panels) * kKeyPanel);
       __syncwarp();
-      for (int p = 0; p < shape.nope_panels; ++p)
-        tma_box3(leader, base + p * kKeyPanel, &m.k, p * 64, h, key_at, bar(sm.own));
-      if (f.dr > 0)
-        tma_box(leader, base + shape.nope_panels * kKeyPanel, &m.tail, 0, key_at, bar(sm.own));
-      for (int p = 0; p < v_panels; ++p)
-        tma_box3(leader, base + v_at + p * kKeyPanel, &m.v, p * 64, h, key_at, bar(sm.own));
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t to = base + half * (kKeyPanel / 2);
+        const int key = key_at + half * kBoxRows;
+        for (int p = 0; p < shape.nope_panels; ++p)
+          tma_box3(leader, to + p * kKeyPanel, &maps.k, p * 64, h, key, bar(sm.own));
+        if (f.dr > 0) tma_box(leader, to + shape.nope_panels * kKeyPanel, &maps.tail, 0, key, bar(sm.own));
+        for (int p = 0; p < v_panels; ++p)
+          tma_box3(leader, to + v_at + p * kKeyPanel, &maps.v, p * 64, h, key, bar(sm.own));
+      }
     }
     int stage = 0, around = 0;
     for (int i = 0; i < n; ++i) {
@@ -402,9 +405,9 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       if (lane == 0) mbar_expect(full, stage_bytes);
       __syncwarp();
       for (int p = 0; p < panels; ++p)
-        tma_box3(leader, to + p * kTokenPanel, &m.q, p < shape.nope_panels ? p * 64 : f.dn, h, t, full);
+        tma_box3(leader, to + p * kTokenPanel, &maps.q, p < shape.nope_panels ? p * 64 : f.dn, h, t, full);
       for (int p = 0; p < v_panels; ++p)
-        tma_box3(leader, to + do_at + p * kTokenPanel, &m.dout, p * 64, h, t, full);
+        tma_box3(leader, to + do_at + p * kTokenPanel, &maps.dout, p * 64, h, t, full);
       if (++stage == stages) stage = 0, ++around;
     }
     if (n > 0) mbar_drain(bar(sm.own), 0);
@@ -470,15 +473,6 @@ inline bool plan(const ExpandedGradArgs &a, const GradShape &shape, Plan &m, int
   smem = own + m.stages * (stage + numbers) + static_cast<int>(sizeof(Small));
   m.score_buffers = 3 * kTokens + ((a.f.dv + 31) & ~31) + D <= 512 ? 2 : 1;
   return m.stages >= 2;
-}
-
-inline bool maps(const ExpandedGradArgs &a, bool bf16, Plan &m) {
-  const ExpandedArgs &f = a.f;
-  return grad_map(&m.q, bf16, f.q, f.dn + f.dr, f.H, f.T, f.ld_q_t, f.ld_q_h, kTokens) &&
-         grad_map(&m.dout, bf16, a.dout, f.dv, f.H, f.T, a.ld_do_t, a.ld_do_h, kTokens) &&
-         grad_map(&m.k, bf16, f.k, f.dn, f.H, f.S, f.ld_k_s, f.ld_k_h, kTile) &&
-         grad_map(&m.v, bf16, f.v, f.dv, f.H, f.S, f.ld_v_s, f.ld_v_h, kTile) &&
-         (f.dr == 0 || tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kTile));
 }
 
 }  // namespace grad_keys

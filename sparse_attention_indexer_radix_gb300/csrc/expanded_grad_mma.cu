@@ -11,6 +11,7 @@ namespace {
 struct GradMma {
   ExpandedGradArgs a;
   GradShape s;
+  GradMaps maps;
   grad_keys::Plan keys;
   grad_tokens::Plan tokens;
   unsigned token_blocks, key_blocks;
@@ -19,10 +20,12 @@ struct GradMma {
 template <class E>
 __global__ void __launch_bounds__(kGradThreads, 1) expanded_grad_mma_kernel(const __grid_constant__ GradMma m) {
   extern __shared__ __align__(1024) unsigned char smem[];
+  wait_for_previous_kernel();  // the tokens' statistics
+  let_next_kernel_start();
   if (blockIdx.x < m.token_blocks)
-    grad_tokens::run<E>(m.a, m.s, m.tokens, smem, blockIdx.x, m.token_blocks);
+    grad_tokens::run<E>(m.a, m.s, m.tokens, m.maps, smem, blockIdx.x, m.token_blocks);
   else
-    grad_keys::run<E>(m.a, m.s, m.keys, smem, blockIdx.x - m.token_blocks, m.key_blocks);
+    grad_keys::run<E>(m.a, m.s, m.keys, m.maps, smem, blockIdx.x - m.token_blocks, m.key_blocks);
 }
 
 GradShape shape_of(const ExpandedGradArgs &a) {
@@ -40,11 +43,23 @@ GradShape shape_of(const ExpandedGradArgs &a) {
   return s;
 }
 
+bool maps_of(const ExpandedGradArgs &a, bool bf16, GradMaps &m) {
+  const ExpandedArgs &f = a.f;
+  // [n, H, cols]; strides of dimensions of one are free, any multiple of 16 bytes.
+  const auto heads = [&](CUtensorMap *to, const void *p, int cols, int64_t n, int64_t ld, int64_t ld_h) {
+    return tensor_map_16bit(to, bf16, p, cols, f.H, f.H == 1 ? 1024 : ld_h, 1, n, n == 1 ? 1024 : ld, kBoxRows);
+  };
+  return heads(&m.q, f.q, f.dn + f.dr, f.T, f.ld_q_t, f.ld_q_h) &&
+         heads(&m.dout, a.dout, f.dv, f.T, a.ld_do_t, a.ld_do_h) &&
+         heads(&m.k, f.k, f.dn, f.S, f.ld_k_s, f.ld_k_h) && heads(&m.v, f.v, f.dv, f.S, f.ld_v_s, f.ld_v_h) &&
+         (f.dr == 0 ||
+          tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kBoxRows));
+}
+
 template <class E>
 int launch(const GradMma &m, int smem, cudaStream_t stream) {
   if (!allow_smem(expanded_grad_mma_kernel<E>, smem, kSmemLimit)) return SATK_ECUDA;
-  expanded_grad_mma_kernel<E><<<m.token_blocks + m.key_blocks, kGradThreads, smem, stream>>>(m);
-  return launch_status();
+  return launch_early(expanded_grad_mma_kernel<E>, m.token_blocks + m.key_blocks, kGradThreads, smem, stream, m);
 }
 
 }  // namespace
@@ -72,7 +87,7 @@ int expanded_grad_mma(const ExpandedGradArgs &a, int dtype, cudaStream_t stream)
   int keys_smem, tokens_smem;
   if (!grad_keys::plan(a, m.s, m.keys, keys_smem) || !grad_tokens::plan(a, m.s, m.tokens, tokens_smem))
     return SATK_EUNSUPPORTED;
-  if (!grad_keys::maps(a, bf16, m.keys) || !grad_tokens::maps(a, bf16, m.tokens)) return SATK_ECUDA;
+  if (!maps_of(a, bf16, m.maps)) return SATK_ECUDA;
   // (one more CTA a head for the rows of no request)
   const int64_t tokens = (tile_slots(a.f.T, a.f.R, kTile) + 1) * a.f.H;
   const int64_t keys = (tile_slots(a.f.S, a.f.R, kTile) + 1) * a.f.H;

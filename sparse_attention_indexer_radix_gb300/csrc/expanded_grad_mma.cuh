@@ -14,6 +14,12 @@ constexpr int kGradThreads = 384;  // warps 0-7 elementwise, 8 MMAs, 9 loads, 10
 constexpr int kTile = 128;         // rows of the tile that a CTA owns
 constexpr int kMaxPanels = 5;      // 64-column panels of a query or key (dn, then the tail)
 
+// The inputs, all read in boxes of 64 columns x 64 rows of a head.
+constexpr int kBoxRows = 64;
+struct GradMaps {
+  CUtensorMap q, dout, k, tail, v;
+};
+
 // Widths in panels, and where a CTA's work lies.
 struct GradShape {
   int nope_panels, panels, v_panels;
@@ -140,12 +146,6 @@ __device__ __forceinline__ void with_shape(int panels, int v_panels, bool full, 
   else if (panels == 3) values(Const<3>());
   else if (panels == 4) values(Const<4>());
   else values(Const<5>());
-}
-
-// The tensor map of [n, H, cols] read in boxes of 64 columns x `rows` rows of a head.
-inline bool grad_map(CUtensorMap *to, bool bf16, const void *p, int cols, int64_t H, int64_t n, int64_t ld,
-                     int64_t ld_h, int rows) {
-  return tensor_map_16bit(to, bf16, p, cols, H, H == 1 ? 1024 : ld_h, 1, n, n == 1 ? 1024 : ld, rows);
 }
 
 }  // namespace satk

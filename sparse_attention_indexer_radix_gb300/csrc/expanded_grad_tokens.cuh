@@ -25,13 +25,13 @@ namespace satk {
 namespace grad_tokens {
 
 constexpr int kKeys = 64;  // of a tile
+static_assert(kKeys == kBoxRows && kTile == 2 * kBoxRows, "boxes");
 constexpr int kOwnPanel = kTile * 128, kPanel = kKeys * 128;  // bytes of 64 columns
 constexpr int kMaxStages = 4;
 
 struct Plan {
   int stages;
   int q_inside, do_inside;  // in tensor memory
-  CUtensorMap q, dout, k, tail, v;
 };
 
 struct Small {
@@ -62,7 +62,7 @@ __device__ __forceinline__ void row_inside(uint32_t at, const E *row, int cols, 
 
 // CTA `block` of `blocks`.
 template <class E>
-__device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &shape, const Plan &m,
+__device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &shape, const Plan &m, const GradMaps &maps,
                                     unsigned char *smem, unsigned block, unsigned blocks) {
   const ExpandedArgs &f = a.f;
   const int panels = shape.panels, v_panels = shape.v_panels, stages = m.stages;
@@ -330,12 +330,17 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
     if (n > 0 && own > 0) {
       if (lane == 0) mbar_expect(bar(sm.own), own);
       __syncwarp();
-      if (!m.q_inside)
-        for (int p = 0; p < panels; ++p)
-          tma_box3(leader, base + p * kOwnPanel, &m.q, p < shape.nope_panels ? p * 64 : f.dn, h, t0, bar(sm.own));
-      if (!m.do_inside)
-        for (int p = 0; p < v_panels; ++p)
-          tma_box3(leader, base + do_at + p * kOwnPanel, &m.dout, p * 64, h, t0, bar(sm.own));
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t to = base + half * (kOwnPanel / 2);
+        const int token = t0 + half * kBoxRows;
+        if (!m.q_inside)
+          for (int p = 0; p < panels; ++p)
+            tma_box3(leader, to + p * kOwnPanel, &maps.q, p < shape.nope_panels ? p * 64 : f.dn, h, token,
+                     bar(sm.own));
+        if (!m.do_inside)
+          for (int p = 0; p < v_panels; ++p)
+            tma_box3(leader, to + do_at + p * kOwnPanel, &maps.dout, p * 64, h, token, bar(sm.own));
+      }
     }
     int stage = 0, around = 0;
     for (int i = 0; i < n; ++i) {
@@ -345,9 +350,9 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       const uint32_t full = bar(sm.full[stage]), to = base + ring_at + stage * stage_bytes;
       if (lane == 0) mbar_expect(full, stage_bytes);
       __syncwarp();
-      for (int p = 0; p < shape.nope_panels; ++p) tma_box3(leader, to + p * kPanel, &m.k, p * 64, h, key, full);
-      if (f.dr > 0) tma_box(leader, to + shape.nope_panels * kPanel, &m.tail, 0, key, full);
-      for (int p = 0; p < v_panels; ++p) tma_box3(leader, to + v_at + p * kPanel, &m.v, p * 64, h, key, full);
+      for (int p = 0; p < shape.nope_panels; ++p) tma_box3(leader, to + p * kPanel, &maps.k, p * 64, h, key, full);
+      if (f.dr > 0) tma_box(leader, to + shape.nope_panels * kPanel, &maps.tail, 0, key, full);
+      for (int p = 0; p < v_panels; ++p) tma_box3(leader, to + v_at + p * kPanel, &maps.v, p * 64, h, key, full);
       if (++stage == stages) stage = 0, ++around;
     }
     if (n > 0 && own > 0) mbar_drain(bar(sm.own), 0);
@@ -390,15 +395,6 @@ inline bool plan(const ExpandedGradArgs &a, const GradShape &shape, Plan &m, int
   if (m.stages > kMaxStages) m.stages = kMaxStages;
   smem = own + m.stages * stage + static_cast<int>(sizeof(Small));
   return m.stages >= 2;
-}
-
-inline bool maps(const ExpandedGradArgs &a, bool bf16, Plan &m) {
-  const ExpandedArgs &f = a.f;
-  return grad_map(&m.q, bf16, f.q, f.dn + f.dr, f.H, f.T, f.ld_q_t, f.ld_q_h, kTile) &&
-         grad_map(&m.dout, bf16, a.dout, f.dv, f.H, f.T, a.ld_do_t, a.ld_do_h, kTile) &&
-         grad_map(&m.k, bf16, f.k, f.dn, f.H, f.S, f.ld_k_s, f.ld_k_h, kKeys) &&
-         grad_map(&m.v, bf16, f.v, f.dv, f.H, f.S, f.ld_v_s, f.ld_v_h, kKeys) &&
-         (f.dr == 0 || tensor_map_16bit(&m.tail, bf16, f.tail, f.dr, f.S, f.S == 1 ? 1024 : f.ld_tail, kKeys));
 }
 
 }  // namespace grad_tokens

@@ -40,6 +40,26 @@ inline bool allow_smem(K kernel, size_t bytes, size_t most = 0) {
                               static_cast<int>(most > bytes ? most : bytes)) == cudaSuccess;
 }
 
+// Launches a kernel that may start before the one before it in the stream has
+// finished (it waits for that itself, before it reads what that wrote).
+template <class... P, class... A>
+inline int launch_early(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                        const A &...args) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(grid);
+  config.blockDim = dim3(block);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&config, kernel, static_cast<P>(args)...);
+  const int rc = launch_status();
+  return e == cudaSuccess ? rc : SATK_ECUDA;
+}
+
 // All the shared memory that a block may have.
 constexpr int kSmemLimit = 227 * 1024;
 
