@@ -143,6 +143,21 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
   const int key_at = sm.place[0], key0 = sm.place[1], rows = sm.place[2], keys = sm.place[3];
   const int token0 = sm.place[4], n_tokens = sm.place[5];
   if (rows == 0) return;
+  // The keys and values are on their way while the tokens' tiles are counted.
+  if (warp == 9) {
+    const uint32_t leader = elect_leader();
+    if (lane == 0) mbar_expect(bar(sm.own), (panels + v_panels) * kKeyPanel);
+    __syncwarp();
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t to = base + half * (kKeyPanel / 2);
+      const int key = key_at + half * kBoxRows;
+      for (int p = 0; p < shape.nope_panels; ++p)
+        tma_box3(leader, to + p * kKeyPanel, &maps.k, p * 64, h, key, bar(sm.own));
+      if (f.dr > 0) tma_box(leader, to + shape.nope_panels * kKeyPanel, &maps.tail, 0, key, bar(sm.own));
+      for (int p = 0; p < v_panels; ++p)
+        tma_box3(leader, to + v_at + p * kKeyPanel, &maps.v, p * 64, h, key, bar(sm.own));
+    }
+  }
   LiveTiles tiles{a.ends + sm.slots, (n_tokens + kTokens - 1) / kTokens, key0};
   {
     int mine = 0;
@@ -166,7 +181,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
     // load that all lanes share costs shared memory as much as any other, and the
     // products need all that it delivers (one key and 32 tokens a thread: 451 cycles
     // of loads a tile).
-    const int half = warp >> 2, row = threadIdx.x & 127, key = key0 + row;
+    const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float2 scale2 = make_float2(f.scale_log2, f.scale_log2);
     int stage = 0, around = 0;
@@ -250,37 +265,29 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       __syncwarp();
       tc_fence_after();
     }
-    const bool nan = *dead != 0 || key < *static_cast<volatile int *>(&sm.odd_end);
-    const int64_t at = key_at + row;
+    // A warp's rows, 64 columns a time (of the tail 32), in turn by the two halves;
+    // the ring is free by now.
+    const int odd = *static_cast<volatile int *>(&sm.odd_end), w0 = (warp & 3) * 32;
+    const bool nan = *dead != 0 || key0 + w0 + lane < odd;
+    const int64_t at = key_at + w0;
+    const int mine = rows - w0;
+    unsigned char *turn = smem + ring_at + warp * 4096;
     E *to_k = static_cast<E *>(a.dk) + at * a.ld_dk_s + h * a.ld_dk_h;
     E *to_v = static_cast<E *>(a.dv) + at * a.ld_dv_s + h * a.ld_dv_h;
     float *to_tail = a.tails + (static_cast<int64_t>(h) * f.S + at) * f.dr;
-    for (int c = half * 16; c < f.dv + D; c += 32) {
-      const int ck = c - f.dv;
-      uint32_t x[16];
-      if (n > 0) {
-        tmem_ld16(x, (ck < 0 ? dv_at + c : dk_at + ck) + lanes);
-        tmem_wait_ld();
-      } else {
-#pragma unroll
-        for (int y = 0; y < 16; ++y) x[y] = 0;
-      }
-      if (row >= rows) {
-        // not one of this request's keys
-      } else if (ck < 0) {
-        store16<E>(to_v + c, x, nan ? NAN : 1.f, shape.vec_v);
-      } else if (ck < f.dn) {
-        store16<E>(to_k + ck, x, nan ? NAN : a.scale, shape.vec_k);
-      } else {
-        const float scale = nan ? NAN : a.scale;
-        float4 *to = reinterpret_cast<float4 *>(to_tail + ck - f.dn);
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          to[y] = make_float4(__uint_as_float(x[4 * y]) * scale, __uint_as_float(x[4 * y + 1]) * scale,
-                              __uint_as_float(x[4 * y + 2]) * scale, __uint_as_float(x[4 * y + 3]) * scale);
-      }
-      __syncwarp();
-    }
+    int turns = 0;
+    for (int c = 0; c < f.dv; c += 64)
+      if ((turns++ & 1) == half)
+        store_rows(turn, dv_at + c + lanes, min(64, f.dv - c), n > 0, nan ? NAN : 1.f, to_v + c, a.ld_dv_s, mine,
+                   shape.vec_v != 0);
+    for (int c = 0; c < f.dn; c += 64)
+      if ((turns++ & 1) == half)
+        store_rows(turn, dk_at + c + lanes, min(64, f.dn - c), n > 0, nan ? NAN : a.scale, to_k + c, a.ld_dk_s,
+                   mine, shape.vec_k != 0);
+    for (int c = 0; c < f.dr; c += 32)
+      if ((turns++ & 1) == half)
+        store_rows(turn, dk_at + f.dn + c + lanes, min(32, f.dr - c), n > 0, nan ? NAN : a.scale, to_tail + c,
+                   f.dr, mine, true);
     tc_fence_before();
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
@@ -383,19 +390,6 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
   } else if (warp == 9) {
     // -------------------------------------------------------------------- loads
     const uint32_t leader = elect_leader();
-    if (n > 0) {
-      if (lane == 0) mbar_expect(bar(sm.own), (panels + v_panels) * kKeyPanel);
-      __syncwarp();
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t to = base + half * (kKeyPanel / 2);
-        const int key = key_at + half * kBoxRows;
-        for (int p = 0; p < shape.nope_panels; ++p)
-          tma_box3(leader, to + p * kKeyPanel, &maps.k, p * 64, h, key, bar(sm.own));
-        if (f.dr > 0) tma_box(leader, to + shape.nope_panels * kKeyPanel, &maps.tail, 0, key, bar(sm.own));
-        for (int p = 0; p < v_panels; ++p)
-          tma_box3(leader, to + v_at + p * kKeyPanel, &maps.v, p * 64, h, key, bar(sm.own));
-      }
-    }
     int stage = 0, around = 0;
     for (int i = 0; i < n; ++i) {
       const int t = token0 + tiles.next() * kTokens;
@@ -410,7 +404,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
         tma_box3(leader, to + do_at + p * kTokenPanel, &maps.dout, p * 64, h, t, full);
       if (++stage == stages) stage = 0, ++around;
     }
-    if (n > 0) mbar_drain(bar(sm.own), 0);
+    mbar_drain(bar(sm.own), 0);
     for (int i = max(0, n - stages); i < n; ++i)
       mbar_drain(bar(sm.full[i % stages]), (i / stages) & 1);
   } else {

@@ -70,21 +70,56 @@ __device__ __forceinline__ void clear_row(unsigned char *tile, int row, int pane
       *reinterpret_cast<uint4 *>(tile + p * stride + row * 128 + (x << 4)) = make_uint4(0, 0, 0, 0);
 }
 
-// Sixteen columns of a gradient row.
-template <class E>
-__device__ __forceinline__ void store16(E *to, const uint32_t (&x)[16], float scale, bool vec) {
-  Pack8<E> p[2];
+// Up to 64 columns (a multiple of 16; of float: 32) of a warp's 32 rows from tensor
+// memory to the first `rows` of them at `to`.  With rows of 16-byte chunks they are
+// turned through 4 KB of shared memory, so that a store covers whole lines of four
+// rows and not 16 bytes of each of 32.  `some`: there is something in tensor memory.
+template <class O>
+__device__ __forceinline__ void store_rows(unsigned char *turn, uint32_t tmem, int cols, bool some, float scale,
+                                           O *to, int64_t ld, int rows, bool vec) {
+  constexpr int kChunk = 16 / sizeof(O);  // values
+  const int lane = threadIdx.x & 31;
+  for (int c = 0; c < cols; c += 16) {
+    uint32_t x[16] = {};
+    if (some) {
+      tmem_ld16(x, tmem + c);
+      tmem_wait_ld();
+    }
+    uint4 chunk[sizeof(O)];
+    if constexpr (sizeof(O) == 4) {
 #pragma unroll
-  for (int y = 0; y < 8; ++y)
-    p[y >> 2].h[y & 3] = Elem<E>::from2(__uint_as_float(x[2 * y]) * scale,
-                                        __uint_as_float(x[2 * y + 1]) * scale);
-  if (vec) {
-    *reinterpret_cast<uint4 *>(to) = p[0].u;
-    *reinterpret_cast<uint4 *>(to + 8) = p[1].u;
-  } else {
+      for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * scale);
 #pragma unroll
-    for (int y = 0; y < 16; ++y) to[y] = (y & 1) ? p[y >> 3].h[(y & 7) >> 1].y : p[y >> 3].h[(y & 7) >> 1].x;
+      for (int y = 0; y < 4; ++y) chunk[y] = make_uint4(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
+    } else {
+      Pack8<O> p[2];
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        p[y >> 2].h[y & 3] = Elem<O>::from2(__uint_as_float(x[2 * y]) * scale, __uint_as_float(x[2 * y + 1]) * scale);
+      chunk[0] = p[0].u, chunk[1] = p[1].u;
+    }
+#pragma unroll
+    for (int y = 0; y < static_cast<int>(sizeof(O)); ++y)
+      *reinterpret_cast<uint4 *>(turn + lane * 128 + (((c / kChunk + y) ^ (lane & 7)) << 4)) = chunk[y];
   }
+  __syncwarp();
+  if (vec) {
+    const int ch = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (r < rows && ch * kChunk < cols)
+        *reinterpret_cast<uint4 *>(to + r * ld + ch * kChunk) =
+            *reinterpret_cast<const uint4 *>(turn + r * 128 + ((ch ^ (r & 7)) << 4));
+    }
+  } else {
+    for (int i = lane; i < rows * cols; i += 32) {
+      const int r = i / cols, c = i - r * cols;
+      to[r * ld + c] = *reinterpret_cast<const O *>(turn + r * 128 + (((c / kChunk) ^ (r & 7)) << 4) +
+                                                    (c % kChunk) * sizeof(O));
+    }
+  }
+  __syncwarp();
 }
 
 // The rows of no request, of one head: zeros by whole warps.
