@@ -194,11 +194,12 @@ __global__ void __launch_bounds__(kDistillThreads) distill_loss_kernel(DistillAr
 
 // A bit a column: it has an entry, it has several; the columns that have several,
 // with their scores.
+template <int ENTRIES>
 struct Listed {
   float2 part[kDistillThreads / 32];
   uint32_t any[kChunk / 32], several[kChunk / 32];
-  int column[SATK_TOPK_MAX_K / 2];
-  float score[SATK_TOPK_MAX_K / 2];
+  int column[ENTRIES / 2];
+  float score[ENTRIES / 2];
   int n;
 };
 
@@ -221,7 +222,8 @@ __device__ __forceinline__ float min_or_nan(float x, float y) {
 template <class E, int PER, bool LISTED>
 __global__ void __launch_bounds__(kDistillThreads) distill_grad_kernel(DistillArgs a) {
   constexpr int kN = Vec16<E>::kN;
-  __shared__ Listed sm;
+  constexpr int kLoads = LISTED ? 2 : kUnroll;  // (zeros need no registers, CTAs do)
+  __shared__ Listed<PER * kDistillThreads> sm;
   const int tid = threadIdx.x;
   const int64_t t = blockIdx.x / a.chunks;
   const int b = static_cast<int>(blockIdx.x % a.chunks) * a.chunk;
@@ -298,15 +300,15 @@ __global__ void __launch_bounds__(kDistillThreads) distill_grad_kernel(DistillAr
     const int n = (e - first) / kN, last = first + n * kN;
     if (tid < first - b) one(b + tid);
     if (tid < e - last) one(last + tid);
-    for (int i = tid; i < n; i += 2 * kDistillThreads) {
-      uint4 u[2];
+    for (int i = tid; i < n; i += kLoads * kDistillThreads) {
+      uint4 u[kLoads];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kLoads; ++j) {
         const int x = i + j * kDistillThreads, v = first + x * kN;
         u[j] = x < n && v < live ? ld_stream(row + v) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kLoads; ++j) {
         const int x = i + j * kDistillThreads, v = first + x * kN;
         if (x >= n) break;
         if (v < live) {
