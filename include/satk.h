@@ -344,12 +344,14 @@ int satk_dcp_emit_rows(const int32_t *ids, int64_t T, int32_t k, int64_t ld_ids,
  *            (-inf when that is empty), what satk_distill_grad takes.
  * Sums are kept in 32 bits.  An entry with p above 0 and a score of -inf makes
  * its row's loss +inf; a NaN or +inf among the scope's scores or the entries'
- * values makes the row's loss (and, among the scores, its lse) NaN.
+ * values makes the row's loss (and, among the scores, its lse) NaN, and so do
+ * scores that are all -inf (lse -inf) where some share is above 0.
  * Errors   : SATK_EINVAL for NULL logits/ids/teacher/loss/lse, an unknown dtype,
  *            kind or scope, rows or cols < 0 or >= 2**31, k outside
  *            1..SATK_TOPK_MAX_K, ld_logits < cols, ld_ids < k or ld_teacher < k
  *            (strides are not used with one row), a temperature that is not
- *            positive and finite, or whose inverse is not.
+ *            positive and finite, or whose inverse is not; SATK_EUNSUPPORTED
+ *            when the rows' CTAs, up to eight a row, pass 2**31.
  */
 int satk_distill_loss(const void *logits, int dtype, int64_t rows, int64_t cols,
                       int64_t ld_logits, const int32_t *row_ends,
@@ -639,8 +641,9 @@ int satk_latent_merge(const void *parts, int dtype, int32_t W, int64_t T,
  *          D < 1, k < 1, cache_rows < 0, a stride below its extent (ld_q_t,
  *          ld_q_h, ld_cache, ld_rows, ld_out; not used at an extent of one), a
  *          scale that is not finite, a dtype other than SATK_BF16 / SATK_F16;
- *          SATK_EUNSUPPORTED for H > 1024 or D > SATK_LATENT_MAX +
- *          SATK_LATENT_TAIL_MAX.
+ *          SATK_EUNSUPPORTED for H > 1024, D > SATK_LATENT_MAX +
+ *          SATK_LATENT_TAIL_MAX, or (widths that are not multiples of 16, rows
+ *          off 16-byte boundaries) T * k >= 2**33.
  */
 int satk_latent_rows_weights(const void *q, int dtype, int64_t T, int32_t H,
                              int32_t D, int64_t ld_q_t, int64_t ld_q_h,
@@ -686,7 +689,8 @@ size_t satk_latent_expanded_grad_workspace_bytes(int64_t T, int64_t S, int32_t R
  * Errors   : as satk_latent_attend_expanded (lse is required); also SATK_EINVAL
  *            for NULL dout/lse/grad_q/grad_k/grad_v/workspace, NULL grad_tail
  *            with dr > 0, workspace not 16-byte aligned or smaller than
- *            satk_latent_expanded_grad_workspace_bytes.
+ *            satk_latent_expanded_grad_workspace_bytes; SATK_EUNSUPPORTED when a
+ *            launch would pass 2**31 CTAs.
  */
 int satk_latent_attend_expanded_grad(
     const void *dout, int64_t ld_do_t, int64_t ld_do_h, const float *dlse,

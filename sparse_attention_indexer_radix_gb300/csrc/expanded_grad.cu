@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kWarps * 32) grad_stats_kernel(ExpandedGradArg
   }
   const int64_t id = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * 2 + lane / kRowLanes;
   const int at = lane % kRowLanes;
+  const unsigned lanes = ((1u << kRowLanes) - 1) << (lane - at);  // of this row
   float sum = 0.f;
   if (id < static_cast<int64_t>(a.f.T) * a.f.H) {
     const int64_t t = id / a.f.H;
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kWarps * 32) grad_stats_kernel(ExpandedGradArg
       for (int c = at; c < a.f.dv; c += kRowLanes) sum = fmaf(Elem<E>::to(dout[c]), Elem<E>::to(out[c]), sum);
     }
 #pragma unroll
-    for (int d = kRowLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(__activemask(), sum, d);
+    for (int d = kRowLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(lanes, sum, d);
     if (at == 0)
       a.stats[static_cast<int64_t>(h) * a.f.T + t] =
           make_float2(a.f.lse[id] * kLog2e, sum - (a.dlse != nullptr ? a.dlse[id] : 0.f));
@@ -101,13 +102,13 @@ __global__ void __launch_bounds__(256) grad_tail_kernel(ExpandedGradArgs a, int6
 template <class E>
 int launch_stats(const ExpandedGradArgs &a, cudaStream_t stream) {
   const int64_t rows = (static_cast<int64_t>(a.f.T) * a.f.H + 2 * kWarps - 1) / (2 * kWarps);
-  const int slots = static_cast<int>(tile_slots(a.f.T, a.f.R, kGradTokens));
-  const int64_t grid = rows + (slots + kWarps - 1) / kWarps;
-  if (grid > INT32_MAX) return SATK_EUNSUPPORTED;
+  const int64_t slots = tile_slots(a.f.T, a.f.R, kGradTokens), grid = rows + (slots + kWarps - 1) / kWarps;
+  if (grid > INT32_MAX || slots > INT32_MAX) return SATK_EUNSUPPORTED;
   const bool vec = a.f.dv % 8 == 0 && rows_of_16_bytes(a.dout, a.f.T, a.ld_do_t, a.f.H, a.ld_do_h) &&
                    rows_of_16_bytes(a.f.out, a.f.T, a.f.ld_out_t, a.f.H, a.f.ld_out_h);
   const auto kernel = vec ? grad_stats_kernel<E, true> : grad_stats_kernel<E, false>;
-  kernel<<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(a, static_cast<unsigned>(rows), slots);
+  kernel<<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(a, static_cast<unsigned>(rows),
+                                                                static_cast<int>(slots));
   return launch_status();
 }
 

@@ -302,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
       const int r = r0 + 4 * g + (lane >> 3);
       dst[g] = base + ring_at + r * 128 + ((ch ^ (r & 7)) << 4);
     }
-    int last_slot = -1, last_phase = 0;  // (the last panel: by then all before it are there)
     int slot = group % m.slots, around = group / m.slots, filled = 0, told = 0, told_slot = slot;
     auto advance = [&](int &at) {
       at += kGroups;
@@ -372,13 +371,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
             tell();
           }
         }
-        last_slot = slot;
-        last_phase = around & 1;
         if (advance(slot)) ++around;
       }
       p -= m.panels;
     }
-    if (gather && last_slot >= 0) mbar_drain(bar(sm.full[last_slot]), last_phase);
+    // The gathers of the ring's last round, whether anyone has waited for them or not.
+    for (int back = 0; gather && back < m.slots; back += kGroups) {
+      slot -= kGroups;
+      if (slot < 0) slot += m.slots, --around;
+      if (around < 0) break;
+      mbar_drain(bar(sm.full[slot]), around & 1);
+    }
     cp_async_wait_all();
     while (told < filled) tell();
   }
@@ -433,11 +436,11 @@ int launch(WeightsMma &m, int smem, cudaStream_t stream) {
 
 }  // namespace
 
-// Widths in steps of 16, rows of 16 bytes.
+// Widths in steps of 16, rows of 16 bytes, counters that stay in 32 bits.
 bool latent_weights_mma_fits(const WeightsArgs &a) {
   WeightsMma m;
   int smem;
-  return a.D % 16 == 0 && a.cache_rows > 0 && rows_of_16_bytes(a.q, a.T, a.ld_q_t, a.H, a.ld_q_h) &&
+  return a.D % 16 == 0 && a.cache_rows > 0 && a.T < INT32_MAX - 4096 && a.k < INT32_MAX - 4096 && rows_of_16_bytes(a.q, a.T, a.ld_q_t, a.H, a.ld_q_h) &&
          rows_of_16_bytes(a.cache, a.cache_rows, a.ld_cache, 1, 0) && plan(a, m, smem);
 }
 
