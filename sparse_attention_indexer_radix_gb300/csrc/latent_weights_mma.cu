@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
       dst[g] = base + ring_at + r * 128 + ((ch ^ (r & 7)) << 4);
     }
     int slot = group % m.slots, around = group / m.slots, filled = 0, told = 0, told_slot = slot;
+    int total = 0;  // panels of all groups
     auto advance = [&](int &at) {
       at += kGroups;
       const bool wrap = at >= m.slots;
@@ -374,14 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
         if (advance(slot)) ++around;
       }
       p -= m.panels;
+      total += m.panels;
     }
     // The gathers of the ring's last round, whether anyone has waited for them or not.
-    for (int back = 0; gather && back < m.slots; back += kGroups) {
-      slot -= kGroups;
-      if (slot < 0) slot += m.slots, --around;
-      if (around < 0) break;
-      mbar_drain(bar(sm.full[slot]), around & 1);
-    }
+    // (An earlier one's slot has had another panel since, and its phase is no longer
+    // told from the next but one.)
+    for (int x = group; gather && x < total; x += kGroups)
+      if (x >= total - m.slots) mbar_drain(bar(sm.full[x % m.slots]), x / m.slots & 1);
     cp_async_wait_all();
     while (told < filled) tell();
   }

@@ -424,6 +424,25 @@ def test_streams_graphs_and_the_same_bits(shape):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("dn,dr,dv", [(128, 64, 128), (256, 0, 128), (192, 64, 64), (208, 48, 128), (64, 0, 64),
+                                      (16, 16, 16), (144, 64, 112)])
+def test_no_wait_is_given_up(dtype, dn, dr, dv):
+    """A call over many tiles takes far less than a wait that is given up (two
+    seconds)."""
+    c = Case(gen(44), dtype, 3, dn, dr, dv, [700, 3, 260], [500, 40, 0])
+    c.forward()
+    first = c.grad()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    again = c.grad()
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) < 500
+    for x, y in zip(first, again):
+        assert x is None or (torch.equal(x, y) and torch.isfinite(x).all())
+
+
 @pytest.mark.parametrize("shape", [3, 5, 9])
 def test_calls_in_a_row_with_cold_caches(shape):
     """The same bits whatever the memory system makes of the order in which loads,

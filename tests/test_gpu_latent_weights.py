@@ -186,6 +186,28 @@ def test_offsets_beyond_32_bits():
     run(q, cache, rows, None, 64, 0.1)
 
 
+@pytest.mark.parametrize("H,D", [(128, 576), (128, 544), (112, 576), (120, 512), (96, 576), (64, 544),
+                                 (256, 320), (16, 64)])
+def test_no_wait_is_given_up(H, D):
+    """Rings of four panels and more, units of every length: a call takes far less
+    than a wait that is given up (two seconds)."""
+    g = gen(26)
+    T, k = 200, 700
+    q, cache, rows, counts = case(g, T, H, D, k, 1000, BF16)
+    lse = torch.full((T, H), 9.0, device=DEV)
+    status = i32([0])
+    call = lambda: satk.latent_rows_weights(q, cache, rows, lse, scale=0.04, counts=counts,  # noqa: E731
+                                            status=status)
+    first = call()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    again = call()
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) < 500 and int(status.item()) == 0
+    assert torch.equal(first, again) and torch.isfinite(first).all()
+
+
 def test_streams_graphs_and_the_same_bits():
     g = gen(25)
     q, cache, rows, counts = case(g, 9, 48, 320, 300, 2000, BF16)
