@@ -143,7 +143,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
   const uint32_t tmem = sm.tmem;
   int low = INT32_MAX, high = 0;
   for (int w = 0; w < 4; ++w) low = min(low, sm.low[w]), high = max(high, sm.high[w]);
-  const int n = (high + kKeys - 1) / kKeys;
+  const int n = high / kKeys + (high % kKeys != 0);
   const int first_masked = low / kKeys;  // the first tile with a key that some token does not see
   const uint32_t dp_at = tmem + 2 * kKeys, dq_at = dp_at + kKeys, q_in = dq_at + D;
   const uint32_t do_in = q_in + (m.q_inside ? D / 2 : 0);
