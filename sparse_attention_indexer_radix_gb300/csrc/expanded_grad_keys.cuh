@@ -16,9 +16,12 @@
 // The tail's gradient is summed over the heads by a kernel of its own, from a part
 // of each head: no atomics, the same bits every time.
 //
-// Bounded by the tensor core: at 192 query/key and 128 value columns a 128 x 64
-// tile is 1280 cycles of products, of which the scores and dP read both operands
-// from shared memory (6 KB in 32 cycles: 1.5 times what it delivers).
+// Bounded by the tensor core: at 192 query/key and 128 value columns a 128 x 64 tile
+// is 1580 cycles of products, of which the scores and dP, both operands in shared
+// memory, take 1000 (50 a step of 16 columns: 6 KB at 128 bytes a cycle).  4096
+// tokens over 8192 keys, 16 heads: 1700 cycles a tile; with the queries' CTAs 600
+// us, the tensor core 67 % active.  The rest are the CTAs' beginnings (5 thousand
+// cycles) and ends (5.5).
 #pragma once
 
 #include "expanded_grad_mma.cuh"
