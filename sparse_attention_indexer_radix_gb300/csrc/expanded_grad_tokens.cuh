@@ -6,8 +6,9 @@
 //   S[token, key] = Q [K | tail]^T         dP[token, key] = dO V^T
 //   dS = exp2(scale S - lse) (dP - delta)  dQ += dS [K | tail]
 // A token is a TMEM lane and a thread.  dS, rounded to the inputs' type, replaces S
-// in tensor memory and is the A operand of the second product.  Q, and dO where
-// there is room too, are A operands in tensor memory as well: with a tile of 64
+// in tensor memory and is the A operand of the second product; with few tokens a
+// request, what the rounding left is a second operand (see kFewTokens).  Q, and dO
+// where there is room too, are A operands in tensor memory as well: with a tile of 64
 // keys a product with both operands in shared memory takes 50 cycles a step of 16
 // columns, one with A in tensor memory 36.  At 192 query/key columns: S 2 x 64, dP
 // 64, Q 96, dQ 192 columns, dO in shared memory.
@@ -63,7 +64,7 @@ __device__ __forceinline__ void row_inside(uint32_t at, const E *row, int cols, 
 }
 
 // CTA `block` of `blocks`.
-template <class E>
+template <class E, bool FEW>
 __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &shape, const Plan &m, const GradMaps &maps,
                                     unsigned char *smem, unsigned block, unsigned blocks) {
   const ExpandedArgs &f = a.f;
@@ -204,15 +205,15 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
           if (k0 + x >= end) dp[x] = 0;
       }
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        union {
-          typename Elem<E>::T2 h;
-          uint32_t u;
-        } pk;
-        pk.h = Elem<E>::from2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]));
-        packed[x] = pk.u;
-      }
+      for (int x = 0; x < 16; ++x)
+        packed[x] = pack16<E>(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]));
       tmem_st16(s_at, packed);  // the first half of this thread's columns of S
+      if (FEW) {  // what the rounding left: the second half
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          packed[x] = pack16_rest<E>(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]), packed[x]);
+        tmem_st16(s_at + 16, packed);
+      }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bar(sm.ready[i & 1]));
@@ -251,7 +252,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       const uint32_t ready = bar(sm.ready[0]), gap = shape.gap;
       const bool two = shape.one_product == 0, q_inside = m.q_inside != 0, do_inside = m.do_inside != 0;
       if (n > 0 && (!q_inside || !do_inside)) mbar_wait(bar(sm.own), 0, dead);
-      with_shape(panels, v_panels, shape.full != 0, [&](auto np, auto vp, auto all) {
+      with_shape<!FEW>(panels, v_panels, shape.full != 0, [&](auto np, auto vp, auto all) {
         // Tile i's place in the ring: its stage, the low words' distance, the phase.
         struct At {
           uint32_t stage = 0, low = 0, phase = 0;
@@ -285,19 +286,23 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
           mbar_wait(looked + 8 * x.stage, x.phase, dead);
           mbar_wait(ready + 8 * (i & 1), i >> 1 & 1, dead);
           tc_fence_after();
-          const uint32_t ds_at = tmem + (i & 1) * kKeys, k = rows_low + x.low;
-          const bool more = i > 0;
-          mma_ts_low(dq_at, ds_at, k, d_q, more);
-          mma_ts_low(dq_at, ds_at + 8, k + 128, d_q, true);
-          mma_ts_low(dq_at, ds_at + 32, k + 256, d_q, true);
-          mma_ts_low(dq_at, ds_at + 40, k + 384, d_q, true);
-          if (all.value == 0 && two) {
-            const uint32_t d = dq_at + f.dn, t = k + tail_step;
-            mma_ts_low(d, ds_at, t, d_t, more);
-            mma_ts_low(d, ds_at + 8, t + 128, d_t, true);
-            mma_ts_low(d, ds_at + 32, t + 256, d_t, true);
-            mma_ts_low(d, ds_at + 40, t + 384, d_t, true);
-          }
+          const uint32_t k = rows_low + x.low;
+          auto from = [&](uint32_t ds_at, bool more) {
+            mma_ts_low(dq_at, ds_at, k, d_q, more);
+            mma_ts_low(dq_at, ds_at + 8, k + 128, d_q, true);
+            mma_ts_low(dq_at, ds_at + 32, k + 256, d_q, true);
+            mma_ts_low(dq_at, ds_at + 40, k + 384, d_q, true);
+            if (all.value == 0 && two) {
+              const uint32_t d = dq_at + f.dn, t = k + tail_step;
+              mma_ts_low(d, ds_at, t, d_t, more);
+              mma_ts_low(d, ds_at + 8, t + 128, d_t, true);
+              mma_ts_low(d, ds_at + 32, t + 256, d_t, true);
+              mma_ts_low(d, ds_at + 40, t + 384, d_t, true);
+            }
+          };
+          const uint32_t ds_at = tmem + (i & 1) * kKeys;
+          from(ds_at, i > 0);
+          if (FEW) from(ds_at + 16, true);
           tc_commit(empty + 8 * x.stage);
         };
         if (n == 0) return;

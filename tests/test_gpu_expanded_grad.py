@@ -5,6 +5,8 @@ Tolerances, with u half a step of the element type (bf16 2^-8, fp16 2^-11):
     score (fp32 sums of D products: D 2^-23 scale sum |q||k|), its exponent;
   dS likewise, and by P (dv 2^-23 (sum |dout||v| + sum |dout||out|) + |dlse| 2^-22)
     from the two sums whose difference it takes;
+    (of calls of up to 16 tokens a request on average, of requests of one tile of
+    tokens: two roundings, the second of what the first left, so u^2 for u)
   with fp16 both lose what is below 2^-25;
   the products' n terms are summed in 32 bits (n 2^-23 of the terms' sizes), the
     tail's over the heads too; a result is rounded once (u of itself, fp16 2^-25)."""
@@ -60,7 +62,7 @@ class Case:
             self.ends, scale=self.scale, dlse=self.dlse, **kw)
 
 
-def definition(c):
+def definition(c, roundings=1):
     """Gradients and tolerances in 64 bits, a request and a head at a time."""
     T, H, D = c.q.shape
     S, _, dn = c.k.shape
@@ -93,7 +95,7 @@ def definition(c):
                 delta = delta - c.dlse[a:b, h, None].double()
                 sums = sums + c.dlse[a:b, h, None].double().abs() * 2.0**-22
             ds = p * (do @ val.T - delta)
-            e = u + (q.abs() @ key.abs().T) * abs(c.scale) * D * 2.0**-23 \
+            e = u**roundings + (q.abs() @ key.abs().T) * abs(c.scale) * D * 2.0**-23 \
                 + (x.abs() + L.abs() + 2) * 2.0**-21
             e_p = torch.where(seen, p * e + tiny, 0.0)
             e_s = torch.where(seen, ds.abs() * e + p * sums + tiny, 0.0)
@@ -151,6 +153,48 @@ def test_shapes(dtype, shape, dlse):
     c = Case(gen(shape), dtype, *SHAPES[shape], dlse=dlse)
     c.forward()
     close(c.grad(), definition(c), "shapes")
+
+
+FEW = [  # H, dn, dr, dv, new, context
+    (1, 16, 0, 16, [1], [0]),
+    (3, 64, 32, 64, [5, 1, 16], [0, 9, 0]),
+    (2, 128, 64, 128, [2, 3, 8], [0, 400, 1100]),
+    (16, 128, 64, 128, [4], [0]),
+    (5, 96, 48, 80, [64, 1, 1, 0, 1, 0], [130, 0, 64, 0, 127, 3]),
+    (2, 192, 64, 128, [7, 0, 33], [100, 0, 0]),
+    (1, 256, 0, 128, [16], [150]),
+    (2, 80, 64, 96, [8] * 9, [0, 1, 56, 120, 121, 249, 500, 0, 0]),
+    (1, 64, 0, 64, [1, 2], [3000, 0]),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("shape", range(len(FEW)))
+def test_few_tokens(dtype, shape):
+    """P and dS as two operands each."""
+    c = Case(gen(100 + shape), dtype, *FEW[shape], dlse=bool(shape & 1))
+    c.forward()
+    close(c.grad(), definition(c, roundings=2), "few tokens")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_few_tokens_beside_many(dtype):
+    """A long request in a call that has few tokens a request on average, and what a
+    call of both kinds has in infinities: a weight of 1 whose rest is 0."""
+    new = [300] + [1] * 30
+    c = Case(gen(120), dtype, 2, 64, 32, 64, new, [40] + [5 * i for i in range(30)], dlse=True)
+    assert sum(new) <= 16 * len(new)
+    c.forward()
+    got, again = c.grad(), c.grad()
+    close(got, definition(c), "few beside many")
+    for x, y in zip(got, again):
+        assert torch.equal(x, y)
+    c.dout[310] = math.inf
+    got = c.grad()
+    assert not torch.isfinite(got[0][310]).any()
+    others = torch.arange(len(c.q), device=DEV) != 310
+    for x, y in zip(got[:1], again[:1]):
+        assert torch.equal(x[others], y[others])
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
