@@ -71,9 +71,10 @@ __device__ __forceinline__ void clear_row(unsigned char *tile, int row, int pane
 }
 
 // Up to 64 columns (a multiple of 16; of float: 32) of a warp's 32 rows from tensor
-// memory to the first `rows` of them at `to`.  With rows of 16-byte chunks they are
-// turned through 4 KB of shared memory, so that a store covers whole lines of four
-// rows and not 16 bytes of each of 32.  `some`: there is something in tensor memory.
+// memory to the first `rows` of them at `to` (`rows` may be more than the warp has: what
+// is left of the tile).  They are turned through the warp's own 4 KB of shared memory:
+// with rows of 16-byte chunks a store then covers whole lines of four rows and not 16
+// bytes of each of 32.  `some`: there is something in tensor memory.
 template <class O>
 __device__ __forceinline__ void store_rows(unsigned char *turn, uint32_t tmem, int cols, bool some, float scale,
                                            O *to, int64_t ld, int rows, bool vec) {
@@ -113,7 +114,8 @@ __device__ __forceinline__ void store_rows(unsigned char *turn, uint32_t tmem, i
             *reinterpret_cast<const uint4 *>(turn + r * 128 + ((ch ^ (r & 7)) << 4));
     }
   } else {
-    for (int i = lane; i < rows * cols; i += 32) {
+    const int n = min(rows, 32) * cols;
+    for (int i = lane; i < n; i += 32) {
       const int r = i / cols, c = i - r * cols;
       to[r * ld + c] = *reinterpret_cast<const O *>(turn + r * 128 + (((c / kChunk) ^ (r & 7)) << 4) +
                                                     (c % kChunk) * sizeof(O));

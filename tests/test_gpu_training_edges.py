@@ -1,0 +1,63 @@
+"""Corners of the training calls: gradients of other layouts than the inputs', rows of
+no size in clusters, lists of very small and very large weights, values and heads
+that do not count, normalisers far from 0, short requests beside long ones.
+
+Tolerances that are not those of the operators' own tests stand at each test."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_indexer_radix_gb300 as satk
+from test_gpu_distill import F32, check, entries, student
+from test_gpu_distill import close as close_rows
+from test_gpu_distill import definition as distilled
+from test_gpu_expanded_grad import Case, close, definition
+from test_gpu_latent import BF16, DEV, F16, U, gen, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sparse_attention_indexer_radix_gb300 import build as satk_build
+    satk_build.build()
+
+
+def placed(x, how):
+    """A tensor like x, full of 7, that starts at an odd element or whose rows or
+    heads lie an odd number of elements apart, and all of its memory."""
+    base, heads, rows = {"base": (1, 0, 0), "heads": (0, 3, 0), "rows": (0, 0, 5)}[how]
+    n, H, w = x.shape if x.dim() == 3 else (x.shape[0], 1, x.shape[1])
+    ld_h = w + heads
+    ld = H * ld_h + rows
+    wide = torch.full((n * ld + 16,), 7.0, dtype=x.dtype, device=DEV)
+    strides = (ld, ld_h, 1) if x.dim() == 3 else (ld, 1)
+    return wide.as_strided(x.shape, strides, base), wide
+
+
+@pytest.mark.parametrize("how", ["base", "heads", "rows"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("shape", [
+    (2, 128, 64, 128, [300, 77], [100, 0]), (3, 96, 48, 80, [129, 64, 250], [31, 0, 0]),
+    (2, 192, 64, 128, [200, 33], [100, 0]), (1, 64, 0, 64, [400], [0]), (4, 16, 16, 16, [130], [5]),
+    (2, 128, 64, 128, [2, 3, 8], [0, 400, 1100]), (2, 144, 64, 112, [8] * 9, [130] * 9)])
+def test_gradients_of_another_layout_than_the_inputs(dtype, how, shape):
+    """Aligned inputs, gradients that are not: the bits of aligned ones, whole, and
+    nothing between their rows."""
+    c = Case(gen(1), dtype, *shape, dlse=True)
+    c.forward()
+    want = c.grad()
+    close(want, definition(c), "aligned")
+    names = [n for n, x in zip(("dq", "dk", "dtail", "dv"), want) if x is not None]
+    for _ in range(3):
+        into = {n: placed(x, how) for n, x in zip(("dq", "dk", "dtail", "dv"), want) if n in names}
+        got = c.grad(**{n: x for n, (x, _) in into.items()})
+        for name, x, y in zip(("dq", "dk", "dtail", "dv"), got, want):
+            assert x is y is None or torch.equal(x, y), name
+        for name, (x, wide) in into.items():
+            x.fill_(7.0)
+            assert (wide == 7).all(), name
