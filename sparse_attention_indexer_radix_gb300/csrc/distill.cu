@@ -102,6 +102,14 @@ __device__ __forceinline__ void scan(Running &r, const E *row, int b, int e, flo
   if (static_cast<int>(threadIdx.x) < e - last) one(last + threadIdx.x);
 }
 
+// The two halves of a cluster barrier, of all threads of all its CTAs.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 template <class E, int PER, bool LISTED>
 __global__ void __launch_bounds__(kDistillThreads) distill_loss_kernel(DistillArgs a) {
   __shared__ float2 part[kDistillThreads / 32];
@@ -109,6 +117,9 @@ __global__ void __launch_bounds__(kDistillThreads) distill_loss_kernel(DistillAr
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
+  // (said here, waited for behind the pass: the first CTA's shared memory may be
+  // written once it has started)
+  if (ctas > 1) cluster_arrive();
   const int64_t t = blockIdx.x / ctas;
   const E *row = static_cast<const E *>(a.logits) + t * a.ld;
   const int end = row_end(a, t);
@@ -156,6 +167,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_loss_kernel(DistillAr
   float2 sums = block_reduce2<false>(make_float2(r.l.x, total), part);
   float m = most.x;
   if (ctas > 1) {
+    cluster_wait();
     if (threadIdx.x == 0) cluster.map_shared_rank(joined, 0)[rank] = make_float2(m, sums.x);
     cluster.sync();
     if (rank != 0) return;

@@ -61,3 +61,20 @@ def test_gradients_of_another_layout_than_the_inputs(dtype, how, shape):
         for name, (x, wide) in into.items():
             x.fill_(7.0)
             assert (wide == 7).all(), name
+
+
+@pytest.mark.parametrize("scope", ["row", "listed"])
+@pytest.mark.parametrize("rows", [1, 2, 7])
+def test_wide_rows_with_little_to_see(rows, scope):
+    """Rows shared by a cluster of which most CTAs have no column."""
+    g = gen(2)
+    cols = 131072
+    logits = student(g, rows, cols, BF16)
+    ids = torch.arange(16, device=DEV, dtype=torch.int32).repeat(rows, 1)
+    x = torch.rand(rows, 16, generator=g, device=DEV)
+    for ends in ([0] * rows, [1] * rows, [(5, 0, 4097, 1, 131072, 16, 131071)[i] for i in range(rows)]):
+        ends = i32(ends)
+        want = check(logits, ids, x, "weights", scope, 1.0, ends)
+        for _ in range(20):
+            got = satk.distill_loss(logits, ids, x, kind="weights", scope=scope, row_ends=ends)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
