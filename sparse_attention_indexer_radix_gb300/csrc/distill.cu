@@ -318,13 +318,14 @@ __global__ void __launch_bounds__(kDistillThreads) distill_grad_kernel(DistillAr
       uint4 u[kLoads];
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const int x = i + j * kDistillThreads, v = first + x * kN;
+        const int x = min(i + j * kDistillThreads, n), v = first + x * kN;
         u[j] = x < n && v < live ? ld_stream(row + v) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const int x = i + j * kDistillThreads, v = first + x * kN;
+        const int x = i + j * kDistillThreads;
         if (x >= n) break;
+        const int v = first + x * kN;
         if (v < live) {
           float2 f[kN / 2];
           Vec16<E>::to(u[j], f);
@@ -339,7 +340,8 @@ __global__ void __launch_bounds__(kDistillThreads) distill_grad_kernel(DistillAr
       }
     }
   } else {
-    for (int v = b + tid; v < e; v += kDistillThreads) one(v);
+    // (counted from the chunk's start: columns go up to 2^31)
+    for (int x = tid; x < e - b; x += kDistillThreads) one(b + x);
   }
   if (!asks) return;
   __syncthreads();

@@ -78,3 +78,25 @@ def test_wide_rows_with_little_to_see(rows, scope):
         for _ in range(20):
             got = satk.distill_loss(logits, ids, x, kind="weights", scope=scope, row_ends=ends)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_of_almost_2_31_columns():
+    """Scores and a gradient of different alignment over the widest row there can be:
+    every column is written once, nothing behind them."""
+    cols = 2**31 - 1
+    logits = torch.zeros(1, cols, dtype=BF16, device=DEV)
+    wide = torch.full((cols + 16,), 7.0, dtype=BF16, device=DEV)
+    out = wide[1:cols + 1].view(1, cols)
+    ids, x = i32([[5, cols - 1, -1]]), torch.tensor([[1.0, 3.0, 9.0]], device=DEV)
+    loss, lse = satk.distill_loss(logits, ids, x, kind="weights")
+    want = math.log(cols)
+    assert abs(lse.item() - want) <= 1e-5
+    assert abs(loss.item() - (want + 0.25 * math.log(0.25) + 0.75 * math.log(0.75))) <= 1e-4
+    dloss = torch.full((1,), float(cols), device=DEV)
+    satk.distill_grad(logits, ids, x, lse, dloss, kind="weights", out=out)
+    assert wide[0] == 7 and (wide[cols + 1:] == 7).all()
+    for v, p in ((5, 0.25), (cols - 1, 0.75)):
+        assert abs(out[0, v].item() / (1 - p * cols) - 1) <= 2.0**-7
+        out[0, v] = 1.0
+    for part in out[0].split(1 << 28):  # (shares of 1, within |lse| 2^-22 of themselves)
+        assert (part == 1).all()
