@@ -687,7 +687,8 @@ size_t satk_latent_expanded_grad_workspace_bytes(int64_t T, int64_t S, int32_t R
  * What a token does not see does not reach its gradient, nor does a token that
  * does not see a key reach that key's, infinities and NaN included; a token
  * whose lse is -inf sees nothing.  A row that is not finite may make all of a
- * gradient row that it does reach NaN.
+ * gradient row that it does reach NaN, and so does a wait inside the GPU that is given
+ * up, which never happens unless the GPU misbehaves.
  * Errors   : as satk_latent_attend_expanded (lse is required); also SATK_EINVAL
  *            for NULL dout/lse/grad_q/grad_k/grad_v/workspace, NULL grad_tail
  *            with dr > 0, workspace not 16-byte aligned or smaller than
@@ -720,8 +721,9 @@ int satk_latent_attend_expanded_grad(
  * read.  With `clear` = 2 it leaves 256 there instead of 0: until the next
  * clearing, each CTA of satk_latent_attend and satk_latent_attend_rows treats
  * the last of its results as if a wait inside the GPU had been given up
- * (SATK_STATUS_STALLED).  The normal build checks nothing and returns 0.  Not part of the
- * pages' interface: a test aid of this library.
+ * (SATK_STATUS_STALLED), and each of satk_latent_attend_expanded_grad's on the
+ * tensor cores that has products all of its own.  The normal build checks nothing
+ * and returns 0.  Not part of the pages' interface: a test aid of this library.
  */
 uint32_t satk_debug_flags(int clear);
 

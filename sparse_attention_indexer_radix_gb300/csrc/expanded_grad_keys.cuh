@@ -281,28 +281,34 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       tc_fence_after();
     }
     // A warp's rows, 64 columns a time (of the tail 32), in turn by the two halves;
-    // the ring is free by now.
+    // the ring is free by now, unless a wait was given up.
     const int odd = *static_cast<volatile int *>(&sm.odd_end), w0 = (warp & 3) * 32;
-    const bool nan = *dead != 0 || key0 + w0 + lane < odd;
+    const bool lost = n > 0 && (*dead != 0 || satk_stall_asked());
+    const bool nan = key0 + w0 + lane < odd;
     const int64_t at = key_at + w0;
     const int mine = rows - w0;
     unsigned char *turn = smem + ring_at + warp * 4096;
     E *to_k = static_cast<E *>(a.dk) + at * a.ld_dk_s + h * a.ld_dk_h;
     E *to_v = static_cast<E *>(a.dv) + at * a.ld_dv_s + h * a.ld_dv_h;
     float *to_tail = a.tails + (static_cast<int64_t>(h) * f.S + at) * f.dr;
-    int turns = 0;
-    for (int c = 0; c < f.dv; c += 64)
-      if ((turns++ & 1) == half)
-        store_rows(turn, dv_at + c + lanes, min(64, f.dv - c), n > 0, nan ? NAN : 1.f, to_v + c, a.ld_dv_s, mine,
-                   shape.vec_v != 0);
-    for (int c = 0; c < f.dn; c += 64)
-      if ((turns++ & 1) == half)
-        store_rows(turn, dk_at + c + lanes, min(64, f.dn - c), n > 0, nan ? NAN : a.scale, to_k + c, a.ld_dk_s,
-                   mine, shape.vec_k != 0);
-    for (int c = 0; c < f.dr; c += 32)
-      if ((turns++ & 1) == half)
-        store_rows(turn, dk_at + f.dn + c + lanes, min(32, f.dr - c), n > 0, nan ? NAN : a.scale, to_tail + c,
-                   f.dr, mine, true);
+    if (lost) {
+      lose_rows(half == 0 ? to_k : to_v, half == 0 ? a.ld_dk_s : a.ld_dv_s, mine, half == 0 ? f.dn : f.dv);
+      if (half == 0) lose_rows(to_tail, f.dr, mine, f.dr);
+    } else {
+      int turns = 0;
+      for (int c = 0; c < f.dv; c += 64)
+        if ((turns++ & 1) == half)
+          store_rows(turn, dv_at + c + lanes, min(64, f.dv - c), n > 0, nan ? NAN : 1.f, to_v + c, a.ld_dv_s, mine,
+                     shape.vec_v != 0);
+      for (int c = 0; c < f.dn; c += 64)
+        if ((turns++ & 1) == half)
+          store_rows(turn, dk_at + c + lanes, min(64, f.dn - c), n > 0, nan ? NAN : a.scale, to_k + c, a.ld_dk_s,
+                     mine, shape.vec_k != 0);
+      for (int c = 0; c < f.dr; c += 32)
+        if ((turns++ & 1) == half)
+          store_rows(turn, dk_at + f.dn + c + lanes, min(32, f.dr - c), n > 0, nan ? NAN : a.scale, to_tail + c,
+                     f.dr, mine, true);
+    }
     tc_fence_before();
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue

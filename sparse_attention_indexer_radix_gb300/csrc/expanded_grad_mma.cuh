@@ -124,6 +124,16 @@ __device__ __forceinline__ void store_rows(unsigned char *turn, uint32_t tmem, i
   __syncwarp();
 }
 
+// The same rows and columns after a wait that was given up: NaN, straight to memory (a
+// copy may still be on its way to any shared memory).
+template <class O>
+__device__ __forceinline__ void lose_rows(O *to, int64_t ld, int rows, int cols) {
+  O nan;
+  if constexpr (sizeof(O) == 4) nan = NAN; else nan = Elem<O>::from(NAN);
+  const int n = min(rows, 32) * cols;
+  for (int i = threadIdx.x & 31; i < n; i += 32) to[i / cols * ld + i % cols] = nan;
+}
+
 // The rows of no request, of one head: zeros by whole warps.
 template <class F>
 __device__ __forceinline__ void rows_outside(const int32_t *starts, int R, int n, F zero) {

@@ -224,14 +224,19 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       tc_fence_after();
     }
     // A warp's rows, 64 columns a time, in turn by the two halves; the ring is free by
-    // now.
-    const bool nan = *dead != 0 || *static_cast<volatile int *>(&sm.odd_key) < end;
+    // now, unless a wait was given up.
+    const bool lost = n > 0 && (*dead != 0 || satk_stall_asked());
+    const bool nan = *static_cast<volatile int *>(&sm.odd_key) < end;
     const int w0 = (warp & 3) * 32;
     unsigned char *turn = smem + ring_at + warp * 4096;
     E *to = static_cast<E *>(a.dq) + static_cast<int64_t>(t0 + w0) * a.ld_dq_t + h * a.ld_dq_h;
-    for (int c = half * 64; c < D; c += 128)
-      store_rows(turn, dq_at + c + lanes, min(64, D - c), n > 0, nan ? NAN : a.scale, to + c, a.ld_dq_t,
-                 n_tokens - w0, shape.vec_q != 0);
+    if (lost) {
+      if (half == 0) lose_rows(to, a.ld_dq_t, n_tokens - w0, D);
+    } else {
+      for (int c = half * 64; c < D; c += 128)
+        store_rows(turn, dq_at + c + lanes, min(64, D - c), n > 0, nan ? NAN : a.scale, to + c, a.ld_dq_t,
+                   n_tokens - w0, shape.vec_q != 0);
+    }
     tc_fence_before();
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue

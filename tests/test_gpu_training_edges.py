@@ -12,6 +12,8 @@ import pytest
 import torch
 
 import sparse_attention_indexer_radix_gb300 as satk
+from sparse_attention_indexer_radix_gb300 import binding
+from sparse_attention_indexer_radix_gb300 import build as satk_build
 from test_gpu_distill import F32, check, entries, student
 from test_gpu_distill import close as close_rows
 from test_gpu_distill import definition as distilled
@@ -23,7 +25,6 @@ pytestmark = pytest.mark.gpu
 
 @pytest.fixture(scope="module", autouse=True)
 def _built():
-    from sparse_attention_indexer_radix_gb300 import build as satk_build
     satk_build.build()
 
 
@@ -100,3 +101,39 @@ def test_rows_of_almost_2_31_columns():
         out[0, v] = 1.0
     for part in out[0].split(1 << 28):  # (shares of 1, within |lse| 2^-22 of themselves)
         assert (part == 1).all()
+
+
+@pytest.mark.parametrize("shape", [(2, 128, 64, 128, [300, 77], [100, 0]), (3, 96, 48, 80, [129, 5], [31, 70]),
+                                   (2, 128, 64, 128, [2, 3, 8], [0, 400, 1100])])
+@pytest.mark.parametrize("how", ["base", None])
+def test_a_given_up_wait_makes_gradients_nan(shape, how):
+    """No wait is made to run out: the debug build, asked to, ends every CTA as after
+    one.  Whole gradient rows are NaN, rows that nothing sees or no request has 0, and
+    nothing between the rows is written; once nothing is asked for all is right again."""
+    dbg = binding.load(satk_build.build(debug=True))
+    c = Case(gen(10), BF16, *shape, spare=(20, 30))
+    hidden = int(c.ks[1])  # the first request's last key
+    c.ends[:int(c.ts[1])] = torch.clamp(c.ends[:int(c.ts[1])], max=hidden - 1)
+    c.forward()
+    names, into = ("dq", "dk", "dtail", "dv"), {}
+    with binding.routed_to(dbg):
+        dbg.satk_debug_flags(1)
+        good = c.grad()
+        if how:
+            into = {n: placed(x, how) for n, x in zip(names, good)}
+        dbg.satk_debug_flags(2)
+        try:
+            bad = c.grad(**{n: x for n, (x, _) in into.items()})
+            torch.cuda.synchronize()
+        finally:
+            assert dbg.satk_debug_flags(1) == 256
+        again = c.grad()
+    close(good, definition(c), "good")
+    T, S = int(c.ts[-1]), int(c.ks[-1])
+    for name, x, end in zip(names, bad, (T, S, S, S)):
+        assert torch.isnan(x[:end]).all() and (x[end:] == 0).all(), name
+    for name, (x, wide) in into.items():
+        x.fill_(7.0)
+        assert (wide == 7).all(), name
+    for x, y in zip(good, again):
+        assert torch.equal(x, y)
