@@ -332,7 +332,8 @@ int satk_dcp_emit_rows(const int32_t *ids, int64_t T, int32_t k, int64_t ld_ids,
  * teacher  : [rows, ld_teacher] of `teacher_dtype`, columns [0, k): the entries'
  *            values x.  Their shares p by `kind`:
  *            SATK_TEACHER_LOGITS   exp(x / temperature) over their sum;
- *            SATK_TEACHER_WEIGHTS  x over the sum of x (satk_latent_rows_weights);
+ *            SATK_TEACHER_WEIGHTS  x over the sum of x (satk_latent_rows_weights),
+ *                                  whatever the size of x;
  *            SATK_TEACHER_PROBS    x as it is (mass may be missing from the list).
  *            A negative weight or probability counts as 0.
  * scope    : what the student's shares q = exp(s / temperature - lse) are

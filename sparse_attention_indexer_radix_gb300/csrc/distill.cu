@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_loss_kernel(DistillAr
   const float2 most = block_reduce2<true>(make_float2(r.m, top), part);
   float ref = finite_or_0(most.x);
   const float x_ref = finite_or_0(most.y);
+  const float unit = a.kind == SATK_TEACHER_WEIGHTS ? list_scale(most.y) : 1.f;
   if (LISTED) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_loss_kernel(DistillAr
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       if (in.id[i] < 0) continue;
-      total += a.kind == SATK_TEACHER_LOGITS ? exp2_fast((in.x[i] - x_ref) * a.c) : in.x[i];
+      total += a.kind == SATK_TEACHER_LOGITS ? exp2_fast((in.x[i] - x_ref) * a.c) : in.x[i] * unit;
     }
   }
   float2 sums = block_reduce2<false>(make_float2(r.l.x, total), part);
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_loss_kernel(DistillAr
       log_w = (in.x[i] - x_ref) * a.inv_tau;
       w = exp2_fast((in.x[i] - x_ref) * a.c);
     } else {
-      w = in.x[i];
+      w = in.x[i] * unit;
       log_w = logf(w);
     }
     if (w == 0.f) continue;
@@ -260,9 +261,11 @@ __global__ void __launch_bounds__(kDistillThreads) distill_grad_kernel(DistillAr
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < PER; ++i) top = fmaxf(top, in.x[i]);
-  const float x_ref = finite_or_0(block_reduce2<true>(make_float2(top, 0.f), sm.part).x);
+  top = block_reduce2<true>(make_float2(top, 0.f), sm.part).x;
+  const float x_ref = finite_or_0(top);
+  const float unit = a.kind == SATK_TEACHER_WEIGHTS ? list_scale(top) : 1.f;
   auto weight = [&](float x) {
-    return a.kind == SATK_TEACHER_LOGITS ? exp2_fast((x - x_ref) * a.c) : x;
+    return a.kind == SATK_TEACHER_LOGITS ? exp2_fast((x - x_ref) * a.c) : x * unit;
   };
   float total = 0.f;
 #pragma unroll

@@ -103,6 +103,14 @@ __device__ __forceinline__ int row_end(const DistillArgs &a, int64_t row) {
   return a.ends == nullptr ? cols : min(max(a.ends[row], 0), cols);
 }
 
+// A power of two that brings a list's largest weight near 1 (from 0 or a number below
+// 2^-126 it is 2^126): sums of scaled weights, and the inverses of those, are numbers
+// of 32 bits whatever the weights' size, and their shares keep their bits.
+__device__ __forceinline__ float list_scale(float most) {
+  const int e = 254 - static_cast<int>(__float_as_uint(most) >> 23);
+  return __uint_as_float(static_cast<uint32_t>(min(max(e, 1), 253)) << 23);
+}
+
 // A thread's share of a row's entries: entry i * threads + threadIdx.x for each
 // i.  id is -1 for one that does not count; x is the teacher's value, for weights
 // and probabilities no less than 0 (a NaN stays one).

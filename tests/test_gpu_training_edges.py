@@ -137,3 +137,29 @@ def test_a_given_up_wait_makes_gradients_nan(shape, how):
         assert (wide == 7).all(), name
     for x, y in zip(good, again):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("size", [1e-44, 1e-39, 1e-30, 1e30, 3e38])
+@pytest.mark.parametrize("scope", ["row", "listed"])
+@pytest.mark.parametrize("k", [2, 600, 2100])
+def test_weights_of_any_size(size, scope, k):
+    """Shares of a sum that 32 bits hold badly, or not at all (the weights
+    themselves are exact): those of their ratios."""
+    g = gen(3)
+    logits = student(g, 4, 5000, F32)
+    ids, x = entries(g, 4, 5000, k, "weights", holes=False)
+    x = x.double() * size
+    x[0, 0], x[0, 1] = 1e-40, 3e-40
+    x[1] *= torch.logspace(-20, 0, k, dtype=torch.float64, device=DEV)
+    x[2, 1] = -1.0
+    x[3, 0] = 1e-42
+    ids[3, -1] = ids[3, 0]
+    check(logits, ids, x.float(), "weights", scope)
+
+
+def test_weights_of_any_size_in_16_bits():
+    g = gen(4)
+    logits = student(g, 3, 700, BF16)
+    ids, x = entries(g, 3, 700, 40, "weights")
+    for dtype, size in ((BF16, 1e-39), (BF16, 3e38), (F16, 1e-6), (F16, 60000.0)):
+        check(logits, ids, (x * size).to(dtype), "weights")
