@@ -344,9 +344,10 @@ int satk_dcp_emit_rows(const int32_t *ids, int64_t T, int32_t k, int64_t ld_ids,
  * lse      : float [rows], log of the sum of exp(s / temperature) over the scope
  *            (-inf when that is empty), what satk_distill_grad takes.
  * Sums are kept in 32 bits.  An entry with p above 0 and a score of -inf makes
- * its row's loss +inf; a NaN or +inf among the scope's scores or the entries'
- * values makes the row's loss (and, among the scores, its lse) NaN, and so do
- * scores that are all -inf (lse -inf) where some share is above 0.
+ * its row's loss +inf; a NaN or +inf among the scope's scores or the values of
+ * the entries that count makes the row's loss (and, among the scores, its lse)
+ * NaN, its gradient too (at the entries at least), and so do scores that are all
+ * -inf (lse -inf) where some share is above 0.
  * Errors   : SATK_EINVAL for NULL logits/ids/teacher/loss/lse, an unknown dtype,
  *            kind or scope, rows or cols < 0 or >= 2**31, k outside
  *            1..SATK_TOPK_MAX_K, ld_logits < cols, ld_ids < k or ld_teacher < k

@@ -360,9 +360,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_grad_kernel(DistillAr
     float p = 0.f, count = 0.f;
     for (int y = lane; y < a.k; y += 32) {
       if (a.ids[t * a.ld_ids + y] != v) continue;
-      float x = teacher_value(a, t * a.ld_teacher + y);
-      if (a.kind != SATK_TEACHER_LOGITS && x < 0.f) x = 0.f;
-      p += weight(x) * norm;
+      p += weight(teacher_value(a, t * a.ld_teacher + y)) * norm;
       count += 1.f;
     }
 #pragma unroll

@@ -90,11 +90,16 @@ __device__ __forceinline__ float2 block_reduce2(float2 x, float2 *at) {
   return x;
 }
 
+// An entry's value; as a weight or probability no less than 0, and NaN if it is not
+// finite (infinite logits make NaN of themselves).
 __device__ __forceinline__ float teacher_value(const DistillArgs &a, int64_t at) {
-  if (a.teacher_dtype == SATK_F32) return static_cast<const float *>(a.teacher)[at];
-  if (a.teacher_dtype == SATK_BF16)
-    return __bfloat162float(static_cast<const __nv_bfloat16 *>(a.teacher)[at]);
-  return __half2float(static_cast<const __half *>(a.teacher)[at]);
+  float x;
+  if (a.teacher_dtype == SATK_F32) x = static_cast<const float *>(a.teacher)[at];
+  else if (a.teacher_dtype == SATK_BF16)
+    x = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.teacher)[at]);
+  else x = __half2float(static_cast<const __half *>(a.teacher)[at]);
+  if (a.kind == SATK_TEACHER_LOGITS) return x;
+  return x < 0.f ? 0.f : x == INFINITY ? NAN : x;
 }
 
 // The visible columns of a row.
@@ -112,8 +117,7 @@ __device__ __forceinline__ float list_scale(float most) {
 }
 
 // A thread's share of a row's entries: entry i * threads + threadIdx.x for each
-// i.  id is -1 for one that does not count; x is the teacher's value, for weights
-// and probabilities no less than 0 (a NaN stays one).
+// i.  id is -1 for one that does not count; x is the teacher's value.
 template <int PER>
 struct Entries {
   int id[PER];
@@ -129,7 +133,6 @@ struct Entries {
         if (v >= 0 && v < end) {
           id[i] = v;
           x[i] = teacher_value(a, row * a.ld_teacher + e);
-          if (a.kind != SATK_TEACHER_LOGITS && x[i] < 0.f) x[i] = 0.f;
         }
       }
     }

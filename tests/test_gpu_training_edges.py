@@ -163,3 +163,30 @@ def test_weights_of_any_size_in_16_bits():
     ids, x = entries(g, 3, 700, 40, "weights")
     for dtype, size in ((BF16, 1e-39), (BF16, 3e38), (F16, 1e-6), (F16, 60000.0)):
         check(logits, ids, (x * size).to(dtype), "weights")
+
+
+@pytest.mark.parametrize("scope", ["row", "listed"])
+@pytest.mark.parametrize("kind", ["logits", "weights", "probs"])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_teacher_values_that_are_not_finite(kind, scope, value):
+    """One among a row's entries makes its loss, and the gradient of its entries, NaN;
+    one that does not count, and other rows, see nothing of it."""
+    g = gen(5)
+    for cols, k, again in ((900, 30, False), (3000, 700, True)):
+        logits = student(g, 5, cols, F32)
+        ids, x = entries(g, 5, cols, k, kind, holes=False)
+        if again:
+            ids[:, 7] = ids[:, 8]  # a column named twice
+        ids[:, 3] = -1
+        one = torch.ones(1, device=DEV)
+        how = dict(kind=kind, scope=scope)
+        clean = satk.distill_loss(logits, ids, x, **how)
+        grad = satk.distill_grad(logits, ids, x, clean[1], one, **how)
+        x[1, 8] = value
+        x[2, 3] = value
+        loss, lse = satk.distill_loss(logits, ids, x, **how)
+        got = satk.distill_grad(logits, ids, x, lse, one, **how)
+        assert torch.isnan(loss[1]) and torch.equal(lse, clean[1])
+        assert torch.isnan(got[1][ids[1][ids[1] >= 0].long()]).all()
+        keep = [0, 2, 3, 4]
+        assert torch.equal(loss[keep], clean[0][keep]) and torch.equal(got[keep], grad[keep])
