@@ -179,34 +179,50 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
           mbar_wait(bar(sm.s_full[b]), (done >> 1) & 1, dead);
           __syncwarp();
           tc_fence_after();
-          float2 sum[4] = {};
+          float2 sum[4];
+          auto add_up = [&](auto careful) {
 #pragma unroll
-          for (int j = 0; j < kHeads / 32; ++j) {
-            if (32 * j >= m.heads) break;
-            uint32_t s[32];
-            const uint32_t at = tmem + b * buffer + 32 * j + lanes;
-            if (32 * j + 32 <= m.heads) {
-              tmem_ld_pairs(s, 0, at);
-              tmem_ld_pairs(s, 16, at + (16u << 16));
-            } else {
-              tmem_ld_pairs_half(s, 0, at);
-              tmem_ld_pairs_half(s, 16, at + (16u << 16));
+            for (int r = 0; r < 4; ++r) sum[r] = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int x = 8; x < 16; ++x) s[x] = s[16 + x] = 0;
+            for (int j = 0; j < kHeads / 32; ++j) {
+              if (32 * j >= m.heads) break;
+              uint32_t s[32];
+              const uint32_t at = tmem + b * buffer + 32 * j + lanes;
+              if (32 * j + 32 <= m.heads) {
+                tmem_ld_pairs(s, 0, at);
+                tmem_ld_pairs(s, 16, at + (16u << 16));
+              } else {
+                tmem_ld_pairs_half(s, 0, at);
+                tmem_ld_pairs_half(s, 16, at + (16u << 16));
+#pragma unroll
+                for (int x = 8; x < 16; ++x) s[x] = s[16 + x] = 0;
+              }
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                const float2 l = less[4 * j + (x >> 1 & 3)];
+                float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
+                                      scale2, l);
+                asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as head_weight)
+                asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.y));
+                e.x = exp2_fast(e.x);
+                e.y = exp2_fast(e.y);
+                if (careful.value != 0) {
+                  if (l.x == -INFINITY) e.x = 0.f;
+                  if (l.y == -INFINITY) e.y = 0.f;
+                }
+                const int r = (x >> 3) * 2 + (x & 1);
+                sum[r] = __fadd2_rn(sum[r], e);
+              }
             }
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
-                                    scale2, less[4 * j + (x >> 1 & 3)]);
-              asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as head_weight)
-              asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.y));
-              e.x = exp2_fast(e.x);
-              e.y = exp2_fast(e.y);
-              const int r = (x >> 3) * 2 + (x & 1);
-              sum[r] = __fadd2_rn(sum[r], e);
-            }
-          }
+          };
+          // A head that adds nothing has -inf for -lse, and so for every exponent but that
+          // of a score that is NaN or infinite: where a NaN comes out, once more with a look
+          // at each head.
+          add_up(Const<0>());
+          const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+          const float check = all.x + all.y;  // (weights are at most 1: no infinity among them)
+          if (__any_sync(~0u, check != check)) add_up(Const<1>());
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sm.s_empty[b]));

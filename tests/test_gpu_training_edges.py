@@ -190,3 +190,43 @@ def test_teacher_values_that_are_not_finite(kind, scope, value):
         assert torch.isnan(got[1][ids[1][ids[1] >= 0].long()]).all()
         keep = [0, 2, 3, 4]
         assert torch.equal(loss[keep], clean[0][keep]) and torch.equal(got[keep], grad[keep])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("H,D", [(5, 96), (16, 64), (17, 544), (130, 192), (5, 35), (33, 17)])
+def test_heads_that_saw_nothing_add_nothing(dtype, H, D):
+    """A head whose lse is -inf adds 0 whatever its queries and the rows hold, and
+    what fills a tile's heads up adds nothing to rows that are not finite: those have
+    the weights that their scores, infinities too, have."""
+    g = gen(6)
+    q = torch.randn(3, H, D, generator=g, device=DEV).to(dtype)
+    q = torch.where(q == 0, 1.0, q)
+    cache = torch.randn(300, D, generator=g, device=DEV).to(dtype)
+    rows = torch.randint(-1, 300, (3, 140), generator=g, device=DEV).int()
+    rows = torch.where((rows == 7) | (rows == 9), 8, rows)
+    lse = torch.randn(3, H, generator=g, device=DEV) + 4
+    lse[0, 1:3] = -math.inf
+    lse[2] = -math.inf
+    call = lambda: satk.latent_rows_weights(q, cache, rows, lse, scale=0.2)  # noqa: E731
+    clean = call()
+    # queries of heads that saw nothing
+    keep = q.clone()
+    q[0, 1, 0], q[0, 2, 3] = math.nan, math.inf
+    q[2, :, 1] = math.nan
+    assert torch.equal(call(), clean) and (clean[2] == 0).all()
+    q = keep
+    # rows with one infinity: a weight of 1 or 0 a head
+    cache[7, 2], cache[9, 4] = math.inf, -math.inf
+    rows[:, 50], rows[:, 139] = 7, 9
+    got = call()
+    live = ~torch.isneginf(lse)
+    for at, col, sign in ((50, 2, 1), (139, 4, -1)):
+        want = (live & (q[:, :, col].float() * sign > 0)).double().sum(1) / H
+        assert ((got[:, at].double() - want).abs() <= want * 2.0**-22).all()
+    others = [j for j in range(140) if j not in (50, 139)]
+    assert torch.equal(got[:, others], clean[:, others])
+    # rows with a NaN: of every head that saw something
+    cache[7, 2] = math.nan
+    got = call()
+    assert torch.isnan(got[:2, 50]).all() and got[2, 50] == 0
+    assert torch.equal(got[:, others], clean[:, others])
