@@ -375,7 +375,9 @@ int satk_distill_loss(const void *logits, int dtype, int64_t rows, int64_t cols,
  * grad     : [rows, ld_grad] of `dtype`; columns [0, cols) are written, those
  *            that are not visible with zeros.  It may be `logits` itself (with
  *            one stride for both); any other overlap is not supported.
- * One rounding to `dtype`; the same bits every time.
+ * One rounding to `dtype`; the same bits every time.  A share q_v is at most 1, and
+ * relies on lse: that has 32 bits, so the share may be off by |lse| 2**-24 of itself
+ * beside its own roundings (at |lse| beyond 2**20 it says no more than that).
  * Errors   : as satk_distill_loss; also SATK_EINVAL for NULL lse/dloss/grad,
  *            dloss_step not 0 or 1, ld_grad < cols, or grad = logits with
  *            another stride; SATK_EUNSUPPORTED when rows times the row's
@@ -637,8 +639,9 @@ int satk_latent_merge(const void *parts, int dtype, int32_t W, int64_t T,
  * out    : float [T, ld_out], columns [0, k): 0 for an entry that is skipped
  *          (negative, past the token's count, or outside the cache, which raises
  *          SATK_STATUS_BAD_ROW).  Columns [k, ld_out) are never written.
- * Sums in 32 bits; a head's weight is at most 1.  A row that is not finite
- * reaches its own entries only.
+ * Sums in 32 bits; a head's weight is at most 1 and relies on lse: that has 32 bits, so
+ * the weight may be off by |lse| 2**-24 of itself beside its own roundings.  A row that
+ * is not finite reaches its own entries only.
  * Errors : SATK_EINVAL for NULL q/cache/rows/lse/out, T < 0, T >= 2**31, H < 1,
  *          D < 1, k < 1, cache_rows < 0, a stride below its extent (ld_q_t,
  *          ld_q_h, ld_cache, ld_rows, ld_out; not used at an extent of one), a

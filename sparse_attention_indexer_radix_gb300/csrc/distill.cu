@@ -247,10 +247,11 @@ __global__ void __launch_bounds__(kDistillThreads) distill_grad_kernel(DistillAr
   E *out = static_cast<E *>(a.grad) + t * a.ld_grad;
   const int end = row_end(a, t);
   const float g = a.dloss[t * a.dloss_step] * a.inv_tau;
-  const float less = -a.lse_in[t] * kLog2e;
-  // The student's share of a score; at most 1, also where scores are so large that
+  const float less = -a.lse_in[t];
+  // The student's share of a score: the difference to lse first, so that only its own
+  // size is rounded on the way to log2; at most 1, also where scores are so large that
   // lse has lost the digits behind the point.
-  auto share = [&](float s) { return exp2_fast(min_or_nan(fmaf(s, a.c, less), 0.f)); };
+  auto share = [&](float s) { return exp2_fast(min_or_nan(fmaf(s, a.inv_tau, less), 0.f) * kLog2e); };
   Entries<PER> in;
   in.load(a, t, end);
   const int words = (e - b + 31) / 32;

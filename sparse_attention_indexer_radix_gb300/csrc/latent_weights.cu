@@ -18,7 +18,7 @@ extern "C" int satk_latent_rows_weights(const void *q, int dtype, int64_t T, int
   if (H > 1024 || D > SATK_LATENT_MAX + SATK_LATENT_TAIL_MAX) return SATK_EUNSUPPORTED;
   if (T == 0) return SATK_OK;
   const WeightsArgs a{q,    static_cast<int>(T), H, D,      ld_q_t,         ld_q_h, cache, cache_rows,
-                      ld_cache, rows,            ld_rows, k, counts, scale * kLog2e, lse,    out,
+                      ld_cache, rows,            ld_rows, k, counts, scale, lse,    out,
                       ld_out,   status};
   if (latent_weights_mma_fits(a)) return latent_weights_mma(a, dtype, as_stream(stream));
   return latent_weights_warp(a, dtype, as_stream(stream));

@@ -15,7 +15,7 @@ struct WeightsArgs {
   int64_t ld_rows;
   int k;
   const int32_t *counts;
-  float scale_log2;
+  float scale;
   const float *lse;
   float *out;
   int64_t ld_out;
@@ -38,13 +38,13 @@ __device__ __forceinline__ int entry_count(const WeightsArgs &a, int t) {
   return a.counts == nullptr ? a.k : min(max(a.counts[t], 0), a.k);
 }
 
-// One head's weight from its score and its normaliser, both in log2: at most 1
-// (scores of a size at which lse has lost the digits behind the point), nothing
-// for a head that saw no key.
-__device__ __forceinline__ float head_weight(float raw, float scale_log2, float lse_log2) {
+// One head's weight from its score and its normaliser: the difference first, so that
+// only its own size is rounded on the way to log2, then at most 1 (scores of a size at
+// which lse has lost the digits behind the point); nothing for a head that saw no key.
+__device__ __forceinline__ float head_weight(float raw, float scale, float lse) {
   float x;
-  asm("min.NaN.f32 %0, %1, 0f00000000;" : "=f"(x) : "f"(fmaf(raw, scale_log2, -lse_log2)));
-  return lse_log2 == -INFINITY ? 0.f : exp2_fast(x);
+  asm("min.NaN.f32 %0, %1, 0f00000000;" : "=f"(x) : "f"(fmaf(raw, scale, -lse)));
+  return lse == -INFINITY ? 0.f : exp2_fast(x * kLog2e);
 }
 
 // The tensor-core kernel: whether it takes this call, and the call.

@@ -143,21 +143,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
     // --------------------------------------------------------------------- sums
     // A thread has two of every eight heads of four entries.
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+    const float2 scale2 = make_float2(a.scale, a.scale), log2e2 = make_float2(kLog2e, kLog2e);
     const float share = 1.f / a.H;
     int done = 0;  // tiles so far
     for (Units w(m); w.more(); w.next()) {
       const int n = w.tiles();
       float *out = a.out + w.t * a.ld_out;
       for (int c = 0; n > 0 && c < m.chunks; ++c) {
-        // -lse in log2; a head that saw nothing, or that is not there, adds nothing
+        // -lse; a head that saw nothing, or that is not there, adds nothing
         float2 less[kHeads / 8];
 #pragma unroll
         for (int j = 0; j < kHeads / 8; ++j) {
           const int h = c * m.heads + 8 * j + 2 * (lane & 3);
           const float *lse = a.lse + static_cast<int64_t>(w.t) * a.H + h;
-          const float x = 8 * j < m.heads && h < a.H ? lse[0] * kLog2e : -INFINITY;
-          const float y = 8 * j < m.heads && h + 1 < a.H ? lse[1] * kLog2e : -INFINITY;
+          const float x = 8 * j < m.heads && h < a.H ? lse[0] : -INFINITY;
+          const float y = 8 * j < m.heads && h + 1 < a.H ? lse[1] : -INFINITY;
           less[j] = make_float2(x == -INFINITY ? x : -x, y == -INFINITY ? y : -y);
         }
         // whether the next tile's entries count
@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
                                       scale2, l);
                 asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as head_weight)
                 asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.y));
+                e = __fmul2_rn(e, log2e2);
                 e.x = exp2_fast(e.x);
                 e.y = exp2_fast(e.y);
                 if (careful.value != 0) {

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kWarps * 32) latent_weights_warp_kernel(Weight
       }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      sum += head_weight(s, a.scale_log2, a.lse[static_cast<int64_t>(t) * a.H + h] * kLog2e);
+      sum += head_weight(s, a.scale, a.lse[static_cast<int64_t>(t) * a.H + h]);
     }
   }
   if (lane == 0) a.out[t * a.ld_out + j] = sum / a.H;

@@ -230,3 +230,54 @@ def test_heads_that_saw_nothing_add_nothing(dtype, H, D):
     got = call()
     assert torch.isnan(got[:2, 50]).all() and got[2, 50] == 0
     assert torch.equal(got[:, others], clean[:, others])
+
+
+@pytest.mark.parametrize("offset", [0.0, 300.0, -5000.0])
+@pytest.mark.parametrize("scope", ["row", "listed"])
+@pytest.mark.parametrize("tau", [1.0, 0.25, 0.7])
+def test_shares_of_far_scores(offset, scope, tau):
+    """The student's share is off by the roundings of s / tau - lse alone, not of a
+    product with lse: 2^-24 of the difference d and, with a 1 / tau that is rounded,
+    of s / tau; d log2(e) 3 more of |d| 2^-24, exp2 2^-22 (and 2^-24 for its use), the
+    products with the row's factors and the sum with p 4 2^-24 of what they take."""
+    g = gen(7)
+    logits = student(g, 4, 3001, F32) + offset
+    ids, x = entries(g, 4, 3001, 40, "weights", holes=False)
+    how = dict(kind="weights", scope=scope, temperature=tau)
+    _, lse = satk.distill_loss(logits, ids, x, **how)
+    one = torch.ones(1, device=DEV)
+    got = satk.distill_grad(logits, ids, x, lse, one, **how).double()
+    at = ids.long()
+    z = logits.double() / tau
+    d = z - lse.double()[:, None]
+    q = torch.exp(torch.clamp(d, max=0.0))
+    p = (x.double() / x.double().sum(1, keepdim=True))
+    listed = torch.zeros_like(q).scatter_(1, at, 1.0)
+    if scope == "listed":
+        q = q * listed
+    share = torch.zeros_like(q).scatter_add_(1, at, p)
+    inexact = 0.0 if tau in (1.0, 0.25) else 1.0
+    tol = q * (d.abs() * 4 + z.abs() * inexact + 4 + 1 + 4) + share * (40 + 8)
+    off = (got - (q - share) / tau).abs() - tol * 2.0**-24 / tau
+    assert off.max().item() <= 1e-30
+
+
+@pytest.mark.parametrize("H,D", [(16, 64), (64, 128), (150, 64), (3, 17)])
+@pytest.mark.parametrize("offset", [0, 400, -3000])
+def test_weights_of_far_scores(H, D, offset):
+    """Products that are exact in 32 bits, so that only scale s - lse (2^-24 of the
+    difference d), its product with log2(e) (3 |d| 2^-24), exp2 (2^-22 and 2^-24) and the
+    sum over the heads (H + 2 roundings) are not."""
+    g = gen(9)
+    q = torch.randint(-4, 5, (3, H, D), generator=g, device=DEV).to(BF16)
+    cache = torch.randint(-4, 5, (200, D), generator=g, device=DEV).to(BF16)
+    q[..., 0], cache[:, 0] = 8.0, offset / 2.0  # (a share of the scores that all have)
+    rows = torch.randint(0, 200, (3, 130), generator=g, device=DEV).int()
+    keys = cache[rows.long()].double()
+    x = torch.einsum("thd,tkd->thk", q.double(), keys) * 0.25
+    lse = torch.logsumexp(x, 2).float()
+    got = satk.latent_rows_weights(q, cache, rows, lse, scale=0.25).double()
+    d = torch.clamp(x - lse.double()[..., None], max=0.0)
+    w = torch.exp(d)
+    tol = (w * (d.abs() * 4 + 5 + H + 2)).mean(1) * 2.0**-24
+    assert ((got - w.mean(1)).abs() <= tol + 1e-37).all()
