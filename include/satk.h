@@ -683,10 +683,10 @@ size_t satk_latent_expanded_grad_workspace_bytes(int64_t T, int64_t S, int32_t R
  *            written whole, zeros for rows that nothing sees or that no request
  *            has.  They overlap nothing else.
  * Sums and the rows' statistics are in 32 bits; P and dS are rounded to `dtype`
- * before their products (in calls of at most 16 tokens a request on average, to two
- * numbers of `dtype` where products are few), the gradients once at the end.  (With
+ * before their products (in requests of at most 64 tokens, to two numbers of `dtype`,
+ * the second what the first one's rounding left), the gradients once at the end.  (With
  * SATK_F16 a dS beyond 65504 is infinite, one below 2**-25 nothing: scale dout
- * accordingly.)
+ * accordingly.)  A request's bits do not depend on what else is in the call.
  * A weight is at most 1, and relies on lse: it is off by about |lse| 2**-23 of
  * itself.  The same bits every time: no sum depends on the order of arrival.
  * What a token does not see does not reach its gradient, nor does a token that

@@ -9,8 +9,8 @@
 // The keys are the M side throughout, so P and dS need no exchange between
 // threads: rounded to the inputs' type (as the forward pass rounds P: off by half
 // a step of themselves), they replace S in tensor memory and are the A operand of
-// the second products; with few tokens a request, what the rounding left is a second
-// operand for keys that one tile of tokens sees (see kFewTokens).  dV and dK stay in tensor memory for the whole call.  S has
+// the second products; for requests of few tokens, what the rounding left is a second
+// operand (see kFewTokens).  dV and dK stay in tensor memory for the whole call.  S has
 // two buffers where they fit (two of 64 columns, dP 64, dV 128, dK 192: 512), so
 // that the scores of the next tile are computed while P and dS of this one are.
 //
@@ -32,6 +32,7 @@ namespace grad_keys {
 
 constexpr int kTokens = kGradTokens;  // of a tile
 static_assert(kTokens == kBoxRows && kTile == 2 * kBoxRows, "boxes");
+static_assert(kFewTokens <= kTokens, "requests of few tokens have one tile of them");
 constexpr int kKeyPanel = kTile * 128, kTokenPanel = kTokens * 128;  // bytes
 constexpr int kMaxStages = 4;
 
@@ -78,8 +79,119 @@ struct LiveTiles {
   }
 };
 
-// CTA `block` of `blocks`.
+// P and dS of n tiles, by the elementwise warps.  A warp has 32 keys (its TMEM lanes)
+// and half of each tile's tokens; a thread two of every eight tokens of four keys, so
+// that it needs few tokens' numbers: a load that all lanes share costs shared memory
+// as much as any other, and the products need all that it delivers (one key and 32
+// tokens a thread: 451 cycles of loads a tile).
 template <class E, bool FEW>
+__device__ __forceinline__ void weigh(const ExpandedArgs &f, Small &sm, Tokens *tokens, uint32_t tmem, uint32_t dp_at,
+                                      int key0, int n, int buffers, int stages, int half, uint32_t lanes) {
+  const float2 scale2 = make_float2(f.scale_log2, f.scale_log2);
+  volatile int *dead = &sm.dead;
+  auto bar = [&](uint64_t &b) { return smem_addr(&b); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int stage = 0, around = 0;
+  for (int i = 0; i < n; ++i) {
+    const int buffer = buffers == 2 ? i & 1 : 0;
+    const uint32_t s_at = tmem + buffer * kTokens + half * 32 + lanes;
+    const Tokens &tk = tokens[stage];
+    uint32_t s[32], dp[32], p16[16], d16[16];
+    mbar_wait(bar(sm.tokens[stage]), around & 1, dead);
+    const bool masked = sm.least[stage][half] < key0 + kTile;
+    float2 less[4], delta[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      less[j] = *reinterpret_cast<const float2 *>(tk.less + half * 32 + 8 * j + 2 * (lane & 3));
+      delta[j] = *reinterpret_cast<const float2 *>(tk.delta + half * 32 + 8 * j + 2 * (lane & 3));
+    }
+    mbar_wait(bar(sm.s_full[buffer]), (buffers == 2 ? i >> 1 : i) & 1, dead);
+    __syncwarp();
+    tc_fence_after();
+    tmem_ld_pairs(s, 0, s_at);
+    tmem_ld_pairs(s, 16, s_at + (16u << 16));
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
+                            scale2, less[x >> 1 & 3]);
+      asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as grad_weight)
+      asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.y));
+      s[2 * x] = __float_as_uint(exp2_fast(e.x));
+      s[2 * x + 1] = __float_as_uint(exp2_fast(e.y));
+    }
+    mbar_wait(bar(sm.dp_full), i & 1, dead);
+    __syncwarp();
+    tc_fence_after();
+    tmem_ld_pairs(dp, 0, dp_at + half * 32 + lanes);
+    tmem_ld_pairs(dp, 16, dp_at + half * 32 + lanes + (16u << 16));
+    tmem_wait_ld();
+    tc_fence_before();
+    mbar_arrive(bar(sm.dp_read));
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const float2 d = __fmul2_rn(
+          make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
+          __fadd2_rn(make_float2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])),
+                     delta[x >> 1 & 3]));
+      dp[2 * x] = __float_as_uint(d.x);
+      dp[2 * x + 1] = __float_as_uint(d.y);
+    }
+    if (masked) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const int2 end = *reinterpret_cast<const int2 *>(tk.end + half * 32 + 8 * (x >> 1 & 3) + 2 * (lane & 3));
+        const int key = key0 + (warp & 3) * 32 + (x >> 3) * 16 + (x & 1) * 8 + (lane >> 2);
+        if (key >= end.x) s[2 * x] = dp[2 * x] = 0;
+        if (key >= end.y) s[2 * x + 1] = dp[2 * x + 1] = 0;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      p16[x] = pack16<E>(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+      d16[x] = pack16<E>(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]));
+    }
+    // This half's 32 columns of scores become 16 of P and 16 of dS.
+    tmem_st_packed(s_at, p16, 0);
+    tmem_st_packed(s_at + (16u << 16), p16, 8);
+    tmem_st_packed(s_at + 16, d16, 0);
+    tmem_st_packed(s_at + 16 + (16u << 16), d16, 8);
+    if (FEW) {  // what their rounding left: in the place of dP
+      const uint32_t rest = dp_at + half * 32 + lanes;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        p16[x] = pack16_rest<E>(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]), p16[x]);
+        d16[x] = pack16_rest<E>(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]), d16[x]);
+      }
+      tmem_st_packed(rest, p16, 0);
+      tmem_st_packed(rest + (16u << 16), p16, 8);
+      tmem_st_packed(rest + 16, d16, 0);
+      tmem_st_packed(rest + 16 + (16u << 16), d16, 8);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(bar(sm.ready[i & 1]));
+    if (++stage == stages) stage = 0, ++around;
+  }
+}
+
+// The same of the one tile of a request of few tokens.  Not inline: in one piece with
+// the other's loop it cost that (packed prompts 128 us for 123).  (The debug build is
+// relocatable: there a function of its own knows nothing of the kernel's registers.)
+#ifdef SATK_DEBUG
+#define SATK_APART __forceinline__
+#else
+#define SATK_APART __noinline__
+#endif
+template <class E>
+__device__ SATK_APART void weigh_few(const ExpandedArgs &f, Small &sm, Tokens *tokens, uint32_t tmem, uint32_t dp_at,
+                                       int key0, int buffers, int stages, int half, uint32_t lanes) {
+  weigh<E, true>(f, sm, tokens, tmem, dp_at, key0, 1, buffers, stages, half, lanes);
+}
+#undef SATK_APART
+
+// CTA `block` of `blocks`.
+template <class E>
 __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &shape, const Plan &m, const GradMaps &maps,
                                     unsigned char *smem, unsigned block, unsigned blocks) {
   const ExpandedArgs &f = a.f;
@@ -175,106 +287,18 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   const int n = sm.live, buffers = m.score_buffers;
-  const bool few = FEW && n == 1;
+  const bool few = n > 0 && n_tokens <= kFewTokens;
   const uint32_t dp_at = tmem + buffers * kTokens, dv_at = dp_at + kTokens;
   const uint32_t dk_at = dv_at + ((f.dv + 31) & ~31);
 
   if (warp < 8) {
     // ------------------------------------------------------- P and dS, results
-    // A warp has 32 keys (its TMEM lanes) and half of each tile's tokens; a thread
-    // two of every eight tokens of four keys, so that it needs few tokens' numbers: a
-    // load that all lanes share costs shared memory as much as any other, and the
-    // products need all that it delivers (one key and 32 tokens a thread: 451 cycles
-    // of loads a tile).
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const float2 scale2 = make_float2(f.scale_log2, f.scale_log2);
-    auto weigh = [&](auto rest_too) {
-      int stage = 0, around = 0;
-      for (int i = 0; i < (rest_too.value != 0 ? 1 : n); ++i) {
-        const int buffer = buffers == 2 ? i & 1 : 0;
-        const uint32_t s_at = tmem + buffer * kTokens + half * 32 + lanes;
-        const Tokens &tk = tokens[stage];
-        uint32_t s[32], dp[32], p16[16], d16[16];
-        mbar_wait(bar(sm.tokens[stage]), around & 1, dead);
-        const bool masked = sm.least[stage][half] < key0 + kTile;
-        float2 less[4], delta[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          less[j] = *reinterpret_cast<const float2 *>(tk.less + half * 32 + 8 * j + 2 * (lane & 3));
-          delta[j] = *reinterpret_cast<const float2 *>(tk.delta + half * 32 + 8 * j + 2 * (lane & 3));
-        }
-        mbar_wait(bar(sm.s_full[buffer]), (buffers == 2 ? i >> 1 : i) & 1, dead);
-        __syncwarp();
-        tc_fence_after();
-        tmem_ld_pairs(s, 0, s_at);
-        tmem_ld_pairs(s, 16, s_at + (16u << 16));
-        tmem_wait_ld();
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
-                                scale2, less[x >> 1 & 3]);
-          asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.x));  // (as grad_weight)
-          asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(e.y));
-          s[2 * x] = __float_as_uint(exp2_fast(e.x));
-          s[2 * x + 1] = __float_as_uint(exp2_fast(e.y));
-        }
-        mbar_wait(bar(sm.dp_full), i & 1, dead);
-        __syncwarp();
-        tc_fence_after();
-        tmem_ld_pairs(dp, 0, dp_at + half * 32 + lanes);
-        tmem_ld_pairs(dp, 16, dp_at + half * 32 + lanes + (16u << 16));
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(bar(sm.dp_read));
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const float2 d = __fmul2_rn(
-              make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
-              __fadd2_rn(make_float2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])),
-                         delta[x >> 1 & 3]));
-          dp[2 * x] = __float_as_uint(d.x);
-          dp[2 * x + 1] = __float_as_uint(d.y);
-        }
-        if (masked) {
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const int2 end = *reinterpret_cast<const int2 *>(tk.end + half * 32 + 8 * (x >> 1 & 3) + 2 * (lane & 3));
-            const int key = key0 + (warp & 3) * 32 + (x >> 3) * 16 + (x & 1) * 8 + (lane >> 2);
-            if (key >= end.x) s[2 * x] = dp[2 * x] = 0;
-            if (key >= end.y) s[2 * x + 1] = dp[2 * x + 1] = 0;
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          p16[x] = pack16<E>(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
-          d16[x] = pack16<E>(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]));
-        }
-        // This half's 32 columns of scores become 16 of P and 16 of dS.
-        tmem_st_packed(s_at, p16, 0);
-        tmem_st_packed(s_at + (16u << 16), p16, 8);
-        tmem_st_packed(s_at + 16, d16, 0);
-        tmem_st_packed(s_at + 16 + (16u << 16), d16, 8);
-        if (rest_too.value != 0) {  // what their rounding left: in the place of dP
-          const uint32_t rest = dp_at + half * 32 + lanes;
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            p16[x] = pack16_rest<E>(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]), p16[x]);
-            d16[x] = pack16_rest<E>(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]), d16[x]);
-          }
-          tmem_st_packed(rest, p16, 0);
-          tmem_st_packed(rest + (16u << 16), p16, 8);
-          tmem_st_packed(rest + 16, d16, 0);
-          tmem_st_packed(rest + 16 + (16u << 16), d16, 8);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(sm.ready[i & 1]));
-        if (++stage == stages) stage = 0, ++around;
-      }
-    };
-    if (few) weigh(Const<FEW>());
-    else weigh(Const<0>());
+    if (few)
+      weigh_few<E>(f, sm, tokens, tmem, dp_at, key0, buffers, stages, half, lanes);
+    else
+      weigh<E, false>(f, sm, tokens, tmem, dp_at, key0, n, buffers, stages, half, lanes);
     if (n > 0) {
       mbar_wait(bar(sm.done), 0, dead);
       __syncwarp();
@@ -330,7 +354,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       const uint32_t ready = bar(sm.ready[0]), gap = shape.gap;
       const bool two = shape.one_product == 0;
       if (n > 0) mbar_wait(bar(sm.own), 0, dead);
-      with_shape<!FEW>(panels, v_panels, shape.full != 0, [&](auto np, auto vp, auto all) {
+      with_shape(panels, v_panels, shape.full != 0, [&](auto np, auto vp, auto all) {
         // Tile i's place in the ring: its stage, the low words' distance, the phase.
         struct At {
           uint32_t stage = 0, low = 0, phase = 0;
@@ -355,7 +379,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
           tc_commit(dp_full);
         };
         // dV and dK of tile i from the buffer that holds its P and dS
-        auto gradients = [&](uint32_t i, uint32_t buffer, At x, auto rest) {
+        auto gradients = [&](uint32_t i, uint32_t buffer, At x) {
           mbar_wait(looked + 8 * x.stage, x.phase, dead);
           mbar_wait(ready + 8 * (i & 1), i >> 1 & 1, dead);
           tc_fence_after();
@@ -378,36 +402,43 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
             }
           };
           from(tmem + buffer * kTokens, i > 0);
-          if (rest.value != 0) from(dp_at, true);
           tc_commit(empty + 8 * x.stage);
         };
         if (n == 0) return;
         At at;
         scores(0, at);
         dps(at);
-        if (few) {
-          gradients(0, 0, at, Const<FEW>());
-        } else if (buffers == 2) {
+        if (buffers == 2) {
           for (int i = 0; i + 1 < n; ++i) {
             const At next = following(at);
             scores(i + 1 & 1, next);
             mbar_wait(dp_read, i & 1, dead);
             tc_fence_after();
             dps(next);
-            gradients(i, i & 1, at, Const<0>());
+            gradients(i, i & 1, at);
             at = next;
           }
-          gradients(n - 1, n - 1 & 1, at, Const<0>());
+          gradients(n - 1, n - 1 & 1, at);
         } else {
           for (int i = 0; i + 1 < n; ++i) {
-            gradients(i, 0, at, Const<0>());
+            gradients(i, 0, at);
             at = following(at);
             scores(0, at);
             dps(at);
           }
-          gradients(n - 1, 0, at, Const<0>());
+          gradients(n - 1, 0, at);
         }
       });
+      if (few) {  // one tile, in the ring's first stage: what the roundings left
+        const uint32_t q = rows_low, o = q + do_step, d = dk_at + f.dn, t = q + tail_step;
+#pragma unroll
+        for (uint32_t x = 0; x < 4; ++x) {
+          const uint32_t p_at = dp_at + (x >> 1) * 32 + (x & 1) * 8;
+          mma_ts_low(dv_at, p_at, o + 128 * x, d_v, true);
+          mma_ts_low(dk_at, p_at + 16, q + 128 * x, d_k, true);
+          mma_ts_low_if(two, d, p_at + 16, t + 128 * x, d_t);
+        }
+      }
       tc_commit(bar(sm.done));
       tc_commit(bar(sm.issued));
       mbar_drain(bar(sm.issued), 0);

@@ -1,9 +1,40 @@
 // expanded_grad_mma.cu -- the backward pass of the expanded attention on the tensor
 // cores: what it takes, its shared memory and tensor maps, its launch.
-#include "expanded_grad_launch.cuh"
+//
+// One launch for both kernels, so that the CTAs of one fill the SMs that the other
+// leaves idle at its end.  Those of the queries come first: each takes about as long as
+// the longest of the keys', whose last ones, with few tokens, come last.
+#include "expanded_grad_keys.cuh"
+#include "expanded_grad_tokens.cuh"
 
 namespace satk {
 namespace {
+
+struct GradMma {
+  ExpandedGradArgs a;
+  GradShape s;
+  GradMaps maps;
+  grad_keys::Plan keys;
+  grad_tokens::Plan tokens;
+  unsigned token_blocks, key_blocks;
+};
+
+template <class E>
+__global__ void __launch_bounds__(kGradThreads, 1) expanded_grad_mma_kernel(const __grid_constant__ GradMma m) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  wait_for_previous_kernel();  // the tokens' statistics
+  let_next_kernel_start();
+  if (blockIdx.x < m.token_blocks)
+    grad_tokens::run<E>(m.a, m.s, m.tokens, m.maps, smem, blockIdx.x, m.token_blocks);
+  else
+    grad_keys::run<E>(m.a, m.s, m.keys, m.maps, smem, blockIdx.x - m.token_blocks, m.key_blocks);
+}
+
+template <class E>
+int launch(const GradMma &m, int smem, cudaStream_t stream) {
+  if (!allow_smem(expanded_grad_mma_kernel<E>, smem, kSmemLimit)) return SATK_ECUDA;
+  return launch_early(expanded_grad_mma_kernel<E>, m.token_blocks + m.key_blocks, kGradThreads, smem, stream, m);
+}
 
 GradShape shape_of(const ExpandedGradArgs &a) {
   const ExpandedArgs &f = a.f;
@@ -66,10 +97,7 @@ int expanded_grad_mma(const ExpandedGradArgs &a, int dtype, cudaStream_t stream)
   m.token_blocks = static_cast<unsigned>(tokens);
   m.key_blocks = static_cast<unsigned>(keys);
   const int smem = keys_smem > tokens_smem ? keys_smem : tokens_smem;
-  if (static_cast<int64_t>(a.f.R) * kFewTokens >= a.f.T)
-    return launch_grad_few(m, bf16, smem, stream);
-  return bf16 ? launch_grad_mma<__nv_bfloat16, false>(m, smem, stream)
-              : launch_grad_mma<__half, false>(m, smem, stream);
+  return bf16 ? launch<__nv_bfloat16>(m, smem, stream) : launch<__half>(m, smem, stream);
 }
 
 }  // namespace satk

@@ -147,13 +147,13 @@ __device__ __forceinline__ void rows_outside(const int32_t *starts, int R, int n
 // P and dS are operands of 16 bits: each is off by up to half a step of itself.  Over
 // many tokens these errors average out, the result's own rounding is as large; over
 // two to eight tokens they do not always (an error of up to 1.8 times that of the
-// formula with 32-bit P and dS where 1.4 is usual, in 10 of 240 gradients).  Calls of
-// up to 16 tokens a request on average take a second operand that holds what the
-// rounding left (none is above 1.5 then): 4 requests of 5 tokens, 16 heads, take 29 us
-// (one operand: 27), 8 requests of 8 tokens behind 2000 keys 199 us (184).  They have a
-// kernel of their own: in one for all calls, the code that others do not run cost five
-// prompts of 391 tokens 4 us of 44.
-constexpr int kFewTokens = 16;
+// formula with 32-bit P and dS where 1.4 is usual, in 10 of 240 gradients).  Requests of
+// one tile of tokens take a second operand that holds what the rounding left (none is
+// above 1.5 then): 8 requests of 8 tokens behind 2000 keys, 16 heads, take 199 us (one
+// operand: 182).  The request alone decides, so its bits do not depend on what else is
+// in the call; requests of many tokens pay for code that they do not run (five prompts of
+// up to 391 tokens 46 us for 44, packed prompts 122 for 120, a chunk 624 for 622).
+constexpr int kFewTokens = 64;
 
 // Two values rounded to 16 bits, and what the rounding left of them likewise: as two
 // operands they stand for some 16 bits of fraction.
@@ -213,13 +213,12 @@ __device__ __forceinline__ void product_over_columns(uint32_t d, uint32_t a, uin
 template <int N>
 using Const = std::integral_constant<int, N>;
 
-// issue(panels, panels of the values, whether all are full) with constants; without
-// BOTH, full ones are issued as others are (a predicate an MMA).
-template <bool BOTH, class F>
+// issue(panels, panels of the values, whether all are full) with constants.
+template <class F>
 __device__ __forceinline__ void with_shape(int panels, int v_panels, bool full, F issue) {
   auto values = [&](auto np) {
-    if (BOTH && full) {
-      if (v_panels == 1) issue(np, Const<1>(), Const<BOTH>()); else issue(np, Const<2>(), Const<BOTH>());
+    if (full) {
+      if (v_panels == 1) issue(np, Const<1>(), Const<1>()); else issue(np, Const<2>(), Const<1>());
     } else {
       if (v_panels == 1) issue(np, Const<1>(), Const<0>()); else issue(np, Const<2>(), Const<0>());
     }

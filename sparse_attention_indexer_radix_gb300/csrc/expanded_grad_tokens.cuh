@@ -6,8 +6,8 @@
 //   S[token, key] = Q [K | tail]^T         dP[token, key] = dO V^T
 //   dS = exp2(scale S - lse) (dP - delta)  dQ += dS [K | tail]
 // A token is a TMEM lane and a thread.  dS, rounded to the inputs' type, replaces S
-// in tensor memory and is the A operand of the second product; with few tokens a
-// request, what the rounding left is a second operand (see kFewTokens).  Q, and dO
+// in tensor memory and is the A operand of the second product; for requests of few
+// tokens, what the rounding left is a second operand (see kFewTokens).  Q, and dO
 // where there is room too, are A operands in tensor memory as well: with a tile of 64
 // keys a product with both operands in shared memory takes 50 cycles a step of 16
 // columns, one with A in tensor memory 36.  At 192 query/key columns: S 2 x 64, dP
@@ -44,7 +44,7 @@ struct Small {
   uint64_t s_full[2], dp_full, dp_read, ready[2], done, issued;
   int low[8], high[8];
   int odd_key;   // the first key that is not finite
-  int place[4];  // first key, keys, first token, tokens
+  int place[5];  // first key, keys, first token, tokens, tokens of the request
   uint32_t tmem;
   int dead;
 };
@@ -64,7 +64,7 @@ __device__ __forceinline__ void row_inside(uint32_t at, const E *row, int cols, 
 }
 
 // CTA `block` of `blocks`.
-template <class E, bool FEW>
+template <class E>
 __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &shape, const Plan &m, const GradMaps &maps,
                                     unsigned char *smem, unsigned block, unsigned blocks) {
   const ExpandedArgs &f = a.f;
@@ -100,6 +100,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       sm.place[1] = keys.end - keys.begin;
       sm.place[2] = real ? mine.begin + tile * kTile : 0;
       sm.place[3] = real ? min(kTile, n - tile * kTile) : 0;
+      sm.place[4] = n;
     }
   }
   if (threadIdx.x == 0) {
@@ -124,6 +125,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
   __syncthreads();
   const int key0 = sm.place[0], keys = sm.place[1], t0 = sm.place[2], n_tokens = sm.place[3];
   if (n_tokens == 0) return;
+  const bool few = sm.place[4] <= kFewTokens;
 
   // Elementwise threads: this thread's token, what it sees and its numbers.
   const int half = warp >> 2, row = threadIdx.x & 127, t = t0 + row;
@@ -208,7 +210,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       for (int x = 0; x < 16; ++x)
         packed[x] = pack16<E>(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]));
       tmem_st16(s_at, packed);  // the first half of this thread's columns of S
-      if (FEW) {  // what the rounding left: the second half
+      if (few) {  // what the rounding left: the second half
 #pragma unroll
         for (int x = 0; x < 16; ++x)
           packed[x] = pack16_rest<E>(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]), packed[x]);
@@ -257,7 +259,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
       const uint32_t ready = bar(sm.ready[0]), gap = shape.gap;
       const bool two = shape.one_product == 0, q_inside = m.q_inside != 0, do_inside = m.do_inside != 0;
       if (n > 0 && (!q_inside || !do_inside)) mbar_wait(bar(sm.own), 0, dead);
-      with_shape<!FEW>(panels, v_panels, shape.full != 0, [&](auto np, auto vp, auto all) {
+      with_shape(panels, v_panels, shape.full != 0, [&](auto np, auto vp, auto all) {
         // Tile i's place in the ring: its stage, the low words' distance, the phase.
         struct At {
           uint32_t stage = 0, low = 0, phase = 0;
@@ -307,7 +309,7 @@ __device__ __forceinline__ void run(const ExpandedGradArgs &a, const GradShape &
           };
           const uint32_t ds_at = tmem + (i & 1) * kKeys;
           from(ds_at, i > 0);
-          if (FEW) from(ds_at + 16, true);
+          if (few) from(ds_at + 16, true);
           tc_commit(empty + 8 * x.stage);
         };
         if (n == 0) return;

@@ -281,3 +281,52 @@ def test_weights_of_far_scores(H, D, offset):
     w = torch.exp(d)
     tol = (w * (d.abs() * 4 + 5 + H + 2)).mean(1) * 2.0**-24
     assert ((got - w.mean(1)).abs() <= tol + 1e-37).all()
+
+
+SHORT = [1, 5, 8, 16, 33, 64]
+
+
+def beside(long, more=0, dtype=BF16):
+    """Short requests, then `long` tokens in a request of their own and `more`
+    requests of none; inputs that depend on the request alone."""
+    new = SHORT + ([long] if long else []) + [0] * more
+    context = [0, 3, 400, 1100, 64, 0] + ([40] if long else []) + [0] * more
+    parts = [Case(gen(50 + r), dtype, 2, 64, 32, 64, [n], [c], dlse=True)
+             for r, (n, c) in enumerate(zip(new, context)) if n]
+    whole = Case(gen(50), dtype, 2, 64, 32, 64, new, context, dlse=True)
+    for name in ("q", "k", "v", "tail", "dout", "dlse"):
+        setattr(whole, name, torch.cat([getattr(p, name) for p in parts]))
+    return whole, parts
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("long,more", [(1, 0), (65, 0), (700, 0), (4000, 0), (700, 300)])
+def test_a_request_does_not_depend_on_the_others(dtype, long, more):
+    """The bits of short requests, whatever else is in the call, and their exactness:
+    P and dS as two operands each."""
+    c, parts = beside(long, more, dtype)
+    c.forward()
+    got = c.grad()
+    for r, p in enumerate(parts):
+        p.forward()
+        want = p.grad()
+        if r < len(SHORT):
+            close(want, definition(p, roundings=2), f"request {r} alone")
+        t, s = slice(c.ts[r], c.ts[r + 1]), slice(c.ks[r], c.ks[r + 1])
+        for x, y, at in zip(got, want, (t, s, s, s)):
+            assert torch.equal(x[at], y), r
+    if long <= 700:
+        close(got, definition(c), "together")
+
+
+@pytest.mark.parametrize("new,context", [([700], [60]), ([65], [0]), ([64], [200]), ([3], [9])])
+def test_requests_of_no_tokens_change_nothing(new, context):
+    c = Case(gen(8), BF16, 2, 128, 64, 128, new, context)
+    c.forward()
+    want = c.grad()
+    for before, after in ((0, 255), (100, 0), (3, 40)):
+        c.ts = np.concatenate([[0] * before, [0, new[0]], [new[0]] * after])
+        n = new[0] + context[0]
+        c.ks = np.concatenate([[0] * before, [0, n], [n] * after])
+        for x, y in zip(c.grad(), want):
+            assert torch.equal(x, y)
