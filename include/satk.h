@@ -352,7 +352,7 @@ int satk_dcp_emit_rows(const int32_t *ids, int64_t T, int32_t k, int64_t ld_ids,
  *            kind or scope, rows or cols < 0 or >= 2**31, k outside
  *            1..SATK_TOPK_MAX_K, ld_logits < cols, ld_ids < k or ld_teacher < k
  *            (strides are not used with one row), a temperature that is not
- *            positive and finite, or whose inverse is not; SATK_EUNSUPPORTED
+ *            positive and finite, or so small (4.2e-39) that log2(e) over it is not; SATK_EUNSUPPORTED
  *            when the rows' CTAs, up to eight a row, pass 2**31.
  */
 int satk_distill_loss(const void *logits, int dtype, int64_t rows, int64_t cols,

@@ -447,7 +447,7 @@ int checked(DistillArgs &a, const void *logits, int dtype, int64_t rows, int64_t
       scope > SATK_DISTILL_LISTED || !std::isfinite(temperature) || !(temperature > 0.f))
     return SATK_EINVAL;
   const float inv_tau = 1.f / temperature;
-  if (!std::isfinite(inv_tau) || inv_tau == 0.f) return SATK_EINVAL;
+  if (!std::isfinite(inv_tau * kLog2e) || inv_tau == 0.f) return SATK_EINVAL;
   a = DistillArgs{};
   a.logits = logits;
   a.rows = rows;
