@@ -471,7 +471,9 @@ int latent_weights_mma(const WeightsArgs &a, int dtype, cudaStream_t stream) {
   if (!tensor_map_16bit(&m.q, bf16, a.q, a.D, a.H, a.H == 1 ? 1024 : a.ld_q_h, m.heads, a.T,
                         a.T == 1 ? static_cast<int64_t>(a.H == 1 ? 1024 : a.ld_q_h) * a.H : a.ld_q_t))
     return SATK_ECUDA;
-  if (!tensor_map_16bit(&m.rows, bf16, a.cache, a.D, a.cache_rows, a.cache_rows == 1 ? 1024 : a.ld_cache, 1))
+  // (an entry names a row below 2^31; a map has 2^32 at most)
+  const int64_t rows = a.cache_rows > INT32_MAX ? INT32_MAX + 1ll : a.cache_rows;
+  if (!tensor_map_16bit(&m.rows, bf16, a.cache, a.D, rows, rows == 1 ? 1024 : a.ld_cache, 1))
     return SATK_ECUDA;
   if (m.slots >= kGroups * kDepth)
     return bf16 ? launch<__nv_bfloat16, kDepth>(m, smem, stream) : launch<__half, kDepth>(m, smem, stream);

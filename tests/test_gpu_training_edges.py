@@ -330,3 +330,21 @@ def test_requests_of_no_tokens_change_nothing(new, context):
         c.ks = np.concatenate([[0] * before, [0, n], [n] * after])
         for x, y in zip(c.grad(), want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_a_cache_of_more_rows_than_an_entry_can_name(H):
+    """Copies and gathers; the call is told of 2^33 rows, of which it is given the first."""
+    g = gen(11)
+    D = 576
+    cache = torch.randn(200, D, generator=g, device=DEV).to(BF16)
+    q = torch.randn(2, H, D, generator=g, device=DEV).to(BF16)
+    rows = torch.randint(-1, 200, (2, 130), generator=g, device=DEV).int()
+    lse = torch.full((2, H), 8.0, device=DEV)
+    want = satk.latent_rows_weights(q, cache, rows, lse, scale=0.05)
+    out = torch.full_like(want, math.nan)
+    rc = binding.lib().satk_latent_rows_weights(
+        q.data_ptr(), binding.SATK_BF16, 2, H, D, H * D, D, cache.data_ptr(), 2**33, D,
+        rows.data_ptr(), 130, 130, None, 0.05, lse.data_ptr(), out.data_ptr(), 130, None,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and torch.equal(out, want)
