@@ -2,7 +2,7 @@
 //
 // Per token and tile of 128 of its entries:
 //   S[entry, head] = K[entry, :] . Q[head, :]      M = 128 entries, N heads
-//   out[entry]     = 1/H sum_head exp2(scale S - lse)
+//   out[entry]     = 1/H sum_head exp(scale S - lse)
 // The entries are the M side, so that what is summed, the heads, lies along the
 // columns of tensor memory.  There is no maximum to look for: lse is known.
 //
@@ -409,8 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_weights_mma_kernel(const _
 
 // Copies in flight: the oldest panel of a group that has not been handed over waits
 // until one kGroups (DEPTH - 1) further on has found room.  512 tokens x 2048 rows of
-// 544 columns: 64 heads (a ring of 9 panels) 131 us with copies two deep, 163 with
-// gathers; 128 heads (a ring of 4) 192 with gathers, 284 with copies one deep.
+// 544 columns, with warm caches: 64 heads (a ring of 9 panels) 131 us with copies two
+// deep, 163 with gathers; 128 heads (a ring of 4) 192 with gathers, 284 with copies one
+// deep.
 constexpr int kDepth = 2;
 static_assert(kMaxSlots >= kGroups, "a group's next slot is less than a round further");
 
